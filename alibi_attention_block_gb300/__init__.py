@@ -21,6 +21,7 @@ from . import _abi
 from ._abi import BlkError  # noqa: F401
 
 __all__ = ["layernorm_bias", "rmsnorm", "qkv_bias_rope_partial", "rope_inplace", "attn_prefill",
+           "attn_prefill_packed", "attn_prefill_packed_workspace_size", "packed_desc",
            "attn_decode", "attn_decode_workspace_size", "decode_desc",
            "linear", "mlp", "block_desc", "forward_workspace_size", "forward_q8_0_workspace_size", "forward", "forward_host", "ForwardGraph", "HostPipe", "model_desc",
            "model_workspace_size", "model_forward",
@@ -132,6 +133,87 @@ def attn_prefill(q, k, v, alibi=False, slopes=None, scale=None, out=None):
     o = torch.empty((B, S, H, d), dtype=q.dtype, device=q.device) if out is None else out
     _abi.check(_lib().blk_attn_prefill(C.byref(desc), _p(q), _p(k), _p(v), _p(slopes), _p(o),
                                        _dt(q), _stream()), "blk_attn_prefill")
+    return o
+
+
+def _on_current_device(*ts):
+    """The library launches on the current device's stream: every tensor of the
+    call has to be there."""
+    dev = torch.cuda.current_device()
+    for t in ts:
+        if t is not None and t.is_cuda and t.device.index != dev:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+
+
+def _shape(t, want, what):
+    if t is not None and tuple(t.shape) != want:
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {want}")
+
+
+def _int32(t, what):
+    if t.dtype != torch.int32:
+        raise TypeError(f"{what} are int32")
+
+
+def _slopes(slopes, n_heads):
+    if slopes is not None:
+        if slopes.dtype != torch.float32:
+            raise TypeError("ALiBi slopes are fp32")
+        _shape(slopes, (n_heads,), "slopes")
+
+
+def _ws_bytes(workspace):
+    return workspace.numel() * workspace.element_size()
+
+
+def packed_desc(tokens, prompts, n_heads, n_kv_heads, head_dim, prefix_len=0, alibi=False,
+                scale=None):
+    return _abi.PackedDesc(tokens, prompts, n_heads, n_kv_heads, head_dim, prefix_len,
+                           -1.0 if scale is None else scale, 1 if alibi else 0)
+
+
+def attn_prefill_packed_workspace_size(desc) -> int:
+    need = C.c_size_t(0)
+    _abi.check(_lib().blk_attn_prefill_packed_workspace_size(C.byref(desc), C.byref(need)),
+               "blk_attn_prefill_packed_workspace_size")
+    return need.value
+
+
+def attn_prefill_packed(q, k, v, cu_seqlens, k_prefix=None, v_prefix=None, alibi=False,
+                        slopes=None, scale=None, out=None, workspace=None):
+    """Causal attention over packed prompts: q [H, T, d], k/v [Hk, T, d] hold
+    the prompts one behind the other, prompt i in rows cu_seqlens[i] ..
+    cu_seqlens[i+1] - 1 (int32 [prompts + 1] on the device). k_prefix /
+    v_prefix [Hk, P, d]: keys that every prompt sees ahead of its own. Returns
+    o [T, H, d]; rows outside every prompt are not written (pass ``out`` to
+    say what they hold)."""
+    _same(q, k, v, k_prefix, v_prefix, out)
+    H, T, d = q.shape
+    Hk = k.shape[0]
+    _shape(k, (Hk, T, d), "k")
+    _shape(v, (Hk, T, d), "v")
+    if (k_prefix is None) != (v_prefix is None):
+        raise ValueError("k_prefix and v_prefix go together")
+    P = 0 if k_prefix is None else k_prefix.shape[1]
+    _shape(k_prefix, (Hk, P, d), "k_prefix")
+    _shape(v_prefix, (Hk, P, d), "v_prefix")
+    if P == 0:
+        k_prefix = v_prefix = None
+    _int32(cu_seqlens, "cu_seqlens")
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens has shape [prompts + 1]")
+    _slopes(slopes, H)
+    _shape(out, (T, H, d), "out")
+    _on_current_device(q, k, v, k_prefix, v_prefix, cu_seqlens, slopes, out, workspace)
+    desc = packed_desc(T, cu_seqlens.numel() - 1, H, Hk, d, P, alibi, scale)
+    if workspace is None:
+        workspace = torch.empty(attn_prefill_packed_workspace_size(desc), dtype=torch.uint8,
+                                device=q.device)
+    o = torch.empty((T, H, d), dtype=q.dtype, device=q.device) if out is None else out
+    _abi.check(_lib().blk_attn_prefill_packed(
+        C.byref(desc), _p(q), _p(k), _p(v), _p(k_prefix), _p(v_prefix), _p(cu_seqlens),
+        _p(slopes), _p(o), _p(workspace), _ws_bytes(workspace), _dt(q), _stream()),
+        "blk_attn_prefill_packed")
     return o
 
 

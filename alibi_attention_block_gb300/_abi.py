@@ -39,6 +39,11 @@ class AttnDesc(C.Structure):
                 ("head_dim", i64), ("softmax_scale", f32), ("causal", i32), ("alibi", i32)]
 
 
+class PackedDesc(C.Structure):
+    _fields_ = [("tokens", i64), ("prompts", i64), ("n_heads", i64), ("n_kv_heads", i64),
+                ("head_dim", i64), ("prefix_len", i64), ("softmax_scale", f32), ("alibi", i32)]
+
+
 class DecodeDesc(C.Structure):
     _fields_ = [("batch", i64), ("max_seq", i64), ("n_heads", i64), ("n_kv_heads", i64),
                 ("head_dim", i64), ("softmax_scale", f32), ("alibi", i32)]
@@ -93,6 +98,10 @@ _PROTOS = {
                                             C.c_int, vp]),
     "blk_rope_inplace": (C.c_int, [vp, vp, i64, i64, i64, i64, i32, f32, C.c_int, vp]),
     "blk_attn_prefill": (C.c_int, [C.POINTER(AttnDesc), vp, vp, vp, vp, vp, C.c_int, vp]),
+    "blk_attn_prefill_packed_workspace_size": (C.c_int, [C.POINTER(PackedDesc),
+                                                         C.POINTER(C.c_size_t)]),
+    "blk_attn_prefill_packed": (C.c_int, [C.POINTER(PackedDesc), vp, vp, vp, vp, vp, vp, vp, vp,
+                                          vp, C.c_size_t, C.c_int, vp]),
     "blk_linear": (C.c_int, [vp, vp, vp, vp, vp, vp, i64, i64, i64, C.c_int, vp]),
     "blk_mlp_workspace_size": (C.c_int, [C.POINTER(MlpDesc), C.POINTER(C.c_size_t)]),
     "blk_mlp": (C.c_int, [C.POINTER(MlpDesc), vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, C.c_size_t,

@@ -136,6 +136,9 @@ size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 bool is_pow2(int64_t v) { return v > 0 && (v & (v - 1)) == 0; }
 
 constexpr int64_t kI32 = 0x7fffffff;
+// rows of a packed batch or a shared prefix: tile coordinates past the end
+// still fit 32 bits
+constexpr int64_t kMaxPackedRows = int64_t(1) << 30;
 
 }  // namespace
 
@@ -306,6 +309,34 @@ blk_status validate_attn_desc(const blk_attn_desc* d) {
     const int64_t nq = (d->seq + 127) / 128;
     BLK_REQUIRE(nq * d->batch * d->n_heads <= kI32, "grid too large");
     return BLK_OK;
+}
+
+blk_status validate_packed_desc(const blk_packed_desc* d) {
+    BLK_REQUIRE(d, "descriptor is NULL");
+    BLK_REQUIRE(d->tokens >= 1 && d->tokens <= kMaxPackedRows, "tokens out of range");
+    BLK_REQUIRE(d->prompts >= 1 && d->prompts <= (int64_t(1) << 20), "prompts out of range");
+    BLK_REQUIRE(d->prefix_len >= 0 && d->prefix_len <= kMaxPackedRows, "prefix_len out of range");
+    BLK_REQUIRE(d->n_heads >= 1 && d->n_kv_heads >= 1 && d->n_heads <= kI32 &&
+                    d->n_heads % d->n_kv_heads == 0,
+                "n_heads must be a positive multiple of n_kv_heads");
+    if (d->head_dim != 64 && d->head_dim != 128 && d->head_dim != 160)
+        return fail(BLK_EUNSUPPORTED, "attention head_dim must be 64, 128 or 160 (got %lld)",
+                    static_cast<long long>(d->head_dim));
+    BLK_REQUIRE(d->alibi == 0 || d->alibi == 1, "alibi must be 0 or 1");
+    BLK_REQUIRE(std::isfinite(d->softmax_scale), "softmax_scale must be finite");
+    // work items: at most one per unit of work and query head
+    const int64_t units = packed_max_units(d->tokens, d->prompts, static_cast<int>(d->n_heads),
+                                           static_cast<int>(d->n_kv_heads),
+                                           static_cast<int>(d->head_dim));
+    BLK_REQUIRE(units <= kI32 / d->n_heads, "tokens, prompts and n_heads too large");
+    return BLK_OK;
+}
+
+size_t packed_ws_bytes(const blk_packed_desc* d) {
+    return align256(sizeof(int4) * (1 + static_cast<size_t>(packed_max_units(
+                                            d->tokens, d->prompts, static_cast<int>(d->n_heads),
+                                            static_cast<int>(d->n_kv_heads),
+                                            static_cast<int>(d->head_dim)))));
 }
 
 blk_status validate_block(const blk_block_desc* d, const blk_block_weights* w,
@@ -624,6 +655,37 @@ blk_status run_attn(const blk_attn_desc* d, const void* q, const void* k, const 
 }
 
 
+blk_status run_attn_packed(const blk_packed_desc* d, const void* q, const void* k, const void* v,
+                           const void* k_prefix, const void* v_prefix, const int32_t* cu_seqlens,
+                           const float* slopes, void* o, void* workspace, DType dt, cudaStream_t s,
+                           DevState* ds) {
+    AttnArgs a{};
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.o = o;
+    a.B = 1;
+    a.S = static_cast<int>(d->tokens);
+    a.H = static_cast<int>(d->n_heads);
+    a.Hk = static_cast<int>(d->n_kv_heads);
+    a.d = static_cast<int>(d->head_dim);
+    a.scale = d->softmax_scale > 0.f ? d->softmax_scale
+                                     : static_cast<float>(1.0 / std::sqrt(static_cast<double>(d->head_dim)));
+    a.alibi = d->alibi;
+    a.slopes = slopes;
+    a.err = ds->err;
+    a.num_sms = ds->sms;
+    PackedArgs p{};
+    p.k_prefix = k_prefix;
+    p.v_prefix = v_prefix;
+    p.cu_seqlens = cu_seqlens;
+    p.prompts = static_cast<int>(d->prompts);
+    p.prefix = static_cast<int>(d->prefix_len);
+    p.plan = static_cast<int4*>(workspace);
+    const cudaError_t e = launch_attention_packed(dt, a, p, s);
+    return e == cudaSuccess ? BLK_OK : cuda_fail(e, "packed attention launch");
+}
+
 blk_status forward_impl(const blk_block_desc* d, const blk_block_weights* w,
                         const blk_q8_weights* q8, const void* x, void* y, void* workspace,
                         size_t ws_bytes, blk_dtype dt, blk_stream_t s, void* const* events,
@@ -851,6 +913,45 @@ blk_status blk_attn_prefill(const blk_attn_desc* d, const void* q, const void* k
     DevState* ds = nullptr;
     if ((st = dev_state(&ds)) != BLK_OK) return st;
     return run_attn(d, q, k, v, alibi_slopes, o, to_dt(dt), reinterpret_cast<cudaStream_t>(s), ds);
+}
+
+blk_status blk_attn_prefill_packed_workspace_size(const blk_packed_desc* d, size_t* bytes) {
+    blk_status st = validate_packed_desc(d);
+    if (st != BLK_OK) return st;
+    BLK_REQUIRE(bytes != nullptr, "bytes is NULL");
+    *bytes = packed_ws_bytes(d);
+    return BLK_OK;
+}
+
+blk_status blk_attn_prefill_packed(const blk_packed_desc* d, const void* q, const void* k,
+                                   const void* v, const void* k_prefix, const void* v_prefix,
+                                   const int32_t* cu_seqlens, const float* alibi_slopes, void* o,
+                                   void* workspace, size_t ws_bytes, blk_dtype dt, blk_stream_t s) {
+    BLK_REQUIRE(valid_dt(dt), "dtype must be BLK_F16 or BLK_BF16");
+    blk_status st = validate_packed_desc(d);
+    if (st != BLK_OK) return st;
+    BLK_CHECK_PTR(q, true);
+    BLK_CHECK_PTR(k, true);
+    BLK_CHECK_PTR(v, true);
+    BLK_CHECK_PTR(k_prefix, d->prefix_len > 0);
+    BLK_CHECK_PTR(v_prefix, d->prefix_len > 0);
+    BLK_REQUIRE(d->prefix_len > 0 || (!k_prefix && !v_prefix),
+                "k_prefix / v_prefix given with prefix_len = 0");
+    BLK_CHECK_PTR(o, true);
+    BLK_REQUIRE(cu_seqlens != nullptr && (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) == 0,
+                "cu_seqlens must be a 4-byte aligned device pointer");
+    BLK_REQUIRE(d->alibi || !alibi_slopes, "alibi_slopes given with alibi = 0");
+    if (d->alibi && !alibi_slopes && !is_pow2(d->n_heads))
+        return fail(BLK_EUNSUPPORTED, "standard ALiBi slopes need a power-of-two head count");
+    BLK_REQUIRE(!alibi_slopes || (reinterpret_cast<uintptr_t>(alibi_slopes) & 3u) == 0,
+                "alibi_slopes must be 4-byte aligned");
+    const size_t need = packed_ws_bytes(d);
+    if (!workspace || ws_bytes < need || !aligned16(workspace))
+        return fail(BLK_EWORKSPACE, "workspace needs %zu bytes, 16-byte aligned", need);
+    DevState* ds = nullptr;
+    if ((st = dev_state(&ds)) != BLK_OK) return st;
+    return run_attn_packed(d, q, k, v, k_prefix, v_prefix, cu_seqlens, alibi_slopes, o, workspace,
+                           to_dt(dt), reinterpret_cast<cudaStream_t>(s), ds);
 }
 
 blk_status blk_linear(const void* x, const void* w, const void* bias, const void* res1,

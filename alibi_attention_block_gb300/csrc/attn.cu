@@ -7,6 +7,115 @@
 
 namespace blk {
 
+namespace {
+
+// ---- packed prompts: the work list -----------------------------------
+// The prompts' lengths are device data, so the list of work units is built on
+// the device, by one block: unit l of a prompt of n units attends to about l
+// key tiles more than unit 0, so a counting sort by l (in kPlanBins bins of
+// 2^shift units), largest first, orders the units heaviest first, as the
+// dense kernels order theirs. The order within a bin is whatever the shared
+// atomics give; every unit is computed alike wherever it stands, so results
+// do not depend on it. A table that is not nondecreasing within [0, tokens]
+// (it cannot be checked on the host) has its entries clamped, and units past
+// the list's room are dropped.
+constexpr int kPlanThreads = 1024, kPlanBins = 2048;
+
+__global__ void __launch_bounds__(kPlanThreads)
+    plan_kernel(const int32_t* cu, int prompts, int tokens, int unit, int shift, int max_units,
+                int4* plan, int pdl) {
+    __shared__ int at[kPlanBins];
+    __shared__ int warp_sum[kPlanThreads / 32];
+    if (pdl) {
+        pdl_wait();
+        pdl_launch_dependents();
+    }
+    const int t = threadIdx.x, lane = t & 31, warp = t / 32;
+    at[t] = 0;
+    at[t + kPlanThreads] = 0;
+    __syncthreads();
+    // one warp per prompt, one lane per unit
+    auto each_unit = [&](auto&& f) {
+        for (int b = warp; b < prompts; b += kPlanThreads / 32) {
+            const int first = min(max(cu[b], 0), tokens);
+            const int len = min(max(cu[b + 1], first), tokens) - first;
+            const int n = len / unit + (len % unit != 0);
+            for (int l = lane; l < n; l += 32) f(first, len, l);
+        }
+    };
+    each_unit([&](int, int, int l) { atomicAdd(&at[l >> shift], 1); });
+    __syncthreads();
+    // exclusive sums from the last bin down: thread t owns bins hi and hi - 1
+    const int hi = kPlanBins - 1 - 2 * t;
+    const int c0 = at[hi], c1 = at[hi - 1];
+    int sum = c0 + c1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+    }
+    if (lane == 31) warp_sum[warp] = sum;
+    __syncthreads();
+    if (warp == 0) {
+        int w = warp_sum[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += v;
+        }
+        warp_sum[lane] = w;
+    }
+    __syncthreads();
+    const int end = sum + (warp ? warp_sum[warp - 1] : 0);
+    at[hi] = end - c0 - c1;
+    at[hi - 1] = end - c1;
+    if (t == 0) plan[0] = make_int4(min(warp_sum[kPlanThreads / 32 - 1], max_units), 0, 0, 0);
+    __syncthreads();
+    each_unit([&](int first, int len, int l) {
+        const int i = atomicAdd(&at[l >> shift], 1);
+        if (i < max_units) plan[1 + i] = make_int4(first, len, l, 0);
+    });
+}
+
+// positions per unit: a query-tile pair, or the GQA kernel's block
+int packed_unit(int H, int Hk, int d) {
+    const bool pair = d == 64 || (d == 128 && H == Hk);
+    return pair ? 256 : gqa_block_positions(H, Hk);
+}
+
+}  // namespace
+
+int64_t packed_max_units(int64_t tokens, int64_t prompts, int H, int Hk, int d) {
+    return tokens / packed_unit(H, Hk, d) + prompts;
+}
+
+cudaError_t launch_attention_packed(DType dt, const AttnArgs& a, const PackedArgs& p,
+                                    cudaStream_t s) {
+    const int unit = packed_unit(a.H, a.Hk, a.d);
+    const int64_t max_units = packed_max_units(a.S, p.prompts, a.H, a.Hk, a.d);
+    int shift = 0;
+    while ((static_cast<int64_t>(a.S / unit) >> shift) >= kPlanBins) ++shift;
+    AttnPack<true> pack;
+    pack.plan = p.plan;
+    pack.prefix = p.prefix;
+    // without a prefix the maps are never used: any valid one will do
+    const void* kp = p.prefix ? p.k_prefix : a.k;
+    const void* vp = p.prefix ? p.v_prefix : a.v;
+    const uint64_t rows = p.prefix ? p.prefix : a.S;
+    if (!make_tmap_3d(&pack.tmPK, dt, kp, a.Hk, rows, a.d, 128) ||
+        !make_tmap_3d(&pack.tmPV, dt, vp, a.Hk, rows, a.d, 128))
+        return cudaErrorInvalidValue;
+    const bool pdl = pdl_allowed(s);
+    cudaError_t e = launch_pdl(pdl, plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p.cu_seqlens,
+                               p.prompts, a.S, unit, shift, static_cast<int>(max_units), p.plan,
+                               pdl ? 1 : 0);
+    if (e != cudaSuccess) return e;
+    if (a.d == 64) return launch_attention_pair64_packed(dt, a, pack, max_units, s);
+    if (a.d == 128 && a.H == a.Hk)
+        return launch_attention_pair128_packed(dt, a, pack, max_units, s);
+    return launch_attention_gqa_packed(dt, a, pack, max_units, s);
+}
+
 cudaError_t launch_attention(DType dt, const AttnArgs& a, cudaStream_t s) {
     if (a.B == 0 || a.S == 0) return cudaSuccess;
     switch (a.d) {

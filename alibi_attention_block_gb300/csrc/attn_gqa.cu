@@ -49,7 +49,7 @@ namespace blk {
 
 namespace {
 
-constexpr int kGqaThreads = 192;
+constexpr int gqa_threads(bool packed) { return packed ? 224 : 192; }  // packed: one more warp
 constexpr int kTQ = 128;  // query rows per tile (G heads x R positions)
 constexpr int kTK = 128;  // keys per tile
 constexpr float kLog2e = 1.4426950408889634f;
@@ -82,14 +82,35 @@ struct GqaPack {
 // This CTA's items: (position block pb, batch b, kv head g, head chunk hc).
 // Round r gives item r*Gd + blockIdx on even rounds and r*Gd + Gd-1-blockIdx
 // on odd ones (Gd = grid size); items are numbered latest block first.
+// Packed prompts (PACKED): a unit of the plan's list is a block of R
+// positions of one prompt; the prefix's nP key tiles come ahead of the
+// prompt's own.
+template <bool PACKED>
 struct GqaCursor {
     int item, it, pb, b, g, hc, p0, nkv;
     bool valid;
+    int start_row, len, nP, prefix;
     __device__ __forceinline__ int item_of(int round) const {
         const int Gd = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
         return round * Gd + ((round & 1) ? Gd - 1 - c : c);
     }
-    __device__ __forceinline__ void decode(const AttnArgs& a, const GqaPack& pk, int nblk) {
+    __device__ __forceinline__ void decode(const AttnArgs& a, const GqaPack& pk,
+                                           const AttnPack<PACKED>& pack, int nblk) {
+        if constexpr (PACKED) {
+            const int per_unit = a.Hk * pk.nhc;
+            const int4 u = pack.plan[1 + item / per_unit];
+            const int rest = item % per_unit;
+            hc = rest % pk.nhc;
+            g = rest / pk.nhc;
+            b = 0;
+            start_row = u.x;
+            len = u.y;
+            p0 = u.z * pk.R;
+            prefix = pack.prefix;
+            nP = (prefix + kTK - 1) / kTK;
+            nkv = nP + (min(p0 + pk.R, len) + kTK - 1) / kTK;
+            return;
+        }
         const int per_block = a.B * a.Hk * pk.nhc;
         pb = nblk - 1 - item / per_block;
         int rest = item % per_block;
@@ -101,30 +122,33 @@ struct GqaCursor {
         const int last = min(p0 + pk.R, a.S);  // one past the block's last position
         nkv = (last + kTK - 1) / kTK;
     }
-    __device__ __forceinline__ void start(const AttnArgs& a, const GqaPack& pk, int nblk,
-                                          int n_items) {
+    __device__ __forceinline__ void start(const AttnArgs& a, const GqaPack& pk,
+                                          const AttnPack<PACKED>& pack, int nblk, int n_items) {
         it = 0;
         item = item_of(0);
         valid = item < n_items;
-        if (valid) decode(a, pk, nblk);
+        if (valid) decode(a, pk, pack, nblk);
     }
-    __device__ __forceinline__ void next(const AttnArgs& a, const GqaPack& pk, int nblk,
-                                         int n_items) {
+    __device__ __forceinline__ void next(const AttnArgs& a, const GqaPack& pk,
+                                          const AttnPack<PACKED>& pack, int nblk, int n_items) {
         ++it;
         item = item_of(it);
         valid = item < n_items;
-        if (valid) decode(a, pk, nblk);
+        if (valid) decode(a, pk, pack, nblk);
     }
 };
 
-template <typename T, int D, bool ALIBI>
-__global__ void __launch_bounds__(kGqaThreads, 1)
+template <typename T, int D, bool ALIBI, bool PACKED>
+__global__ void __launch_bounds__(gqa_threads(PACKED), 1)
     attn_gqa_kernel(const __grid_constant__ CUtensorMap tmQ,
                     const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const AttnArgs a,
-                    const GqaPack pk) {
+                    const GqaPack pk, const __grid_constant__ AttnPack<PACKED> pack) {
     using Cfg = GqaCfg<D>;
     constexpr int kQB = Cfg::kQBufs, kKS = Cfg::kKStages, kVS = Cfg::kVStages;
+    // packed ALiBi: key tiles from the diagonal down, as in attn_pair.cu (the
+    // bias is largest there, so the rescale of O stays rare)
+    constexpr bool kRev = ALIBI && PACKED;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align_1024(smem_raw);
     const uint32_t sQ = smem_u32(smem);
@@ -143,13 +167,16 @@ __global__ void __launch_bounds__(kGqaThreads, 1)
     auto k_empty = [&](int i) { return bar0 + 104u + 8u * i; };
     auto v_full = [&](int i) { return bar0 + 120u + 8u * i; };
     auto v_empty = [&](int i) { return bar0 + 136u + 8u * i; };
+    // packed: V tile i is ready once the last warp has seen it land and
+    // cleared the rows behind the prompt's end
+    auto v_ready = [&](int i) { return PACKED ? bar0 + 160u + 8u * i : v_full(i); };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kOffBar + 152);
 
     const int warp = threadIdx.x / 32;
     const int lane = threadIdx.x & 31;
     const int G = pk.G, R = pk.R;
     const int nblk = (a.S + R - 1) / R;
-    const int n_items = nblk * a.B * a.Hk * pk.nhc;
+    int n_items = nblk * a.B * a.Hk * pk.nhc;
 
     if (threadIdx.x == 0) {
         for (int x = 0; x < 2; ++x) {
@@ -161,6 +188,7 @@ __global__ void __launch_bounds__(kGqaThreads, 1)
             mbar_init(k_empty(x), 1);
             mbar_init(v_full(x), 1);
             mbar_init(v_empty(x), 1);
+            if (PACKED) mbar_init(v_ready(x), 1);
         }
         mbar_init(p_full, 4);
         mbar_init(pv_done, 1);
@@ -182,22 +210,36 @@ __global__ void __launch_bounds__(kGqaThreads, 1)
         pdl_wait();  // inputs written by the previous kernel are visible from here on
         pdl_launch_dependents();
     }
+    if constexpr (PACKED) n_items = pack.plan[0].x * a.Hk * pk.nhc;
 
     if (warp == 0) {
         if (lane == 0) {
             const uint64_t pol_kv = l2_evict_last_policy(), pol_q = l2_evict_first_policy();
-            GqaCursor c;
-            c.start(a, pk, nblk, n_items);
+            GqaCursor<PACKED> c;
+            c.start(a, pk, pack, nblk, n_items);
             int gk = 0, gv = 0;  // K and V tiles loaded so far (ring positions)
             bool ok = true;
+            // the map and first row of step j's key tile
+            auto tile_source = [&](int j, const CUtensorMap* own, bool v, int& krow) {
+                if constexpr (PACKED) {
+                    const int kt = kRev ? c.nkv - 1 - j : j;
+                    krow = kt < c.nP ? kt * kTK : c.start_row + (kt - c.nP) * kTK;
+                    return kt < c.nP ? (v ? &pack.tmPV : &pack.tmPK) : own;
+                } else {
+                    krow = j * kTK;
+                    return own;
+                }
+            };
             auto load_k = [&](int j) -> bool {
                 const int st = gk % kKS;
                 if (!mbar_wait(k_empty(st), ((gk / kKS) & 1) ^ 1u, a.err)) return false;
                 mbar_expect_tx(k_full(st), Cfg::kTileBytes);
+                int krow;
+                const CUtensorMap* m = tile_source(j, &tmK, false, krow);
 #pragma unroll
                 for (int sub = 0; sub < Cfg::kSub; ++sub)
-                    tma_load_3d_hint(sK + st * Cfg::kTileBytes + sub * kTK * 128, &tmK, k_full(st),
-                                sub * 64, j * kTK, c.b * a.Hk + c.g, pol_kv);
+                    tma_load_3d_hint(sK + st * Cfg::kTileBytes + sub * kTK * 128, m, k_full(st),
+                                sub * 64, krow, c.b * a.Hk + c.g, pol_kv);
                 ++gk;
                 return true;
             };
@@ -205,10 +247,12 @@ __global__ void __launch_bounds__(kGqaThreads, 1)
                 const int st = gv % kVS;
                 if (!mbar_wait(v_empty(st), ((gv / kVS) & 1) ^ 1u, a.err)) return false;
                 mbar_expect_tx(v_full(st), Cfg::kTileBytes);
+                int krow;
+                const CUtensorMap* m = tile_source(j, &tmV, true, krow);
 #pragma unroll
                 for (int sub = 0; sub < Cfg::kSub; ++sub)
-                    tma_load_3d_hint(sV + st * Cfg::kTileBytes + sub * kTK * 128, &tmV, v_full(st),
-                                sub * 64, j * kTK, c.b * a.Hk + c.g, pol_kv);
+                    tma_load_3d_hint(sV + st * Cfg::kTileBytes + sub * kTK * 128, m, v_full(st),
+                                sub * 64, krow, c.b * a.Hk + c.g, pol_kv);
                 ++gv;
                 return true;
             };
@@ -224,7 +268,8 @@ __global__ void __launch_bounds__(kGqaThreads, 1)
 #pragma unroll
                     for (int sub = 0; sub < Cfg::kSub; ++sub)
                         tma_load_3d_hint(sQ + qb * Cfg::kTileBytes + sub * kTQ * 128 + i * R * 128,
-                                    &tmQ, q_full(qb), sub * 64, c.p0,
+                                    &tmQ, q_full(qb), sub * 64,
+                                    (PACKED ? c.start_row : 0) + c.p0,
                                     c.b * a.H + c.g * G + c.hc * pk.Gt + i, pol_q);
                 }
                 // consumption order: K(0), then K(j+1) ahead of V(j)
@@ -233,7 +278,7 @@ __global__ void __launch_bounds__(kGqaThreads, 1)
                     if (j + 1 < c.nkv) ok = load_k(j + 1);
                     if (ok) ok = load_v(j);
                 }
-                c.next(a, pk, nblk, n_items);
+                c.next(a, pk, pack, nblk, n_items);
             }
         }
     } else if (warp == 1) {
@@ -273,7 +318,7 @@ __global__ void __launch_bounds__(kGqaThreads, 1)
             // overwrites O, so it also waits for the previous item's read-out)
             auto issue_pv = [&](bool first) -> bool {
                 const int st = gv % kVS;
-                if (!mbar_wait(v_full(st), (gv / kVS) & 1, a.err)) return false;
+                if (!mbar_wait(v_ready(st), (gv / kVS) & 1, a.err)) return false;
                 if (!mbar_wait(p_full, gp & 1, a.err)) return false;
                 if (first && itx > 0 && !mbar_wait(o_free, (itx - 1) & 1, a.err)) return false;
                 tc_fence_after();
@@ -288,8 +333,8 @@ __global__ void __launch_bounds__(kGqaThreads, 1)
                 ++gp;
                 return true;
             };
-            GqaCursor c;
-            c.start(a, pk, nblk, n_items);
+            GqaCursor<PACKED> c;
+            c.start(a, pk, pack, nblk, n_items);
             bool ok = true;
             while (ok && c.valid) {
                 const int qb = c.it % kQB;
@@ -305,7 +350,32 @@ __global__ void __launch_bounds__(kGqaThreads, 1)
                     if (ok) ok = issue_pv(j == 0);
                 }
                 ++itx;
-                c.next(a, pk, nblk, n_items);
+                c.next(a, pk, pack, nblk, n_items);
+            }
+        }
+    } else if (PACKED && warp == 6) {
+        if constexpr (PACKED) {
+            // passes each V tile on, the rows behind the prompt's end cleared
+            // (see attn_pair.cu)
+            GqaCursor<PACKED> c;
+            c.start(a, pk, pack, nblk, n_items);
+            int gv = 0;
+            bool ok = true;
+            while (ok && c.valid) {
+                for (int j = 0; j < c.nkv; ++j, ++gv) {
+                    const int kt = kRev ? c.nkv - 1 - j : j;
+                    const int st = gv % kVS;
+                    if (!mbar_wait(v_full(st), (gv / kVS) & 1, a.err)) {
+                        ok = false;
+                        break;
+                    }
+                    const int rows = kt < c.nP ? kTK : c.len - (kt - c.nP) * kTK;
+                    if (rows < kTK)
+                        clear_tile_rows<Cfg::kSub>(sV + st * Cfg::kTileBytes, kTK, rows, lane);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(v_ready(st));
+                }
+                c.next(a, pk, pack, nblk, n_items);
             }
         }
     } else {
@@ -320,8 +390,8 @@ __global__ void __launch_bounds__(kGqaThreads, 1)
         const int hl = row / R;          // head of this row within the tile
         const int rpos = row - hl * R;   // position offset within the block
         float slope_l2 = 0.f;
-        GqaCursor c;
-        c.start(a, pk, nblk, n_items);
+        GqaCursor<PACKED> c;
+        c.start(a, pk, pack, nblk, n_items);
         int g = 0;  // key tiles processed (across items)
         bool ok = true;
         bool pend = false;      // an item's O is still in TMEM
@@ -338,7 +408,8 @@ __global__ void __launch_bounds__(kGqaThreads, 1)
                                                      static_cast<float>(a.H));
                 slope_l2 = slope * kLog2e;
             }
-            const int lim_abs = min(pos, a.S - 1);  // keys <= lim_abs are visible
+            const int S_own = PACKED ? c.len : a.S;
+            const int lim_abs = min(pos, S_own - 1);  // (own) keys <= lim_abs are visible
             float m_used = -INFINITY;  // running max, log2 domain
             float l = 0.f;
             for (int j = 0; j < c.nkv; ++j, ++g) {
@@ -353,16 +424,31 @@ __global__ void __launch_bounds__(kGqaThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_free(sb));
-                const int kbase = j * kTK;
+                const int kt = kRev ? c.nkv - 1 - j : j;  // key tile of this step
+                const int kbase = (PACKED ? kt - c.nP : j) * kTK;  // packed: < 0 in the prefix
                 if constexpr (ALIBI) {
-                    const float sk = slope_l2 * static_cast<float>(kbase);
+                    // packed: key positions from the block's first (a row's
+                    // constant), small where the weight is not
+                    const int kpos = !PACKED      ? kbase
+                                     : kbase >= 0 ? kbase - c.p0
+                                                  : kt * kTK - c.prefix - c.p0;
+                    const float sk = slope_l2 * static_cast<float>(kpos);
 #pragma unroll
                     for (int i = 0; i < kTK; ++i)
                         r[i] = __float_as_uint(fmaf(__uint_as_float(r[i]), scale_l2,
                                                     fmaf(slope_l2, static_cast<float>(i), sk)));
                 }
-                if (kbase + kTK - 1 > c.p0 || kbase + kTK > a.S) {
-                    const int lim = lim_abs - kbase;
+                bool masked;
+                int lim;
+                if constexpr (PACKED) {
+                    masked = kbase >= 0 ? kbase + kTK - 1 > c.p0 || kbase + kTK > c.len
+                                        : (kt + 1) * kTK > c.prefix;
+                    lim = kbase >= 0 ? lim_abs - kbase : c.prefix - 1 - kt * kTK;
+                } else {
+                    masked = kbase + kTK - 1 > c.p0 || kbase + kTK > a.S;
+                    lim = lim_abs - kbase;
+                }
+                if (masked) {
 #pragma unroll
                     for (int i = 0; i < kTK; ++i)
                         if (i > lim) r[i] = __float_as_uint(-INFINITY);
@@ -460,9 +546,9 @@ __global__ void __launch_bounds__(kGqaThreads, 1)
             if (!ok) break;
             pend = true;
             pend_l = l;
-            pend_row = (in_group && pos < a.S) ? (static_cast<int64_t>(c.b) * a.S + pos) * a.H + h
-                                               : -1;
-            c.next(a, pk, nblk, n_items);
+            const int64_t row0 = PACKED ? c.start_row : static_cast<int64_t>(c.b) * a.S;
+            pend_row = (in_group && pos < S_own) ? (row0 + pos) * a.H + h : -1;
+            c.next(a, pk, pack, nblk, n_items);
         }
         // the last item's O
         if (ok && pend && mbar_wait(pv_done, (g - 1) & 1, a.err)) {
@@ -493,8 +579,9 @@ __global__ void __launch_bounds__(kGqaThreads, 1)
     }
 }
 
-template <typename T, int D, bool ALIBI>
-cudaError_t launch_gqa_d(DType dt, const AttnArgs& a, const GqaPack& pk, cudaStream_t s) {
+template <typename T, int D, bool ALIBI, bool PACKED>
+cudaError_t launch_gqa_d(DType dt, const AttnArgs& a, const GqaPack& pk,
+                         const AttnPack<PACKED>& pack, int64_t items, cudaStream_t s) {
     const int R = pk.R;
     using Cfg = GqaCfg<D>;
     CUtensorMap tq, tk, tv;
@@ -502,42 +589,63 @@ cudaError_t launch_gqa_d(DType dt, const AttnArgs& a, const GqaPack& pk, cudaStr
         !make_tmap_3d(&tk, dt, a.k, static_cast<uint64_t>(a.B) * a.Hk, a.S, D, kTK) ||
         !make_tmap_3d(&tv, dt, a.v, static_cast<uint64_t>(a.B) * a.Hk, a.S, D, kTK))
         return cudaErrorInvalidValue;
-    auto kern = attn_gqa_kernel<T, D, ALIBI>;
+    auto kern = attn_gqa_kernel<T, D, ALIBI, PACKED>;
     {
         const cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(kern), Cfg::kSmem);
         if (e != cudaSuccess) return e;
     }
-    const int64_t items = static_cast<int64_t>((a.S + R - 1) / R) * a.B * a.Hk * pk.nhc;
     if (items > 0x7fffffff) return cudaErrorInvalidValue;
     const int64_t grid = items < a.num_sms ? items : a.num_sms;
     AttnArgs ap = a;
     ap.pdl = pdl_allowed(s);
-    (void)launch_pdl(ap.pdl != 0, kern, dim3(static_cast<unsigned>(grid)), dim3(kGqaThreads), Cfg::kSmem, s,
-                     tq, tk, tv, ap, pk);
+    (void)launch_pdl(ap.pdl != 0, kern, dim3(static_cast<unsigned>(grid)), dim3(gqa_threads(PACKED)),
+                     Cfg::kSmem, s, tq, tk, tv, ap, pk, pack);
     return cudaGetLastError();
 }
 
-template <typename T, int D>
-cudaError_t launch_gqa_a(DType dt, const AttnArgs& a, const GqaPack& pk, cudaStream_t s) {
-    return a.alibi ? launch_gqa_d<T, D, true>(dt, a, pk, s)
-                   : launch_gqa_d<T, D, false>(dt, a, pk, s);
+template <typename T, int D, bool PACKED>
+cudaError_t launch_gqa_a(DType dt, const AttnArgs& a, const GqaPack& pk,
+                         const AttnPack<PACKED>& pack, int64_t items, cudaStream_t s) {
+    return a.alibi ? launch_gqa_d<T, D, true>(dt, a, pk, pack, items, s)
+                   : launch_gqa_d<T, D, false>(dt, a, pk, pack, items, s);
+}
+
+template <bool PACKED>
+cudaError_t launch_gqa(DType dt, const AttnArgs& a, const GqaPack& pk, const AttnPack<PACKED>& pack,
+                       int64_t items, cudaStream_t s) {
+    if (dt == DType::F16)
+        return a.d == 128 ? launch_gqa_a<__half, 128>(dt, a, pk, pack, items, s)
+                          : launch_gqa_a<__half, 160>(dt, a, pk, pack, items, s);
+    return a.d == 128 ? launch_gqa_a<__nv_bfloat16, 128>(dt, a, pk, pack, items, s)
+                      : launch_gqa_a<__nv_bfloat16, 160>(dt, a, pk, pack, items, s);
+}
+
+GqaPack gqa_pack(int H, int Hk) {
+    GqaPack pk;
+    pk.G = H / Hk;
+    pk.Gt = pk.G < 16 ? pk.G : 16;
+    pk.R = (kTQ / pk.Gt) / 8 * 8;
+    pk.nhc = (pk.G + pk.Gt - 1) / pk.Gt;
+    return pk;
 }
 
 }  // namespace
 
+int gqa_block_positions(int H, int Hk) { return gqa_pack(H, Hk).R; }
+
 cudaError_t launch_attention_gqa(DType dt, const AttnArgs& a, cudaStream_t s) {
     if (a.Hk <= 0 || a.H % a.Hk || (a.d != 128 && a.d != 160)) return cudaErrorInvalidValue;
     if (a.B == 0 || a.S == 0) return cudaSuccess;
-    GqaPack pk;
-    pk.G = a.H / a.Hk;
-    pk.Gt = pk.G < 16 ? pk.G : 16;
-    pk.R = (kTQ / pk.Gt) / 8 * 8;
-    pk.nhc = (pk.G + pk.Gt - 1) / pk.Gt;
-    if (dt == DType::F16)
-        return a.d == 128 ? launch_gqa_a<__half, 128>(dt, a, pk, s)
-                          : launch_gqa_a<__half, 160>(dt, a, pk, s);
-    return a.d == 128 ? launch_gqa_a<__nv_bfloat16, 128>(dt, a, pk, s)
-                      : launch_gqa_a<__nv_bfloat16, 160>(dt, a, pk, s);
+    const GqaPack pk = gqa_pack(a.H, a.Hk);
+    const int64_t items = static_cast<int64_t>((a.S + pk.R - 1) / pk.R) * a.B * a.Hk * pk.nhc;
+    return launch_gqa(dt, a, pk, AttnPack<false>{}, items, s);
+}
+
+cudaError_t launch_attention_gqa_packed(DType dt, const AttnArgs& a, const AttnPack<true>& pack,
+                                        int64_t max_units, cudaStream_t s) {
+    if (a.Hk <= 0 || a.H % a.Hk || (a.d != 128 && a.d != 160)) return cudaErrorInvalidValue;
+    const GqaPack pk = gqa_pack(a.H, a.Hk);
+    return launch_gqa(dt, a, pk, pack, max_units * a.Hk * pk.nhc, s);
 }
 
 }  // namespace blk

@@ -82,7 +82,9 @@ struct PairCfg {
     // tile), one per item parity
     static constexpr int kOffTabBar = kOffBar + 256;
     static constexpr int kOffBias = kOffTabBar + 16;
-    static constexpr int kSmem = kOffBias + 2 * 2 * kTK * 4 + 1024;  // + alignment slack
+    // packed prompts: one more barrier per V stage
+    static constexpr int kOffVReady = kOffBias + 2 * 2 * kTK * 4;
+    static constexpr int kSmem = kOffVReady + 8 * kStages + 1024;  // + alignment slack
     static constexpr uint32_t kColP = 256;              // P_x at kColP + 64 x
     static constexpr uint32_t kColO = 384;              // O_x at kColO + D x
     static constexpr uint32_t kTmemCols = 512;
@@ -92,14 +94,36 @@ struct PairCfg {
 // 2i+1 (the second absent when the tile count is odd and i is the last pair).
 // Round r gives item r*G + blockIdx on even rounds and r*G + G-1-blockIdx on
 // odd ones; items are numbered heaviest pair first.
+//
+// Packed prompts (PACKED): items are (unit, head); a unit is a query-tile
+// pair of one prompt, from the plan's list (heaviest first), and the prompt's
+// nP prefix tiles come ahead of its own key tiles.
+template <bool PACKED>
 struct PairCursor {
     int item, it, i, b, h, g, nA, nB;
     bool valid;
+    // packed: the prompt's first row and length, the prefix's key tiles
+    int start_row, len, nP, prefix;
     __device__ __forceinline__ int item_of(int round) const {
         const int G = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
         return round * G + ((round & 1) ? G - 1 - c : c);
     }
-    __device__ __forceinline__ void decode(const AttnArgs& a, int nq, int np) {
+    __device__ __forceinline__ void decode(const AttnArgs& a, const AttnPack<PACKED>& pack, int nq,
+                                           int np) {
+        if constexpr (PACKED) {
+            const int4 u = pack.plan[1 + item / a.H];
+            h = item % a.H;
+            b = 0;
+            g = h / (a.H / a.Hk);
+            start_row = u.x;
+            len = u.y;
+            i = u.z;
+            prefix = pack.prefix;
+            nP = (prefix + kTK - 1) / kTK;
+            nA = nP + 2 * i + 1;
+            nB = (2 * i + 1) * kTQ < len ? nP + 2 * i + 2 : 0;
+            return;
+        }
         const int bh_count = a.B * a.H;
         i = np - 1 - item / bh_count;
         const int bh = item % bh_count;
@@ -109,26 +133,29 @@ struct PairCursor {
         nA = 2 * i + 1;                          // key tiles of query tile 2i
         nB = (2 * i + 1 < nq) ? 2 * i + 2 : 0;   // of query tile 2i+1, if present
     }
-    __device__ __forceinline__ void start(const AttnArgs& a, int nq, int np, int n_items) {
+    __device__ __forceinline__ void start(const AttnArgs& a, const AttnPack<PACKED>& pack, int nq, int np,
+                                          int n_items) {
         it = 0;
         item = item_of(0);
         valid = item < n_items;
-        if (valid) decode(a, nq, np);
+        if (valid) decode(a, pack, nq, np);
     }
-    __device__ __forceinline__ void next(const AttnArgs& a, int nq, int np, int n_items) {
+    __device__ __forceinline__ void next(const AttnArgs& a, const AttnPack<PACKED>& pack, int nq, int np,
+                                          int n_items) {
         ++it;
         item = item_of(it);
         valid = item < n_items;
-        if (valid) decode(a, nq, np);
+        if (valid) decode(a, pack, nq, np);
     }
     __device__ __forceinline__ int n_kv() const { return nB ? nB : nA; }
 };
 
-template <typename T, int D, bool ALIBI>
+template <typename T, int D, bool ALIBI, bool PACKED>
 __global__ void __launch_bounds__(kPairThreads, 1)
     attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ,
                      const __grid_constant__ CUtensorMap tmK,
-                     const __grid_constant__ CUtensorMap tmV, const AttnArgs a) {
+                     const __grid_constant__ CUtensorMap tmV, const AttnArgs a,
+                     const __grid_constant__ AttnPack<PACKED> pack) {
     using Cfg = PairCfg<D>;
     constexpr int kStages = Cfg::kStages;
     // With ALiBi the key tiles are walked from the diagonal down: the bias
@@ -154,6 +181,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     auto v_full = [&](int i) { return bar0 + 112u + 8u * (kStages + i); };
     auto k_empty = [&](int i) { return bar0 + 112u + 8u * (2 * kStages + i); };
     auto v_empty = [&](int i) { return bar0 + 112u + 8u * (3 * kStages + i); };
+    // packed: V tile i is ready once warp 3 has seen it land and cleared the
+    // rows behind the prompt's end
+    auto v_ready = [&](int i) { return PACKED ? sQ + Cfg::kOffVReady + 8u * i : v_full(i); };
     uint32_t* tmem_slot =
         reinterpret_cast<uint32_t*>(smem + Cfg::kOffBar + 112 + 32 * kStages);
 
@@ -161,7 +191,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const int lane = threadIdx.x & 31;
     const int nq = (a.S + kTQ - 1) / kTQ;
     const int np = (nq + 1) / 2;
-    const int n_items = np * a.B * a.H;
+    int n_items = np * a.B * a.H;
 
     if (threadIdx.x == 0) {
         for (int x = 0; x < 2; ++x) {
@@ -180,6 +210,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             mbar_init(v_full(i), 1);
             mbar_init(k_empty(i), 2);
             mbar_init(v_empty(i), 2);
+            if (PACKED) mbar_init(v_ready(i), 1);
         }
         fence_barrier_init();
         tma_prefetch_desc(&tmQ);
@@ -198,6 +229,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         pdl_wait();  // inputs written by the previous kernel are visible from here on
         pdl_launch_dependents();
     }
+    if constexpr (PACKED) n_items = pack.plan[0].x * a.H;
     // registers: the launch gives every thread kLaunchRegs; warpgroup 0 (TMA,
     // MMA issue) gives most of its share to the two softmax warpgroups, which
     // hold a row's 128 scores and 64 packed probabilities at once
@@ -208,8 +240,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if (warp == 0) {
         if (lane == 0) {
             const uint64_t pol_kv = l2_evict_last_policy(), pol_q = l2_evict_first_policy();
-            PairCursor c;
-            c.start(a, nq, np, n_items);
+            PairCursor<PACKED> c;
+            c.start(a, pack, nq, np, n_items);
             int gkv = 0;  // K/V tiles loaded so far (ring position)
             bool ok = true;
             while (ok && c.valid) {
@@ -220,7 +252,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
                     for (int sub = 0; sub < Cfg::kSub; ++sub)
                         tma_load_3d_hint(sQ + (2 * qb + x) * Cfg::kQBytes + sub * kTQ * 128, &tmQ,
-                                    q_full(qb), sub * 64, (2 * c.i + x) * kTQ, c.b * a.H + c.h, pol_q);
+                                    q_full(qb), sub * 64, (PACKED ? c.start_row : 0) + (2 * c.i + x) * kTQ,
+                                    c.b * a.H + c.h, pol_q);
                 }
                 const int nkv = c.n_kv();
                 for (int j = 0; j < nkv; ++j, ++gkv) {
@@ -228,6 +261,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     const int st = gkv % kStages;
                     const uint32_t ph = (gkv / kStages) & 1;
                     const uint32_t sK = sKV + (2 * st) * Cfg::kKVBytes;
+                    const CUtensorMap *mK = &tmK, *mV = &tmV;
+                    int krow = kt * kTK;
+                    if constexpr (PACKED) {
+                        if (kt < c.nP) {
+                            mK = &pack.tmPK;
+                            mV = &pack.tmPV;
+                        } else {
+                            krow = c.start_row + (kt - c.nP) * kTK;
+                        }
+                    }
                     if (!mbar_wait_inl(k_empty(st), ph ^ 1u, a.err)) {
                         ok = false;
                         break;
@@ -235,7 +278,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     mbar_expect_tx(k_full(st), Cfg::kKVBytes);
 #pragma unroll
                     for (int sub = 0; sub < Cfg::kSub; ++sub)
-                        tma_load_3d_hint(sK + sub * kTK * 128, &tmK, k_full(st), sub * 64, kt * kTK,
+                        tma_load_3d_hint(sK + sub * kTK * 128, mK, k_full(st), sub * 64, krow,
                                     c.b * a.Hk + c.g, pol_kv);
                     if (!mbar_wait_inl(v_empty(st), ph ^ 1u, a.err)) {
                         ok = false;
@@ -244,10 +287,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     mbar_expect_tx(v_full(st), Cfg::kKVBytes);
 #pragma unroll
                     for (int sub = 0; sub < Cfg::kSub; ++sub)
-                        tma_load_3d_hint(sK + Cfg::kKVBytes + sub * kTK * 128, &tmV, v_full(st),
-                                    sub * 64, kt * kTK, c.b * a.Hk + c.g, pol_kv);
+                        tma_load_3d_hint(sK + Cfg::kKVBytes + sub * kTK * 128, mV, v_full(st),
+                                    sub * 64, krow, c.b * a.Hk + c.g, pol_kv);
                 }
-                c.next(a, nq, np, n_items);
+                c.next(a, pack, nq, np, n_items);
             }
         }
     } else if (warp == 1 || warp == 2) {
@@ -297,8 +340,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 ++gp;
                 return true;
             };
-            PairCursor c;
-            c.start(a, nq, np, n_items);
+            PairCursor<PACKED> c;
+            c.start(a, pack, nq, np, n_items);
             int gkv = 0;
             bool ok = true;
             while (ok && c.valid) {
@@ -335,7 +378,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         tc_commit(k_empty(stn));
                         if (j + 1 == qlast) tc_commit(q_empty(qb));
                     }
-                    if (!mbar_wait_inl(v_full(stj), (gj / kStages) & 1, a.err)) {
+                    if (!mbar_wait_inl(v_ready(stj), (gj / kStages) & 1, a.err)) {
                         ok = false;
                         break;
                     }
@@ -347,8 +390,33 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 }
                 gkv += nkv;
                 if (nx > 0) ++itx;
-                c.next(a, nq, np, n_items);
+                c.next(a, pack, nq, np, n_items);
             }
+        }
+    } else if constexpr (PACKED) {
+        // warp 3: passes each V tile on once it has landed, the rows behind
+        // the prompt's end (the next prompt's) cleared: their P is 0, but 0
+        // times a non-finite value of another prompt is not
+        PairCursor<PACKED> c;
+        c.start(a, pack, nq, np, n_items);
+        int gkv = 0;
+        bool ok = true;
+        while (ok && c.valid) {
+            const int nkv = c.n_kv();
+            for (int j = 0; j < nkv; ++j, ++gkv) {
+                const int kt = kRev ? nkv - 1 - j : j;
+                const int st = gkv % kStages;
+                if (!mbar_wait_inl(v_full(st), (gkv / kStages) & 1, a.err)) {
+                    ok = false;
+                    break;
+                }
+                const int rows = kt < c.nP ? kTK : c.len - (kt - c.nP) * kTK;
+                if (rows < kTK)
+                    clear_tile_rows<Cfg::kSub>(sKV + (2 * st + 1) * Cfg::kKVBytes, kTK, rows, lane);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(v_ready(st));
+            }
+            c.next(a, pack, nq, np, n_items);
         }
     }
     } else {
@@ -363,8 +431,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const uint32_t tO = tmem_base + Cfg::kColO + D * x;
         const uint32_t tP = tmem_base + Cfg::kColP + 64u * x;
         const float scale_l2 = a.scale * kLog2e;
-        PairCursor c;
-        c.start(a, nq, np, n_items);
+        PairCursor<PACKED> c;
+        c.start(a, pack, nq, np, n_items);
         int g = 0;  // key tiles processed (across items)
         bool ok = true;
         // The read-out of an item's O waits for its last PV; it is deferred to
@@ -377,7 +445,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         while (ok && c.valid) {
             const int nx = x ? c.nB : c.nA;
             if (nx == 0) {
-                c.next(a, nq, np, n_items);
+                c.next(a, pack, nq, np, n_items);
                 continue;
             }
             const int qt = 2 * c.i + x;
@@ -419,7 +487,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_free(x));
                 const int kt = kRev ? nx - 1 - j : j;  // key tile of this step
-                const int kbase = kt * kTK;
+                // packed ALiBi: key positions count from the query tile's first
+                // (a row's constant), so that slope * position stays small,
+                // hence exact, where its weight is not
+                const int kbase = !PACKED        ? kt * kTK
+                                  : kt >= c.nP ? (kt - c.nP - qt) * kTK
+                                               : kt * kTK - c.prefix - qt * kTK;
                 // ALiBi: u = s*scale*log2(e) + slope*log2(e)*i, one paired FMA
                 // per two scores from the column table; the tile's uniform
                 // part slope*log2(e)*kbase joins the max and the exponent
@@ -440,8 +513,18 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         r[i + 3] = __float_as_uint(u3);
                     }
                 }
-                if (kt == qt || kbase + kTK > a.S) {
-                    const int lim = min(qpos, a.S - 1) - kbase;  // keys <= lim are visible
+                bool masked;
+                int lim;  // keys <= lim are visible
+                if constexpr (PACKED) {
+                    const int kown = (kt - c.nP) * kTK;  // own key position, < 0 in the prefix
+                    masked = kt >= c.nP ? kt - c.nP == qt || kown + kTK > c.len
+                                        : (kt + 1) * kTK > c.prefix;
+                    lim = kt >= c.nP ? min(qpos, c.len - 1) - kown : c.prefix - 1 - kt * kTK;
+                } else {
+                    masked = kt == qt || kbase + kTK > a.S;
+                    lim = min(qpos, a.S - 1) - kbase;
+                }
+                if (masked) {
 #pragma unroll
                     for (int i = 0; i < kTK; ++i)
                         if (i > lim) r[i] = __float_as_uint(-INFINITY);
@@ -536,8 +619,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             if (!ok) break;
             pend = true;
             pend_l = l;
-            pend_row = qpos < a.S ? (static_cast<int64_t>(c.b) * a.S + qpos) * a.H + c.h : -1;
-            c.next(a, nq, np, n_items);
+            if constexpr (PACKED)
+                pend_row = qpos < c.len ? (static_cast<int64_t>(c.start_row) + qpos) * a.H + c.h : -1;
+            else
+                pend_row = qpos < a.S ? (static_cast<int64_t>(c.b) * a.S + qpos) * a.H + c.h : -1;
+            c.next(a, pack, nq, np, n_items);
         }
         // the last item's O
         if (ok && pend && mbar_wait_inl(pv_done(x), (g - 1) & 1, a.err)) {
@@ -565,8 +651,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
 }
 
-template <typename T, bool ALIBI>
-cudaError_t launch_pair(DType dt, const AttnArgs& a, cudaStream_t s) {
+template <typename T, bool ALIBI, bool PACKED>
+cudaError_t launch_pair(DType dt, const AttnArgs& a, const AttnPack<PACKED>& pack, int64_t items,
+                        cudaStream_t s) {
     constexpr int D = 64;
     using Cfg = PairCfg<D>;
     CUtensorMap tq, tk, tv;
@@ -574,30 +661,42 @@ cudaError_t launch_pair(DType dt, const AttnArgs& a, cudaStream_t s) {
         !make_tmap_3d(&tk, dt, a.k, static_cast<uint64_t>(a.B) * a.Hk, a.S, D, kTK) ||
         !make_tmap_3d(&tv, dt, a.v, static_cast<uint64_t>(a.B) * a.Hk, a.S, D, kTK))
         return cudaErrorInvalidValue;
-    auto kern = attn_pair_kernel<T, D, ALIBI>;
+    auto kern = attn_pair_kernel<T, D, ALIBI, PACKED>;
     {
         const cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(kern), Cfg::kSmem);
         if (e != cudaSuccess) return e;
     }
-    const int64_t nq = (a.S + kTQ - 1) / kTQ;
-    const int64_t items = (nq + 1) / 2 * a.B * a.H;
     if (items > 0x7fffffff) return cudaErrorInvalidValue;
     const int64_t grid = items < a.num_sms ? items : a.num_sms;
     AttnArgs ap = a;
     ap.pdl = pdl_allowed(s);
     (void)launch_pdl(ap.pdl != 0, kern, dim3(static_cast<unsigned>(grid)), dim3(kPairThreads), Cfg::kSmem, s,
-                     tq, tk, tv, ap);
+                     tq, tk, tv, ap, pack);
     return cudaGetLastError();
+}
+
+template <bool PACKED>
+cudaError_t launch_pair_t(DType dt, const AttnArgs& a, const AttnPack<PACKED>& pack, int64_t items,
+                          cudaStream_t s) {
+    if (dt == DType::F16)
+        return a.alibi ? launch_pair<__half, true>(dt, a, pack, items, s)
+                       : launch_pair<__half, false>(dt, a, pack, items, s);
+    return a.alibi ? launch_pair<__nv_bfloat16, true>(dt, a, pack, items, s)
+                   : launch_pair<__nv_bfloat16, false>(dt, a, pack, items, s);
 }
 
 }  // namespace
 
 cudaError_t launch_attention_pair64(DType dt, const AttnArgs& a, cudaStream_t s) {
     if (a.d != 64) return cudaErrorInvalidValue;
-    if (dt == DType::F16)
-        return a.alibi ? launch_pair<__half, true>(dt, a, s) : launch_pair<__half, false>(dt, a, s);
-    return a.alibi ? launch_pair<__nv_bfloat16, true>(dt, a, s)
-                   : launch_pair<__nv_bfloat16, false>(dt, a, s);
+    const int64_t nq = (a.S + kTQ - 1) / kTQ;
+    return launch_pair_t(dt, a, AttnPack<false>{}, (nq + 1) / 2 * a.B * a.H, s);
+}
+
+cudaError_t launch_attention_pair64_packed(DType dt, const AttnArgs& a, const AttnPack<true>& pack,
+                                           int64_t max_units, cudaStream_t s) {
+    if (a.d != 64) return cudaErrorInvalidValue;
+    return launch_pair_t(dt, a, pack, max_units * a.H, s);
 }
 
 }  // namespace blk

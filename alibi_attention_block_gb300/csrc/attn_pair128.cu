@@ -65,14 +65,33 @@ struct Cfg {
     static constexpr uint32_t kTmemCols = 512;
 };
 
+// Packed prompts (PACKED): as in attn_pair.cu, items are (unit of the plan's
+// list, head) and the prefix's nP key tiles come ahead of the prompt's own.
+template <bool PACKED>
 struct PairCursor {
     int item, it, i, b, h, g, nA, nB;
     bool valid;
+    int start_row, len, nP, prefix;
     __device__ __forceinline__ int item_of(int round) const {
         const int G = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
         return round * G + ((round & 1) ? G - 1 - c : c);
     }
-    __device__ __forceinline__ void decode(const AttnArgs& a, int nq, int np) {
+    __device__ __forceinline__ void decode(const AttnArgs& a, const AttnPack<PACKED>& pack, int nq,
+                                           int np) {
+        if constexpr (PACKED) {
+            const int4 u = pack.plan[1 + item / a.H];
+            h = item % a.H;
+            b = 0;
+            g = h / (a.H / a.Hk);
+            start_row = u.x;
+            len = u.y;
+            i = u.z;
+            prefix = pack.prefix;
+            nP = (prefix + kTK - 1) / kTK;
+            nA = nP + 2 * i + 1;
+            nB = (2 * i + 1) * kTQ < len ? nP + 2 * i + 2 : 0;
+            return;
+        }
         const int bh_count = a.B * a.H;
         i = np - 1 - item / bh_count;
         const int bh = item % bh_count;
@@ -82,26 +101,29 @@ struct PairCursor {
         nA = 2 * i + 1;
         nB = (2 * i + 1 < nq) ? 2 * i + 2 : 0;
     }
-    __device__ __forceinline__ void start(const AttnArgs& a, int nq, int np, int n_items) {
+    __device__ __forceinline__ void start(const AttnArgs& a, const AttnPack<PACKED>& pack, int nq, int np,
+                                          int n_items) {
         it = 0;
         item = item_of(0);
         valid = item < n_items;
-        if (valid) decode(a, nq, np);
+        if (valid) decode(a, pack, nq, np);
     }
-    __device__ __forceinline__ void next(const AttnArgs& a, int nq, int np, int n_items) {
+    __device__ __forceinline__ void next(const AttnArgs& a, const AttnPack<PACKED>& pack, int nq, int np,
+                                          int n_items) {
         ++it;
         item = item_of(it);
         valid = item < n_items;
-        if (valid) decode(a, nq, np);
+        if (valid) decode(a, pack, nq, np);
     }
     __device__ __forceinline__ int n_kv() const { return nB ? nB : nA; }
 };
 
-template <typename T, bool ALIBI>
+template <typename T, bool ALIBI, bool PACKED>
 __global__ void __launch_bounds__(kP128Threads, 1)
     attn_pair128_kernel(const __grid_constant__ CUtensorMap tmQ,
                         const __grid_constant__ CUtensorMap tmK,
-                        const __grid_constant__ CUtensorMap tmV, const AttnArgs a) {
+                        const __grid_constant__ CUtensorMap tmV, const AttnArgs a,
+                        const __grid_constant__ AttnPack<PACKED> pack) {
     constexpr int kStages = Cfg::kStages;
     // With ALiBi the key tiles are walked from the diagonal down: the bias
     // +slope*j is largest there, so the row max is set by the first tile and
@@ -125,13 +147,17 @@ __global__ void __launch_bounds__(kP128Threads, 1)
     auto v_full = [&](int i) { return bar0 + 96u + 8u * (kStages + i); };
     auto k_empty = [&](int i) { return bar0 + 96u + 8u * (2 * kStages + i); };
     auto v_empty = [&](int i) { return bar0 + 96u + 8u * (3 * kStages + i); };
+    // packed: V tile i is ready once warp 3 has seen it land and cleared the
+    // rows behind the prompt's end
+    auto v_ready = [&](int i) { return PACKED ? bar0 + 112u + 32u * kStages + 8u * i : v_full(i); };
+    static_assert(112 + 40 * kStages <= 256, "barrier space");
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kOffBar + 104 + 32 * kStages);
 
     const int warp = threadIdx.x / 32;
     const int lane = threadIdx.x & 31;
     const int nq = (a.S + kTQ - 1) / kTQ;
     const int np = (nq + 1) / 2;
-    const int n_items = np * a.B * a.H;
+    int n_items = np * a.B * a.H;
 
     if (threadIdx.x == 0) {
         for (int x = 0; x < 2; ++x) {
@@ -149,6 +175,7 @@ __global__ void __launch_bounds__(kP128Threads, 1)
             mbar_init(v_full(i), 1);
             mbar_init(k_empty(i), 1);
             mbar_init(v_empty(i), 1);
+            if (PACKED) mbar_init(v_ready(i), 1);
         }
         mbar_init(s_free, 4);
         fence_barrier_init();
@@ -168,14 +195,15 @@ __global__ void __launch_bounds__(kP128Threads, 1)
         pdl_wait();  // inputs written by the previous kernel are visible from here on
         pdl_launch_dependents();
     }
+    if constexpr (PACKED) n_items = pack.plan[0].x * a.H;
     static_assert(4 * kRegsControl + 8 * kRegsSoftmax <= 12 * kLaunchRegs,
                   "register split exceeds the launch's registers");
     if (warp < 4) {
         setmaxnreg_dec<kRegsControl>();
         if (warp == 0 && lane == 0) {
             const uint64_t pol_kv = l2_evict_last_policy(), pol_q = l2_evict_first_policy();
-            PairCursor c;
-            c.start(a, nq, np, n_items);
+            PairCursor<PACKED> c;
+            c.start(a, pack, nq, np, n_items);
             int gkv = 0;
             int itq[2] = {0, 0};  // Q fills per query tile
             bool ok = true;
@@ -189,7 +217,8 @@ __global__ void __launch_bounds__(kP128Threads, 1)
 #pragma unroll
                     for (int sub = 0; sub < Cfg::kSub; ++sub)
                         tma_load_3d_hint(sQ + x * Cfg::kQBytes + sub * kTQ * 128, &tmQ, q_full(x),
-                                    sub * 64, (2 * c.i + x) * kTQ, c.b * a.H + c.h, pol_q);
+                                    sub * 64, (PACKED ? c.start_row : 0) + (2 * c.i + x) * kTQ,
+                                    c.b * a.H + c.h, pol_q);
                     ++itq[x];
                 }
                 const int nkv = c.n_kv();
@@ -198,6 +227,16 @@ __global__ void __launch_bounds__(kP128Threads, 1)
                     const int st = gkv % kStages;
                     const uint32_t ph = (gkv / kStages) & 1;
                     const uint32_t sK = sKV + (2 * st) * Cfg::kKVBytes;
+                    const CUtensorMap *mK = &tmK, *mV = &tmV;
+                    int krow = kt * kTK;
+                    if constexpr (PACKED) {
+                        if (kt < c.nP) {
+                            mK = &pack.tmPK;
+                            mV = &pack.tmPV;
+                        } else {
+                            krow = c.start_row + (kt - c.nP) * kTK;
+                        }
+                    }
                     if (!mbar_wait_inl(k_empty(st), ph ^ 1u, a.err)) {
                         ok = false;
                         break;
@@ -205,7 +244,7 @@ __global__ void __launch_bounds__(kP128Threads, 1)
                     mbar_expect_tx(k_full(st), Cfg::kKVBytes);
 #pragma unroll
                     for (int sub = 0; sub < Cfg::kSub; ++sub)
-                        tma_load_3d_hint(sK + sub * kTK * 128, &tmK, k_full(st), sub * 64, kt * kTK,
+                        tma_load_3d_hint(sK + sub * kTK * 128, mK, k_full(st), sub * 64, krow,
                                     c.b * a.Hk + c.g, pol_kv);
                     if (!mbar_wait_inl(v_empty(st), ph ^ 1u, a.err)) {
                         ok = false;
@@ -214,10 +253,10 @@ __global__ void __launch_bounds__(kP128Threads, 1)
                     mbar_expect_tx(v_full(st), Cfg::kKVBytes);
 #pragma unroll
                     for (int sub = 0; sub < Cfg::kSub; ++sub)
-                        tma_load_3d_hint(sK + Cfg::kKVBytes + sub * kTK * 128, &tmV, v_full(st),
-                                    sub * 64, kt * kTK, c.b * a.Hk + c.g, pol_kv);
+                        tma_load_3d_hint(sK + Cfg::kKVBytes + sub * kTK * 128, mV, v_full(st),
+                                    sub * 64, krow, c.b * a.Hk + c.g, pol_kv);
                 }
-                c.next(a, nq, np, n_items);
+                c.next(a, pack, nq, np, n_items);
             }
         } else if (warp == 1 && lane == 0) {
             constexpr uint32_t fmt = dt_traits<T>::mma_fmt;
@@ -267,8 +306,8 @@ __global__ void __launch_bounds__(kP128Threads, 1)
                 ++gp[x];
                 return true;
             };
-            PairCursor c;
-            c.start(a, nq, np, n_items);
+            PairCursor<PACKED> c;
+            c.start(a, pack, nq, np, n_items);
             int gkv = 0;
             int itq[2] = {0, 0};
             bool ok = true;
@@ -298,7 +337,7 @@ __global__ void __launch_bounds__(kP128Threads, 1)
                     const int gj = gkv + j;
                     const int stj = gj % kStages;
                     const bool more = j + 1 < nkv;
-                    if (!mbar_wait_inl(v_full(stj), (gj / kStages) & 1, a.err)) {
+                    if (!mbar_wait_inl(v_ready(stj), (gj / kStages) & 1, a.err)) {
                         ok = false;
                         break;
                     }
@@ -328,7 +367,34 @@ __global__ void __launch_bounds__(kP128Threads, 1)
                     if (more) tc_commit(k_empty((gj + 1) % kStages));
                 }
                 gkv += nkv;
-                c.next(a, nq, np, n_items);
+                c.next(a, pack, nq, np, n_items);
+            }
+        } else if (PACKED && warp == 3) {
+            if constexpr (PACKED) {
+                // passes each V tile on, the rows behind the prompt's end
+                // cleared (see attn_pair.cu)
+                PairCursor<PACKED> c;
+                c.start(a, pack, nq, np, n_items);
+                int gkv = 0;
+                bool ok = true;
+                while (ok && c.valid) {
+                    const int nkv = c.n_kv();
+                    for (int j = 0; j < nkv; ++j, ++gkv) {
+                        const int kt = kRev ? nkv - 1 - j : j;
+                        const int st = gkv % kStages;
+                        if (!mbar_wait_inl(v_full(st), (gkv / kStages) & 1, a.err)) {
+                            ok = false;
+                            break;
+                        }
+                        const int rows = kt < c.nP ? kTK : c.len - (kt - c.nP) * kTK;
+                        if (rows < kTK)
+                            clear_tile_rows<Cfg::kSub>(sKV + (2 * st + 1) * Cfg::kKVBytes, kTK, rows,
+                                                       lane);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(v_ready(st));
+                    }
+                    c.next(a, pack, nq, np, n_items);
+                }
             }
         }
     } else {
@@ -341,8 +407,8 @@ __global__ void __launch_bounds__(kP128Threads, 1)
         const uint32_t tP = tmem_base + Cfg::kColP + 64u * x;
         const uint32_t tO = tmem_base + Cfg::kColO + D * x;
         const float scale_l2 = a.scale * kLog2e;
-        PairCursor c;
-        c.start(a, nq, np, n_items);
+        PairCursor<PACKED> c;
+        c.start(a, pack, nq, np, n_items);
         int g = 0;
         bool ok = true;
         bool pend = false;
@@ -372,7 +438,7 @@ __global__ void __launch_bounds__(kP128Threads, 1)
         while (ok && c.valid) {
             const int nx = x ? c.nB : c.nA;
             if (nx == 0) {
-                c.next(a, nq, np, n_items);
+                c.next(a, pack, nq, np, n_items);
                 continue;
             }
             const int qt = 2 * c.i + x;
@@ -414,7 +480,10 @@ __global__ void __launch_bounds__(kP128Threads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_free);
                 const int kt = kRev ? nx - 1 - j : j;  // key tile of this step
-                const int kbase = kt * kTK;
+                // packed ALiBi: key positions from the query tile's first
+                const int kbase = !PACKED        ? kt * kTK
+                                  : kt >= c.nP ? (kt - c.nP - qt) * kTK
+                                               : kt * kTK - c.prefix - qt * kTK;
                 // ALiBi: u = s*scale*log2(e) + slope*log2(e)*i, one paired FMA
                 // per two scores from the column table; the tile's uniform
                 // part slope*log2(e)*kbase joins the max and the exponent
@@ -438,8 +507,18 @@ __global__ void __launch_bounds__(kP128Threads, 1)
                         r[i + 3] = __float_as_uint(u3);
                     }
                 }
-                if (kt == qt || kbase + kTK > a.S) {
-                    const int lim = min(qpos, a.S - 1) - kbase;
+                bool masked;
+                int lim;  // keys <= lim are visible
+                if constexpr (PACKED) {
+                    const int kown = (kt - c.nP) * kTK;
+                    masked = kt >= c.nP ? kt - c.nP == qt || kown + kTK > c.len
+                                        : (kt + 1) * kTK > c.prefix;
+                    lim = kt >= c.nP ? min(qpos, c.len - 1) - kown : c.prefix - 1 - kt * kTK;
+                } else {
+                    masked = kt == qt || kbase + kTK > a.S;
+                    lim = min(qpos, a.S - 1) - kbase;
+                }
+                if (masked) {
 #pragma unroll
                     for (int i = 0; i < kTK; ++i)
                         if (i > lim) r[i] = __float_as_uint(-INFINITY);
@@ -520,8 +599,11 @@ __global__ void __launch_bounds__(kP128Threads, 1)
             if (!ok) break;
             pend = true;
             pend_l = l;
-            pend_row = qpos < a.S ? (static_cast<int64_t>(c.b) * a.S + qpos) * a.H + c.h : -1;
-            c.next(a, nq, np, n_items);
+            if constexpr (PACKED)
+                pend_row = qpos < c.len ? (static_cast<int64_t>(c.start_row) + qpos) * a.H + c.h : -1;
+            else
+                pend_row = qpos < a.S ? (static_cast<int64_t>(c.b) * a.S + qpos) * a.H + c.h : -1;
+            c.next(a, pack, nq, np, n_items);
         }
         // the last item's O
         if (ok && pend) {
@@ -538,38 +620,50 @@ __global__ void __launch_bounds__(kP128Threads, 1)
     }
 }
 
-template <typename T, bool ALIBI>
-cudaError_t launch_pair128_t(DType dt, const AttnArgs& a, cudaStream_t s) {
+template <typename T, bool ALIBI, bool PACKED>
+cudaError_t launch_pair128_t(DType dt, const AttnArgs& a, const AttnPack<PACKED>& pack,
+                             int64_t items, cudaStream_t s) {
     CUtensorMap tq, tk, tv;
     if (!make_tmap_3d(&tq, dt, a.q, static_cast<uint64_t>(a.B) * a.H, a.S, D, kTQ) ||
         !make_tmap_3d(&tk, dt, a.k, static_cast<uint64_t>(a.B) * a.Hk, a.S, D, kTK) ||
         !make_tmap_3d(&tv, dt, a.v, static_cast<uint64_t>(a.B) * a.Hk, a.S, D, kTK))
         return cudaErrorInvalidValue;
-    auto kern = attn_pair128_kernel<T, ALIBI>;
+    auto kern = attn_pair128_kernel<T, ALIBI, PACKED>;
     {
         const cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(kern), Cfg::kSmem);
         if (e != cudaSuccess) return e;
     }
-    const int64_t nq = (a.S + kTQ - 1) / kTQ;
-    const int64_t items = (nq + 1) / 2 * a.B * a.H;
     if (items > 0x7fffffff) return cudaErrorInvalidValue;
     const int64_t grid = items < a.num_sms ? items : a.num_sms;
     AttnArgs ap = a;
     ap.pdl = pdl_allowed(s);
     (void)launch_pdl(ap.pdl != 0, kern, dim3(static_cast<unsigned>(grid)), dim3(kP128Threads), Cfg::kSmem, s,
-                     tq, tk, tv, ap);
+                     tq, tk, tv, ap, pack);
     return cudaGetLastError();
+}
+
+template <bool PACKED>
+cudaError_t launch_pair128(DType dt, const AttnArgs& a, const AttnPack<PACKED>& pack, int64_t items,
+                           cudaStream_t s) {
+    if (dt == DType::F16)
+        return a.alibi ? launch_pair128_t<__half, true>(dt, a, pack, items, s)
+                       : launch_pair128_t<__half, false>(dt, a, pack, items, s);
+    return a.alibi ? launch_pair128_t<__nv_bfloat16, true>(dt, a, pack, items, s)
+                   : launch_pair128_t<__nv_bfloat16, false>(dt, a, pack, items, s);
 }
 
 }  // namespace
 
 cudaError_t launch_attention_pair128(DType dt, const AttnArgs& a, cudaStream_t s) {
     if (a.d != 128) return cudaErrorInvalidValue;
-    if (dt == DType::F16)
-        return a.alibi ? launch_pair128_t<__half, true>(dt, a, s)
-                       : launch_pair128_t<__half, false>(dt, a, s);
-    return a.alibi ? launch_pair128_t<__nv_bfloat16, true>(dt, a, s)
-                   : launch_pair128_t<__nv_bfloat16, false>(dt, a, s);
+    const int64_t nq = (a.S + kTQ - 1) / kTQ;
+    return launch_pair128(dt, a, AttnPack<false>{}, (nq + 1) / 2 * a.B * a.H, s);
+}
+
+cudaError_t launch_attention_pair128_packed(DType dt, const AttnArgs& a, const AttnPack<true>& pack,
+                                            int64_t max_units, cudaStream_t s) {
+    if (a.d != 128) return cudaErrorInvalidValue;
+    return launch_pair128(dt, a, pack, max_units * a.H, s);
 }
 
 }  // namespace blk

@@ -654,6 +654,20 @@ __device__ __forceinline__ float ex2_approx(float x) {
     return y;
 }
 
+// Zero rows [first, rows) of a tile of SUB slices of 128-byte rows (swizzled
+// or not: a swizzle stays within a row) with a whole warp, and make the
+// stores visible to the async proxy (the tensor core's reads).
+template <int SUB>
+__device__ __forceinline__ void clear_tile_rows(uint32_t tile, int rows, int first, int lane) {
+    const int n = (rows - first) * 8;  // 16-byte pieces per slice
+#pragma unroll
+    for (int sub = 0; sub < SUB; ++sub) {
+        const uint32_t at = tile + static_cast<uint32_t>((sub * rows + first) * 128);
+        for (int i = lane; i < n; i += 32) st_shared_v4(at + i * 16, 0u, 0u, 0u, 0u);
+    }
+    fence_proxy_async_smem();
+}
+
 // Round a dynamic shared-memory pointer up so its shared-window offset is a
 // multiple of 1024 bytes (the 128B-swizzle atom); callers reserve 1 KB slack.
 __device__ __forceinline__ uint8_t* align_1024(uint8_t* p) {

@@ -132,6 +132,40 @@ struct AttnArgs {
     int num_sms;          // persistent grid size
 };
 cudaError_t launch_attention(DType dt, const AttnArgs& a, cudaStream_t s);
+
+// ---- K3p: the same kernels over packed prompts (attn.cu: plan and dispatch)
+// What a packed launch needs besides AttnArgs (B = 1, S = packed rows): maps
+// of the shared prefix's keys and values [Hk, prefix, d], and the plan in the
+// workspace: plan[0].x units, then for each {first row, length, unit} of a
+// prompt, heaviest first. A unit is a query-tile pair (256 positions) or the
+// GQA kernel's block of R positions. Empty for dense batches.
+template <bool PACKED>
+struct AttnPack {};
+template <>
+struct AttnPack<true> {
+    CUtensorMap tmPK, tmPV;
+    const int4* plan;
+    int prefix;
+};
+struct PackedArgs {
+    const void* k_prefix;  // [Hk, prefix, d]
+    const void* v_prefix;
+    const int32_t* cu_seqlens;  // device [prompts + 1]
+    int prompts, prefix;
+    int4* plan;                 // workspace: 1 + packed_max_units(...) entries
+};
+// upper bound of a packed call's units (the plan's room)
+int64_t packed_max_units(int64_t tokens, int64_t prompts, int H, int Hk, int d);
+cudaError_t launch_attention_packed(DType dt, const AttnArgs& a, const PackedArgs& p,
+                                    cudaStream_t s);
+cudaError_t launch_attention_pair64_packed(DType dt, const AttnArgs& a, const AttnPack<true>& pack,
+                                           int64_t max_units, cudaStream_t s);
+cudaError_t launch_attention_pair128_packed(DType dt, const AttnArgs& a, const AttnPack<true>& pack,
+                                            int64_t max_units, cudaStream_t s);
+cudaError_t launch_attention_gqa_packed(DType dt, const AttnArgs& a, const AttnPack<true>& pack,
+                                        int64_t max_units, cudaStream_t s);
+// positions per unit of the GQA kernel
+int gqa_block_positions(int H, int Hk);
 // head_dim 64 / 128: the paired-query-tile kernels (attn_pair.cu, attn_pair128.cu)
 cudaError_t launch_attention_pair64(DType dt, const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_attention_pair128(DType dt, const AttnArgs& a, cudaStream_t s);

@@ -163,6 +163,48 @@ typedef struct {
 blk_status blk_attn_prefill(const blk_attn_desc* d, const void* q, const void* k, const void* v,
                             const float* alibi_slopes, void* o, blk_dtype dt, blk_stream_t s);
 
+typedef struct {
+    int64_t tokens;      /* rows of q, k, v and o: the prompts one behind the other (1 .. 2^30) */
+    int64_t prompts;     /* 1 .. 2^20 */
+    int64_t n_heads, n_kv_heads, head_dim;
+    int64_t prefix_len;  /* keys that every prompt shares, ahead of its own (0 .. 2^30) */
+    float softmax_scale; /* <= 0 -> head_dim^-0.5 */
+    int32_t alibi;       /* 0 off; 1: score -= slope_h * (query_pos - key_pos) */
+} blk_packed_desc;
+
+/* blk_attn_prefill over prompts of different lengths packed in one token axis
+ * (the same attention, nnterp "stablelm" 03 Notes and "Bloom in a sovereign
+ * engine", Contribution, per prompt), optionally each behind a prefix that
+ * all prompts share:
+ *   q [H, tokens, d]; k, v [Hk, tokens, d] (what blk_qkv_bias_rope_partial
+ *     writes for batch 1, seq = tokens: a rotary by packed position gives a
+ *     prompt the same scores, they depend on position differences only)
+ *   k_prefix, v_prefix [Hk, prefix_len, d]: keys at positions 0 ..
+ *     prefix_len - 1 of every prompt; both NULL when prefix_len is 0. With a
+ *     rotary, the prompts' q and k must carry positions from prefix_len on.
+ *   cu_seqlens: device int32 [prompts + 1]: prompt i is rows cu_seqlens[i] ..
+ *     cu_seqlens[i+1] - 1, at positions prefix_len, prefix_len + 1, ...; its
+ *     row t sees the prefix and its prompt's rows up to t. Lengths of zero
+ *     are allowed. The table is read on the device, so it cannot be checked
+ *     here: it must be nondecreasing within [0, tokens]; of any other table
+ *     the entries are clamped (wrong rows, but no access outside the tensors)
+ *   alibi_slopes: as for blk_attn_prefill
+ *   o [tokens, H, d]; rows outside every prompt (ahead of cu_seqlens[0],
+ *     behind the last entry) are left as they were
+ * A prompt's results do not depend on the other prompts, nor on what rows
+ * outside it hold (NaN included). As in blk_attn_prefill, a key that a row
+ * does not see has weight 0, so a non-finite value (v) of a later token of
+ * the same prompt and 128-key tile makes a NaN.
+ * GQA: kv head = h / (H / Hk). head_dim in {64, 128, 160}. Two launches (the
+ * work list, the attention); the workspace holds the work list, at least
+ * blk_attn_prefill_packed_workspace_size bytes, 16-byte aligned; calls whose
+ * kernels overlap on the GPU need a workspace each. */
+blk_status blk_attn_prefill_packed_workspace_size(const blk_packed_desc* d, size_t* bytes);
+blk_status blk_attn_prefill_packed(const blk_packed_desc* d, const void* q, const void* k,
+                                   const void* v, const void* k_prefix, const void* v_prefix,
+                                   const int32_t* cu_seqlens, const float* alibi_slopes, void* o,
+                                   void* workspace, size_t ws_bytes, blk_dtype dt, blk_stream_t s);
+
 /* ---- decode step ------------------------------------------------------ */
 
 typedef struct {

@@ -1,0 +1,74 @@
+"""blk_attn_prefill_packed without a GPU: workspace size and refusals, before
+any CUDA call."""
+import ctypes as C
+
+import pytest
+
+from alibi_attention_block_gb300 import _abi, build
+
+FAKE = 0x100000  # 16-byte-aligned stand-in address; validation rejects before any access
+BIG = 1 << 40
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return _abi.load()
+
+
+def desc(tokens=1000, prompts=7, H=32, Hk=8, d=128, prefix=0, scale=-1.0, alibi=0):
+    return _abi.PackedDesc(tokens, prompts, H, Hk, d, prefix, scale, alibi)
+
+
+def call(lib, d, q=FAKE, k=FAKE, v=FAKE, kp=None, vp=None, cu=FAKE, slopes=None, o=FAKE, ws=FAKE,
+         n=BIG, dt=1):
+    return lib.blk_attn_prefill_packed(C.byref(d), q, k, v, kp, vp, cu, slopes, o, ws, n, dt, None)
+
+
+@pytest.mark.parametrize("H,Hk,d,unit", [(32, 32, 64, 256), (8, 2, 64, 256), (16, 16, 128, 256),
+                                         (32, 8, 128, 32), (32, 8, 160, 32), (6, 2, 128, 40),
+                                         (32, 1, 160, 8), (2, 2, 160, 128)])
+def test_workspace_size(lib, H, Hk, d, unit):
+    """One 16-byte entry for each unit that the prompts can have at most, and
+    one for their count, in whole 256 bytes."""
+    need = C.c_size_t(0)
+    assert lib.blk_attn_prefill_packed_workspace_size(C.byref(desc(1000, 7, H, Hk, d)),
+                                                      C.byref(need)) == _abi.BLK_OK
+    assert need.value == -(-16 * (1 + 1000 // unit + 7) // 256) * 256
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(tokens=0), _abi.BLK_EINVAL), (dict(tokens=(1 << 30) + 1), _abi.BLK_EINVAL),
+    (dict(prompts=0), _abi.BLK_EINVAL), (dict(prompts=(1 << 20) + 1), _abi.BLK_EINVAL),
+    (dict(prefix=-1), _abi.BLK_EINVAL), (dict(prefix=(1 << 30) + 1), _abi.BLK_EINVAL),
+    (dict(H=30), _abi.BLK_EINVAL), (dict(H=0), _abi.BLK_EINVAL), (dict(Hk=0), _abi.BLK_EINVAL),
+    (dict(d=96), _abi.BLK_EUNSUPPORTED), (dict(d=32), _abi.BLK_EUNSUPPORTED),
+    (dict(alibi=2), _abi.BLK_EINVAL), (dict(scale=float("nan")), _abi.BLK_EINVAL),
+    (dict(tokens=1 << 30, H=4096, Hk=4096, d=64), _abi.BLK_EINVAL),
+])
+def test_descriptor_refusals(lib, bad, status):
+    need = C.c_size_t(0)
+    assert lib.blk_attn_prefill_packed_workspace_size(C.byref(desc(**bad)), C.byref(need)) == status
+    assert call(lib, desc(**bad), kp=FAKE, vp=FAKE) == status
+
+
+def test_argument_refusals(lib):
+    d = desc()
+    assert lib.blk_attn_prefill_packed_workspace_size(C.byref(d), None) == _abi.BLK_EINVAL
+    assert lib.blk_attn_prefill_packed_workspace_size(None, None) == _abi.BLK_EINVAL
+    for name in ("q", "k", "v", "cu", "o"):
+        assert call(lib, d, **{name: None}) == _abi.BLK_EINVAL, name
+    for name in ("q", "k", "v", "o"):
+        assert call(lib, d, **{name: FAKE + 8}) == _abi.BLK_EINVAL, name
+    assert call(lib, d, cu=FAKE + 2) == _abi.BLK_EINVAL
+    assert call(lib, d, dt=2) == _abi.BLK_EINVAL
+    assert call(lib, d, kp=FAKE) == _abi.BLK_EINVAL          # a prefix of length 0
+    p = desc(prefix=5)
+    assert call(lib, p, kp=FAKE) == _abi.BLK_EINVAL          # v_prefix missing
+    assert call(lib, p, kp=FAKE, vp=FAKE + 4) == _abi.BLK_EINVAL
+    assert call(lib, d, slopes=FAKE) == _abi.BLK_EINVAL      # slopes without ALiBi
+    assert call(lib, desc(alibi=1), slopes=FAKE + 2) == _abi.BLK_EINVAL
+    assert call(lib, desc(H=24, Hk=8, alibi=1)) == _abi.BLK_EUNSUPPORTED
+    assert call(lib, d, ws=None) == _abi.BLK_EWORKSPACE
+    assert call(lib, d, ws=FAKE + 4) == _abi.BLK_EWORKSPACE
+    assert call(lib, d, n=64) == _abi.BLK_EWORKSPACE
