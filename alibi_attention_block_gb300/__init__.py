@@ -23,6 +23,7 @@ from ._abi import BlkError  # noqa: F401
 __all__ = ["layernorm_bias", "rmsnorm", "qkv_bias_rope_partial", "rope_inplace", "attn_prefill",
            "attn_prefill_packed", "attn_prefill_packed_workspace_size", "packed_desc",
            "attn_decode", "attn_decode_workspace_size", "decode_desc",
+           "attn_decode_shared", "attn_decode_shared_workspace_size", "decode_shared_desc",
            "linear", "mlp", "block_desc", "forward_workspace_size", "forward_q8_0_workspace_size", "forward", "forward_host", "ForwardGraph", "HostPipe", "model_desc",
            "model_workspace_size", "model_forward",
            "check_device_status", "BlkError", "library_path"]
@@ -249,6 +250,55 @@ def attn_decode(q, k_cache, v_cache, lens, alibi=False, slopes=None, scale=None,
     _abi.check(_lib().blk_attn_decode(C.byref(desc), _p(q), _p(k_cache), _p(v_cache), _p(lens),
                                       _p(slopes), _p(o), _p(workspace), workspace.numel(), _dt(q),
                                       _stream()), "blk_attn_decode")
+    return o
+
+
+def decode_shared_desc(batch, max_seq, n_heads, n_kv_heads, head_dim, prefix_len, alibi=False,
+                       scale=None):
+    return _abi.DecodeSharedDesc(batch, max_seq, n_heads, n_kv_heads, head_dim, prefix_len,
+                                 -1.0 if scale is None else scale, 1 if alibi else 0)
+
+
+def attn_decode_shared_workspace_size(desc) -> int:
+    need = C.c_size_t(0)
+    _abi.check(_lib().blk_attn_decode_shared_workspace_size(C.byref(desc), C.byref(need)),
+               "blk_attn_decode_shared_workspace_size")
+    return need.value
+
+
+def attn_decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, lens, alibi=False, slopes=None,
+                       scale=None, out=None, workspace=None):
+    """One decode step of a batch that shares a prefix: q [B, H, d] (newest
+    token of each sequence, at position P + lens[b] - 1) against k/v_prefix
+    [Hk, P, d] (None: no prefix), stored once, and each sequence's own caches
+    [B, Hk, S_max, d] of lens[b] keys (int32 [B] on the device; 0: the
+    sequence takes no part, its row is zero). Returns o [B, H, d]."""
+    _same(q, k_prefix, v_prefix, k_cache, v_cache, out)
+    B, H, d = q.shape
+    Hk, S_max = k_cache.shape[1], k_cache.shape[2]
+    _shape(k_cache, (B, Hk, S_max, d), "k_cache")
+    _shape(v_cache, (B, Hk, S_max, d), "v_cache")
+    if (k_prefix is None) != (v_prefix is None):
+        raise ValueError("k_prefix and v_prefix go together")
+    P = 0 if k_prefix is None else k_prefix.shape[1]
+    _shape(k_prefix, (Hk, P, d), "k_prefix")
+    _shape(v_prefix, (Hk, P, d), "v_prefix")
+    if P == 0:
+        k_prefix = v_prefix = None
+    _int32(lens, "lens")
+    _shape(lens, (B,), "lens")
+    _slopes(slopes, H)
+    _shape(out, (B, H, d), "out")
+    _on_current_device(q, k_prefix, v_prefix, k_cache, v_cache, lens, slopes, out, workspace)
+    desc = decode_shared_desc(B, S_max, H, Hk, d, P, alibi, scale)
+    if workspace is None:
+        workspace = torch.empty(attn_decode_shared_workspace_size(desc), dtype=torch.uint8,
+                                device=q.device)
+    o = torch.empty_like(q) if out is None else out
+    _abi.check(_lib().blk_attn_decode_shared(
+        C.byref(desc), _p(q), _p(k_prefix), _p(v_prefix), _p(k_cache), _p(v_cache), _p(lens),
+        _p(slopes), _p(o), _p(workspace), _ws_bytes(workspace), _dt(q), _stream()),
+        "blk_attn_decode_shared")
     return o
 
 

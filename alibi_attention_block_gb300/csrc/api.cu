@@ -232,6 +232,22 @@ bool make_tmap_3d(CUtensorMap* m, DType dt, const void* base, uint64_t planes, u
     return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_queries(CUtensorMap* m, DType dt, const void* base, uint64_t batch,
+                       uint64_t kv_heads, uint64_t group, uint64_t d, uint32_t box_batch) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {d, group, kv_heads, batch};
+    const cuuint64_t strides[3] = {d * 2, group * d * 2, kv_heads * group * d * 2};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(group), 1, box_batch};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUresult r = fn(m, dt == DType::F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                              : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                          4, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 }  // namespace blk
 
 using namespace blk;
@@ -894,6 +910,86 @@ blk_status blk_attn_decode(const blk_decode_desc* d, const void* q, const void* 
     a.alibi = d->alibi;
     const cudaError_t e = launch_attention_decode(to_dt(dt), a, reinterpret_cast<cudaStream_t>(s));
     return e == cudaSuccess ? BLK_OK : cuda_fail(e, "decode attention launch");
+}
+
+static blk_status validate_shared_desc(const blk_decode_shared_desc* d) {
+    BLK_REQUIRE(d != nullptr, "desc is NULL");
+    const blk_decode_desc own{d->batch, d->max_seq, d->n_heads, d->n_kv_heads, d->head_dim,
+                              d->softmax_scale, d->alibi};
+    blk_status st = validate_decode_desc(&own);
+    if (st != BLK_OK) return st;
+    BLK_REQUIRE(d->prefix_len >= 0 && d->prefix_len <= kMaxPackedRows, "prefix_len out of range");
+    BLK_REQUIRE(shared_tiles(d->batch, d->n_heads, d->n_kv_heads, d->prefix_len) <= kI32 - 512,
+                "batch, n_heads and prefix_len too large");
+    return BLK_OK;
+}
+
+static size_t shared_ws_bytes(const blk_decode_shared_desc* d) {
+    return static_cast<size_t>(shared_layout(d->batch, d->n_heads, d->n_kv_heads, d->head_dim,
+                                             d->prefix_len, d->max_seq).total);
+}
+
+blk_status blk_attn_decode_shared_workspace_size(const blk_decode_shared_desc* d, size_t* bytes) {
+    blk_status st = validate_shared_desc(d);
+    if (st != BLK_OK) return st;
+    BLK_REQUIRE(bytes != nullptr, "bytes is NULL");
+    *bytes = shared_ws_bytes(d);
+    return BLK_OK;
+}
+
+blk_status blk_attn_decode_shared(const blk_decode_shared_desc* d, const void* q,
+                                  const void* k_prefix, const void* v_prefix, const void* k_cache,
+                                  const void* v_cache, const int32_t* lens,
+                                  const float* alibi_slopes, void* o, void* workspace,
+                                  size_t ws_bytes, blk_dtype dt, blk_stream_t s) {
+    BLK_REQUIRE(valid_dt(dt), "dtype must be BLK_F16 or BLK_BF16");
+    blk_status st = validate_shared_desc(d);
+    if (st != BLK_OK) return st;
+    BLK_CHECK_PTR(q, true);
+    BLK_CHECK_PTR(k_prefix, d->prefix_len > 0);
+    BLK_CHECK_PTR(v_prefix, d->prefix_len > 0);
+    BLK_REQUIRE(d->prefix_len > 0 || (!k_prefix && !v_prefix),
+                "k_prefix / v_prefix given with prefix_len = 0");
+    BLK_CHECK_PTR(k_cache, true);
+    BLK_CHECK_PTR(v_cache, true);
+    BLK_CHECK_PTR(o, true);
+    BLK_REQUIRE(lens != nullptr && (reinterpret_cast<uintptr_t>(lens) & 3u) == 0,
+                "lens must be a 4-byte aligned device pointer");
+    BLK_REQUIRE(d->alibi || !alibi_slopes, "alibi_slopes given with alibi = 0");
+    if (d->alibi && !alibi_slopes && !is_pow2(d->n_heads))
+        return fail(BLK_EUNSUPPORTED, "standard ALiBi slopes need a power-of-two head count");
+    BLK_REQUIRE(!alibi_slopes || (reinterpret_cast<uintptr_t>(alibi_slopes) & 3u) == 0,
+                "alibi_slopes must be 4-byte aligned");
+    const size_t need = shared_ws_bytes(d);
+    if (!workspace || ws_bytes < need || !aligned16(workspace))
+        return fail(BLK_EWORKSPACE, "workspace needs %zu bytes, 16-byte aligned", need);
+    DevState* ds = nullptr;
+    if ((st = dev_state(&ds)) != BLK_OK) return st;
+    SharedArgs a{};
+    a.own.q = q;
+    a.own.k = k_cache;
+    a.own.v = v_cache;
+    a.own.o = o;
+    a.own.lens = lens;
+    a.own.slopes = alibi_slopes;
+    a.own.B = static_cast<int>(d->batch);
+    a.own.H = static_cast<int>(d->n_heads);
+    a.own.Hk = static_cast<int>(d->n_kv_heads);
+    a.own.d = static_cast<int>(d->head_dim);
+    a.own.S_max = static_cast<int>(d->max_seq);
+    a.own.parts = decode_parts(d->batch, d->n_kv_heads, d->max_seq, d->head_dim, ds->sms);
+    a.own.scale = d->softmax_scale > 0.f ? d->softmax_scale
+                                         : 1.0f / std::sqrt(static_cast<float>(d->head_dim));
+    a.own.alibi = d->alibi;
+    a.k_prefix = k_prefix;
+    a.v_prefix = v_prefix;
+    a.P = static_cast<int>(d->prefix_len);
+    a.ws = static_cast<uint8_t*>(workspace);
+    a.err = ds->err;
+    a.num_sms = ds->sms;
+    const cudaError_t e =
+        launch_attention_decode_shared(to_dt(dt), a, reinterpret_cast<cudaStream_t>(s));
+    return e == cudaSuccess ? BLK_OK : cuda_fail(e, "shared-prefix decode attention launch");
 }
 
 blk_status blk_attn_prefill(const blk_attn_desc* d, const void* q, const void* k, const void* v,

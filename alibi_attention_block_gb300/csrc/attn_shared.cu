@@ -1,0 +1,665 @@
+// K6s: one decode step of attention for a batch that shares a prefix.
+//
+// Sequence b's newest query q[b, h] attends to the prefix's P keys, stored
+// once for the batch (k/v_prefix [Hk, P, d]), and to its own cache. Softmax
+// parts over disjoint key sets merge by their (max, sum), so the prefix is one
+// product for the whole batch: for a kv head, the queries of all sequences and
+// of the head's group are the rows of Q, and S = Q K^T, O = P V run on the
+// tensor cores with each prefix byte read once instead of once per sequence.
+// (the attention of nnterp "stablelm" 03 Notes; ALiBi as in "Bloom in a
+// sovereign engine", Contribution, with the query at position
+// P + lens[b] - 1.)
+//
+// Pass 1 (prefix_kernel): persistent, one CTA per SM. A unit is (kv head, 128
+// query rows: 128 / G sequences); its P keys are nkt tiles of 128. The units'
+// tiles in one line are cut into equal ranges, one per CTA (each range covers
+// at most a few units; no CTA has more than one tile above another), and a
+// CTA's stay in a unit is a segment with a partial result of its own. A chain
+// of one query tile (scores, softmax, PV, one after the other) leaves tensor
+// core and memory idle most of the time, so a segment's tiles go alternately
+// to two streams A and B with the same queries, each with its own running
+// maximum, sum and O in TMEM. 12 warps as in attn_pair.cu:
+//   warp 0      TMA: the segment's queries (one 4D box: d, group, kv head,
+//               batch), then K_A, K_B, V_A, V_B tiles into one ring
+//   warps 1, 2  MMA-issuing thread of stream A, of stream B
+//   warps 4..7, 8..11  softmax of A, of B, one thread per query row. At the
+//               end of a segment both streams' statistics meet in shared
+//               memory, and each warpgroup merges half of the columns of the
+//               two O from TMEM and writes them to the workspace in fp32.
+// TMEM columns: S_A [0, 128), S_B [128, 256); head_dim 64: P_A, P_B
+// [256, 384), O_A, O_B [384, 512); head_dim 128: P over its own S, O_A, O_B
+// [256, 512) (so the next S waits for the PV that reads P).
+// Pass 2 (decode_partial_kernel, attn_decode.cu): the sequences' own caches.
+// Pass 3 (shared_combine_kernel): one warp per (b, query head) merges the
+// prefix's segments and the own cache's parts.
+#include "internal.h"
+
+namespace blk {
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kTQ = 128, kTK = 128;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescaleThreshold = 8.0f;  // log2 of the largest unnormalised p
+constexpr uint32_t kLaunchRegs = 168, kRegsControl = 64, kRegsSoftmax = 208;
+
+struct PrefixArgs {
+    int pdl;
+    float* po;     // [segments][128][D] partial outputs
+    float2* pm;    // [segments][128] (max, sum), log2 domain
+    const float* slopes;
+    unsigned* err;
+    int B, H, Hk, G, P;
+    int nkt;       // key tiles
+    int nrt;       // row tiles per kv head
+    int W;         // tiles in all: Hk * nrt * nkt
+    float scale;
+    int alibi;
+};
+
+template <int D>
+struct Cfg {
+    static constexpr int kSub = D / 64;
+    static constexpr int kTile = kSub * 128 * 128;     // Q, K or V tile
+    static constexpr int kSlots = D == 64 ? 12 : 5;    // ring of K and V tiles
+    static constexpr int kOffRing = kTile;
+    static constexpr int kOffStats = kOffRing + kSlots * kTile;  // [2][2][128] float2
+    static constexpr int kOffBar = kOffStats + 2 * 2 * 128 * 8;
+    static constexpr int kSmem = kOffBar + 512 + 1024;  // + alignment slack
+    static constexpr bool kPOverS = D != 64;
+    static constexpr uint32_t kColP = kPOverS ? 0 : 256, kPStep = kPOverS ? 128 : 64;
+    static constexpr uint32_t kColO = kPOverS ? 256 : 384;
+    static_assert(kColO + 2 * D <= 512 && kSmem <= 232448, "TMEM or shared memory");
+};
+
+// A CTA's segments: tiles [t, hi) of unit u, key tiles from klo; processed
+// from the last key tile down (with ALiBi the bias is largest there).
+struct Segments {
+    int t, end, u, n, klo, it;
+    bool valid;
+    __device__ __forceinline__ void set(const PrefixArgs& a) {
+        valid = t < end;
+        if (!valid) return;
+        u = t / a.nkt;
+        klo = t - u * a.nkt;
+        n = min(end - t, a.nkt - klo);
+    }
+    __device__ __forceinline__ void start(const PrefixArgs& a) {
+        t = static_cast<int>(static_cast<int64_t>(blockIdx.x) * a.W / gridDim.x);
+        end = static_cast<int>(static_cast<int64_t>(blockIdx.x + 1) * a.W / gridDim.x);
+        it = 0;
+        set(a);
+    }
+    __device__ __forceinline__ void next(const PrefixArgs& a) {
+        t += n;
+        ++it;
+        set(a);
+    }
+    // tiles of stream x
+    __device__ __forceinline__ int tiles(int x) const { return (n + 1 - x) / 2; }
+};
+
+template <typename T, int D, bool ALIBI>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                  const __grid_constant__ CUtensorMap tmV, const PrefixArgs a) {
+    using C = Cfg<D>;
+    constexpr int kSlots = C::kSlots;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = align_1024(smem_raw);
+    const uint32_t sQ = smem_u32(smem);
+    const uint32_t sRing = sQ + C::kOffRing;
+    const uint32_t bar0 = sQ + C::kOffBar;
+    auto s_full = [&](int x) { return bar0 + 8u * x; };
+    auto s_free = [&](int x) { return bar0 + 16u + 8u * x; };
+    auto p_full = [&](int x) { return bar0 + 32u + 8u * x; };
+    auto pv_done = [&](int x) { return bar0 + 48u + 8u * x; };
+    const uint32_t q_full = bar0 + 64u, q_empty = bar0 + 72u;
+    const uint32_t stats_full = bar0 + 80u, o_free = bar0 + 88u;
+    auto full = [&](int i) { return bar0 + 96u + 8u * i; };
+    auto empty = [&](int i) { return bar0 + 96u + 8u * (kSlots + i); };
+    static_assert(96 + 16 * kSlots + 4 <= 512, "barrier space");
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 96 + 16 * kSlots);
+
+    const int warp = threadIdx.x / 32;
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(s_full(x), 1);
+            mbar_init(s_free(x), 4);
+            mbar_init(p_full(x), 4);
+            mbar_init(pv_done(x), 1);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 2);
+        mbar_init(stats_full, 8);
+        mbar_init(o_free, 8);
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(full(i), 1);
+            mbar_init(empty(i), 1);
+        }
+        fence_barrier_init();
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    if (a.pdl) {
+        pdl_wait();
+        pdl_launch_dependents();
+    }
+    static_assert(4 * kRegsControl + 8 * kRegsSoftmax <= 12 * kLaunchRegs,
+                  "register split exceeds the launch's registers");
+    if (warp < 4) {
+        setmaxnreg_dec<kRegsControl>();
+        if (warp == 0 && lane == 0) {
+            // read again by the kv head's other row tiles, if it has any
+            const uint64_t pol = a.nrt > 1 ? l2_evict_last_policy() : l2_evict_first_policy();
+            Segments c;
+            c.start(a);
+            int r = 0;  // tiles put into the ring
+            bool ok = true;
+            while (ok && c.valid) {
+                const int g = c.u / a.nrt, rt = c.u - g * a.nrt;
+                if (!mbar_wait_inl(q_empty, (c.it & 1) ^ 1u, a.err)) break;
+                mbar_expect_tx(q_full, C::kTile);
+#pragma unroll
+                for (int sub = 0; sub < C::kSub; ++sub)
+                    tma_load_4d(sQ + sub * kTQ * 128, &tmQ, q_full, sub * 64, 0, g,
+                                rt * (kTQ / a.G));
+                auto load = [&](const CUtensorMap* m, int i) -> bool {
+                    const int sl = r % kSlots;
+                    if (!mbar_wait_inl(empty(sl), ((r / kSlots) & 1) ^ 1u, a.err)) return false;
+                    mbar_expect_tx(full(sl), C::kTile);
+                    const int row = (c.klo + c.n - 1 - i) * kTK;
+#pragma unroll
+                    for (int sub = 0; sub < C::kSub; ++sub)
+                        tma_load_3d_hint(sRing + sl * C::kTile + sub * kTK * 128, m, full(sl),
+                                         sub * 64, row, g, pol);
+                    ++r;
+                    return true;
+                };
+                for (int i = 0; i < c.n && ok; i += 2) {
+                    const bool two = i + 1 < c.n;
+                    ok = load(&tmK, i) && (!two || load(&tmK, i + 1)) && load(&tmV, i) &&
+                         (!two || load(&tmV, i + 1));
+                }
+                c.next(a);
+            }
+        } else if ((warp == 1 || warp == 2) && lane == 0) {
+            const int x = warp - 1;
+            constexpr uint32_t fmt = dt_traits<T>::mma_fmt;
+            constexpr uint32_t idesc_s = make_idesc_f16(fmt, kTQ, kTK, false);
+            constexpr uint32_t idesc_o = make_idesc_f16(fmt, kTQ, D, true);
+            constexpr uint64_t kAtom = (kTQ * 128) >> 4;
+            constexpr uint64_t kSlotStep = C::kTile >> 4;
+            const uint64_t dq = make_sdesc_sw128(sQ, 16, 1024);
+            const uint64_t dk0 = make_sdesc_sw128(sRing, 16, 1024);
+            const uint64_t dv0 = make_sdesc_sw128(sRing, kTK * 128, 1024);
+            const uint32_t tS = tmem_base + 128u * x;
+            const uint32_t tP = tmem_base + C::kColP + C::kPStep * x;
+            const uint32_t tO = tmem_base + C::kColO + D * x;
+            int gs = 0, gp = 0;  // S and PV products issued
+            auto issue_s = [&](int r) -> bool {
+                const int sl = r % kSlots;
+                if (!mbar_wait_inl(full(sl), (r / kSlots) & 1, a.err)) return false;
+                if (gs > 0) {
+                    // the softmax has read the previous S; P over S: the
+                    // previous PV has read P
+                    if (C::kPOverS ? !mbar_wait_inl(pv_done(x), (gs - 1) & 1, a.err)
+                                   : !mbar_wait_inl(s_free(x), (gs - 1) & 1, a.err))
+                        return false;
+                }
+                tc_fence_after();
+                const uint64_t dk = dk0 + sl * kSlotStep;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint64_t off = (ks / 4) * kAtom + (ks % 4) * 2;
+                    tc_mma_ss(tS, dq + off, dk + off, idesc_s, ks > 0 ? 1u : 0u);
+                }
+                tc_commit(s_full(x));
+                tc_commit(empty(sl));
+                ++gs;
+                return true;
+            };
+            auto issue_pv = [&](int r, bool first, int it) -> bool {
+                const int sl = r % kSlots;
+                if (!mbar_wait_inl(full(sl), (r / kSlots) & 1, a.err)) return false;
+                if (!mbar_wait_inl(p_full(x), gp & 1, a.err)) return false;
+                if (first && it > 0 && !mbar_wait_inl(o_free, (it - 1) & 1, a.err)) return false;
+                tc_fence_after();
+                const uint64_t dv = dv0 + sl * kSlotStep;
+#pragma unroll
+                for (int ks = 0; ks < kTK / 16; ++ks)
+                    tc_mma_ts(tO, tP + ks * 8, dv + ks * ((16 * 128) >> 4), idesc_o,
+                              (!first || ks > 0) ? 1u : 0u);
+                tc_commit(pv_done(x));
+                tc_commit(empty(sl));
+                ++gp;
+                return true;
+            };
+            Segments c;
+            c.start(a);
+            int r0 = 0;  // ring position of the segment's first tile
+            bool ok = true;
+            while (ok && c.valid) {
+                const int nx = c.tiles(x);
+                // ring positions of this stream's i-th K and V tile
+                auto pos_k = [&](int i) { return r0 + 4 * i + x; };
+                auto pos_v = [&](int i) { return r0 + 4 * i + x + (2 * i + 1 < c.n ? 2 : 1); };
+                if (!mbar_wait_inl(q_full, c.it & 1, a.err)) break;
+                if (C::kPOverS) {
+                    for (int i = 0; i < nx && ok; ++i) {
+                        ok = issue_s(pos_k(i));
+                        if (ok && i + 1 == nx) tc_commit(q_empty);
+                        ok = ok && issue_pv(pos_v(i), i == 0, c.it);
+                    }
+                } else {
+                    // S of the next tile ahead of PV of this one
+                    if (nx > 0) ok = issue_s(pos_k(0));
+                    if (ok && nx == 1) tc_commit(q_empty);
+                    for (int i = 0; i < nx && ok; ++i) {
+                        if (i + 1 < nx) {
+                            ok = issue_s(pos_k(i + 1));
+                            if (ok && i + 2 == nx) tc_commit(q_empty);
+                        }
+                        ok = ok && issue_pv(pos_v(i), i == 0, c.it);
+                    }
+                }
+                if (ok && nx == 0) tc_commit(q_empty);
+                r0 += 2 * c.n;
+                c.next(a);
+            }
+        }
+    } else {
+        setmaxnreg_inc<kRegsSoftmax>();
+        const int x = (warp - 4) >> 2;
+        const int quarter = warp & 3;
+        const int row = quarter * 32 + lane;
+        const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+        const uint32_t tS = tmem_base + 128u * x + lane_off;
+        const uint32_t tP = tmem_base + C::kColP + C::kPStep * x + lane_off;
+        const uint32_t tO = tmem_base + C::kColO + D * x + lane_off;
+        const float scale_l2 = a.scale * kLog2e;
+        float2* stats = reinterpret_cast<float2*>(smem + C::kOffStats);
+        Segments c;
+        c.start(a);
+        int g = 0;             // tiles of this stream so far
+        int gy = 0;            // of the other stream
+        bool ok = true;
+        while (ok && c.valid) {
+            const int kvh = c.u / a.nrt, rt = c.u - kvh * a.nrt;
+            const int nx = c.tiles(x), ny = c.tiles(1 - x);
+            float m_used = -INFINITY;  // running max, log2 domain
+            float l = 0.f;
+            float slope_l2 = 0.f;
+            if constexpr (ALIBI) {
+                const int h = kvh * a.G + row % a.G;
+                slope_l2 = kLog2e * (a.slopes ? a.slopes[h]
+                                              : exp2f(-8.0f * static_cast<float>(h + 1) /
+                                                      static_cast<float>(a.H)));
+            }
+            for (int i = 0; i < nx; ++i, ++g) {
+                if (!mbar_wait_inl(s_full(x), g & 1, a.err)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                uint32_t r[kTK];
+                tmem_ld128(tS, r);
+                if (!C::kPOverS) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(s_free(x));
+                }
+                const int kbase = (c.klo + c.n - 1 - (2 * i + x)) * kTK;
+                if constexpr (ALIBI) {
+                    // + slope * (key - P), the distance to the query's own
+                    // part of the row's bias being left to the merge
+                    const float sk = slope_l2 * static_cast<float>(kbase - a.P);
+                    const uint64_t sc2 = f2_pack(scale_l2, scale_l2);
+                    const uint64_t sl2 = f2_pack(slope_l2, slope_l2), sk2 = f2_pack(sk, sk);
+#pragma unroll
+                    for (int k = 0; k < kTK; k += 2) {
+                        float b0, b1, u0, u1;
+                        ffma2(static_cast<float>(k), static_cast<float>(k + 1), sl2, sk2, b0, b1);
+                        ffma2(__uint_as_float(r[k]), __uint_as_float(r[k + 1]), sc2,
+                              f2_pack(b0, b1), u0, u1);
+                        r[k] = __float_as_uint(u0);
+                        r[k + 1] = __float_as_uint(u1);
+                    }
+                }
+                if (kbase + kTK > a.P) {
+                    const int lim = a.P - 1 - kbase;  // keys <= lim exist
+#pragma unroll
+                    for (int k = 0; k < kTK; ++k)
+                        if (k > lim) r[k] = __float_as_uint(-INFINITY);
+                }
+                float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < kTK; k += 8) {
+                    m0 = fmax3f(m0, __uint_as_float(r[k]), __uint_as_float(r[k + 1]));
+                    m1 = fmax3f(m1, __uint_as_float(r[k + 2]), __uint_as_float(r[k + 3]));
+                    m2 = fmax3f(m2, __uint_as_float(r[k + 4]), __uint_as_float(r[k + 5]));
+                    m3 = fmax3f(m3, __uint_as_float(r[k + 6]), __uint_as_float(r[k + 7]));
+                }
+                float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+                if constexpr (!ALIBI) mx *= scale_l2;  // scale > 0: max commutes with it
+                float corr = 1.f;
+                if (mx > m_used + kRescaleThreshold) {
+                    corr = ex2_approx(m_used - mx);
+                    m_used = mx;
+                }
+                const uint64_t mul2 = f2_pack(ALIBI ? 1.f : scale_l2, ALIBI ? 1.f : scale_l2);
+                const uint64_t neg2 = f2_pack(-m_used, -m_used);
+                uint64_t acc0 = f2_pack(0.f, 0.f), acc1 = acc0;
+                uint32_t pk[kTK / 2];
+#pragma unroll
+                for (int k = 0; k < kTK; k += 4) {
+                    float e0, e1, e2, e3;
+                    ffma2(__uint_as_float(r[k]), __uint_as_float(r[k + 1]), mul2, neg2, e0, e1);
+                    ffma2(__uint_as_float(r[k + 2]), __uint_as_float(r[k + 3]), mul2, neg2, e2,
+                          e3);
+                    const float p0 = ex2_approx(e0), p1 = ex2_approx(e1);
+                    const float p2 = ex2_approx(e2), p3 = ex2_approx(e3);
+                    fadd2_acc(acc0, p0, p1);
+                    fadd2_acc(acc1, p2, p3);
+                    pk[k / 2] = dt_traits<T>::pack2(p0, p1);
+                    pk[k / 2 + 1] = dt_traits<T>::pack2(p2, p3);
+                }
+                if (i > 0) {  // the previous PV has read P, and O is settled
+                    if (!mbar_wait_inl(pv_done(x), (g - 1) & 1, a.err)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                }
+                tmem_st64_nowait(tP, pk);
+                if (i > 0 && __any_sync(0xffffffffu, corr != 1.f)) {
+#pragma unroll 1
+                    for (int cc = 0; cc < D / 16; ++cc) {
+                        uint32_t o[16];
+                        tmem_ld16(tO + cc * 16, o);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+                        tmem_st16_nowait(tO + cc * 16, o);
+                    }
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full(x));
+                float s0, s1, s2, s3;
+                f2_unpack(acc0, s0, s1);
+                f2_unpack(acc1, s2, s3);
+                l = l * corr + ((s0 + s1) + (s2 + s3));
+            }
+            if (!ok) break;
+            gy += ny;
+            // the segment's result: both streams' statistics through shared
+            // memory (double-buffered by segment: no stream gets two ahead),
+            // then this warpgroup's half of the columns of both O
+            float2* st = stats + (c.it & 1) * 2 * kTQ;
+            st[x * kTQ + row] = make_float2(m_used, l);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(stats_full);
+            if (!mbar_wait_inl(stats_full, c.it & 1, a.err) ||
+                (nx > 0 && !mbar_wait_inl(pv_done(x), (g - 1) & 1, a.err)) ||
+                (ny > 0 && !mbar_wait_inl(pv_done(1 - x), (gy - 1) & 1, a.err))) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const float2 sa = st[row], sb = st[kTQ + row];
+            const float m = fmaxf(sa.x, sb.x);
+            const float wa = sa.x == -INFINITY ? 0.f : ex2_approx(sa.x - m);
+            const float wb = sb.x == -INFINITY ? 0.f : ex2_approx(sb.x - m);
+            const bool has_b = c.n > 1;
+            const int64_t rec = (static_cast<int64_t>(blockIdx.x) + c.u) * kTQ + row;
+            const bool mine = rt * (kTQ / a.G) + row / a.G < a.B;
+            if (mine && x == 0) a.pm[rec] = make_float2(m, wa * sa.y + wb * sb.y);
+            float* dst = a.po + rec * D + x * (D / 2);
+            const uint32_t tA = tmem_base + C::kColO + lane_off + x * (D / 2);
+#pragma unroll 1
+            for (int cc = 0; cc < D / 32; ++cc) {
+                uint32_t oa[16], ob[16];
+                tmem_ld16(tA + cc * 16, oa);
+                if (has_b) tmem_ld16(tA + D + cc * 16, ob);
+                if (!mine) continue;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    float f[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        f[e] = wa * __uint_as_float(oa[v * 4 + e]);
+                        if (has_b) f[e] = fmaf(wb, __uint_as_float(ob[v * 4 + e]), f[e]);
+                    }
+                    *reinterpret_cast<float4*>(dst + cc * 16 + v * 4) =
+                        make_float4(f[0], f[1], f[2], f[3]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_free);
+            c.next(a);
+        }
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, 512);
+    }
+}
+
+// o = sum_i w_i O_i / sum_i w_i l_i over the prefix's segments and the own
+// cache's parts, w_i = 2^(m_i - max m): one warp per (b, query head). With
+// ALiBi the prefix's maxima still lack the row's -slope * (lens[b] - 1).
+struct CombineArgs {
+    int pdl;
+    const float* po;
+    const float2* pm;
+    const float* rec;  // [B, H, parts, D + 2]
+    const int32_t* lens;
+    const float* slopes;
+    void* o;
+    int B, H, G, max_seq, parts, alibi;
+    int nkt, nrt, W, grid;  // of the prefix pass; W 0: no prefix
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(128) shared_combine_kernel(const CombineArgs a) {
+    constexpr int kCols = D / 32;
+    if (a.pdl) {
+        pdl_wait();
+        pdl_launch_dependents();
+    }
+    const int lane = threadIdx.x & 31;
+    const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / 32;
+    if (w >= static_cast<int64_t>(a.B) * a.H) return;
+    const int b = static_cast<int>(w / a.H), h = static_cast<int>(w - static_cast<int64_t>(b) * a.H);
+    const int n = min(max(a.lens[b], 0), a.max_seq);
+    T* dst = static_cast<T*>(a.o) + w * D + lane * kCols;
+    float o[kCols];
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) o[c] = 0.f;
+    float mx = -INFINITY, lsum = 0.f;
+    if (n > 0) {
+        // the prefix's segments of this row: CTAs c0 .. c1, record c + unit
+        int seg0 = 0, nseg = 0;
+        const int per = kTQ / a.G;  // sequences per row tile
+        const int rt = b / per;
+        const int row = (b - rt * per) * a.G + h % a.G;
+        float shift = 0.f;
+        if (a.W) {
+            const int u = h / a.G * a.nrt + rt;
+            const int64_t t0 = static_cast<int64_t>(u) * a.nkt, t1 = t0 + a.nkt - 1;
+            const int c0 = static_cast<int>(((t0 + 1) * a.grid - 1) / a.W);
+            const int c1 = static_cast<int>(((t1 + 1) * a.grid - 1) / a.W);
+            seg0 = c0 + u;
+            nseg = c1 - c0 + 1;
+            if (a.alibi) {
+                const float sl = a.slopes ? a.slopes[h]
+                                          : exp2f(-8.0f * static_cast<float>(h + 1) /
+                                                  static_cast<float>(a.H));
+                shift = sl * kLog2e * static_cast<float>(n - 1);
+            }
+        }
+        const float* own = a.rec + w * a.parts * (D + 2);
+        const int total = nseg + a.parts;
+        // 32 records at a time: lane i holds record i's (max, sum)
+        for (int base = 0; base < total; base += 32) {
+            const int i = base + lane;
+            float m = -INFINITY, l = 0.f;
+            if (i < nseg) {
+                const float2 s = a.pm[static_cast<int64_t>(seg0 + i) * kTQ + row];
+                m = s.x - shift;
+                l = s.y;
+            } else if (i < total) {
+                m = own[(i - nseg) * (D + 2)];
+                l = own[(i - nseg) * (D + 2) + 1];
+            }
+            float mb = m;
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, s));
+            const float mn = fmaxf(mx, mb);
+            const float keep = mx == -INFINITY ? 0.f : exp2f(mx - mn);
+            const float wgt = m == -INFINITY ? 0.f : exp2f(m - mn);
+            float ls = wgt * l;
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, s);
+            lsum = fmaf(lsum, keep, ls);
+            mx = mn;
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) o[c] *= keep;
+            const int cnt = min(32, total - base);
+#pragma unroll 4
+            for (int j = 0; j < cnt; ++j) {
+                const int k = base + j;
+                const float wj = __shfl_sync(0xffffffffu, wgt, j);
+                const float* src = k < nseg
+                                       ? a.po + (static_cast<int64_t>(seg0 + k) * kTQ + row) * D
+                                       : own + (k - nseg) * (D + 2) + 2;
+#pragma unroll
+                for (int c = 0; c < kCols; c += 2) {
+                    const float2 f = *reinterpret_cast<const float2*>(src + lane * kCols + c);
+                    // a part without keys has weight 0 and zeros
+                    o[c] = fmaf(wj, f.x, o[c]);
+                    o[c + 1] = fmaf(wj, f.y, o[c + 1]);
+                }
+            }
+        }
+    }
+    const float inv = lsum > 0.f ? 1.0f / lsum : 0.f;
+#pragma unroll
+    for (int c = 0; c < kCols; c += 2)
+        *reinterpret_cast<uint32_t*>(dst + c) = dt_traits<T>::pack2(o[c] * inv, o[c + 1] * inv);
+}
+
+template <typename T, int D, bool ALIBI>
+cudaError_t launch_prefix(DType dt, const SharedArgs& s, const PrefixArgs& p, int grid,
+                          cudaStream_t st) {
+    using C = Cfg<D>;
+    CUtensorMap tq, tk, tv;
+    if (!make_tmap_queries(&tq, dt, s.own.q, p.B, p.Hk, p.G, D, kTQ / p.G) ||
+        !make_tmap_3d(&tk, dt, s.k_prefix, p.Hk, p.P, D, kTK) ||
+        !make_tmap_3d(&tv, dt, s.v_prefix, p.Hk, p.P, D, kTK))
+        return cudaErrorInvalidValue;
+    auto kern = prefix_kernel<T, D, ALIBI>;
+    const cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(kern), C::kSmem);
+    if (e != cudaSuccess) return e;
+    PrefixArgs a = p;
+    a.pdl = pdl_allowed(st);
+    return launch_pdl(a.pdl != 0, kern, dim3(grid), dim3(kThreads), C::kSmem, st, tq, tk, tv, a);
+}
+
+template <typename T, int D>
+cudaError_t launch_t(DType dt, const SharedArgs& s, cudaStream_t st) {
+    const DecodeArgs& d = s.own;
+    const int G = d.H / d.Hk;
+    PrefixArgs p{};
+    p.nkt = (s.P + kTK - 1) / kTK;
+    p.nrt = (d.B + kTQ / G - 1) / (kTQ / G);
+    p.W = d.Hk * p.nrt * p.nkt;
+    int grid = s.num_sms < kSharedMaxGrid ? s.num_sms : kSharedMaxGrid;
+    if (grid > p.W) grid = p.W;
+    const SharedLayout L = shared_layout(d.B, d.H, d.Hk, D, s.P, d.S_max);
+    p.po = reinterpret_cast<float*>(s.ws + L.po);
+    p.pm = reinterpret_cast<float2*>(s.ws + L.pm);
+    p.slopes = d.slopes;
+    p.err = s.err;
+    p.B = d.B;
+    p.H = d.H;
+    p.Hk = d.Hk;
+    p.G = G;
+    p.P = s.P;
+    p.scale = d.scale;
+    p.alibi = d.alibi;
+    cudaError_t e;
+    if (p.W) {
+        e = d.alibi ? launch_prefix<T, D, true>(dt, s, p, grid, st)
+                    : launch_prefix<T, D, false>(dt, s, p, grid, st);
+        if (e != cudaSuccess) return e;
+    }
+    DecodeArgs own = d;
+    own.ws = reinterpret_cast<float*>(s.ws + L.own);
+    e = launch_decode_partial(dt, own, st);
+    if (e != cudaSuccess) return e;
+    CombineArgs c{};
+    c.po = p.po;
+    c.pm = p.pm;
+    c.rec = own.ws;
+    c.lens = d.lens;
+    c.slopes = d.slopes;
+    c.o = d.o;
+    c.B = d.B;
+    c.H = d.H;
+    c.G = G;
+    c.max_seq = d.S_max;
+    c.parts = d.parts;
+    c.alibi = d.alibi;
+    c.nkt = p.nkt;
+    c.nrt = p.nrt;
+    c.W = p.W;
+    c.grid = grid;
+    c.pdl = pdl_allowed(st);
+    const int64_t warps = static_cast<int64_t>(d.B) * d.H;
+    return launch_pdl(c.pdl != 0, shared_combine_kernel<T, D>,
+                      dim3(static_cast<unsigned>((warps + 3) / 4)), dim3(128), 0, st, c);
+}
+
+}  // namespace
+
+SharedLayout shared_layout(int64_t B, int64_t H, int64_t Hk, int64_t d, int64_t P, int64_t S_max) {
+    const int64_t G = H / Hk, nrt = (B + kTQ / G - 1) / (kTQ / G);
+    const int64_t segs = P ? kSharedMaxGrid + Hk * nrt : 0;
+    auto up = [](int64_t n) { return (n + 255) / 256 * 256; };
+    SharedLayout L;
+    L.po = 0;
+    L.pm = up(segs * kTQ * d * 4);
+    L.own = L.pm + up(segs * kTQ * 8);
+    L.total = L.own + up(B * H * decode_parts_max(S_max) * (d + 2) * 4);
+    return L;
+}
+
+int64_t shared_tiles(int64_t B, int64_t H, int64_t Hk, int64_t P) {
+    const int64_t G = H / Hk;
+    return Hk * ((B + kTQ / G - 1) / (kTQ / G)) * ((P + kTK - 1) / kTK);
+}
+
+cudaError_t launch_attention_decode_shared(DType dt, const SharedArgs& s, cudaStream_t st) {
+    if (dt == DType::F16)
+        return s.own.d == 64 ? launch_t<__half, 64>(dt, s, st) : launch_t<__half, 128>(dt, s, st);
+    return s.own.d == 64 ? launch_t<__nv_bfloat16, 64>(dt, s, st)
+                         : launch_t<__nv_bfloat16, 128>(dt, s, st);
+}
+
+}  // namespace blk

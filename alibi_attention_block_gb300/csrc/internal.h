@@ -186,9 +186,30 @@ struct DecodeArgs {
     int alibi;
 };
 cudaError_t launch_attention_decode(DType dt, const DecodeArgs& a, cudaStream_t s);
+// its first pass alone: (max, sum, output) of each part in the workspace
+cudaError_t launch_decode_partial(DType dt, const DecodeArgs& a, cudaStream_t s);
 // number of key ranges per (batch, kv head), and its device-independent bound
 int decode_parts(int64_t B, int64_t Hk, int64_t S_max, int64_t head_dim, int num_sms);
 int decode_parts_max(int64_t S_max);
+
+// ---- K6s: decode step of a batch that shares a prefix (attn_shared.cu)
+struct SharedArgs {
+    DecodeArgs own;        // the sequences' own caches (its ws is set by the launcher)
+    const void* k_prefix;  // [Hk, P, d]
+    const void* v_prefix;
+    int P;
+    uint8_t* ws;           // shared_layout(...).total bytes
+    unsigned* err;
+    int num_sms;
+};
+constexpr int kSharedMaxGrid = 256;  // CTAs of the prefix pass at most
+struct SharedLayout {
+    int64_t po, pm, own, total;  // byte offsets in the workspace, and its size
+};
+SharedLayout shared_layout(int64_t B, int64_t H, int64_t Hk, int64_t d, int64_t P, int64_t S_max);
+// (kv head, row tile, key tile) triples of the prefix pass
+int64_t shared_tiles(int64_t B, int64_t H, int64_t Hk, int64_t P);
+cudaError_t launch_attention_decode_shared(DType dt, const SharedArgs& s, cudaStream_t st);
 
 // ---- per-device state and error reporting shared with other entry points (api.cu)
 // SM count and device error word of the current device (set up on first use).
@@ -240,5 +261,10 @@ bool make_tmap_2d_plain(CUtensorMap* m, CUtensorMapDataType type, uint32_t elem_
 // (64-byte rows) with the 64-byte swizzle.
 bool make_tmap_3d(CUtensorMap* m, DType dt, const void* base, uint64_t planes, uint64_t rows,
                   uint64_t cols, uint32_t box_rows, uint32_t box_cols = 64);
+// 4D map of decode queries [batch, kv heads, group, d] with a {64, group, 1,
+// box_batch} box (128-byte swizzle): the queries of box_batch sequences for
+// one kv head, a row of 64 columns each, group index fastest.
+bool make_tmap_queries(CUtensorMap* m, DType dt, const void* base, uint64_t batch,
+                       uint64_t kv_heads, uint64_t group, uint64_t d, uint32_t box_batch);
 
 }  // namespace blk

@@ -234,6 +234,40 @@ blk_status blk_attn_decode(const blk_decode_desc* d, const void* q, const void* 
                            void* o, void* workspace, size_t ws_bytes, blk_dtype dt,
                            blk_stream_t s);
 
+typedef struct {
+    int64_t batch, max_seq, n_heads, n_kv_heads, head_dim;
+    int64_t prefix_len;  /* keys that every sequence shares, ahead of its own (0 .. 2^30) */
+    float softmax_scale; /* <= 0 -> head_dim^-0.5 */
+    int32_t alibi;       /* 0 off; 1: score -= slope_h * (query_pos - key_pos) */
+} blk_decode_shared_desc;
+
+/* One decode step of attention for a batch whose sequences share a prefix (a
+ * system prompt, a document) that is stored and read once:
+ *   q [batch, H, d]: each sequence's newest token, at position prefix_len +
+ *     lens[b] - 1
+ *   k_prefix, v_prefix [Hk, prefix_len, d]: positions 0 .. prefix_len - 1 of
+ *     every sequence; both NULL when prefix_len is 0
+ *   k_cache, v_cache [batch, Hk, max_seq, d]: each sequence's own keys behind
+ *     the prefix, entries 0 .. lens[b] - 1 at positions prefix_len ..
+ *     prefix_len + lens[b] - 1 (the newest token's already written); later
+ *     entries are not read
+ *   lens: device int32 [batch], each in [1, max_seq]; read on the device, a
+ *     value outside the range is clamped to it, and a length of 0 marks a
+ *     sequence that takes no part: its output row is zero
+ *   alibi_slopes: as for blk_attn_prefill
+ *   o [batch, H, d], as blk_attn_decode would give it with the prefix copied
+ *     in front of each sequence's cache
+ * GQA: kv head = h / (H / Hk), H / Hk in {1, 2, 4, 8}; head_dim 64 or 128.
+ * The workspace holds partial results, at least
+ * blk_attn_decode_shared_workspace_size bytes, 16-byte aligned; calls whose
+ * kernels overlap on the GPU need a workspace each. */
+blk_status blk_attn_decode_shared_workspace_size(const blk_decode_shared_desc* d, size_t* bytes);
+blk_status blk_attn_decode_shared(const blk_decode_shared_desc* d, const void* q,
+                                  const void* k_prefix, const void* v_prefix, const void* k_cache,
+                                  const void* v_cache, const int32_t* lens,
+                                  const float* alibi_slopes, void* o, void* workspace,
+                                  size_t ws_bytes, blk_dtype dt, blk_stream_t s);
+
 /* ---- linear and MLP --------------------------------------------------- */
 
 /* y = x W^T [+ bias] [+ res1] [+ res2] on tcgen05 tensor cores.

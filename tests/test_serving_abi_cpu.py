@@ -1,5 +1,5 @@
-"""blk_attn_prefill_packed without a GPU: workspace size and refusals, before
-any CUDA call."""
+"""blk_attn_prefill_packed and blk_attn_decode_shared without a GPU: workspace
+sizes and refusals, before any CUDA call."""
 import ctypes as C
 
 import pytest
@@ -72,3 +72,48 @@ def test_argument_refusals(lib):
     assert call(lib, d, ws=None) == _abi.BLK_EWORKSPACE
     assert call(lib, d, ws=FAKE + 4) == _abi.BLK_EWORKSPACE
     assert call(lib, d, n=64) == _abi.BLK_EWORKSPACE
+
+
+# ---------------------------------------------- blk_attn_decode_shared --
+
+def shared(batch=4, max_seq=64, H=32, Hk=8, d=128, prefix=100, scale=-1.0, alibi=0):
+    return _abi.DecodeSharedDesc(batch, max_seq, H, Hk, d, prefix, scale, alibi)
+
+
+def step(lib, d, q=FAKE, kp=FAKE, vp=FAKE, k=FAKE, v=FAKE, lens=FAKE, slopes=None, o=FAKE, ws=FAKE,
+         n=BIG, dt=1):
+    return lib.blk_attn_decode_shared(C.byref(d), q, kp, vp, k, v, lens, slopes, o, ws, n, dt, None)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(batch=0), _abi.BLK_EINVAL), (dict(max_seq=0), _abi.BLK_EINVAL),
+    (dict(prefix=-1), _abi.BLK_EINVAL), (dict(prefix=(1 << 30) + 1), _abi.BLK_EINVAL),
+    (dict(H=30), _abi.BLK_EINVAL), (dict(H=24, Hk=8), _abi.BLK_EUNSUPPORTED),
+    (dict(d=160), _abi.BLK_EUNSUPPORTED), (dict(d=32), _abi.BLK_EUNSUPPORTED),
+    (dict(alibi=3), _abi.BLK_EINVAL), (dict(scale=float("inf")), _abi.BLK_EINVAL),
+    (dict(batch=1 << 20, max_seq=1, Hk=32, prefix=1 << 20), _abi.BLK_EINVAL),  # too many tiles
+])
+def test_shared_descriptor_refusals(lib, bad, status):
+    need = C.c_size_t(0)
+    assert lib.blk_attn_decode_shared_workspace_size(C.byref(shared(**bad)), C.byref(need)) == status
+    assert step(lib, shared(**bad)) == status
+
+
+def test_shared_argument_refusals(lib):
+    d = shared()
+    need = C.c_size_t(0)
+    assert lib.blk_attn_decode_shared_workspace_size(C.byref(d), C.byref(need)) == _abi.BLK_OK
+    assert lib.blk_attn_decode_shared_workspace_size(C.byref(d), None) == _abi.BLK_EINVAL
+    for name in ("q", "kp", "vp", "k", "v", "o", "lens"):
+        assert step(lib, d, **{name: None}) == _abi.BLK_EINVAL, name
+    for name in ("q", "kp", "vp", "k", "v", "o"):
+        assert step(lib, d, **{name: FAKE + 8}) == _abi.BLK_EINVAL, name
+    assert step(lib, d, lens=FAKE + 1) == _abi.BLK_EINVAL
+    assert step(lib, d, dt=7) == _abi.BLK_EINVAL
+    assert step(lib, shared(prefix=0)) == _abi.BLK_EINVAL     # a prefix of length 0
+    assert step(lib, d, slopes=FAKE) == _abi.BLK_EINVAL       # slopes without ALiBi
+    assert step(lib, shared(alibi=1), slopes=FAKE + 2) == _abi.BLK_EINVAL
+    assert step(lib, shared(H=48, Hk=12, alibi=1)) == _abi.BLK_EUNSUPPORTED
+    assert step(lib, d, ws=None) == _abi.BLK_EWORKSPACE
+    assert step(lib, d, ws=FAKE + 8) == _abi.BLK_EWORKSPACE
+    assert step(lib, d, n=need.value - 1) == _abi.BLK_EWORKSPACE
