@@ -20,7 +20,10 @@
 // to two streams A and B with the same queries, each with its own running
 // maximum, sum and O in TMEM. 12 warps as in attn_pair.cu:
 //   warp 0      TMA: the segment's queries (one 4D box: d, group, kv head,
-//               batch), then K_A, K_B, V_A, V_B tiles into one ring
+//               batch), then K_A, K_B, V_A, V_B tiles, each stream's into a
+//               ring of its own (a ring that both read would need both to
+//               release each slot: a stream that skips the other's tiles
+//               cannot tell a slot's phases apart by their parity)
 //   warps 1, 2  MMA-issuing thread of stream A, of stream B
 //   warps 4..7, 8..11  softmax of A, of B, one thread per query row. At the
 //               end of a segment both streams' statistics meet in shared
@@ -42,7 +45,7 @@ constexpr int kThreads = 384;
 constexpr int kTQ = 128, kTK = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 of the largest unnormalised p
-constexpr uint32_t kLaunchRegs = 168, kRegsControl = 64, kRegsSoftmax = 208;
+constexpr uint32_t kLaunchRegs = 168;
 
 struct PrefixArgs {
     int pdl;
@@ -62,12 +65,15 @@ template <int D>
 struct Cfg {
     static constexpr int kSub = D / 64;
     static constexpr int kTile = kSub * 128 * 128;     // Q, K or V tile
-    static constexpr int kSlots = D == 64 ? 12 : 5;    // ring of K and V tiles
+    static constexpr int kSlots = D == 64 ? 6 : 2;     // a stream's ring of K and V tiles
     static constexpr int kOffRing = kTile;
-    static constexpr int kOffStats = kOffRing + kSlots * kTile;  // [2][2][128] float2
+    static constexpr int kOffStats = kOffRing + 2 * kSlots * kTile;  // [2][2][128] float2
     static constexpr int kOffBar = kOffStats + 2 * 2 * 128 * 8;
     static constexpr int kSmem = kOffBar + 512 + 1024;  // + alignment slack
     static constexpr bool kPOverS = D != 64;
+    // per-thread registers of the control warps and of the softmax warps
+    static constexpr uint32_t kRegsControl = D == 64 ? 64 : 88;
+    static constexpr uint32_t kRegsSoftmax = 208;
     static constexpr uint32_t kColP = kPOverS ? 0 : 256, kPStep = kPOverS ? 128 : 64;
     static constexpr uint32_t kColO = kPOverS ? 256 : 384;
     static_assert(kColO + 2 * D <= 512 && kSmem <= 232448, "TMEM or shared memory");
@@ -117,10 +123,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto pv_done = [&](int x) { return bar0 + 48u + 8u * x; };
     const uint32_t q_full = bar0 + 64u, q_empty = bar0 + 72u;
     const uint32_t stats_full = bar0 + 80u, o_free = bar0 + 88u;
-    auto full = [&](int i) { return bar0 + 96u + 8u * i; };
-    auto empty = [&](int i) { return bar0 + 96u + 8u * (kSlots + i); };
-    static_assert(96 + 16 * kSlots + 4 <= 512, "barrier space");
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 96 + 16 * kSlots);
+    // slot i of stream x's ring
+    auto full = [&](int x, int i) { return bar0 + 96u + 8u * (kSlots * x + i); };
+    auto empty = [&](int x, int i) { return bar0 + 96u + 8u * (kSlots * (2 + x) + i); };
+    static_assert(96 + 32 * kSlots + 4 <= 512, "barrier space");
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 96 + 32 * kSlots);
 
     const int warp = threadIdx.x / 32;
     const int lane = threadIdx.x & 31;
@@ -130,15 +137,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(s_free(x), 4);
             mbar_init(p_full(x), 4);
             mbar_init(pv_done(x), 1);
+            for (int i = 0; i < kSlots; ++i) {
+                mbar_init(full(x, i), 1);
+                mbar_init(empty(x, i), 1);
+            }
         }
         mbar_init(q_full, 1);
         mbar_init(q_empty, 2);
         mbar_init(stats_full, 8);
         mbar_init(o_free, 8);
-        for (int i = 0; i < kSlots; ++i) {
-            mbar_init(full(i), 1);
-            mbar_init(empty(i), 1);
-        }
         fence_barrier_init();
         tma_prefetch_desc(&tmQ);
         tma_prefetch_desc(&tmK);
@@ -156,16 +163,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         pdl_wait();
         pdl_launch_dependents();
     }
-    static_assert(4 * kRegsControl + 8 * kRegsSoftmax <= 12 * kLaunchRegs,
+    static_assert(4 * C::kRegsControl + 8 * C::kRegsSoftmax <= 12 * kLaunchRegs,
                   "register split exceeds the launch's registers");
     if (warp < 4) {
-        setmaxnreg_dec<kRegsControl>();
+        setmaxnreg_dec<C::kRegsControl>();
         if (warp == 0 && lane == 0) {
             // read again by the kv head's other row tiles, if it has any
             const uint64_t pol = a.nrt > 1 ? l2_evict_last_policy() : l2_evict_first_policy();
             Segments c;
             c.start(a);
-            int r = 0;  // tiles put into the ring
+            int rx[2] = {0, 0};  // tiles put into each ring
             bool ok = true;
             while (ok && c.valid) {
                 const int g = c.u / a.nrt, rt = c.u - g * a.nrt;
@@ -175,22 +182,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int sub = 0; sub < C::kSub; ++sub)
                     tma_load_4d(sQ + sub * kTQ * 128, &tmQ, q_full, sub * 64, 0, g,
                                 rt * (kTQ / a.G));
-                auto load = [&](const CUtensorMap* m, int i) -> bool {
-                    const int sl = r % kSlots;
-                    if (!mbar_wait_inl(empty(sl), ((r / kSlots) & 1) ^ 1u, a.err)) return false;
-                    mbar_expect_tx(full(sl), C::kTile);
+                // step i's tile for its stream x = i & 1
+                auto load = [&](const CUtensorMap* m, int i, int x) -> bool {
+                    const int r = rx[x], sl = r % kSlots;
+                    if (!mbar_wait_inl(empty(x, sl), ((r / kSlots) & 1) ^ 1u, a.err)) return false;
+                    mbar_expect_tx(full(x, sl), C::kTile);
                     const int row = (c.klo + c.n - 1 - i) * kTK;
 #pragma unroll
                     for (int sub = 0; sub < C::kSub; ++sub)
-                        tma_load_3d_hint(sRing + sl * C::kTile + sub * kTK * 128, m, full(sl),
-                                         sub * 64, row, g, pol);
-                    ++r;
+                        tma_load_3d_hint(sRing + (kSlots * x + sl) * C::kTile + sub * kTK * 128, m,
+                                         full(x, sl), sub * 64, row, g, pol);
+                    ++rx[x];
                     return true;
                 };
                 for (int i = 0; i < c.n && ok; i += 2) {
                     const bool two = i + 1 < c.n;
-                    ok = load(&tmK, i) && (!two || load(&tmK, i + 1)) && load(&tmV, i) &&
-                         (!two || load(&tmV, i + 1));
+                    ok = load(&tmK, i, 0) && (!two || load(&tmK, i + 1, 1)) &&
+                         load(&tmV, i, 0) && (!two || load(&tmV, i + 1, 1));
                 }
                 c.next(a);
             }
@@ -202,15 +210,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint64_t kAtom = (kTQ * 128) >> 4;
             constexpr uint64_t kSlotStep = C::kTile >> 4;
             const uint64_t dq = make_sdesc_sw128(sQ, 16, 1024);
-            const uint64_t dk0 = make_sdesc_sw128(sRing, 16, 1024);
-            const uint64_t dv0 = make_sdesc_sw128(sRing, kTK * 128, 1024);
+            const uint32_t ring = sRing + kSlots * x * C::kTile;
+            const uint64_t dk0 = make_sdesc_sw128(ring, 16, 1024);
+            const uint64_t dv0 = make_sdesc_sw128(ring, kTK * 128, 1024);
             const uint32_t tS = tmem_base + 128u * x;
             const uint32_t tP = tmem_base + C::kColP + C::kPStep * x;
             const uint32_t tO = tmem_base + C::kColO + D * x;
             int gs = 0, gp = 0;  // S and PV products issued
             auto issue_s = [&](int r) -> bool {
                 const int sl = r % kSlots;
-                if (!mbar_wait_inl(full(sl), (r / kSlots) & 1, a.err)) return false;
+                if (!mbar_wait_inl(full(x, sl), (r / kSlots) & 1, a.err)) return false;
                 if (gs > 0) {
                     // the softmax has read the previous S; P over S: the
                     // previous PV has read P
@@ -226,13 +235,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_mma_ss(tS, dq + off, dk + off, idesc_s, ks > 0 ? 1u : 0u);
                 }
                 tc_commit(s_full(x));
-                tc_commit(empty(sl));
+                tc_commit(empty(x, sl));
                 ++gs;
                 return true;
             };
             auto issue_pv = [&](int r, bool first, int it) -> bool {
                 const int sl = r % kSlots;
-                if (!mbar_wait_inl(full(sl), (r / kSlots) & 1, a.err)) return false;
+                if (!mbar_wait_inl(full(x, sl), (r / kSlots) & 1, a.err)) return false;
                 if (!mbar_wait_inl(p_full(x), gp & 1, a.err)) return false;
                 if (first && it > 0 && !mbar_wait_inl(o_free, (it - 1) & 1, a.err)) return false;
                 tc_fence_after();
@@ -242,19 +251,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_mma_ts(tO, tP + ks * 8, dv + ks * ((16 * 128) >> 4), idesc_o,
                               (!first || ks > 0) ? 1u : 0u);
                 tc_commit(pv_done(x));
-                tc_commit(empty(sl));
+                tc_commit(empty(x, sl));
                 ++gp;
                 return true;
             };
             Segments c;
             c.start(a);
-            int r0 = 0;  // ring position of the segment's first tile
+            int r0 = 0;  // ring position of the segment's first tile (K, V, K, V, ...)
             bool ok = true;
             while (ok && c.valid) {
                 const int nx = c.tiles(x);
-                // ring positions of this stream's i-th K and V tile
-                auto pos_k = [&](int i) { return r0 + 4 * i + x; };
-                auto pos_v = [&](int i) { return r0 + 4 * i + x + (2 * i + 1 < c.n ? 2 : 1); };
+                auto pos_k = [&](int i) { return r0 + 2 * i; };
+                auto pos_v = [&](int i) { return r0 + 2 * i + 1; };
                 if (!mbar_wait_inl(q_full, c.it & 1, a.err)) break;
                 if (C::kPOverS) {
                     for (int i = 0; i < nx && ok; ++i) {
@@ -275,12 +283,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (ok && nx == 0) tc_commit(q_empty);
-                r0 += 2 * c.n;
+                r0 += 2 * nx;
                 c.next(a);
             }
         }
     } else {
-        setmaxnreg_inc<kRegsSoftmax>();
+        setmaxnreg_inc<C::kRegsSoftmax>();
         const int x = (warp - 4) >> 2;
         const int quarter = warp & 3;
         const int row = quarter * 32 + lane;
@@ -434,18 +442,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t oa[16], ob[16];
                 tmem_ld16(tA + cc * 16, oa);
                 if (has_b) tmem_ld16(tA + D + cc * 16, ob);
-                if (!mine) continue;
+                if (mine) {
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    float f[4];
+                    for (int v = 0; v < 4; ++v) {
+                        float f[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        f[e] = wa * __uint_as_float(oa[v * 4 + e]);
-                        if (has_b) f[e] = fmaf(wb, __uint_as_float(ob[v * 4 + e]), f[e]);
+                        for (int e = 0; e < 4; ++e) {
+                            f[e] = wa * __uint_as_float(oa[v * 4 + e]);
+                            if (has_b) f[e] = fmaf(wb, __uint_as_float(ob[v * 4 + e]), f[e]);
+                        }
+                        *reinterpret_cast<float4*>(dst + cc * 16 + v * 4) =
+                            make_float4(f[0], f[1], f[2], f[3]);
                     }
-                    *reinterpret_cast<float4*>(dst + cc * 16 + v * 4) =
-                        make_float4(f[0], f[1], f[2], f[3]);
                 }
+                __syncwarp();  // TMEM loads are whole-warp instructions
             }
             tc_fence_before();
             __syncwarp();

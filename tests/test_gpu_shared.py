@@ -135,6 +135,22 @@ def test_lengths_clamped_and_deterministic():
     assert torch.equal(call([7, 8, 9]), call([7, 8, 9]))
 
 
+@pytest.mark.parametrize("H,Hk,d", [(16, 4, 128), (8, 8, 64), (8, 8, 128)])
+def test_back_to_back_over_a_long_prefix(H, Hk, d):
+    """Every query row in use and many key tiles per CTA, so that the two
+    streams run far apart while loads are late: 25 steps without a pause give
+    the same bits, and rows of them are the oracle's."""
+    B, P, S = 64, 16384, 256
+    q, kp, vp, k, v = inputs(B, H, Hk, d, P, S, "bf16", 91)
+    lens = [1 + (37 * i) % S for i in range(B)]
+    args = [to_dev(t) for t in (q, kp, vp, k, v)] + [torch.tensor(lens, dtype=torch.int32, device="cuda")]
+    outs = [blk.attn_decode_shared(*args) for _ in range(25)]
+    blk.check_device_status()
+    assert all(torch.equal(o, outs[0]) for o in outs)
+    for b in (0, 29, 33, 63):
+        check(outs[0][b:b + 1], q[b:b + 1], kp, vp, k[b:b + 1], v[b:b + 1], lens[b:b + 1], "bf16", name=f"row {b}")
+
+
 def test_scale_and_workspace():
     B, H, Hk, d, P, S = 4, 8, 8, 128, 400, 20
     q, kp, vp, k, v = inputs(B, H, Hk, d, P, S, "fp16", 41)
