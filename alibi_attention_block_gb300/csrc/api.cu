@@ -926,7 +926,7 @@ static blk_status validate_shared_desc(const blk_decode_shared_desc* d) {
 
 static size_t shared_ws_bytes(const blk_decode_shared_desc* d) {
     return static_cast<size_t>(shared_layout(d->batch, d->n_heads, d->n_kv_heads, d->head_dim,
-                                             d->prefix_len, d->max_seq).total);
+                                             d->prefix_len).total);
 }
 
 blk_status blk_attn_decode_shared_workspace_size(const blk_decode_shared_desc* d, size_t* bytes) {
@@ -977,7 +977,6 @@ blk_status blk_attn_decode_shared(const blk_decode_shared_desc* d, const void* q
     a.own.Hk = static_cast<int>(d->n_kv_heads);
     a.own.d = static_cast<int>(d->head_dim);
     a.own.S_max = static_cast<int>(d->max_seq);
-    a.own.parts = decode_parts(d->batch, d->n_kv_heads, d->max_seq, d->head_dim, ds->sms);
     a.own.scale = d->softmax_scale > 0.f ? d->softmax_scale
                                          : 1.0f / std::sqrt(static_cast<float>(d->head_dim));
     a.own.alibi = d->alibi;

@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_combine_kernel(DecodeArgs 
 }
 
 template <typename T, int D, int G>
-cudaError_t launch_g(const DecodeArgs& a, bool combine, cudaStream_t s) {
+cudaError_t launch_g(const DecodeArgs& a, cudaStream_t s) {
     const int64_t items = static_cast<int64_t>(a.B) * a.Hk * a.parts;
     constexpr int kW = DecCfg<D>::kWarps;
     // head_dim 128 with G >= 2: a block of two warps per item sharing one
@@ -289,28 +289,27 @@ cudaError_t launch_g(const DecodeArgs& a, bool combine, cudaStream_t s) {
     const int64_t blocks = HS == 1 ? (items + kW - 1) / kW : items;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     kern<<<static_cast<unsigned>(blocks), HS == 1 ? 32 * kW : 32 * HS, kSmem, s>>>(a);
-    if (!combine) return cudaGetLastError();
     const int64_t cw = static_cast<int64_t>(a.B) * a.H;
     decode_combine_kernel<T, D><<<static_cast<unsigned>((cw + 3) / 4), kDecThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 
 template <typename T, int D>
-cudaError_t launch_d(const DecodeArgs& a, bool combine, cudaStream_t s) {
+cudaError_t launch_d(const DecodeArgs& a, cudaStream_t s) {
     switch (a.H / a.Hk) {
-        case 1: return launch_g<T, D, 1>(a, combine, s);
-        case 2: return launch_g<T, D, 2>(a, combine, s);
-        case 4: return launch_g<T, D, 4>(a, combine, s);
-        case 8: return launch_g<T, D, 8>(a, combine, s);
+        case 1: return launch_g<T, D, 1>(a, s);
+        case 2: return launch_g<T, D, 2>(a, s);
+        case 4: return launch_g<T, D, 4>(a, s);
+        case 8: return launch_g<T, D, 8>(a, s);
         default: return cudaErrorInvalidValue;
     }
 }
 
 template <typename T>
-cudaError_t launch_t(const DecodeArgs& a, bool combine, cudaStream_t s) {
+cudaError_t launch_t(const DecodeArgs& a, cudaStream_t s) {
     switch (a.d) {
-        case 64: return launch_d<T, 64>(a, combine, s);
-        case 128: return launch_d<T, 128>(a, combine, s);
+        case 64: return launch_d<T, 64>(a, s);
+        case 128: return launch_d<T, 128>(a, s);
         default: return cudaErrorInvalidValue;
     }
 }
@@ -338,13 +337,8 @@ int decode_parts(int64_t B, int64_t Hk, int64_t S_max, int64_t head_dim, int num
 
 cudaError_t launch_attention_decode(DType dt, const DecodeArgs& a, cudaStream_t s) {
     if (a.B == 0) return cudaSuccess;
-    if (dt == DType::F16) return launch_t<__half>(a, true, s);
-    return launch_t<__nv_bfloat16>(a, true, s);
-}
-
-cudaError_t launch_decode_partial(DType dt, const DecodeArgs& a, cudaStream_t s) {
-    if (dt == DType::F16) return launch_t<__half>(a, false, s);
-    return launch_t<__nv_bfloat16>(a, false, s);
+    if (dt == DType::F16) return launch_t<__half>(a, s);
+    return launch_t<__nv_bfloat16>(a, s);
 }
 
 }  // namespace blk

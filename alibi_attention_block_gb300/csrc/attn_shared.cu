@@ -32,9 +32,9 @@
 // TMEM columns: S_A [0, 128), S_B [128, 256); head_dim 64: P_A, P_B
 // [256, 384), O_A, O_B [384, 512); head_dim 128: P over its own S, O_A, O_B
 // [256, 512) (so the next S waits for the PV that reads P).
-// Pass 2 (decode_partial_kernel, attn_decode.cu): the sequences' own caches.
+// Pass 2 (own_kernel, attn_own.cu): the sequences' own caches.
 // Pass 3 (shared_combine_kernel): one warp per (b, query head) merges the
-// prefix's segments and the own cache's parts.
+// segments of both passes.
 #include "internal.h"
 
 namespace blk {
@@ -471,17 +471,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // o = sum_i w_i O_i / sum_i w_i l_i over the prefix's segments and the own
-// cache's parts, w_i = 2^(m_i - max m): one warp per (b, query head). With
+// cache's, w_i = 2^(m_i - max m): one warp per (b, query head). With
 // ALiBi the prefix's maxima still lack the row's -slope * (lens[b] - 1).
 struct CombineArgs {
     int pdl;
     const float* po;
     const float2* pm;
-    const float* rec;  // [B, H, parts, D + 2]
+    const float* own_po;
+    const float2* own_pm;
+    const int32_t* cum;
     const int32_t* lens;
     const float* slopes;
     void* o;
-    int B, H, G, max_seq, parts, alibi;
+    int B, H, G, max_seq, alibi, own_grid;
     int nkt, nrt, W, grid;  // of the prefix pass; W 0: no prefix
 };
 
@@ -523,8 +525,16 @@ __global__ void __launch_bounds__(128) shared_combine_kernel(const CombineArgs a
                 shift = sl * kLog2e * static_cast<float>(n - 1);
             }
         }
-        const float* own = a.rec + w * a.parts * (D + 2);
-        const int total = nseg + a.parts;
+        // and the own cache's, of unit (b, kv head)
+        const int Hk = a.H / a.G, g = h / a.G;
+        const int64_t own_w = static_cast<int64_t>(a.cum[a.B]) * Hk;
+        const int nt = (n + kTK - 1) / kTK;
+        const int64_t t0 = static_cast<int64_t>(a.cum[b]) * Hk + static_cast<int64_t>(g) * nt;
+        const int64_t ctas = min(static_cast<int64_t>(a.own_grid), own_w);
+        const int c0 = static_cast<int>(((t0 + 1) * ctas - 1) / own_w);
+        const int c1 = static_cast<int>(((t0 + nt) * ctas - 1) / own_w);
+        const int64_t own0 = (static_cast<int64_t>(c0) + static_cast<int64_t>(b) * Hk + g) * a.G + h % a.G;
+        const int total = nseg + c1 - c0 + 1;
         // 32 records at a time: lane i holds record i's (max, sum)
         for (int base = 0; base < total; base += 32) {
             const int i = base + lane;
@@ -534,8 +544,9 @@ __global__ void __launch_bounds__(128) shared_combine_kernel(const CombineArgs a
                 m = s.x - shift;
                 l = s.y;
             } else if (i < total) {
-                m = own[(i - nseg) * (D + 2)];
-                l = own[(i - nseg) * (D + 2) + 1];
+                const float2 s = a.own_pm[own0 + static_cast<int64_t>(i - nseg) * a.G];
+                m = s.x;
+                l = s.y;
             }
             float mb = m;
 #pragma unroll
@@ -557,11 +568,10 @@ __global__ void __launch_bounds__(128) shared_combine_kernel(const CombineArgs a
                 const float wj = __shfl_sync(0xffffffffu, wgt, j);
                 const float* src = k < nseg
                                        ? a.po + (static_cast<int64_t>(seg0 + k) * kTQ + row) * D
-                                       : own + (k - nseg) * (D + 2) + 2;
+                                       : a.own_po + (own0 + static_cast<int64_t>(k - nseg) * a.G) * D;
 #pragma unroll
                 for (int c = 0; c < kCols; c += 2) {
                     const float2 f = *reinterpret_cast<const float2*>(src + lane * kCols + c);
-                    // a part without keys has weight 0 and zeros
                     o[c] = fmaf(wj, f.x, o[c]);
                     o[c + 1] = fmaf(wj, f.y, o[c + 1]);
                 }
@@ -601,7 +611,7 @@ cudaError_t launch_t(DType dt, const SharedArgs& s, cudaStream_t st) {
     p.W = d.Hk * p.nrt * p.nkt;
     int grid = s.num_sms < kSharedMaxGrid ? s.num_sms : kSharedMaxGrid;
     if (grid > p.W) grid = p.W;
-    const SharedLayout L = shared_layout(d.B, d.H, d.Hk, D, s.P, d.S_max);
+    const SharedLayout L = shared_layout(d.B, d.H, d.Hk, D, s.P);
     p.po = reinterpret_cast<float*>(s.ws + L.po);
     p.pm = reinterpret_cast<float2*>(s.ws + L.pm);
     p.slopes = d.slopes;
@@ -619,14 +629,29 @@ cudaError_t launch_t(DType dt, const SharedArgs& s, cudaStream_t st) {
                     : launch_prefix<T, D, false>(dt, s, p, grid, st);
         if (e != cudaSuccess) return e;
     }
-    DecodeArgs own = d;
-    own.ws = reinterpret_cast<float*>(s.ws + L.own);
-    e = launch_decode_partial(dt, own, st);
+    OwnArgs own{};
+    own.po = reinterpret_cast<float*>(s.ws + L.own_po);
+    own.pm = reinterpret_cast<float2*>(s.ws + L.own_pm);
+    own.cum = reinterpret_cast<int32_t*>(s.ws + L.cum);
+    own.lens = d.lens;
+    own.slopes = d.slopes;
+    own.err = s.err;
+    own.B = d.B;
+    own.H = d.H;
+    own.Hk = d.Hk;
+    own.S_max = d.S_max;
+    own.grid = 2 * s.num_sms < kOwnMaxGrid ? 2 * s.num_sms : kOwnMaxGrid;
+    own.scale = d.scale;
+    own.alibi = d.alibi;
+    e = launch_attention_own(dt, own, D, d.q, d.k, d.v, st);
     if (e != cudaSuccess) return e;
     CombineArgs c{};
     c.po = p.po;
     c.pm = p.pm;
-    c.rec = own.ws;
+    c.own_po = own.po;
+    c.own_pm = own.pm;
+    c.cum = own.cum;
+    c.own_grid = own.grid;
     c.lens = d.lens;
     c.slopes = d.slopes;
     c.o = d.o;
@@ -634,7 +659,6 @@ cudaError_t launch_t(DType dt, const SharedArgs& s, cudaStream_t st) {
     c.H = d.H;
     c.G = G;
     c.max_seq = d.S_max;
-    c.parts = d.parts;
     c.alibi = d.alibi;
     c.nkt = p.nkt;
     c.nrt = p.nrt;
@@ -648,15 +672,18 @@ cudaError_t launch_t(DType dt, const SharedArgs& s, cudaStream_t st) {
 
 }  // namespace
 
-SharedLayout shared_layout(int64_t B, int64_t H, int64_t Hk, int64_t d, int64_t P, int64_t S_max) {
+SharedLayout shared_layout(int64_t B, int64_t H, int64_t Hk, int64_t d, int64_t P) {
     const int64_t G = H / Hk, nrt = (B + kTQ / G - 1) / (kTQ / G);
     const int64_t segs = P ? kSharedMaxGrid + Hk * nrt : 0;
     auto up = [](int64_t n) { return (n + 255) / 256 * 256; };
     SharedLayout L;
     L.po = 0;
     L.pm = up(segs * kTQ * d * 4);
-    L.own = L.pm + up(segs * kTQ * 8);
-    L.total = L.own + up(B * H * decode_parts_max(S_max) * (d + 2) * 4);
+    L.own_po = L.pm + up(segs * kTQ * 8);
+    const int64_t own = (kOwnMaxGrid + B * Hk) * G;
+    L.own_pm = L.own_po + up(own * d * 4);
+    L.cum = L.own_pm + up(own * 8);
+    L.total = L.cum + up((B + 1) * 4);
     return L;
 }
 

@@ -186,15 +186,13 @@ struct DecodeArgs {
     int alibi;
 };
 cudaError_t launch_attention_decode(DType dt, const DecodeArgs& a, cudaStream_t s);
-// its first pass alone: (max, sum, output) of each part in the workspace
-cudaError_t launch_decode_partial(DType dt, const DecodeArgs& a, cudaStream_t s);
 // number of key ranges per (batch, kv head), and its device-independent bound
 int decode_parts(int64_t B, int64_t Hk, int64_t S_max, int64_t head_dim, int num_sms);
 int decode_parts_max(int64_t S_max);
 
 // ---- K6s: decode step of a batch that shares a prefix (attn_shared.cu)
 struct SharedArgs {
-    DecodeArgs own;        // the sequences' own caches (its ws is set by the launcher)
+    DecodeArgs own;        // the sequences' own caches (ws and parts unused)
     const void* k_prefix;  // [Hk, P, d]
     const void* v_prefix;
     int P;
@@ -202,11 +200,30 @@ struct SharedArgs {
     unsigned* err;
     int num_sms;
 };
-constexpr int kSharedMaxGrid = 256;  // CTAs of the prefix pass at most
+constexpr int kSharedMaxGrid = 256;   // CTAs of the prefix pass at most
+constexpr int kOwnMaxGrid = 512;      // CTAs of the own caches' pass at most
 struct SharedLayout {
-    int64_t po, pm, own, total;  // byte offsets in the workspace, and its size
+    // byte offsets in the workspace, and its size: the prefix's partial
+    // outputs and statistics, the own caches', their running tile counts
+    int64_t po, pm, own_po, own_pm, cum, total;
 };
-SharedLayout shared_layout(int64_t B, int64_t H, int64_t Hk, int64_t d, int64_t P, int64_t S_max);
+SharedLayout shared_layout(int64_t B, int64_t H, int64_t Hk, int64_t d, int64_t P);
+// the own caches' pass (attn_own.cu): partial results of its segments, record
+// c + b * Hk + g for CTA c's stay in unit (b, g)
+struct OwnArgs {
+    int pdl;
+    float* po;      // [records][G][d]
+    float2* pm;     // [records][G] (max, sum), log2 domain
+    int32_t* cum;   // [B + 1] 128-key tiles ahead of each sequence (per kv head)
+    const int32_t* lens;
+    const float* slopes;
+    unsigned* err;
+    int B, H, Hk, S_max, grid;
+    float scale;
+    int alibi;
+};
+cudaError_t launch_attention_own(DType dt, const OwnArgs& a, int d, const void* q, const void* k,
+                                 const void* v, cudaStream_t s);
 // (kv head, row tile, key tile) triples of the prefix pass
 int64_t shared_tiles(int64_t B, int64_t H, int64_t Hk, int64_t P);
 cudaError_t launch_attention_decode_shared(DType dt, const SharedArgs& s, cudaStream_t st);
