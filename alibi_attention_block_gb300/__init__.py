@@ -14,6 +14,7 @@ full-width or per-head qk-norm; partial NeoX rotary or ALiBi.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 
 import torch
 
@@ -62,7 +63,7 @@ def _same(dt_tensor, *ts):
 
 
 def _stream():
-    return C.c_void_p(torch.cuda.current_stream().cuda_stream)
+    return C.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
 def layernorm_bias(x, gamma, beta=None, residual=None, eps=1e-5, out=None):
@@ -137,34 +138,32 @@ def attn_prefill(q, k, v, alibi=False, slopes=None, scale=None, out=None):
     return o
 
 
-def _on_current_device(*ts):
-    """The library launches on the current device's stream: every tensor of the
-    call has to be there."""
-    dev = torch.cuda.current_device()
+def _pointers(dtype, dev, *ts):
+    """Device pointers of contiguous tensors of one type on device dev (None
+    stays None): _same and _p for a call's tensors in one pass (these calls
+    can be shorter than a dozen separate checks)."""
+    out = []
     for t in ts:
-        if t is not None and t.is_cuda and t.device.index != dev:
+        if t is None:
+            out.append(None)
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("expected a torch.Tensor")
+        if t.dtype is not dtype:
+            raise TypeError(f"expected a {dtype} tensor, got {t.dtype}")
+        if t.get_device() != dev:
+            if not t.is_cuda:
+                raise ValueError("tensors passed to the block library must be CUDA tensors")
             raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+        if not t.is_contiguous():
+            raise ValueError("tensors passed to the block library must be contiguous")
+        out.append(t.data_ptr())
+    return out
 
 
 def _shape(t, want, what):
-    if t is not None and tuple(t.shape) != want:
+    if t is not None and t.shape != want:
         raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {want}")
-
-
-def _int32(t, what):
-    if t.dtype != torch.int32:
-        raise TypeError(f"{what} are int32")
-
-
-def _slopes(slopes, n_heads):
-    if slopes is not None:
-        if slopes.dtype != torch.float32:
-            raise TypeError("ALiBi slopes are fp32")
-        _shape(slopes, (n_heads,), "slopes")
-
-
-def _ws_bytes(workspace):
-    return workspace.numel() * workspace.element_size()
 
 
 def packed_desc(tokens, prompts, n_heads, n_kv_heads, head_dim, prefix_len=0, alibi=False,
@@ -180,6 +179,24 @@ def attn_prefill_packed_workspace_size(desc) -> int:
     return need.value
 
 
+@functools.lru_cache(maxsize=256)
+def _packed_plan(*args):
+    """(descriptor by reference, workspace bytes) of a call's sizes."""
+    desc = packed_desc(*args)
+    return C.byref(desc), attn_prefill_packed_workspace_size(desc)
+
+
+def _prefix_len(k_prefix, v_prefix, n_kv_heads, head_dim):
+    if (k_prefix is None) != (v_prefix is None):
+        raise ValueError("k_prefix and v_prefix go together")
+    if k_prefix is None:
+        return 0
+    P = k_prefix.shape[1]
+    _shape(k_prefix, (n_kv_heads, P, head_dim), "k_prefix")
+    _shape(v_prefix, (n_kv_heads, P, head_dim), "v_prefix")
+    return P
+
+
 def attn_prefill_packed(q, k, v, cu_seqlens, k_prefix=None, v_prefix=None, alibi=False,
                         slopes=None, scale=None, out=None, workspace=None):
     """Causal attention over packed prompts: q [H, T, d], k/v [Hk, T, d] hold
@@ -188,33 +205,30 @@ def attn_prefill_packed(q, k, v, cu_seqlens, k_prefix=None, v_prefix=None, alibi
     v_prefix [Hk, P, d]: keys that every prompt sees ahead of its own. Returns
     o [T, H, d]; rows outside every prompt are not written (pass ``out`` to
     say what they hold)."""
-    _same(q, k, v, k_prefix, v_prefix, out)
+    dt = _dt(q)
     H, T, d = q.shape
     Hk = k.shape[0]
     _shape(k, (Hk, T, d), "k")
     _shape(v, (Hk, T, d), "v")
-    if (k_prefix is None) != (v_prefix is None):
-        raise ValueError("k_prefix and v_prefix go together")
-    P = 0 if k_prefix is None else k_prefix.shape[1]
-    _shape(k_prefix, (Hk, P, d), "k_prefix")
-    _shape(v_prefix, (Hk, P, d), "v_prefix")
+    P = _prefix_len(k_prefix, v_prefix, Hk, d)
     if P == 0:
         k_prefix = v_prefix = None
-    _int32(cu_seqlens, "cu_seqlens")
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
         raise ValueError("cu_seqlens has shape [prompts + 1]")
-    _slopes(slopes, H)
+    _shape(slopes, (H,), "slopes")
     _shape(out, (T, H, d), "out")
-    _on_current_device(q, k, v, k_prefix, v_prefix, cu_seqlens, slopes, out, workspace)
-    desc = packed_desc(T, cu_seqlens.numel() - 1, H, Hk, d, P, alibi, scale)
+    desc, need = _packed_plan(T, cu_seqlens.numel() - 1, H, Hk, d, P, alibi, scale)
     if workspace is None:
-        workspace = torch.empty(attn_prefill_packed_workspace_size(desc), dtype=torch.uint8,
-                                device=q.device)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     o = torch.empty((T, H, d), dtype=q.dtype, device=q.device) if out is None else out
+    dev = torch.cuda.current_device()
+    qp, kp, vp, kpp, vpp, op = _pointers(q.dtype, dev, q, k, v, k_prefix, v_prefix, o)
+    (cup,) = _pointers(torch.int32, dev, cu_seqlens)
+    (sp,) = _pointers(torch.float32, dev, slopes)
+    (wp,) = _pointers(workspace.dtype, dev, workspace)
     _abi.check(_lib().blk_attn_prefill_packed(
-        C.byref(desc), _p(q), _p(k), _p(v), _p(k_prefix), _p(v_prefix), _p(cu_seqlens),
-        _p(slopes), _p(o), _p(workspace), _ws_bytes(workspace), _dt(q), _stream()),
-        "blk_attn_prefill_packed")
+        desc, qp, kp, vp, kpp, vpp, cup, sp, op, wp, workspace.nbytes, dt,
+        torch._C._cuda_getCurrentRawStream(dev)), "blk_attn_prefill_packed")
     return o
 
 
@@ -266,6 +280,13 @@ def attn_decode_shared_workspace_size(desc) -> int:
     return need.value
 
 
+@functools.lru_cache(maxsize=256)
+def _decode_shared_plan(*args):
+    """(descriptor by reference, workspace bytes) of a call's sizes."""
+    desc = decode_shared_desc(*args)
+    return C.byref(desc), attn_decode_shared_workspace_size(desc)
+
+
 def attn_decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, lens, alibi=False, slopes=None,
                        scale=None, out=None, workspace=None):
     """One decode step of a batch that shares a prefix: q [B, H, d] (newest
@@ -273,32 +294,29 @@ def attn_decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, lens, alibi=Fals
     [Hk, P, d] (None: no prefix), stored once, and each sequence's own caches
     [B, Hk, S_max, d] of lens[b] keys (int32 [B] on the device; 0: the
     sequence takes no part, its row is zero). Returns o [B, H, d]."""
-    _same(q, k_prefix, v_prefix, k_cache, v_cache, out)
+    dt = _dt(q)
     B, H, d = q.shape
     Hk, S_max = k_cache.shape[1], k_cache.shape[2]
     _shape(k_cache, (B, Hk, S_max, d), "k_cache")
     _shape(v_cache, (B, Hk, S_max, d), "v_cache")
-    if (k_prefix is None) != (v_prefix is None):
-        raise ValueError("k_prefix and v_prefix go together")
-    P = 0 if k_prefix is None else k_prefix.shape[1]
-    _shape(k_prefix, (Hk, P, d), "k_prefix")
-    _shape(v_prefix, (Hk, P, d), "v_prefix")
+    P = _prefix_len(k_prefix, v_prefix, Hk, d)
     if P == 0:
         k_prefix = v_prefix = None
-    _int32(lens, "lens")
     _shape(lens, (B,), "lens")
-    _slopes(slopes, H)
+    _shape(slopes, (H,), "slopes")
     _shape(out, (B, H, d), "out")
-    _on_current_device(q, k_prefix, v_prefix, k_cache, v_cache, lens, slopes, out, workspace)
-    desc = decode_shared_desc(B, S_max, H, Hk, d, P, alibi, scale)
+    desc, need = _decode_shared_plan(B, S_max, H, Hk, d, P, alibi, scale)
     if workspace is None:
-        workspace = torch.empty(attn_decode_shared_workspace_size(desc), dtype=torch.uint8,
-                                device=q.device)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     o = torch.empty_like(q) if out is None else out
+    dev = torch.cuda.current_device()
+    qp, kpp, vpp, kp, vp, op = _pointers(q.dtype, dev, q, k_prefix, v_prefix, k_cache, v_cache, o)
+    (lp,) = _pointers(torch.int32, dev, lens)
+    (sp,) = _pointers(torch.float32, dev, slopes)
+    (wp,) = _pointers(workspace.dtype, dev, workspace)
     _abi.check(_lib().blk_attn_decode_shared(
-        C.byref(desc), _p(q), _p(k_prefix), _p(v_prefix), _p(k_cache), _p(v_cache), _p(lens),
-        _p(slopes), _p(o), _p(workspace), _ws_bytes(workspace), _dt(q), _stream()),
-        "blk_attn_decode_shared")
+        desc, qp, kpp, vpp, kp, vp, lp, sp, op, wp, workspace.nbytes, dt,
+        torch._C._cuda_getCurrentRawStream(dev)), "blk_attn_decode_shared")
     return o
 
 
