@@ -21,7 +21,10 @@
 // in boxes of 16 keys, multiplied over ceil(keys / 16) steps, and the values
 // behind its end are cleared: 0 times what an unused cache entry holds need
 // not be 0.
-// 6 warps: TMA; MMA issue (S(t+1) ahead of PV(t)); four of softmax.
+// 6 warps: TMA; MMA issue; four of softmax. The MMA thread issues what is ready
+// first, S of the next tile or PV of this one: with S always ahead, a tile's PV
+// waited for the next tile's keys to arrive (a memory latency per tile, 3000
+// to 4000 clocks). A segment's O is read out during the next one's first tile.
 // TMEM columns: S [0, 32) and O^T [32, 64), both double-buffered (by tile, by
 // segment).
 #include "internal.h"
@@ -153,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     extern __shared__ uint8_t smem_raw[];
     __shared__ int64_t sh_lo, sh_hi, sh_base;
     __shared__ int sh_b0;
-    __shared__ int sh_sum[kThreads];
+    __shared__ int sh_sum[kThreads / 32];
     uint8_t* smem = align_1024(smem_raw);
     const uint32_t sKV = smem_u32(smem);
     const uint32_t sQ = sKV + C::kOffQ, sP = sKV + C::kOffP;
@@ -201,8 +204,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         tmem_alloc(smem_u32(tmem_slot), 64);
         tmem_relinquish();
     }
+    // Behind the prefix pass there is nothing to wait for: that kernel lets
+    // this one start only after its own wait, when everything enqueued before
+    // it (the caches' writers, the previous merge, which reads this workspace)
+    // has completed. The wait is made up for at the end, so that this grid's
+    // completion stands for both.
     if (a.pdl) {
-        pdl_wait();
+        if (!a.after_prefix) pdl_wait();
         pdl_launch_dependents();
     }
     // this CTA's range of tiles: thread i sums the tiles of a run of sequences
@@ -210,16 +218,22 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int b_lo = min(static_cast<int>(threadIdx.x) * per, a.B), b_hi = min(b_lo + per, a.B);
     int mine = 0;
     for (int b = b_lo; b < b_hi; ++b) mine += (own_len(a, b) + kTK - 1) / kTK;
-    sh_sum[threadIdx.x] = mine;
+    int upto = mine;  // inclusive sum over the warp's threads, then over all
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (lane == 31) sh_sum[warp] = upto;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    int before = 0, total = 0;
-    for (int i = 0; i < kThreads; ++i) {
-        const int v = sh_sum[i];
-        if (i < static_cast<int>(threadIdx.x)) before += v;
-        total += v;
+    int before = upto - mine, total = 0;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) {
+        if (i < warp) before += sh_sum[i];
+        total += sh_sum[i];
     }
     const int64_t W = static_cast<int64_t>(total) * a.Hk;
     // with fewer tiles than CTAs, one for each of the first W (the merge
@@ -310,60 +324,104 @@ __global__ void __launch_bounds__(kThreads, 2)
             const uint64_t dv0 = make_sdesc_sw128(sKV, kTK * 128, 1024);
             const uint64_t dq0 = make_sdesc_sw128(sQ, 16, 1024);
             const uint64_t dp0 = make_sdesc_sw128(sP, 16, 1024);
-            // O^T += V^T P^T of tile t: `keys` of it, first of segment seg or not
-            auto issue_pv = [&](int t, int keys, bool first, int seg) -> bool {
-                const int r = 2 * t + 1, sl = r % kSlots;
-                if (!mbar_wait(full(sl), (r / kSlots) & 1, a.err)) return false;
-                if (!mbar_wait(p_full(t & 1), (t >> 1) & 1, a.err)) return false;
-                if (first && seg > 1 && !mbar_wait(o_free(seg & 1), ((seg >> 1) - 1) & 1, a.err))
-                    return false;
-                tc_fence_after();
-                const uint64_t dv = dv0 + sl * kSlotStep;
-                const uint64_t dp = dp0 + (t & 1) * (C::kPBytes >> 4);
-                const int steps = (min(keys, kTK) + 15) / 16;
-                for (int ks = 0; ks < steps; ++ks)
-                    tc_mma_ss(tmem_base + 32u + 16u * (seg & 1), dv + ks * ((16 * 128) >> 4),
-                              dp + (ks / 4) * (1024 >> 4) + (ks % 4) * 2, idesc_o,
-                              (!first || ks > 0) ? 1u : 0u);
-                tc_commit(pv_done(t & 1));
-                tc_commit(empty(sl));
+            struct Tile {
+                int t, it, keys;  // running number, segment, keys of it (may exceed kTK)
+                bool first, last; // of its segment
+            };
+            int i = 0;
+            auto next_tile = [&](Tile& x, int t) -> bool {
+                if (!c.valid) return false;
+                x.t = t;
+                x.it = c.it;
+                x.keys = c.len - (c.first + c.n - 1 - i) * kTK;
+                x.first = i == 0;
+                x.last = ++i == c.n;
+                if (x.last) {
+                    c.next(a);
+                    i = 0;
+                }
                 return true;
             };
-            int t = 0;  // tiles so far
-            int p_keys = 0, p_seg = 0;
-            bool p_first = false, ok = true;
-            while (ok && c.valid) {
-                for (int i = 0; i < c.n && ok; ++i, ++t) {
-                    // S of tile t, then PV of tile t - 1
-                    const int r = 2 * t, sl = r % kSlots;
-                    if (i == 0 && !mbar_wait(q_full(c.it & 1), (c.it >> 1) & 1, a.err)) {
-                        ok = false;
-                        break;
-                    }
-                    if (!mbar_wait(full(sl), (r / kSlots) & 1, a.err) ||
-                        (t > 1 && !mbar_wait(s_free(t & 1), ((t >> 1) - 1) & 1, a.err))) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint64_t dk = dk0 + sl * kSlotStep;
-                    const uint64_t dq = dq0 + (c.it & 1) * (C::kQBytes >> 4);
+            // S^T = K Q^T: the keys and (first tile) queries are there, and the
+            // softmax has read the S buffer's last tile
+            auto s_ready = [&](const Tile& x) {
+                const int r = 2 * x.t;
+                return mbar_test(full(r % kSlots), (r / kSlots) & 1) &&
+                       (!x.first || mbar_test(q_full(x.it & 1), (x.it >> 1) & 1)) &&
+                       (x.t < 2 || mbar_test(s_free(x.t & 1), ((x.t >> 1) - 1) & 1));
+            };
+            auto issue_s = [&](const Tile& x) {
+                tc_fence_after();
+                const int sl = 2 * x.t % kSlots;
+                const uint64_t dk = dk0 + sl * kSlotStep;
+                const uint64_t dq = dq0 + (x.it & 1) * (C::kQBytes >> 4);
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks)
-                        tc_mma_ss(tmem_base + 16u * (t & 1), dk + (ks / 4) * kAtom + (ks % 4) * 2,
-                                  dq + (ks / 4) * (1024 >> 4) + (ks % 4) * 2, idesc_s,
-                                  ks > 0 ? 1u : 0u);
-                    tc_commit(s_full(t & 1));
-                    tc_commit(empty(sl));
-                    if (i + 1 == c.n) tc_commit(q_empty(c.it & 1));
-                    if (t > 0) ok = issue_pv(t - 1, p_keys, p_first, p_seg);
-                    p_keys = c.len - (c.first + c.n - 1 - i) * kTK;
-                    p_first = i == 0;
-                    p_seg = c.it;
+                for (int ks = 0; ks < D / 16; ++ks)
+                    tc_mma_ss(tmem_base + 16u * (x.t & 1), dk + (ks / 4) * kAtom + (ks % 4) * 2,
+                              dq + (ks / 4) * (1024 >> 4) + (ks % 4) * 2, idesc_s, ks > 0 ? 1u : 0u);
+                tc_commit(s_full(x.t & 1));
+                tc_commit(empty(sl));
+                if (x.last) tc_commit(q_empty(x.it & 1));
+            };
+            // O^T += V^T P^T: the values and P are there, and (first tile) the O
+            // buffer's last segment has been read out
+            auto pv_ready = [&](const Tile& x) {
+                const int r = 2 * x.t + 1;
+                return mbar_test(full(r % kSlots), (r / kSlots) & 1) &&
+                       mbar_test(p_full(x.t & 1), (x.t >> 1) & 1) &&
+                       (!x.first || x.it < 2 || mbar_test(o_free(x.it & 1), ((x.it >> 1) - 1) & 1));
+            };
+            auto issue_pv = [&](const Tile& x) {
+                tc_fence_after();
+                const int sl = (2 * x.t + 1) % kSlots;
+                const uint64_t dv = dv0 + sl * kSlotStep;
+                const uint64_t dp = dp0 + (x.t & 1) * (C::kPBytes >> 4);
+                const int steps = (min(x.keys, kTK) + 15) / 16;
+#pragma unroll
+                for (int ks = 0; ks < kTK / 16; ++ks)
+                    if (ks < steps)
+                        tc_mma_ss(tmem_base + 32u + 16u * (x.it & 1), dv + ks * ((16 * 128) >> 4),
+                                  dp + (ks / 4) * (1024 >> 4) + (ks % 4) * 2, idesc_o,
+                                  (!x.first || ks > 0) ? 1u : 0u);
+                tc_commit(pv_done(x.t & 1));
+                tc_commit(empty(sl));
+            };
+            Tile now, nxt;
+            bool have = next_tile(now, 0), more = true, s_out = false, pv_out = false;
+            bool ahead = false;  // S of nxt is out
+            if (have) more = next_tile(nxt, 1);
+            uint64_t t0 = globaltimer_ns();
+            for (uint32_t spin = 1; have; ++spin) {
+                bool did = false;
+                if (!s_out) {
+                    if (s_ready(now)) {
+                        issue_s(now);
+                        s_out = did = true;
+                    }
+                } else if (more && !ahead && s_ready(nxt)) {
+                    issue_s(nxt);
+                    ahead = did = true;
                 }
-                c.next(a);
+                if (s_out && !pv_out && pv_ready(now)) {
+                    issue_pv(now);
+                    pv_out = did = true;
+                }
+                if (pv_out) {  // on to the next tile
+                    have = more;
+                    now = nxt;
+                    s_out = ahead;
+                    pv_out = ahead = false;
+                    if (more) more = next_tile(nxt, now.t + 1);
+                }
+                if (did) {
+                    spin = 0;
+                } else if (spin == 1) {
+                    t0 = globaltimer_ns();
+                } else if ((spin & 63u) == 0u && globaltimer_ns() - t0 > kWaitLimitNs) {
+                    report_error(a.err, DEV_ERR_TIMEOUT);
+                    break;
+                }
             }
-            if (ok && t > 0) issue_pv(t - 1, p_keys, p_first, p_seg);
         }
     } else {
         const int quarter = warp & 3;
@@ -378,6 +436,27 @@ __global__ void __launch_bounds__(kThreads, 2)
         float* red_sum = reinterpret_cast<float*>(smem + C::kOffSum);
         int t = 0;
         bool ok = true;
+        // a segment's O is in TMEM until its last PV has completed: read out
+        // behind the next segment's first tile
+        bool pend = false;
+        int pend_t = 0, pend_buf = 0;
+        int64_t pend_rec = 0;
+        auto read_out = [&]() -> bool {
+            if (!mbar_wait(pv_done(pend_t & 1), (pend_t >> 1) & 1, a.err)) return false;
+            tc_fence_after();
+            uint32_t o[G];
+            tmem_ldn<G>(tO + 16u * pend_buf, o);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_free(pend_buf));
+            if (has_dim) {
+#pragma unroll
+                for (int h = 0; h < G; ++h)
+                    a.po[(pend_rec * G + h) * D + dim] = __uint_as_float(o[h]);
+            }
+            __syncwarp();
+            return true;
+        };
         while (ok && c.valid) {
             float m[G], l[G], slope[G];
 #pragma unroll
@@ -485,6 +564,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full(t & 1));
+                if (pend) {
+                    ok = read_out();
+                    pend = false;
+                    if (!ok) break;
+                }
             }
             if (!ok) break;
             // the segment's result
@@ -497,21 +581,16 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(sum_full);
-            if (!mbar_wait(sum_full, c.it & 1, a.err)) break;
-            if (!mbar_wait(pv_done((t - 1) & 1), ((t - 1) >> 1) & 1, a.err)) break;
-            tc_fence_after();
-            uint32_t o[G];
-            tmem_ldn<G>(tO + 16u * (c.it & 1), o);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(o_free(c.it & 1));
+            if (!mbar_wait(sum_full, c.it & 1, a.err)) {
+                ok = false;
+                break;
+            }
             const int64_t rec = static_cast<int64_t>(blockIdx.x) +
                                 (static_cast<int64_t>(c.b) * a.Hk + c.g);
-            if (has_dim) {
-#pragma unroll
-                for (int h = 0; h < G; ++h)
-                    a.po[(rec * G + h) * D + dim] = __uint_as_float(o[h]);
-            }
+            pend = true;
+            pend_t = t - 1;
+            pend_buf = c.it & 1;
+            pend_rec = rec;
             if (quarter == 0 && lane < G) {
                 const float4 w = *reinterpret_cast<const float4*>(red_sum + (c.it & 1) * 32 + lane * 4);
                 float mh = m[0];
@@ -522,12 +601,14 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             c.next(a);
         }
+        if (ok && pend) read_out();
     }
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem_base, 64);
     }
+    if (a.pdl && a.after_prefix) pdl_wait();
 }
 
 template <typename T, int D, int G>

@@ -212,6 +212,7 @@ SharedLayout shared_layout(int64_t B, int64_t H, int64_t Hk, int64_t d, int64_t 
 // c + b * Hk + g for CTA c's stay in unit (b, g)
 struct OwnArgs {
     int pdl;
+    int after_prefix;  // launched behind the prefix pass, whose results it does not need
     float* po;      // [records][G][d]
     float2* pm;     // [records][G] (max, sum), log2 domain
     int32_t* cum;   // [B + 1] 128-key tiles ahead of each sequence (per kv head)

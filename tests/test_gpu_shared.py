@@ -135,19 +135,23 @@ def test_lengths_clamped_and_deterministic():
     assert torch.equal(call([7, 8, 9]), call([7, 8, 9]))
 
 
-@pytest.mark.parametrize("H,Hk,d", [(16, 4, 128), (8, 8, 64), (8, 8, 128)])
-def test_back_to_back_over_a_long_prefix(H, Hk, d):
+@pytest.mark.parametrize("B,H,Hk,d,P,S", [
+    (64, 16, 4, 128, 16384, 256), (64, 8, 8, 64, 16384, 256), (64, 8, 8, 128, 16384, 256),
+    (256, 4, 4, 64, 5000, 20), (200, 4, 1, 64, 20000, 20),
+    # three row tiles per kv head and many kv heads: CTAs pass through several
+    # units, with and without a second row tile
+    (300, 200, 200, 64, 100, 3), (257, 160, 160, 128, 200, 3), (72, 320, 40, 128, 400, 3)])
+def test_back_to_back(B, H, Hk, d, P, S):
     """Every query row in use and many key tiles per CTA, so that the two
     streams run far apart while loads are late: 25 steps without a pause give
     the same bits, and rows of them are the oracle's."""
-    B, P, S = 64, 16384, 256
     q, kp, vp, k, v = inputs(B, H, Hk, d, P, S, "bf16", 91)
     lens = [1 + (37 * i) % S for i in range(B)]
     args = [to_dev(t) for t in (q, kp, vp, k, v)] + [torch.tensor(lens, dtype=torch.int32, device="cuda")]
     outs = [blk.attn_decode_shared(*args) for _ in range(25)]
     blk.check_device_status()
     assert all(torch.equal(o, outs[0]) for o in outs)
-    for b in (0, 29, 33, 63):
+    for b in (0, B // 2 - 3, B - 1):
         check(outs[0][b:b + 1], q[b:b + 1], kp, vp, k[b:b + 1], v[b:b + 1], lens[b:b + 1], "bf16", name=f"row {b}")
 
 
