@@ -218,16 +218,18 @@ def attn_prefill_packed(q, k, v, cu_seqlens, k_prefix=None, v_prefix=None, alibi
     _shape(slopes, (H,), "slopes")
     _shape(out, (T, H, d), "out")
     desc, need = _packed_plan(T, cu_seqlens.numel() - 1, H, Hk, d, P, alibi, scale)
-    if workspace is None:
+    if workspace is None and need:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     o = torch.empty((T, H, d), dtype=q.dtype, device=q.device) if out is None else out
     dev = torch.cuda.current_device()
     qp, kp, vp, kpp, vpp, op = _pointers(q.dtype, dev, q, k, v, k_prefix, v_prefix, o)
     (cup,) = _pointers(torch.int32, dev, cu_seqlens)
     (sp,) = _pointers(torch.float32, dev, slopes)
-    (wp,) = _pointers(workspace.dtype, dev, workspace)
+    wp, wn = None, 0
+    if workspace is not None:
+        (wp,), wn = _pointers(workspace.dtype, dev, workspace), workspace.nbytes
     _abi.check(_lib().blk_attn_prefill_packed(
-        desc, qp, kp, vp, kpp, vpp, cup, sp, op, wp, workspace.nbytes, dt,
+        desc, qp, kp, vp, kpp, vpp, cup, sp, op, wp, wn, dt,
         torch._C._cuda_getCurrentRawStream(dev)), "blk_attn_prefill_packed")
     return o
 

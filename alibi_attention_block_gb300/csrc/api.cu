@@ -349,10 +349,10 @@ blk_status validate_packed_desc(const blk_packed_desc* d) {
 }
 
 size_t packed_ws_bytes(const blk_packed_desc* d) {
-    return align256(sizeof(int4) * (1 + static_cast<size_t>(packed_max_units(
-                                            d->tokens, d->prompts, static_cast<int>(d->n_heads),
-                                            static_cast<int>(d->n_kv_heads),
-                                            static_cast<int>(d->head_dim)))));
+    return align256(sizeof(int4) * static_cast<size_t>(packed_plan_entries(
+                                       d->tokens, d->prompts, static_cast<int>(d->n_heads),
+                                       static_cast<int>(d->n_kv_heads),
+                                       static_cast<int>(d->head_dim))));
 }
 
 blk_status validate_block(const blk_block_desc* d, const blk_block_weights* w,
@@ -1041,7 +1041,7 @@ blk_status blk_attn_prefill_packed(const blk_packed_desc* d, const void* q, cons
     BLK_REQUIRE(!alibi_slopes || (reinterpret_cast<uintptr_t>(alibi_slopes) & 3u) == 0,
                 "alibi_slopes must be 4-byte aligned");
     const size_t need = packed_ws_bytes(d);
-    if (!workspace || ws_bytes < need || !aligned16(workspace))
+    if (need && (!workspace || ws_bytes < need || !aligned16(workspace)))
         return fail(BLK_EWORKSPACE, "workspace needs %zu bytes, 16-byte aligned", need);
     DevState* ds = nullptr;
     if ((st = dev_state(&ds)) != BLK_OK) return st;

@@ -11,7 +11,8 @@ namespace {
 
 // ---- packed prompts: the work list -----------------------------------
 // The prompts' lengths are device data, so the list of work units is built on
-// the device, by one block: unit l of a prompt of n units attends to about l
+// the device: a short one by every CTA of the attention kernel for itself
+// (attn_plan.cuh), a long one by one block ahead of it: unit l of a prompt of n units attends to about l
 // key tiles more than unit 0, so a counting sort by l (in kPlanBins bins of
 // 2^shift units), largest first, orders the units heaviest first, as the
 // dense kernels order theirs. The order within a bin is whatever the shared
@@ -89,6 +90,11 @@ int64_t packed_max_units(int64_t tokens, int64_t prompts, int H, int Hk, int d) 
     return tokens / packed_unit(H, Hk, d) + prompts;
 }
 
+int64_t packed_plan_entries(int64_t tokens, int64_t prompts, int H, int Hk, int d) {
+    const int64_t units = packed_max_units(tokens, prompts, H, Hk, d);
+    return prompts <= kPlanCtaPrompts && units <= kPlanCtaUnits ? 0 : 1 + units;
+}
+
 cudaError_t launch_attention_packed(DType dt, const AttnArgs& a, const PackedArgs& p,
                                     cudaStream_t s) {
     const int unit = packed_unit(a.H, a.Hk, a.d);
@@ -96,7 +102,10 @@ cudaError_t launch_attention_packed(DType dt, const AttnArgs& a, const PackedArg
     int shift = 0;
     while ((static_cast<int64_t>(a.S / unit) >> shift) >= kPlanBins) ++shift;
     AttnPack<true> pack;
-    pack.plan = p.plan;
+    const bool listed = packed_plan_entries(a.S, p.prompts, a.H, a.Hk, a.d) != 0;
+    pack.plan = listed ? p.plan : nullptr;
+    pack.cu_seqlens = p.cu_seqlens;
+    pack.prompts = p.prompts;
     pack.prefix = p.prefix;
     // without a prefix the maps are never used: any valid one will do
     const void* kp = p.prefix ? p.k_prefix : a.k;
@@ -105,11 +114,13 @@ cudaError_t launch_attention_packed(DType dt, const AttnArgs& a, const PackedArg
     if (!make_tmap_3d(&pack.tmPK, dt, kp, a.Hk, rows, a.d, 128) ||
         !make_tmap_3d(&pack.tmPV, dt, vp, a.Hk, rows, a.d, 128))
         return cudaErrorInvalidValue;
-    const bool pdl = pdl_allowed(s);
-    cudaError_t e = launch_pdl(pdl, plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p.cu_seqlens,
-                               p.prompts, a.S, unit, shift, static_cast<int>(max_units), p.plan,
-                               pdl ? 1 : 0);
-    if (e != cudaSuccess) return e;
+    if (listed) {
+        const bool pdl = pdl_allowed(s);
+        const cudaError_t e = launch_pdl(pdl, plan_kernel, dim3(1), dim3(kPlanThreads), 0, s,
+                                         p.cu_seqlens, p.prompts, a.S, unit, shift,
+                                         static_cast<int>(max_units), p.plan, pdl ? 1 : 0);
+        if (e != cudaSuccess) return e;
+    }
     if (a.d == 64) return launch_attention_pair64_packed(dt, a, pack, max_units, s);
     if (a.d == 128 && a.H == a.Hk)
         return launch_attention_pair128_packed(dt, a, pack, max_units, s);

@@ -43,6 +43,7 @@
 // TMEM columns: S0 [0, 128), S1 [128, 256), P [256, 320) (two 16-bit values
 // per column), O [320, 320 + d).
 // Query scale head_dim^-0.5 follows nnterp "stablelm" 03 Notes.
+#include "attn_plan.cuh"
 #include "internal.h"
 
 namespace blk {
@@ -87,6 +88,7 @@ struct GqaPack {
 // prompt's own.
 template <bool PACKED>
 struct GqaCursor {
+    using Plan = typename PlanStorage<PACKED>::type;
     int item, it, pb, b, g, hc, p0, nkv;
     bool valid;
     int start_row, len, nP, prefix;
@@ -95,17 +97,17 @@ struct GqaCursor {
         return round * Gd + ((round & 1) ? Gd - 1 - c : c);
     }
     __device__ __forceinline__ void decode(const AttnArgs& a, const GqaPack& pk,
-                                           const AttnPack<PACKED>& pack, int nblk) {
+                                           const AttnPack<PACKED>& pack, const Plan& plan, int nblk) {
         if constexpr (PACKED) {
             const int per_unit = a.Hk * pk.nhc;
-            const int4 u = pack.plan[1 + item / per_unit];
+            const PlanUnit u = plan_unit(pack, plan, item / per_unit);
             const int rest = item % per_unit;
             hc = rest % pk.nhc;
             g = rest / pk.nhc;
             b = 0;
-            start_row = u.x;
-            len = u.y;
-            p0 = u.z * pk.R;
+            start_row = u.first;
+            len = u.len;
+            p0 = u.l * pk.R;
             prefix = pack.prefix;
             nP = (prefix + kTK - 1) / kTK;
             nkv = nP + (min(p0 + pk.R, len) + kTK - 1) / kTK;
@@ -123,18 +125,18 @@ struct GqaCursor {
         nkv = (last + kTK - 1) / kTK;
     }
     __device__ __forceinline__ void start(const AttnArgs& a, const GqaPack& pk,
-                                          const AttnPack<PACKED>& pack, int nblk, int n_items) {
+                                          const AttnPack<PACKED>& pack, const Plan& plan, int nblk, int n_items) {
         it = 0;
         item = item_of(0);
         valid = item < n_items;
-        if (valid) decode(a, pk, pack, nblk);
+        if (valid) decode(a, pk, pack, plan, nblk);
     }
     __device__ __forceinline__ void next(const AttnArgs& a, const GqaPack& pk,
-                                          const AttnPack<PACKED>& pack, int nblk, int n_items) {
+                                          const AttnPack<PACKED>& pack, const Plan& plan, int nblk, int n_items) {
         ++it;
         item = item_of(it);
         valid = item < n_items;
-        if (valid) decode(a, pk, pack, nblk);
+        if (valid) decode(a, pk, pack, plan, nblk);
     }
 };
 
@@ -150,6 +152,7 @@ __global__ void __launch_bounds__(gqa_threads(PACKED), 1)
     // bias is largest there, so the rescale of O stays rare)
     constexpr bool kRev = ALIBI && PACKED;
     extern __shared__ uint8_t smem_raw[];
+    __shared__ typename PlanStorage<PACKED>::type plan;
     uint8_t* smem = align_1024(smem_raw);
     const uint32_t sQ = smem_u32(smem);
     const uint32_t sK = sQ + Cfg::kOffK;
@@ -210,13 +213,16 @@ __global__ void __launch_bounds__(gqa_threads(PACKED), 1)
         pdl_wait();  // inputs written by the previous kernel are visible from here on
         pdl_launch_dependents();
     }
-    if constexpr (PACKED) n_items = pack.plan[0].x * a.Hk * pk.nhc;
+    if constexpr (PACKED) {
+        if (!pack.plan) build_plan(plan, pack.cu_seqlens, pack.prompts, a.S, pk.R);
+        n_items = plan_units(pack, plan) * a.Hk * pk.nhc;
+    }
 
     if (warp == 0) {
         if (lane == 0) {
             const uint64_t pol_kv = l2_evict_last_policy(), pol_q = l2_evict_first_policy();
             GqaCursor<PACKED> c;
-            c.start(a, pk, pack, nblk, n_items);
+            c.start(a, pk, pack, plan, nblk, n_items);
             int gk = 0, gv = 0;  // K and V tiles loaded so far (ring positions)
             bool ok = true;
             // the map and first row of step j's key tile
@@ -278,7 +284,7 @@ __global__ void __launch_bounds__(gqa_threads(PACKED), 1)
                     if (j + 1 < c.nkv) ok = load_k(j + 1);
                     if (ok) ok = load_v(j);
                 }
-                c.next(a, pk, pack, nblk, n_items);
+                c.next(a, pk, pack, plan, nblk, n_items);
             }
         }
     } else if (warp == 1) {
@@ -334,7 +340,7 @@ __global__ void __launch_bounds__(gqa_threads(PACKED), 1)
                 return true;
             };
             GqaCursor<PACKED> c;
-            c.start(a, pk, pack, nblk, n_items);
+            c.start(a, pk, pack, plan, nblk, n_items);
             bool ok = true;
             while (ok && c.valid) {
                 const int qb = c.it % kQB;
@@ -350,7 +356,7 @@ __global__ void __launch_bounds__(gqa_threads(PACKED), 1)
                     if (ok) ok = issue_pv(j == 0);
                 }
                 ++itx;
-                c.next(a, pk, pack, nblk, n_items);
+                c.next(a, pk, pack, plan, nblk, n_items);
             }
         }
     } else if (PACKED && warp == 6) {
@@ -358,7 +364,7 @@ __global__ void __launch_bounds__(gqa_threads(PACKED), 1)
             // passes each V tile on, the rows behind the prompt's end cleared
             // (see attn_pair.cu)
             GqaCursor<PACKED> c;
-            c.start(a, pk, pack, nblk, n_items);
+            c.start(a, pk, pack, plan, nblk, n_items);
             int gv = 0;
             bool ok = true;
             while (ok && c.valid) {
@@ -375,7 +381,7 @@ __global__ void __launch_bounds__(gqa_threads(PACKED), 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(v_ready(st));
                 }
-                c.next(a, pk, pack, nblk, n_items);
+                c.next(a, pk, pack, plan, nblk, n_items);
             }
         }
     } else {
@@ -391,7 +397,7 @@ __global__ void __launch_bounds__(gqa_threads(PACKED), 1)
         const int rpos = row - hl * R;   // position offset within the block
         float slope_l2 = 0.f;
         GqaCursor<PACKED> c;
-        c.start(a, pk, pack, nblk, n_items);
+        c.start(a, pk, pack, plan, nblk, n_items);
         int g = 0;  // key tiles processed (across items)
         bool ok = true;
         bool pend = false;      // an item's O is still in TMEM
@@ -548,7 +554,7 @@ __global__ void __launch_bounds__(gqa_threads(PACKED), 1)
             pend_l = l;
             const int64_t row0 = PACKED ? c.start_row : static_cast<int64_t>(c.b) * a.S;
             pend_row = (in_group && pos < S_own) ? (row0 + pos) * a.H + h : -1;
-            c.next(a, pk, pack, nblk, n_items);
+            c.next(a, pk, pack, plan, nblk, n_items);
         }
         // the last item's O
         if (ok && pend && mbar_wait(pv_done, (g - 1) & 1, a.err)) {

@@ -52,6 +52,7 @@
 // the persistent CTAs in alternating directions.
 // Query scale head_dim^-0.5 and GQA (kv head = h / (H/Hk)) follow nnterp
 // "stablelm" 03 Notes.
+#include "attn_plan.cuh"
 #include "internal.h"
 
 namespace blk {
@@ -100,6 +101,7 @@ struct PairCfg {
 // nP prefix tiles come ahead of its own key tiles.
 template <bool PACKED>
 struct PairCursor {
+    using Plan = typename PlanStorage<PACKED>::type;
     int item, it, i, b, h, g, nA, nB;
     bool valid;
     // packed: the prompt's first row and length, the prefix's key tiles
@@ -108,16 +110,16 @@ struct PairCursor {
         const int G = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
         return round * G + ((round & 1) ? G - 1 - c : c);
     }
-    __device__ __forceinline__ void decode(const AttnArgs& a, const AttnPack<PACKED>& pack, int nq,
+    __device__ __forceinline__ void decode(const AttnArgs& a, const AttnPack<PACKED>& pack, const Plan& plan, int nq,
                                            int np) {
         if constexpr (PACKED) {
-            const int4 u = pack.plan[1 + item / a.H];
+            const PlanUnit u = plan_unit(pack, plan, item / a.H);
             h = item % a.H;
             b = 0;
             g = h / (a.H / a.Hk);
-            start_row = u.x;
-            len = u.y;
-            i = u.z;
+            start_row = u.first;
+            len = u.len;
+            i = u.l;
             prefix = pack.prefix;
             nP = (prefix + kTK - 1) / kTK;
             nA = nP + 2 * i + 1;
@@ -133,19 +135,19 @@ struct PairCursor {
         nA = 2 * i + 1;                          // key tiles of query tile 2i
         nB = (2 * i + 1 < nq) ? 2 * i + 2 : 0;   // of query tile 2i+1, if present
     }
-    __device__ __forceinline__ void start(const AttnArgs& a, const AttnPack<PACKED>& pack, int nq, int np,
+    __device__ __forceinline__ void start(const AttnArgs& a, const AttnPack<PACKED>& pack, const Plan& plan, int nq, int np,
                                           int n_items) {
         it = 0;
         item = item_of(0);
         valid = item < n_items;
-        if (valid) decode(a, pack, nq, np);
+        if (valid) decode(a, pack, plan, nq, np);
     }
-    __device__ __forceinline__ void next(const AttnArgs& a, const AttnPack<PACKED>& pack, int nq, int np,
+    __device__ __forceinline__ void next(const AttnArgs& a, const AttnPack<PACKED>& pack, const Plan& plan, int nq, int np,
                                           int n_items) {
         ++it;
         item = item_of(it);
         valid = item < n_items;
-        if (valid) decode(a, pack, nq, np);
+        if (valid) decode(a, pack, plan, nq, np);
     }
     __device__ __forceinline__ int n_kv() const { return nB ? nB : nA; }
 };
@@ -165,6 +167,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     // slopes above 1/23.
     constexpr bool kRev = ALIBI;
     extern __shared__ uint8_t smem_raw[];
+    __shared__ typename PlanStorage<PACKED>::type plan;
     uint8_t* smem = align_1024(smem_raw);
     const uint32_t sQ = smem_u32(smem);      // Q[buf][x] at (2 buf + x) tiles
     const uint32_t sKV = sQ + Cfg::kOffKV;   // stage s: K at 2s, V at 2s + 1 tiles
@@ -229,7 +232,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         pdl_wait();  // inputs written by the previous kernel are visible from here on
         pdl_launch_dependents();
     }
-    if constexpr (PACKED) n_items = pack.plan[0].x * a.H;
+    if constexpr (PACKED) {
+        if (!pack.plan) build_plan(plan, pack.cu_seqlens, pack.prompts, a.S, 2 * kTQ);
+        n_items = plan_units(pack, plan) * a.H;
+    }
     // registers: the launch gives every thread kLaunchRegs; warpgroup 0 (TMA,
     // MMA issue) gives most of its share to the two softmax warpgroups, which
     // hold a row's 128 scores and 64 packed probabilities at once
@@ -241,7 +247,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         if (lane == 0) {
             const uint64_t pol_kv = l2_evict_last_policy(), pol_q = l2_evict_first_policy();
             PairCursor<PACKED> c;
-            c.start(a, pack, nq, np, n_items);
+            c.start(a, pack, plan, nq, np, n_items);
             int gkv = 0;  // K/V tiles loaded so far (ring position)
             bool ok = true;
             while (ok && c.valid) {
@@ -290,7 +296,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         tma_load_3d_hint(sK + Cfg::kKVBytes + sub * kTK * 128, mV, v_full(st),
                                     sub * 64, krow, c.b * a.Hk + c.g, pol_kv);
                 }
-                c.next(a, pack, nq, np, n_items);
+                c.next(a, pack, plan, nq, np, n_items);
             }
         }
     } else if (warp == 1 || warp == 2) {
@@ -341,7 +347,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 return true;
             };
             PairCursor<PACKED> c;
-            c.start(a, pack, nq, np, n_items);
+            c.start(a, pack, plan, nq, np, n_items);
             int gkv = 0;
             bool ok = true;
             while (ok && c.valid) {
@@ -390,7 +396,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 }
                 gkv += nkv;
                 if (nx > 0) ++itx;
-                c.next(a, pack, nq, np, n_items);
+                c.next(a, pack, plan, nq, np, n_items);
             }
         }
     } else if constexpr (PACKED) {
@@ -398,7 +404,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         // the prompt's end (the next prompt's) cleared: their P is 0, but 0
         // times a non-finite value of another prompt is not
         PairCursor<PACKED> c;
-        c.start(a, pack, nq, np, n_items);
+        c.start(a, pack, plan, nq, np, n_items);
         int gkv = 0;
         bool ok = true;
         while (ok && c.valid) {
@@ -416,7 +422,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(v_ready(st));
             }
-            c.next(a, pack, nq, np, n_items);
+            c.next(a, pack, plan, nq, np, n_items);
         }
     }
     } else {
@@ -432,7 +438,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const uint32_t tP = tmem_base + Cfg::kColP + 64u * x;
         const float scale_l2 = a.scale * kLog2e;
         PairCursor<PACKED> c;
-        c.start(a, pack, nq, np, n_items);
+        c.start(a, pack, plan, nq, np, n_items);
         int g = 0;  // key tiles processed (across items)
         bool ok = true;
         // The read-out of an item's O waits for its last PV; it is deferred to
@@ -445,7 +451,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         while (ok && c.valid) {
             const int nx = x ? c.nB : c.nA;
             if (nx == 0) {
-                c.next(a, pack, nq, np, n_items);
+                c.next(a, pack, plan, nq, np, n_items);
                 continue;
             }
             const int qt = 2 * c.i + x;
@@ -623,7 +629,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 pend_row = qpos < c.len ? (static_cast<int64_t>(c.start_row) + qpos) * a.H + c.h : -1;
             else
                 pend_row = qpos < a.S ? (static_cast<int64_t>(c.b) * a.S + qpos) * a.H + c.h : -1;
-            c.next(a, pack, nq, np, n_items);
+            c.next(a, pack, plan, nq, np, n_items);
         }
         // the last item's O
         if (ok && pend && mbar_wait_inl(pv_done(x), (g - 1) & 1, a.err)) {

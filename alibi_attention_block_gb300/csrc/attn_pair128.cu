@@ -33,6 +33,7 @@
 //               warpgroup's first tile of its next item.
 // Query scale head_dim^-0.5 and GQA (kv head = h / (H/Hk)) follow nnterp
 // "stablelm" 03 Notes; ALiBi "Bloom in a sovereign engine", Contribution.
+#include "attn_plan.cuh"
 #include "internal.h"
 
 namespace blk {
@@ -69,6 +70,7 @@ struct Cfg {
 // list, head) and the prefix's nP key tiles come ahead of the prompt's own.
 template <bool PACKED>
 struct PairCursor {
+    using Plan = typename PlanStorage<PACKED>::type;
     int item, it, i, b, h, g, nA, nB;
     bool valid;
     int start_row, len, nP, prefix;
@@ -76,16 +78,16 @@ struct PairCursor {
         const int G = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
         return round * G + ((round & 1) ? G - 1 - c : c);
     }
-    __device__ __forceinline__ void decode(const AttnArgs& a, const AttnPack<PACKED>& pack, int nq,
+    __device__ __forceinline__ void decode(const AttnArgs& a, const AttnPack<PACKED>& pack, const Plan& plan, int nq,
                                            int np) {
         if constexpr (PACKED) {
-            const int4 u = pack.plan[1 + item / a.H];
+            const PlanUnit u = plan_unit(pack, plan, item / a.H);
             h = item % a.H;
             b = 0;
             g = h / (a.H / a.Hk);
-            start_row = u.x;
-            len = u.y;
-            i = u.z;
+            start_row = u.first;
+            len = u.len;
+            i = u.l;
             prefix = pack.prefix;
             nP = (prefix + kTK - 1) / kTK;
             nA = nP + 2 * i + 1;
@@ -101,19 +103,19 @@ struct PairCursor {
         nA = 2 * i + 1;
         nB = (2 * i + 1 < nq) ? 2 * i + 2 : 0;
     }
-    __device__ __forceinline__ void start(const AttnArgs& a, const AttnPack<PACKED>& pack, int nq, int np,
+    __device__ __forceinline__ void start(const AttnArgs& a, const AttnPack<PACKED>& pack, const Plan& plan, int nq, int np,
                                           int n_items) {
         it = 0;
         item = item_of(0);
         valid = item < n_items;
-        if (valid) decode(a, pack, nq, np);
+        if (valid) decode(a, pack, plan, nq, np);
     }
-    __device__ __forceinline__ void next(const AttnArgs& a, const AttnPack<PACKED>& pack, int nq, int np,
+    __device__ __forceinline__ void next(const AttnArgs& a, const AttnPack<PACKED>& pack, const Plan& plan, int nq, int np,
                                           int n_items) {
         ++it;
         item = item_of(it);
         valid = item < n_items;
-        if (valid) decode(a, pack, nq, np);
+        if (valid) decode(a, pack, plan, nq, np);
     }
     __device__ __forceinline__ int n_kv() const { return nB ? nB : nA; }
 };
@@ -132,6 +134,7 @@ __global__ void __launch_bounds__(kP128Threads, 1)
     // slopes above 1/23.
     constexpr bool kRev = ALIBI;
     extern __shared__ uint8_t smem_raw[];
+    __shared__ typename PlanStorage<PACKED>::type plan;
     uint8_t* smem = align_1024(smem_raw);
     const uint32_t sQ = smem_u32(smem);     // Q_x at x tiles
     const uint32_t sKV = sQ + Cfg::kOffKV;  // stage s: K at 2s, V at 2s + 1 tiles
@@ -195,7 +198,10 @@ __global__ void __launch_bounds__(kP128Threads, 1)
         pdl_wait();  // inputs written by the previous kernel are visible from here on
         pdl_launch_dependents();
     }
-    if constexpr (PACKED) n_items = pack.plan[0].x * a.H;
+    if constexpr (PACKED) {
+        if (!pack.plan) build_plan(plan, pack.cu_seqlens, pack.prompts, a.S, 2 * kTQ);
+        n_items = plan_units(pack, plan) * a.H;
+    }
     static_assert(4 * kRegsControl + 8 * kRegsSoftmax <= 12 * kLaunchRegs,
                   "register split exceeds the launch's registers");
     if (warp < 4) {
@@ -203,7 +209,7 @@ __global__ void __launch_bounds__(kP128Threads, 1)
         if (warp == 0 && lane == 0) {
             const uint64_t pol_kv = l2_evict_last_policy(), pol_q = l2_evict_first_policy();
             PairCursor<PACKED> c;
-            c.start(a, pack, nq, np, n_items);
+            c.start(a, pack, plan, nq, np, n_items);
             int gkv = 0;
             int itq[2] = {0, 0};  // Q fills per query tile
             bool ok = true;
@@ -256,7 +262,7 @@ __global__ void __launch_bounds__(kP128Threads, 1)
                         tma_load_3d_hint(sK + Cfg::kKVBytes + sub * kTK * 128, mV, v_full(st),
                                     sub * 64, krow, c.b * a.Hk + c.g, pol_kv);
                 }
-                c.next(a, pack, nq, np, n_items);
+                c.next(a, pack, plan, nq, np, n_items);
             }
         } else if (warp == 1 && lane == 0) {
             constexpr uint32_t fmt = dt_traits<T>::mma_fmt;
@@ -307,7 +313,7 @@ __global__ void __launch_bounds__(kP128Threads, 1)
                 return true;
             };
             PairCursor<PACKED> c;
-            c.start(a, pack, nq, np, n_items);
+            c.start(a, pack, plan, nq, np, n_items);
             int gkv = 0;
             int itq[2] = {0, 0};
             bool ok = true;
@@ -367,14 +373,14 @@ __global__ void __launch_bounds__(kP128Threads, 1)
                     if (more) tc_commit(k_empty((gj + 1) % kStages));
                 }
                 gkv += nkv;
-                c.next(a, pack, nq, np, n_items);
+                c.next(a, pack, plan, nq, np, n_items);
             }
         } else if (PACKED && warp == 3) {
             if constexpr (PACKED) {
                 // passes each V tile on, the rows behind the prompt's end
                 // cleared (see attn_pair.cu)
                 PairCursor<PACKED> c;
-                c.start(a, pack, nq, np, n_items);
+                c.start(a, pack, plan, nq, np, n_items);
                 int gkv = 0;
                 bool ok = true;
                 while (ok && c.valid) {
@@ -393,7 +399,7 @@ __global__ void __launch_bounds__(kP128Threads, 1)
                         __syncwarp();
                         if (lane == 0) mbar_arrive(v_ready(st));
                     }
-                    c.next(a, pack, nq, np, n_items);
+                    c.next(a, pack, plan, nq, np, n_items);
                 }
             }
         }
@@ -408,7 +414,7 @@ __global__ void __launch_bounds__(kP128Threads, 1)
         const uint32_t tO = tmem_base + Cfg::kColO + D * x;
         const float scale_l2 = a.scale * kLog2e;
         PairCursor<PACKED> c;
-        c.start(a, pack, nq, np, n_items);
+        c.start(a, pack, plan, nq, np, n_items);
         int g = 0;
         bool ok = true;
         bool pend = false;
@@ -438,7 +444,7 @@ __global__ void __launch_bounds__(kP128Threads, 1)
         while (ok && c.valid) {
             const int nx = x ? c.nB : c.nA;
             if (nx == 0) {
-                c.next(a, pack, nq, np, n_items);
+                c.next(a, pack, plan, nq, np, n_items);
                 continue;
             }
             const int qt = 2 * c.i + x;
@@ -603,7 +609,7 @@ __global__ void __launch_bounds__(kP128Threads, 1)
                 pend_row = qpos < c.len ? (static_cast<int64_t>(c.start_row) + qpos) * a.H + c.h : -1;
             else
                 pend_row = qpos < a.S ? (static_cast<int64_t>(c.b) * a.S + qpos) * a.H + c.h : -1;
-            c.next(a, pack, nq, np, n_items);
+            c.next(a, pack, plan, nq, np, n_items);
         }
         // the last item's O
         if (ok && pend) {

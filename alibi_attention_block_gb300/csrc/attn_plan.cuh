@@ -1,0 +1,85 @@
+// The work list of packed prompts (see attn.cu), as the attention kernels read
+// it: from the workspace, or built by every CTA for itself in shared memory.
+#pragma once
+
+#include "internal.h"
+
+namespace blk {
+
+// One unit of work: unit l (256 or R positions from l * unit on) of the prompt
+// at rows first .. first + len - 1.
+struct PlanUnit {
+    int first, len, l;
+};
+
+// A small list is built by each CTA: the table's entries are in L2, and a
+// kernel that only builds the list costs its launch and 2.6 us (chat turns, 16
+// prompts: @PLAN@). Every CTA has to come to the same order, so no atomics:
+// prompts are ranked by their number of units (ties by index), and unit l of
+// the prompt of rank r comes behind all units above l, at place r among those
+// of level l.
+struct PlanSmem {
+    int first[kPlanCtaPrompts], len[kPlanCtaPrompts], n[kPlanCtaPrompts];
+    int sorted_n[kPlanCtaPrompts];
+    uint16_t sorted_b[kPlanCtaPrompts];
+    uint32_t list[kPlanCtaUnits];  // prompt << 16 | l
+    int total;
+};
+struct PlanNone {};
+template <bool PACKED>
+struct PlanStorage { using type = PlanNone; };
+template <>
+struct PlanStorage<true> { using type = PlanSmem; };
+
+// All threads of the block; ends with a block barrier. The table's entries are
+// clamped to a nondecreasing pair within [0, tokens], and units past the
+// list's room dropped.
+__device__ __forceinline__ void build_plan(PlanSmem& p, const int32_t* cu, int prompts, int tokens,
+                                           int unit) {
+    const int nt = static_cast<int>(blockDim.x), t = static_cast<int>(threadIdx.x);
+    for (int b = t; b < prompts; b += nt) {
+        const int first = min(max(cu[b], 0), tokens);
+        const int len = min(max(cu[b + 1], first), tokens) - first;
+        p.first[b] = first;
+        p.len[b] = len;
+        p.n[b] = (len + unit - 1) / unit;
+    }
+    __syncthreads();
+    for (int b = t; b < prompts; b += nt) {
+        const int n = p.n[b];
+        int rank = 0;
+        for (int o = 0; o < prompts; ++o) {
+            const int v = p.n[o];
+            rank += v > n || (v == n && o < b);
+        }
+        p.sorted_n[rank] = n;
+        p.sorted_b[rank] = static_cast<uint16_t>(b);
+    }
+    __syncthreads();
+    const int levels = p.sorted_n[0];
+    if (t == 0 && levels == 0) p.total = 0;
+    for (int l = t; l < levels; l += nt) {
+        int at = 0, r = 0;  // units above level l; prompts that have level l
+        for (; r < prompts && p.sorted_n[r] > l; ++r) at += p.sorted_n[r] - 1 - l;
+        if (l == 0) p.total = min(at + r, kPlanCtaUnits);
+        for (int i = 0; i < r && at + i < kPlanCtaUnits; ++i)
+            p.list[at + i] = static_cast<uint32_t>(p.sorted_b[i]) << 16 | static_cast<uint32_t>(l);
+    }
+    __syncthreads();
+}
+
+template <typename Plan>
+__device__ __forceinline__ int plan_units(const AttnPack<true>& pack, const Plan& p) {
+    return pack.plan ? pack.plan[0].x : p.total;
+}
+template <typename Plan>
+__device__ __forceinline__ PlanUnit plan_unit(const AttnPack<true>& pack, const Plan& p, int i) {
+    if (pack.plan) {
+        const int4 u = pack.plan[1 + i];
+        return PlanUnit{u.x, u.y, u.z};
+    }
+    const uint32_t e = p.list[i];
+    return PlanUnit{p.first[e >> 16], p.len[e >> 16], static_cast<int>(e & 0xffffu)};
+}
+
+}  // namespace blk

@@ -136,7 +136,7 @@ cudaError_t launch_attention(DType dt, const AttnArgs& a, cudaStream_t s);
 // ---- K3p: the same kernels over packed prompts (attn.cu: plan and dispatch)
 // What a packed launch needs besides AttnArgs (B = 1, S = packed rows): maps
 // of the shared prefix's keys and values [Hk, prefix, d], and the plan in the
-// workspace: plan[0].x units, then for each {first row, length, unit} of a
+// workspace (longer lists): plan[0].x units, then for each {first row, length, unit} of a
 // prompt, heaviest first. A unit is a query-tile pair (256 positions) or the
 // GQA kernel's block of R positions. Empty for dense batches.
 template <bool PACKED>
@@ -144,18 +144,23 @@ struct AttnPack {};
 template <>
 struct AttnPack<true> {
     CUtensorMap tmPK, tmPV;
-    const int4* plan;
-    int prefix;
+    const int4* plan;           // or nullptr: each CTA builds its own (attn_plan.cuh)
+    const int32_t* cu_seqlens;
+    int prompts, prefix;
 };
+// up to these sizes the list is built by each CTA, without a workspace
+constexpr int kPlanCtaPrompts = 256, kPlanCtaUnits = 2048;
 struct PackedArgs {
     const void* k_prefix;  // [Hk, prefix, d]
     const void* v_prefix;
     const int32_t* cu_seqlens;  // device [prompts + 1]
     int prompts, prefix;
-    int4* plan;                 // workspace: 1 + packed_max_units(...) entries
+    int4* plan;                 // workspace: packed_plan_entries(...) entries
 };
-// upper bound of a packed call's units (the plan's room)
+// upper bound of a packed call's units
 int64_t packed_max_units(int64_t tokens, int64_t prompts, int H, int Hk, int d);
+// entries of the work list in the workspace (0: no list there)
+int64_t packed_plan_entries(int64_t tokens, int64_t prompts, int H, int Hk, int d);
 cudaError_t launch_attention_packed(DType dt, const AttnArgs& a, const PackedArgs& p,
                                     cudaStream_t s);
 cudaError_t launch_attention_pair64_packed(DType dt, const AttnArgs& a, const AttnPack<true>& pack,

@@ -195,10 +195,12 @@ typedef struct {
  * outside it hold (NaN included). As in blk_attn_prefill, a key that a row
  * does not see has weight 0, so a non-finite value (v) of a later token of
  * the same prompt and 128-key tile makes a NaN.
- * GQA: kv head = h / (H / Hk). head_dim in {64, 128, 160}. Two launches (the
- * work list, the attention); the workspace holds the work list, at least
- * blk_attn_prefill_packed_workspace_size bytes, 16-byte aligned; calls whose
- * kernels overlap on the GPU need a workspace each. */
+ * GQA: kv head = h / (H / Hk). head_dim in {64, 128, 160}. One launch; above
+ * 256 prompts or a few hundred thousand tokens a second one ahead of it makes
+ * the work list in the workspace, which then has at least
+ * blk_attn_prefill_packed_workspace_size bytes, 16-byte aligned (0 bytes: none
+ * is needed, NULL will do); calls whose kernels overlap on the GPU need a
+ * workspace each. */
 blk_status blk_attn_prefill_packed_workspace_size(const blk_packed_desc* d, size_t* bytes);
 blk_status blk_attn_prefill_packed(const blk_packed_desc* d, const void* q, const void* k,
                                    const void* v, const void* k_prefix, const void* v_prefix,

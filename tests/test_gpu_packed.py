@@ -155,6 +155,20 @@ def test_prompts_do_not_touch_each_other(H, Hk, d, P):
         assert torch.equal(o[cu[i]:cu[i + 1]], good[cu[i]:cu[i + 1]])
 
 
+@pytest.mark.parametrize("H,Hk,d", [(2, 2, 64), (2, 2, 128), (4, 1, 128), (4, 1, 160)])
+def test_list_in_the_workspace(H, Hk, d):
+    """The same prompts, and empty ones behind them that make the table too
+    long for the CTAs' own lists: the same bits."""
+    lens = [100, 257, 300, 1, 513]
+    cu = ends(lens)
+    q, k, v, kp, vp = inputs(H, Hk, cu[-1], d, 150, "bf16", 17)
+    args = to_dev(q), to_dev(k), to_dev(v)
+    pre = dict(k_prefix=to_dev(kp), v_prefix=to_dev(vp))
+    a = blk.attn_prefill_packed(*args, table(cu), **pre)
+    b = blk.attn_prefill_packed(*args, table(cu + [cu[-1]] * 300), **pre)
+    assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("d", [64, 128, 160])
 def test_growing_scores_rescale(d):
     """Keys whose scores rise along the prompt move the running maximum at
@@ -191,10 +205,12 @@ def test_table_is_clamped():
     assert torch.equal(o, blk.attn_prefill_packed(*args, table([0, 300])))
 
 
-def test_many_prompts():
-    """More prompts than the list's builder has warps, each a few tokens."""
+@pytest.mark.parametrize("prompts", [255, 700])
+def test_many_prompts(prompts):
+    """Many prompts of a few tokens, the list built by each CTA (up to 256) or
+    in the workspace."""
     rng = np.random.default_rng(0)
-    lens = [int(x) for x in rng.integers(0, 5, 700)] + [300]
+    lens = [int(x) for x in rng.integers(0, 5, prompts)] + [300]
     cu = ends(lens)
     q, k, v, _, _ = inputs(2, 1, cu[-1], 64, 0, "fp16", 6)
     o = blk.attn_prefill_packed(to_dev(q), to_dev(k), to_dev(v), table(cu), alibi=True)
@@ -222,6 +238,7 @@ def test_graph_replay_and_other_stream():
     cu = table([0, 250, 251, 600])
     ws = torch.empty(blk.attn_prefill_packed_workspace_size(blk.packed_desc(600, 3, 8, 2, 128, 140)),
                      dtype=torch.uint8, device="cuda")
+    assert ws.numel() == 0
     out = torch.zeros((600, 8, 128), dtype=torch.bfloat16, device="cuda")
 
     def call():
@@ -267,6 +284,7 @@ def test_binding_refuses():
     with pytest.raises(ValueError):
         blk.attn_prefill_packed(q, k, v, cu, out=q)
     with pytest.raises(blk.BlkError):
-        blk.attn_prefill_packed(q, k, v, cu, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+        blk.attn_prefill_packed(q, k, v, torch.zeros(400, dtype=torch.int32, device="cuda"),
+                                workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
     with pytest.raises(blk.BlkError):
         blk.attn_prefill_packed(q, k, v, cu, slopes=torch.ones(4, device="cuda"))

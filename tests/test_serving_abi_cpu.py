@@ -29,12 +29,17 @@ def call(lib, d, q=FAKE, k=FAKE, v=FAKE, kp=None, vp=None, cu=FAKE, slopes=None,
                                          (32, 8, 128, 32), (32, 8, 160, 32), (6, 2, 128, 40),
                                          (32, 1, 160, 8), (2, 2, 160, 128)])
 def test_workspace_size(lib, H, Hk, d, unit):
-    """One 16-byte entry for each unit that the prompts can have at most, and
-    one for their count, in whole 256 bytes."""
+    """Nothing up to 256 prompts and 2048 units; above, one 16-byte entry for
+    each unit that the prompts can have at most, and one for their count, in
+    whole 256 bytes."""
     need = C.c_size_t(0)
-    assert lib.blk_attn_prefill_packed_workspace_size(C.byref(desc(1000, 7, H, Hk, d)),
-                                                      C.byref(need)) == _abi.BLK_OK
-    assert need.value == -(-16 * (1 + 1000 // unit + 7) // 256) * 256
+    for tokens, prompts in ((1000, 7), (1000, 256), (1000, 257), ((2048 - 3) * unit, 3),
+                            ((2048 - 3) * unit, 4), (1 << 20, 5000)):
+        units = tokens // unit + prompts
+        assert lib.blk_attn_prefill_packed_workspace_size(
+            C.byref(desc(tokens, prompts, H, Hk, d)), C.byref(need)) == _abi.BLK_OK
+        small = prompts <= 256 and units <= 2048
+        assert need.value == (0 if small else -(-16 * (1 + units) // 256) * 256)
 
 
 @pytest.mark.parametrize("bad,status", [
@@ -69,9 +74,10 @@ def test_argument_refusals(lib):
     assert call(lib, d, slopes=FAKE) == _abi.BLK_EINVAL      # slopes without ALiBi
     assert call(lib, desc(alibi=1), slopes=FAKE + 2) == _abi.BLK_EINVAL
     assert call(lib, desc(H=24, Hk=8, alibi=1)) == _abi.BLK_EUNSUPPORTED
-    assert call(lib, d, ws=None) == _abi.BLK_EWORKSPACE
-    assert call(lib, d, ws=FAKE + 4) == _abi.BLK_EWORKSPACE
-    assert call(lib, d, n=64) == _abi.BLK_EWORKSPACE
+    many = desc(prompts=300)  # a work list in the workspace
+    assert call(lib, many, ws=None) == _abi.BLK_EWORKSPACE
+    assert call(lib, many, ws=FAKE + 4) == _abi.BLK_EWORKSPACE
+    assert call(lib, many, n=64) == _abi.BLK_EWORKSPACE
 
 
 # ---------------------------------------------- blk_attn_decode_shared --
