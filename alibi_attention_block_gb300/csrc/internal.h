@@ -205,31 +205,44 @@ struct SharedArgs {
     unsigned* err;
     int num_sms;
 };
-constexpr int kSharedMaxGrid = 256;   // CTAs of the prefix pass at most
-constexpr int kOwnMaxGrid = 512;      // CTAs of the own caches' pass at most
+constexpr int kSharedMaxGrid = 512;  // CTAs of the kernel at most
 struct SharedLayout {
     // byte offsets in the workspace, and its size: the prefix's partial
     // outputs and statistics, the own caches', their running tile counts
     int64_t po, pm, own_po, own_pm, cum, total;
 };
 SharedLayout shared_layout(int64_t B, int64_t H, int64_t Hk, int64_t d, int64_t P);
-// the own caches' pass (attn_own.cu): partial results of its segments, record
-// c + b * Hk + g for CTA c's stay in unit (b, g)
-struct OwnArgs {
+struct SharedMaps {
+    CUtensorMap pq, pk, pv;            // prefix: queries (4D), keys, values
+    CUtensorMap oq, ok, ov, ok16, ov16;  // own caches; *16: boxes of 16 keys
+};
+struct SharedKernelArgs {
     int pdl;
-    int after_prefix;  // launched behind the prefix pass, whose results it does not need
-    float* po;      // [records][G][d]
-    float2* pm;     // [records][G] (max, sum), log2 domain
+    // prefix: partial outputs [segments][D / 8][128 rows][8] (a thread holds a
+    // row and writes whole 32-byte sectors that join its neighbours') and
+    // statistics [segments][128] (max, sum; log2 domain); segment record
+    // c + u for CTA c's stay in unit u = kv head * nrt + row tile
+    float* po;
+    float2* pm;
+    // own caches: [segments][G][D] and [segments][G]; record c + b * Hk + g for
+    // range c's stay in unit (b, g)
+    float* own_po;
+    float2* own_pm;
     int32_t* cum;   // [B + 1] 128-key tiles ahead of each sequence (per kv head)
     const int32_t* lens;
     const float* slopes;
     unsigned* err;
-    int B, H, Hk, S_max, grid;
+    int B, H, Hk, G, P, S_max;
+    int nkt;          // key tiles of the prefix
+    int nrt;          // row tiles per kv head
+    int W;            // prefix tiles in all: Hk * nrt * nkt
+    int prefix_ctas;  // CTAs with a prefix range: min(grid, W)
+    int grid;
     float scale;
     int alibi;
 };
-cudaError_t launch_attention_own(DType dt, const OwnArgs& a, int d, const void* q, const void* k,
-                                 const void* v, cudaStream_t s);
+cudaError_t launch_shared_f16(int d, const SharedMaps& tm, const SharedKernelArgs& a, cudaStream_t s);
+cudaError_t launch_shared_bf16(int d, const SharedMaps& tm, const SharedKernelArgs& a, cudaStream_t s);
 // (kv head, row tile, key tile) triples of the prefix pass
 int64_t shared_tiles(int64_t B, int64_t H, int64_t Hk, int64_t P);
 cudaError_t launch_attention_decode_shared(DType dt, const SharedArgs& s, cudaStream_t st);
