@@ -1,7 +1,7 @@
 // K6s host side and merge: one decode step of attention for a batch that
 // shares a prefix. The kernel (attn_shared.cuh) leaves partial results of the
-// prefix and of the sequences' own caches; the merge has one warp per
-// (sequence, query head).
+// prefix and of the sequences' own caches; the merge has a lane per
+// query row.
 #include "internal.h"
 
 namespace blk {
@@ -12,8 +12,16 @@ constexpr int kTQ = 128, kTK = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // o = sum_i w_i O_i / sum_i w_i l_i over the prefix's segments and the own
-// cache's, w_i = 2^(m_i - max m): one warp per (b, query head). With
+// cache's, w_i = 2^(m_i - max m), in one pass with a running maximum. With
 // ALiBi the prefix's maxima still lack the row's -slope * (lens[b] - 1).
+// A lane holds one query row (of 32 rows of a kv head that lie together in the
+// prefix's records), a warp eight output columns: a record's 32 bytes per lane
+// are 1 KB in one piece, and no value crosses lanes. (One warp per row, 16 bytes
+// per lane: 806 instructions per row, 10.9 us for 8192 rows, latency-bound in
+// 2.25 waves; this: 6.6.) Where a row has eight segments or more (SPLIT) the
+// four warps of a block take them in turn and join their sums in shared memory:
+// a warp alone waits for four loads at a time (16 rows of 16 heads x 128 with 20
+// segments: 8.4 us, split @COMBS@).
 struct CombineArgs {
     int pdl;
     const float* po;
@@ -26,12 +34,12 @@ struct CombineArgs {
     void* o;
     int B, H, G, max_seq, alibi, grid;
     int nkt, nrt, W, prefix_ctas;  // of the prefix; W 0: none
+    int row_blocks;                // blocks of 32 rows per kv head
 };
 
 // The CTA whose range [c * W / n, (c + 1) * W / n) holds tile t, n CTAs in all
 // (at most 512, W >= n): c * W < (t + 1) * n <= (c + 1) * W, from an estimate
-// in floating point that is off by one at most. (Four 64-bit divisions per row
-// were most of the merge's instructions: 11.3 us for 8192 rows, @COMB@ without.)
+// in floating point that is off by one at most.
 __device__ __forceinline__ int cta_of(int64_t t, int64_t W, int n) {
     const int64_t x = (t + 1) * n;
     int c = static_cast<int>(static_cast<float>(t) * (static_cast<float>(n) / static_cast<float>(W)));
@@ -40,133 +48,111 @@ __device__ __forceinline__ int cta_of(int64_t t, int64_t W, int n) {
     return c;
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(128, 6) shared_combine_kernel(const CombineArgs a) {
-    // a record's D floats are read 16 bytes per lane: head_dim 64 takes half a
-    // warp, so two records at a time
-    constexpr int kLanes = D / 4, kAtOnce = 32 / kLanes;
+struct Merge {
+    float m = -INFINITY, l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    __device__ __forceinline__ void add(float pm, float pl, const float4 x, const float4 y) {
+        const float mn = fmaxf(m, pm);
+        const float keep = m == -INFINITY ? 0.f : exp2f(m - mn);
+        const float w = pm == -INFINITY ? 0.f : exp2f(pm - mn);
+        m = mn;
+        l = fmaf(l, keep, w * pl);
+        const float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = fmaf(o[e], keep, w * f[e]);
+    }
+};
+
+template <typename T, int D, bool SPLIT>
+__global__ void __launch_bounds__(128) shared_combine_kernel(const CombineArgs a) {
+    constexpr int kCols = SPLIT ? D / 8 : D / 32;  // blocks over the columns
+    constexpr int kStep = SPLIT ? 4 : 1;           // a warp's step over segments
+    __shared__ float part[SPLIT ? 4 : 1][10][32];
     if (a.pdl) {
         pdl_wait();
         pdl_launch_dependents();
     }
     const int lane = threadIdx.x & 31;
-    const unsigned w = blockIdx.x * 4 + threadIdx.x / 32;  // B * H < 2^31
-    if (w >= static_cast<unsigned>(a.B) * static_cast<unsigned>(a.H)) return;
-    const int b = static_cast<int>(w / static_cast<unsigned>(a.H)), h = static_cast<int>(w) - b * a.H;
-    const int Hk = a.H / a.G, g = h / a.G;
-    const int c4 = lane % kLanes, half = lane / kLanes;
-    // The prefix's segments of this row: CTAs c0 .. c1, record c + unit. Where
-    // they are is known at once, so the first of them are on their way while
-    // the lengths, which say where the own cache's are, still come.
-    int64_t seg0 = 0;  // the first one's first row
-    int nseg = 0, row = 0;
-    if (a.W) {
-        const int per = kTQ / a.G;  // sequences per unit
-        const int u = g * a.nrt + b / per;
-        row = b % per * a.G + h % a.G;  // of the unit
-        const int64_t p0 = static_cast<int64_t>(u) * a.nkt;
-        const int c0 = cta_of(p0, a.W, a.prefix_ctas), c1 = cta_of(p0 + a.nkt - 1, a.W, a.prefix_ctas);
-        seg0 = static_cast<int64_t>(c0 + u) * kTQ;
-        nseg = c1 - c0 + 1;
-    }
-    auto prefix_part = [&](int k) -> const float4& {
-        return *reinterpret_cast<const float4*>(
-            a.po + (seg0 + static_cast<int64_t>(k) * kTQ) * D + (c4 / 2 * kTQ + row) * 8 + c4 % 2 * 4);
-    };
-    auto prefix_stat = [&](int k) { return a.pm[seg0 + static_cast<int64_t>(k) * kTQ + row]; };
-    constexpr int kLoads = 8 / kAtOnce;  // of 8 records, in flight together
-    float4 f[kLoads];
-#pragma unroll
-    for (int x = 0; x < kLoads; ++x)
-        if (x * kAtOnce + half < nseg) f[x] = prefix_part(x * kAtOnce + half);
-    float2 stat = make_float2(-INFINITY, 0.f);  // lane i: record i's (max, sum)
-    if (lane < nseg) stat = prefix_stat(lane);
-    const int tiles = a.cum[a.B], before = a.cum[b];
+    const int warp = threadIdx.x / 32;
+    const int blk = blockIdx.x / kCols;  // (kv head, 32 rows)
+    const int col8 = SPLIT ? blockIdx.x % kCols : blockIdx.x % kCols * 4 + warp;
+    const int first = SPLIT ? warp : 0;  // this warp's first segment
+    const int g = blk / a.row_blocks;
+    const int R = (blk - g * a.row_blocks) * 32 + lane;  // row of the kv head
+    const bool mine = R / a.G < a.B;
+    const int b = mine ? R / a.G : a.B - 1, h = g * a.G + R % a.G;
+    const int Hk = a.H / a.G;
     const int n = min(max(a.lens[b], 0), a.max_seq);
-    float o[4] = {0.f, 0.f, 0.f, 0.f};
-    float mx = -INFINITY, lsum = 0.f;
+    const int tiles = a.cum[a.B], before = a.cum[b];
+    Merge r;
+    float shift = 0.f;
+    if (a.alibi) {
+        const float sl = a.slopes ? a.slopes[h]
+                                  : exp2f(-8.0f * static_cast<float>(h + 1) / static_cast<float>(a.H));
+        shift = sl * kLog2e * static_cast<float>(n - 1);
+    }
+    if (a.W) {
+        // the prefix's segments of this row tile: CTAs c0 .. c1, record c + unit
+        const int u = g * a.nrt + R / kTQ, row = R % kTQ;
+        const int64_t t0 = static_cast<int64_t>(u) * a.nkt;
+        const int c0 = cta_of(t0, a.W, a.prefix_ctas), c1 = cta_of(t0 + a.nkt - 1, a.W, a.prefix_ctas);
+        const int64_t rec = static_cast<int64_t>(c0 + u) * kTQ;
+        const float* p = a.po + rec * D + (col8 * kTQ + row) * 8;
+        const float2* s = a.pm + rec + row;
+#pragma unroll 4
+        for (int k = first; k <= c1 - c0; k += kStep) {
+            const float4* q = reinterpret_cast<const float4*>(p + static_cast<int64_t>(k) * kTQ * D);
+            const float4 x = q[0], y = q[1];
+            const float2 ml = s[static_cast<int64_t>(k) * kTQ];
+            r.add(ml.x - shift, ml.y, x, y);
+        }
+    }
     if (n > 0) {
         // the own cache's segments, of unit (b, kv head)
-        const int64_t own_w = static_cast<int64_t>(tiles) * Hk;
+        const int64_t W = static_cast<int64_t>(tiles) * Hk;
         const int nt = (n + kTK - 1) / kTK;
         const int64_t t0 = static_cast<int64_t>(before) * Hk + static_cast<int64_t>(g) * nt;
-        const int ctas = static_cast<int>(min(static_cast<int64_t>(a.grid), own_w));
-        const int c0 = cta_of(t0, own_w, ctas), c1 = cta_of(t0 + nt - 1, own_w, ctas);
-        const int64_t own0 = (static_cast<int64_t>(c0) + static_cast<int64_t>(b) * Hk + g) * a.G + h % a.G;
-        const int total = nseg + c1 - c0 + 1;
-        float shift = 0.f;
-        if (a.alibi) {
-            const float sl = a.slopes ? a.slopes[h]
-                                      : exp2f(-8.0f * static_cast<float>(h + 1) /
-                                              static_cast<float>(a.H));
-            shift = sl * kLog2e * static_cast<float>(n - 1);
-        }
-        for (int base = 0; base < total; base += 32) {
-            const int i = base + lane;
-            if (i >= nseg || base > 0) {
-                stat = make_float2(-INFINITY, 0.f);
-                if (i < nseg) stat = prefix_stat(i);
-                else if (i < total) stat = a.own_pm[own0 + static_cast<int64_t>(i - nseg) * a.G];
-            }
-            const float m = i < nseg ? stat.x - shift : stat.x;
-            float mb = m;
-#pragma unroll
-            for (int s = 16; s > 0; s >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, s));
-            const float mn = fmaxf(mx, mb);
-            const float keep = mx == -INFINITY ? 0.f : exp2f(mx - mn);
-            const float wgt = m == -INFINITY ? 0.f : exp2f(m - mn);
-            float ls = wgt * stat.y;
-#pragma unroll
-            for (int s = 16; s > 0; s >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, s);
-            lsum = fmaf(lsum, keep, ls);
-            mx = mn;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] *= keep;
-            // (each half of a warp, or the whole, in record order)
-            const int cnt = min(32, total - base);
-#pragma unroll 1
-            for (int j0 = 0; j0 < cnt; j0 += 8) {
-#pragma unroll
-                for (int x = 0; x < kLoads; ++x) {
-                    const int j = j0 + x * kAtOnce + half, k = base + j;
-                    if (k < nseg) {
-                        if (base + j0 > 0) f[x] = prefix_part(k);
-                    } else if (j < cnt) {
-                        f[x] = reinterpret_cast<const float4*>(
-                            a.own_po + (own0 + static_cast<int64_t>(k - nseg) * a.G) * D)[c4];
-                    }
-                }
-#pragma unroll
-                for (int x = 0; x < kLoads; ++x) {
-                    const int j = j0 + x * kAtOnce + half;
-                    const float wj = __shfl_sync(0xffffffffu, wgt, j & 31);
-                    if (j < cnt) {
-                        o[0] = fmaf(wj, f[x].x, o[0]);
-                        o[1] = fmaf(wj, f[x].y, o[1]);
-                        o[2] = fmaf(wj, f[x].z, o[2]);
-                        o[3] = fmaf(wj, f[x].w, o[3]);
-                    }
-                }
-            }
+        const int ctas = static_cast<int>(min(static_cast<int64_t>(a.grid), W));
+        const int c0 = cta_of(t0, W, ctas), c1 = cta_of(t0 + nt - 1, W, ctas);
+        const int64_t rec = (static_cast<int64_t>(c0) + static_cast<int64_t>(b) * Hk + g) * a.G + R % a.G;
+        const float* p = a.own_po + rec * D + col8 * 8;
+        const float2* s = a.own_pm + rec;
+#pragma unroll 2
+        for (int k = first; k <= c1 - c0; k += kStep) {
+            const float4* q = reinterpret_cast<const float4*>(p + static_cast<int64_t>(k) * a.G * D);
+            const float4 x = q[0], y = q[1];
+            const float2 ml = s[static_cast<int64_t>(k) * a.G];
+            r.add(ml.x, ml.y, x, y);
         }
     }
-    if constexpr (kAtOnce == 2) {
+    if constexpr (SPLIT) {
+        part[warp][0][lane] = r.m;
+        part[warp][1][lane] = r.l;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] += __shfl_xor_sync(0xffffffffu, o[e], 16);
+        for (int e = 0; e < 8; ++e) part[warp][2 + e][lane] = r.o[e];
+        __syncthreads();
+        if (warp > 0) return;
+        for (int i = 1; i < 4; ++i)
+            r.add(part[i][0][lane], part[i][1][lane],
+                  make_float4(part[i][2][lane], part[i][3][lane], part[i][4][lane], part[i][5][lane]),
+                  make_float4(part[i][6][lane], part[i][7][lane], part[i][8][lane], part[i][9][lane]));
     }
-    const float inv = lsum > 0.f ? 1.0f / lsum : 0.f;
-    if (lane < kLanes) {
-        const uint2 v = make_uint2(dt_traits<T>::pack2(o[0] * inv, o[1] * inv),
-                                   dt_traits<T>::pack2(o[2] * inv, o[3] * inv));
-        *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + static_cast<int64_t>(w) * D + lane * 4) = v;
-    }
+    if (!mine) return;
+    // a sequence of length 0 takes no part
+    const float inv = n > 0 && r.l > 0.f ? 1.0f / r.l : 0.f;
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = n > 0 ? r.o[e] * inv : 0.f;
+    store8(static_cast<T*>(a.o) + (static_cast<int64_t>(b) * a.H + h) * D + col8 * 8, f);
 }
 
 template <typename T, int D>
 cudaError_t launch_combine(const CombineArgs& c, cudaStream_t st) {
-    const int64_t warps = static_cast<int64_t>(c.B) * c.H;
-    return launch_pdl(c.pdl != 0, shared_combine_kernel<T, D>,
-                      dim3(static_cast<unsigned>((warps + 3) / 4)), dim3(128), 0, st, c);
+    const int Hk = c.H / c.G;
+    const bool split = c.W && c.prefix_ctas >= 7 * Hk * c.nrt;  // segments of a unit, less one
+    const int64_t blocks = static_cast<int64_t>(Hk) * c.row_blocks * (split ? D / 8 : D / 32);
+    return launch_pdl(c.pdl != 0,
+                      split ? shared_combine_kernel<T, D, true> : shared_combine_kernel<T, D, false>,
+                      dim3(static_cast<unsigned>(blocks)), dim3(128), 0, st, c);
 }
 
 }  // namespace
@@ -255,6 +241,7 @@ cudaError_t launch_attention_decode_shared(DType dt, const SharedArgs& s, cudaSt
     c.nrt = a.nrt;
     c.W = a.W;
     c.prefix_ctas = a.prefix_ctas;
+    c.row_blocks = static_cast<int>((static_cast<int64_t>(a.B) * a.G + 31) / 32);
     if (dt == DType::F16)
         return d.d == 64 ? launch_combine<__half, 64>(c, st) : launch_combine<__half, 128>(c, st);
     return d.d == 64 ? launch_combine<__nv_bfloat16, 64>(c, st)

@@ -923,10 +923,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         tmem_alloc(smem_u32(tmem_slot), 256);
         tmem_relinquish();
     }
-    if (a.pdl) {
-        pdl_wait();
-        pdl_launch_dependents();
-    }
+    if (a.pdl) pdl_wait();
     // this CTA's range of the own caches' tiles: thread i sums the tiles of a
     // run of sequences
     const int per = (a.B + kThreads - 1) / kThreads;
@@ -981,17 +978,21 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (threadIdx.x == 0) a.cum[a.B] = total;
     }
     __syncthreads();
-    OwnSegments own;
-    own.start(a, sh_lo, sh_hi, sh_b0, sh_base);
-
     // each warp goes on to the own caches as it is done with the prefix
     const bool ok = prefix_phase<T, D>(a, tm.pq, tm.pk, tm.pv, smem_u32(smem), bar_p, tmem, warp, lane);
-    if (ok)
+    if (ok) {
+        OwnSegments own;
+        own.start(a, sh_lo, sh_hi, sh_b0, sh_base);
         own_phase<T, D, G>(a, tm.oq, tm.ok, tm.ov, tm.ok16, tm.ov16, own, smem, bar_o, tmem, warp, lane);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, 256);
+    // The merge may come in now. Earlier its blocks only took the SM's room as
+    // CTAs ended (at the start of this kernel: 36.9 us against 33.6 for 32 x 32 x
+    // 64 heads, 8192 shared keys).
+    if (a.pdl) pdl_launch_dependents();
 }
 
 template <typename T, int D, int G>
