@@ -143,22 +143,31 @@ def _pointers(dtype, dev, *ts):
     stays None): _same and _p for a call's tensors in one pass (these calls
     can be shorter than a dozen separate checks)."""
     out = []
-    for t in ts:
-        if t is None:
-            out.append(None)
-            continue
-        if not isinstance(t, torch.Tensor):
-            raise TypeError("expected a torch.Tensor")
-        if t.dtype is not dtype:
-            raise TypeError(f"expected a {dtype} tensor, got {t.dtype}")
-        if t.get_device() != dev:
-            if not t.is_cuda:
-                raise ValueError("tensors passed to the block library must be CUDA tensors")
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
-        if not t.is_contiguous():
-            raise ValueError("tensors passed to the block library must be contiguous")
-        out.append(t.data_ptr())
+    try:
+        for t in ts:
+            if t is None:
+                out.append(None)
+            elif t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+                out.append(t.data_ptr())
+            else:
+                _refuse(t, dtype, dev)
+    except AttributeError:
+        raise TypeError("expected a torch.Tensor") from None
     return out
+
+
+def _workspace(t, dev):
+    return _pointers(t.dtype, dev, t)[0], t.nbytes
+
+
+def _refuse(t, dtype, dev):
+    if t.dtype is not dtype:
+        raise TypeError(f"expected a {dtype} tensor, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError("tensors passed to the block library must be CUDA tensors")
+    if t.get_device() != dev:
+        raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+    raise ValueError("tensors passed to the block library must be contiguous")
 
 
 def _shape(t, want, what):
@@ -218,16 +227,17 @@ def attn_prefill_packed(q, k, v, cu_seqlens, k_prefix=None, v_prefix=None, alibi
     _shape(slopes, (H,), "slopes")
     _shape(out, (T, H, d), "out")
     desc, need = _packed_plan(T, cu_seqlens.numel() - 1, H, Hk, d, P, alibi, scale)
+    dev = torch.cuda.current_device()
+    qp, kp, vp, kpp, vpp, op = _pointers(q.dtype, dev, q, k, v, k_prefix, v_prefix, out)
+    (cup,) = _pointers(torch.int32, dev, cu_seqlens)
+    sp = None if slopes is None else _pointers(torch.float32, dev, slopes)[0]
     if workspace is None and need:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    o = torch.empty((T, H, d), dtype=q.dtype, device=q.device) if out is None else out
-    dev = torch.cuda.current_device()
-    qp, kp, vp, kpp, vpp, op = _pointers(q.dtype, dev, q, k, v, k_prefix, v_prefix, o)
-    (cup,) = _pointers(torch.int32, dev, cu_seqlens)
-    (sp,) = _pointers(torch.float32, dev, slopes)
-    wp, wn = None, 0
-    if workspace is not None:
-        (wp,), wn = _pointers(workspace.dtype, dev, workspace), workspace.nbytes
+    wp, wn = (None, 0) if workspace is None else _workspace(workspace, dev)
+    o = out
+    if o is None:
+        o = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
+        op = o.data_ptr()
     _abi.check(_lib().blk_attn_prefill_packed(
         desc, qp, kp, vp, kpp, vpp, cup, sp, op, wp, wn, dt,
         torch._C._cuda_getCurrentRawStream(dev)), "blk_attn_prefill_packed")
@@ -308,16 +318,19 @@ def attn_decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, lens, alibi=Fals
     _shape(slopes, (H,), "slopes")
     _shape(out, (B, H, d), "out")
     desc, need = _decode_shared_plan(B, S_max, H, Hk, d, P, alibi, scale)
+    dev = torch.cuda.current_device()
+    qp, kpp, vpp, kp, vp, op = _pointers(q.dtype, dev, q, k_prefix, v_prefix, k_cache, v_cache, out)
+    (lp,) = _pointers(torch.int32, dev, lens)
+    sp = None if slopes is None else _pointers(torch.float32, dev, slopes)[0]
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    o = torch.empty_like(q) if out is None else out
-    dev = torch.cuda.current_device()
-    qp, kpp, vpp, kp, vp, op = _pointers(q.dtype, dev, q, k_prefix, v_prefix, k_cache, v_cache, o)
-    (lp,) = _pointers(torch.int32, dev, lens)
-    (sp,) = _pointers(torch.float32, dev, slopes)
-    (wp,) = _pointers(workspace.dtype, dev, workspace)
+    wp, wn = _workspace(workspace, dev)
+    o = out
+    if o is None:
+        o = torch.empty_like(q)
+        op = o.data_ptr()
     _abi.check(_lib().blk_attn_decode_shared(
-        desc, qp, kpp, vpp, kp, vp, lp, sp, op, wp, workspace.nbytes, dt,
+        desc, qp, kpp, vpp, kp, vp, lp, sp, op, wp, wn, dt,
         torch._C._cuda_getCurrentRawStream(dev)), "blk_attn_decode_shared")
     return o
 

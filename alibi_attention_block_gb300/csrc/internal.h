@@ -205,7 +205,7 @@ struct SharedArgs {
     unsigned* err;
     int num_sms;
 };
-constexpr int kSharedMaxGrid = 512;  // CTAs of the kernel at most
+constexpr int kSharedMaxGrid = 320;  // CTAs of the kernel at most
 struct SharedLayout {
     // byte offsets in the workspace, and its size: the prefix's partial
     // outputs and statistics, the own caches', their running tile counts
