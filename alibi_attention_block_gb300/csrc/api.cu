@@ -343,7 +343,7 @@ blk_status validate_packed_desc(const blk_packed_desc* d) {
     // work items: at most one per unit of work and query head
     const int64_t units = packed_max_units(d->tokens, d->prompts, static_cast<int>(d->n_heads),
                                            static_cast<int>(d->n_kv_heads),
-                                           static_cast<int>(d->head_dim));
+                                           static_cast<int>(d->head_dim), d->alibi != 0);
     BLK_REQUIRE(units <= kI32 / d->n_heads, "tokens, prompts and n_heads too large");
     return BLK_OK;
 }
@@ -352,7 +352,7 @@ size_t packed_ws_bytes(const blk_packed_desc* d) {
     return align256(sizeof(int4) * static_cast<size_t>(packed_plan_entries(
                                        d->tokens, d->prompts, static_cast<int>(d->n_heads),
                                        static_cast<int>(d->n_kv_heads),
-                                       static_cast<int>(d->head_dim))));
+                                       static_cast<int>(d->head_dim), d->alibi != 0)));
 }
 
 blk_status validate_block(const blk_block_desc* d, const blk_block_weights* w,

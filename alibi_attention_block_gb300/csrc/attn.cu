@@ -78,31 +78,37 @@ __global__ void __launch_bounds__(kPlanThreads)
     });
 }
 
-// positions per unit: a query-tile pair, or the GQA kernel's block
-int packed_unit(int H, int Hk, int d) {
-    const bool pair = d == 64 || (d == 128 && H == Hk);
-    return pair ? 256 : gqa_block_positions(H, Hk);
+// a query-tile pair per item, or one tile (attn_gqa.cu)
+bool packed_pairs(int H, int Hk, int d, bool alibi) {
+    return d == 64 || (d == 128 && (H == Hk || !alibi));
+}
+// positions per unit
+int packed_unit(int H, int Hk, int d, bool alibi) {
+    if (d == 64) return 256;
+    int G, Gt, R, nhc;
+    gqa_tile(H, Hk, &G, &Gt, &R, &nhc);
+    return packed_pairs(H, Hk, d, alibi) ? 2 * R : R;
 }
 
 }  // namespace
 
-int64_t packed_max_units(int64_t tokens, int64_t prompts, int H, int Hk, int d) {
-    return tokens / packed_unit(H, Hk, d) + prompts;
+int64_t packed_max_units(int64_t tokens, int64_t prompts, int H, int Hk, int d, bool alibi) {
+    return tokens / packed_unit(H, Hk, d, alibi) + prompts;
 }
 
-int64_t packed_plan_entries(int64_t tokens, int64_t prompts, int H, int Hk, int d) {
-    const int64_t units = packed_max_units(tokens, prompts, H, Hk, d);
+int64_t packed_plan_entries(int64_t tokens, int64_t prompts, int H, int Hk, int d, bool alibi) {
+    const int64_t units = packed_max_units(tokens, prompts, H, Hk, d, alibi);
     return prompts <= kPlanCtaPrompts && units <= kPlanCtaUnits ? 0 : 1 + units;
 }
 
 cudaError_t launch_attention_packed(DType dt, const AttnArgs& a, const PackedArgs& p,
                                     cudaStream_t s) {
-    const int unit = packed_unit(a.H, a.Hk, a.d);
-    const int64_t max_units = packed_max_units(a.S, p.prompts, a.H, a.Hk, a.d);
+    const int unit = packed_unit(a.H, a.Hk, a.d, a.alibi != 0);
+    const int64_t max_units = packed_max_units(a.S, p.prompts, a.H, a.Hk, a.d, a.alibi != 0);
     int shift = 0;
     while ((static_cast<int64_t>(a.S / unit) >> shift) >= kPlanBins) ++shift;
     AttnPack<true> pack;
-    const bool listed = packed_plan_entries(a.S, p.prompts, a.H, a.Hk, a.d) != 0;
+    const bool listed = packed_plan_entries(a.S, p.prompts, a.H, a.Hk, a.d, a.alibi != 0) != 0;
     pack.plan = listed ? p.plan : nullptr;
     pack.cu_seqlens = p.cu_seqlens;
     pack.prompts = p.prompts;
@@ -122,7 +128,7 @@ cudaError_t launch_attention_packed(DType dt, const AttnArgs& a, const PackedArg
         if (e != cudaSuccess) return e;
     }
     if (a.d == 64) return launch_attention_pair64_packed(dt, a, pack, max_units, s);
-    if (a.d == 128 && a.H == a.Hk)
+    if (packed_pairs(a.H, a.Hk, a.d, a.alibi != 0))
         return launch_attention_pair128_packed(dt, a, pack, max_units, s);
     return launch_attention_gqa_packed(dt, a, pack, max_units, s);
 }

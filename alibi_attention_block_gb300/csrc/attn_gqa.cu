@@ -637,7 +637,13 @@ GqaPack gqa_pack(int H, int Hk) {
 
 }  // namespace
 
-int gqa_block_positions(int H, int Hk) { return gqa_pack(H, Hk).R; }
+void gqa_tile(int H, int Hk, int* G, int* Gt, int* R, int* nhc) {
+    const GqaPack pk = gqa_pack(H, Hk);
+    *G = pk.G;
+    *Gt = pk.Gt;
+    *R = pk.R;
+    *nhc = pk.nhc;
+}
 
 cudaError_t launch_attention_gqa(DType dt, const AttnArgs& a, cudaStream_t s) {
     if (a.Hk <= 0 || a.H % a.Hk || (a.d != 128 && a.d != 160)) return cudaErrorInvalidValue;

@@ -137,7 +137,7 @@ cudaError_t launch_attention(DType dt, const AttnArgs& a, cudaStream_t s);
 // What a packed launch needs besides AttnArgs (B = 1, S = packed rows): maps
 // of the shared prefix's keys and values [Hk, prefix, d], and the plan in the
 // workspace (longer lists): plan[0].x units, then for each {first row, length, unit} of a
-// prompt, heaviest first. A unit is a query-tile pair (256 positions) or the
+// prompt, heaviest first. A unit is a query-tile pair (2 R positions) or the
 // GQA kernel's block of R positions. Empty for dense batches.
 template <bool PACKED>
 struct AttnPack {};
@@ -147,6 +147,7 @@ struct AttnPack<true> {
     const int4* plan;           // or nullptr: each CTA builds its own (attn_plan.cuh)
     const int32_t* cu_seqlens;
     int prompts, prefix;
+    int G, Gt, R, nhc;          // gqa_tile (attn_pair128.cu)
 };
 // up to these sizes the list is built by each CTA, without a workspace
 constexpr int kPlanCtaPrompts = 256, kPlanCtaUnits = 2048;
@@ -158,9 +159,9 @@ struct PackedArgs {
     int4* plan;                 // workspace: packed_plan_entries(...) entries
 };
 // upper bound of a packed call's units
-int64_t packed_max_units(int64_t tokens, int64_t prompts, int H, int Hk, int d);
+int64_t packed_max_units(int64_t tokens, int64_t prompts, int H, int Hk, int d, bool alibi);
 // entries of the work list in the workspace (0: no list there)
-int64_t packed_plan_entries(int64_t tokens, int64_t prompts, int H, int Hk, int d);
+int64_t packed_plan_entries(int64_t tokens, int64_t prompts, int H, int Hk, int d, bool alibi);
 cudaError_t launch_attention_packed(DType dt, const AttnArgs& a, const PackedArgs& p,
                                     cudaStream_t s);
 cudaError_t launch_attention_pair64_packed(DType dt, const AttnArgs& a, const AttnPack<true>& pack,
@@ -169,8 +170,9 @@ cudaError_t launch_attention_pair128_packed(DType dt, const AttnArgs& a, const A
                                             int64_t max_units, cudaStream_t s);
 cudaError_t launch_attention_gqa_packed(DType dt, const AttnArgs& a, const AttnPack<true>& pack,
                                         int64_t max_units, cudaStream_t s);
-// positions per unit of the GQA kernel
-int gqa_block_positions(int H, int Hk);
+// a group's query heads in a tile of 128 rows: G heads per kv head, Gt of them
+// per tile, R positions of each, nhc tiles per group
+void gqa_tile(int H, int Hk, int* G, int* Gt, int* R, int* nhc);
 // head_dim 64 / 128: the paired-query-tile kernels (attn_pair.cu, attn_pair128.cu)
 cudaError_t launch_attention_pair64(DType dt, const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_attention_pair128(DType dt, const AttnArgs& a, cudaStream_t s);

@@ -25,10 +25,10 @@ def call(lib, d, q=FAKE, k=FAKE, v=FAKE, kp=None, vp=None, cu=FAKE, slopes=None,
     return lib.blk_attn_prefill_packed(C.byref(d), q, k, v, kp, vp, cu, slopes, o, ws, n, dt, None)
 
 
-@pytest.mark.parametrize("H,Hk,d,unit", [(32, 32, 64, 256), (8, 2, 64, 256), (16, 16, 128, 256),
-                                         (32, 8, 128, 32), (32, 8, 160, 32), (6, 2, 128, 40),
-                                         (32, 1, 160, 8), (2, 2, 160, 128)])
-def test_workspace_size(lib, H, Hk, d, unit):
+@pytest.mark.parametrize("H,Hk,d,alibi,unit", [
+    (32, 32, 64, 0, 256), (8, 2, 64, 1, 256), (16, 16, 128, 1, 256), (32, 8, 128, 0, 64),
+    (32, 8, 128, 1, 32), (32, 8, 160, 0, 32), (6, 2, 128, 0, 80), (32, 1, 160, 1, 8), (2, 2, 160, 0, 128)])
+def test_workspace_size(lib, H, Hk, d, alibi, unit):
     """Nothing up to 256 prompts and 2048 units; above, one 16-byte entry for
     each unit that the prompts can have at most, and one for their count, in
     whole 256 bytes."""
@@ -37,7 +37,7 @@ def test_workspace_size(lib, H, Hk, d, unit):
                             ((2048 - 3) * unit, 4), (1 << 20, 5000)):
         units = tokens // unit + prompts
         assert lib.blk_attn_prefill_packed_workspace_size(
-            C.byref(desc(tokens, prompts, H, Hk, d)), C.byref(need)) == _abi.BLK_OK
+            C.byref(desc(tokens, prompts, H, Hk, d, alibi=alibi)), C.byref(need)) == _abi.BLK_OK
         small = prompts <= 256 and units <= 2048
         assert need.value == (0 if small else -(-16 * (1 + units) // 256) * 256)
 
