@@ -118,6 +118,7 @@ cudaError_t launch_attention_packed(DType dt, const AttnArgs& a, const PackedArg
     const void* vp = p.prefix ? p.v_prefix : a.v;
     const uint64_t rows = p.prefix ? p.prefix : a.S;
     if (!make_tmap_3d(&pack.tmPK, dt, kp, a.Hk, rows, a.d, 128) ||
+        !make_tmap_3d(&pack.tmPK2, dt, kp, a.Hk, rows, a.d, 128, 32) ||
         !make_tmap_3d(&pack.tmPV, dt, vp, a.Hk, rows, a.d, 128))
         return cudaErrorInvalidValue;
     if (listed) {

@@ -61,12 +61,20 @@ template <int D>
 struct GqaCfg {
     static_assert(D == 128 || D == 160, "GQA-packed attention is built for head_dim 128 and 160");
     static constexpr int kSub = (D + 63) / 64;          // 64-column slices per row
-    static constexpr int kTileBytes = kSub * 128 * 128;  // 128 rows x kSub x 128 B
+    // V tile: 128 rows x kSub x 128 B (head_dim 160 padded to 192 columns, one
+    // descriptor for the whole row). Q and K tiles keep only the 32 columns of
+    // head_dim 160's last slice, as a slice of 64-byte rows with the 64-byte
+    // swizzle: what that saves makes room for a second V stage (with one, the
+    // next V was loaded only after the PV product: @V2@).
+    static constexpr bool kHalf = D % 64 != 0;
+    static constexpr int kFull = D / 64;                 // whole slices
+    static constexpr int kTileBytes = kSub * 128 * 128;
+    static constexpr int kQKBytes = kFull * 128 * 128 + (kHalf ? 128 * 64 : 0);
     static constexpr int kQBufs = D > 128 ? 1 : 2;
     static constexpr int kKStages = 2;
-    static constexpr int kVStages = D > 128 ? 1 : 2;
-    static constexpr int kOffK = kQBufs * kTileBytes;
-    static constexpr int kOffV = kOffK + kKStages * kTileBytes;
+    static constexpr int kVStages = 2;
+    static constexpr int kOffK = kQBufs * kQKBytes;
+    static constexpr int kOffV = kOffK + kKStages * kQKBytes;
     static constexpr int kOffBar = kOffV + kVStages * kTileBytes;
     static constexpr int kSmem = kOffBar + 256 + 1024;   // + barriers + alignment slack
     static constexpr uint32_t kTmemCols = 512;
@@ -144,7 +152,9 @@ template <typename T, int D, bool ALIBI, bool PACKED>
 __global__ void __launch_bounds__(gqa_threads(PACKED), 1)
     attn_gqa_kernel(const __grid_constant__ CUtensorMap tmQ,
                     const __grid_constant__ CUtensorMap tmK,
-                    const __grid_constant__ CUtensorMap tmV, const AttnArgs a,
+                    const __grid_constant__ CUtensorMap tmV,
+                    const __grid_constant__ CUtensorMap tmQ2,
+                    const __grid_constant__ CUtensorMap tmK2, const AttnArgs a,
                     const GqaPack pk, const __grid_constant__ AttnPack<PACKED> pack) {
     using Cfg = GqaCfg<D>;
     constexpr int kQB = Cfg::kQBufs, kKS = Cfg::kKStages, kVS = Cfg::kVStages;
@@ -225,27 +235,37 @@ __global__ void __launch_bounds__(gqa_threads(PACKED), 1)
             c.start(a, pk, pack, plan, nblk, n_items);
             int gk = 0, gv = 0;  // K and V tiles loaded so far (ring positions)
             bool ok = true;
-            // the map and first row of step j's key tile
-            auto tile_source = [&](int j, const CUtensorMap* own, bool v, int& krow) {
+            // the first row of step j's key tile, and whether it is the prefix's
+            auto tile_source = [&](int j, int& krow) -> bool {
                 if constexpr (PACKED) {
                     const int kt = kRev ? c.nkv - 1 - j : j;
                     krow = kt < c.nP ? kt * kTK : c.start_row + (kt - c.nP) * kTK;
-                    return kt < c.nP ? (v ? &pack.tmPV : &pack.tmPK) : own;
+                    return kt < c.nP;
                 } else {
                     krow = j * kTK;
-                    return own;
+                    return false;
                 }
             };
             auto load_k = [&](int j) -> bool {
                 const int st = gk % kKS;
                 if (!mbar_wait(k_empty(st), ((gk / kKS) & 1) ^ 1u, a.err)) return false;
-                mbar_expect_tx(k_full(st), Cfg::kTileBytes);
+                mbar_expect_tx(k_full(st), Cfg::kQKBytes);
                 int krow;
-                const CUtensorMap* m = tile_source(j, &tmK, false, krow);
+                const CUtensorMap *m = &tmK, *m2 = &tmK2;
+                if (tile_source(j, krow)) {
+                    if constexpr (PACKED) {
+                        m = &pack.tmPK;
+                        m2 = &pack.tmPK2;
+                    }
+                }
+                const uint32_t dst = sK + st * Cfg::kQKBytes;
 #pragma unroll
-                for (int sub = 0; sub < Cfg::kSub; ++sub)
-                    tma_load_3d_hint(sK + st * Cfg::kTileBytes + sub * kTK * 128, m, k_full(st),
-                                sub * 64, krow, c.b * a.Hk + c.g, pol_kv);
+                for (int sub = 0; sub < Cfg::kFull; ++sub)
+                    tma_load_3d_hint(dst + sub * kTK * 128, m, k_full(st), sub * 64, krow,
+                                     c.b * a.Hk + c.g, pol_kv);
+                if constexpr (Cfg::kHalf)
+                    tma_load_3d_hint(dst + Cfg::kFull * kTK * 128, m2, k_full(st), Cfg::kFull * 64, krow,
+                                     c.b * a.Hk + c.g, pol_kv);
                 ++gk;
                 return true;
             };
@@ -254,7 +274,10 @@ __global__ void __launch_bounds__(gqa_threads(PACKED), 1)
                 if (!mbar_wait(v_empty(st), ((gv / kVS) & 1) ^ 1u, a.err)) return false;
                 mbar_expect_tx(v_full(st), Cfg::kTileBytes);
                 int krow;
-                const CUtensorMap* m = tile_source(j, &tmV, true, krow);
+                const CUtensorMap* m = &tmV;
+                if (tile_source(j, krow)) {
+                    if constexpr (PACKED) m = &pack.tmPV;
+                }
 #pragma unroll
                 for (int sub = 0; sub < Cfg::kSub; ++sub)
                     tma_load_3d_hint(sV + st * Cfg::kTileBytes + sub * kTK * 128, m, v_full(st),
@@ -269,14 +292,18 @@ __global__ void __launch_bounds__(gqa_threads(PACKED), 1)
                 // slice; rows past the chunk's heads keep stale values and are
                 // never written out
                 const int nh = min(pk.Gt, G - c.hc * pk.Gt);
-                mbar_expect_tx(q_full(qb), static_cast<uint32_t>(Cfg::kSub * nh * R * 128));
+                mbar_expect_tx(q_full(qb), static_cast<uint32_t>(nh * R * D * 2));
                 for (int i = 0; i < nh; ++i) {
+                    const int qrow = (PACKED ? c.start_row : 0) + c.p0;
+                    const int plane = c.b * a.H + c.g * G + c.hc * pk.Gt + i;
+                    const uint32_t dst = sQ + qb * Cfg::kQKBytes;
 #pragma unroll
-                    for (int sub = 0; sub < Cfg::kSub; ++sub)
-                        tma_load_3d_hint(sQ + qb * Cfg::kTileBytes + sub * kTQ * 128 + i * R * 128,
-                                    &tmQ, q_full(qb), sub * 64,
-                                    (PACKED ? c.start_row : 0) + c.p0,
-                                    c.b * a.H + c.g * G + c.hc * pk.Gt + i, pol_q);
+                    for (int sub = 0; sub < Cfg::kFull; ++sub)
+                        tma_load_3d_hint(dst + sub * kTQ * 128 + i * R * 128, &tmQ, q_full(qb), sub * 64,
+                                         qrow, plane, pol_q);
+                    if constexpr (Cfg::kHalf)
+                        tma_load_3d_hint(dst + Cfg::kFull * kTQ * 128 + i * R * 64, &tmQ2, q_full(qb),
+                                         Cfg::kFull * 64, qrow, plane, pol_q);
                 }
                 // consumption order: K(0), then K(j+1) ahead of V(j)
                 ok = load_k(0);
@@ -292,27 +319,36 @@ __global__ void __launch_bounds__(gqa_threads(PACKED), 1)
             constexpr uint32_t fmt = dt_traits<T>::mma_fmt;
             constexpr uint32_t idesc_s = make_idesc_f16(fmt, kTQ, kTK, false);
             constexpr uint32_t idesc_o = make_idesc_f16(fmt, kTQ, D, true);
-            constexpr uint64_t kTileStep = Cfg::kTileBytes >> 4;
+            constexpr uint64_t kVStep = Cfg::kTileBytes >> 4, kQKStep = Cfg::kQKBytes >> 4;
             constexpr uint64_t kSubStep = (kTQ * 128) >> 4;  // next 64-column slice
             const uint64_t dq0 = make_sdesc_sw128(sQ, 16, 1024);
             const uint64_t dk0 = make_sdesc_sw128(sK, 16, 1024);
             const uint64_t dv0 = make_sdesc_sw128(sV, kTK * 128, 1024);
+            // the half slice of Q and K (64-byte rows)
+            const uint64_t dqh0 = make_sdesc_sw64(sQ + Cfg::kFull * kTQ * 128, 16, 512);
+            const uint64_t dkh0 = make_sdesc_sw64(sK + Cfg::kFull * kTK * 128, 16, 512);
             const uint32_t tP = tmem_base + kColP;
             const uint32_t tO = tmem_base + kColO;
             int gk = 0, gv = 0, gs = 0, gp = 0, itx = 0;
             // S(buffer gs % 2) = Q K^T, once the softmax has read that buffer's
             // previous scores
-            auto issue_s = [&](uint64_t dq) -> bool {
+            auto issue_s = [&](int qb) -> bool {
                 const int st = gk % kKS;
                 const int sb = gs & 1;
                 if (!mbar_wait(k_full(st), (gk / kKS) & 1, a.err)) return false;
                 if (gs >= 2 && !mbar_wait(s_free(sb), ((gs >> 1) - 1) & 1, a.err)) return false;
                 tc_fence_after();
-                const uint64_t dk = dk0 + st * kTileStep;
+                const uint64_t dq = dq0 + qb * kQKStep, dk = dk0 + st * kQKStep;
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
+                for (int ks = 0; ks < Cfg::kFull * 4; ++ks) {
                     const uint64_t off = (ks / 4) * kSubStep + (ks % 4) * 2;
                     tc_mma_ss(tmem_base + 128u * sb, dq + off, dk + off, idesc_s, ks > 0 ? 1u : 0u);
+                }
+                if constexpr (Cfg::kHalf) {
+                    const uint64_t dqh = dqh0 + qb * kQKStep, dkh = dkh0 + st * kQKStep;
+#pragma unroll
+                    for (int ks = 0; ks < 2; ++ks)
+                        tc_mma_ss(tmem_base + 128u * sb, dqh + ks * 2, dkh + ks * 2, idesc_s, 1u);
                 }
                 tc_commit(s_full(sb));
                 tc_commit(k_empty(st));
@@ -328,7 +364,7 @@ __global__ void __launch_bounds__(gqa_threads(PACKED), 1)
                 if (!mbar_wait(p_full, gp & 1, a.err)) return false;
                 if (first && itx > 0 && !mbar_wait(o_free, (itx - 1) & 1, a.err)) return false;
                 tc_fence_after();
-                const uint64_t dv = dv0 + st * kTileStep;
+                const uint64_t dv = dv0 + st * kVStep;
 #pragma unroll
                 for (int ks = 0; ks < kTK / 16; ++ks)
                     tc_mma_ts(tO, tP + ks * 8, dv + ks * ((16 * 128) >> 4), idesc_o,
@@ -345,12 +381,11 @@ __global__ void __launch_bounds__(gqa_threads(PACKED), 1)
             while (ok && c.valid) {
                 const int qb = c.it % kQB;
                 if (!mbar_wait(q_full(qb), (c.it / kQB) & 1, a.err)) break;
-                const uint64_t dq = dq0 + qb * kTileStep;
-                ok = issue_s(dq);
+                ok = issue_s(qb);
                 if (ok && c.nkv == 1) tc_commit(q_empty(qb));
                 for (int j = 0; ok && j < c.nkv; ++j) {
                     if (j + 1 < c.nkv) {
-                        ok = issue_s(dq);
+                        ok = issue_s(qb);
                         if (ok && j + 2 == c.nkv) tc_commit(q_empty(qb));
                     }
                     if (ok) ok = issue_pv(j == 0);
@@ -590,8 +625,11 @@ cudaError_t launch_gqa_d(DType dt, const AttnArgs& a, const GqaPack& pk,
                          const AttnPack<PACKED>& pack, int64_t items, cudaStream_t s) {
     const int R = pk.R;
     using Cfg = GqaCfg<D>;
-    CUtensorMap tq, tk, tv;
+    // (the half-slice maps are used at head_dim 160 only)
+    CUtensorMap tq, tk, tv, tq2, tk2;
     if (!make_tmap_3d(&tq, dt, a.q, static_cast<uint64_t>(a.B) * a.H, a.S, D, R) ||
+        !make_tmap_3d(&tq2, dt, a.q, static_cast<uint64_t>(a.B) * a.H, a.S, D, R, 32) ||
+        !make_tmap_3d(&tk2, dt, a.k, static_cast<uint64_t>(a.B) * a.Hk, a.S, D, kTK, 32) ||
         !make_tmap_3d(&tk, dt, a.k, static_cast<uint64_t>(a.B) * a.Hk, a.S, D, kTK) ||
         !make_tmap_3d(&tv, dt, a.v, static_cast<uint64_t>(a.B) * a.Hk, a.S, D, kTK))
         return cudaErrorInvalidValue;
@@ -605,7 +643,7 @@ cudaError_t launch_gqa_d(DType dt, const AttnArgs& a, const GqaPack& pk,
     AttnArgs ap = a;
     ap.pdl = pdl_allowed(s);
     (void)launch_pdl(ap.pdl != 0, kern, dim3(static_cast<unsigned>(grid)), dim3(gqa_threads(PACKED)),
-                     Cfg::kSmem, s, tq, tk, tv, ap, pk, pack);
+                     Cfg::kSmem, s, tq, tk, tv, tq2, tk2, ap, pk, pack);
     return cudaGetLastError();
 }
 

@@ -19,8 +19,8 @@ struct PlanUnit {
 // the prompt of rank r comes behind all units above l, at place r among those
 // of level l.
 struct PlanSmem {
-    int first[kPlanCtaPrompts], len[kPlanCtaPrompts], n[kPlanCtaPrompts];
-    int sorted_n[kPlanCtaPrompts];
+    int first[kPlanCtaPrompts], len[kPlanCtaPrompts];
+    int n[kPlanCtaPrompts], sorted_n[kPlanCtaPrompts];
     uint16_t sorted_b[kPlanCtaPrompts];
     uint32_t list[kPlanCtaUnits];  // prompt << 16 | l
     int total;

@@ -525,6 +525,13 @@ __device__ __forceinline__ uint64_t make_sdesc_sw128(uint32_t saddr, uint32_t lb
     return d;
 }
 
+// The same with the 64-byte swizzle ([61,64) = 4): K-major rows of 64 bytes,
+// 8-row groups SBO = 512 bytes apart.
+__device__ __forceinline__ uint64_t make_sdesc_sw64(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    return (make_sdesc_sw128(saddr, lbo, sbo) & ~(static_cast<uint64_t>(7u) << 61)) |
+           (static_cast<uint64_t>(4u) << 61);
+}
+
 // 32 lanes x 32 consecutive 32-bit TMEM columns per warp; thread t gets lane
 // (taddr.lane + t). The wait is inside the same asm so the results are ready.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {

@@ -143,14 +143,14 @@ template <bool PACKED>
 struct AttnPack {};
 template <>
 struct AttnPack<true> {
-    CUtensorMap tmPK, tmPV;
+    CUtensorMap tmPK, tmPV, tmPK2;  // tmPK2: boxes of 32 columns (head_dim 160)
     const int4* plan;           // or nullptr: each CTA builds its own (attn_plan.cuh)
     const int32_t* cu_seqlens;
     int prompts, prefix;
     int G, Gt, R, nhc;          // gqa_tile (attn_pair128.cu)
 };
 // up to these sizes the list is built by each CTA, without a workspace
-constexpr int kPlanCtaPrompts = 256, kPlanCtaUnits = 2048;
+constexpr int kPlanCtaPrompts = 256, kPlanCtaUnits = 1024;
 struct PackedArgs {
     const void* k_prefix;  // [Hk, prefix, d]
     const void* v_prefix;

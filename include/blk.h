@@ -196,8 +196,9 @@ typedef struct {
  * does not see has weight 0, so a non-finite value (v) of a later token of
  * the same prompt and 128-key tile makes a NaN.
  * GQA: kv head = h / (H / Hk). head_dim in {64, 128, 160}. One launch; above
- * 256 prompts or a few hundred thousand tokens a second one ahead of it makes
- * the work list in the workspace, which then has at least
+ * 256 prompts or some ten to hundred thousand tokens (by the head layout) a
+ * second one ahead of it makes the work list in the workspace, which then has at
+ * least
  * blk_attn_prefill_packed_workspace_size bytes, 16-byte aligned (0 bytes: none
  * is needed, NULL will do); calls whose kernels overlap on the GPU need a
  * workspace each. */

@@ -29,16 +29,16 @@ def call(lib, d, q=FAKE, k=FAKE, v=FAKE, kp=None, vp=None, cu=FAKE, slopes=None,
     (32, 32, 64, 0, 256), (8, 2, 64, 1, 256), (16, 16, 128, 1, 256), (32, 8, 128, 0, 64),
     (32, 8, 128, 1, 32), (32, 8, 160, 0, 32), (6, 2, 128, 0, 80), (32, 1, 160, 1, 8), (2, 2, 160, 0, 128)])
 def test_workspace_size(lib, H, Hk, d, alibi, unit):
-    """Nothing up to 256 prompts and 2048 units; above, one 16-byte entry for
+    """Nothing up to 256 prompts and 1024 units; above, one 16-byte entry for
     each unit that the prompts can have at most, and one for their count, in
     whole 256 bytes."""
     need = C.c_size_t(0)
-    for tokens, prompts in ((1000, 7), (1000, 256), (1000, 257), ((2048 - 3) * unit, 3),
-                            ((2048 - 3) * unit, 4), (1 << 20, 5000)):
+    for tokens, prompts in ((1000, 7), (1000, 256), (1000, 257), ((1024 - 3) * unit, 3),
+                            ((1024 - 3) * unit, 4), (1 << 20, 5000)):
         units = tokens // unit + prompts
         assert lib.blk_attn_prefill_packed_workspace_size(
             C.byref(desc(tokens, prompts, H, Hk, d, alibi=alibi)), C.byref(need)) == _abi.BLK_OK
-        small = prompts <= 256 and units <= 2048
+        small = prompts <= 256 and units <= 1024
         assert need.value == (0 if small else -(-16 * (1 + units) // 256) * 256)
 
 
