@@ -98,14 +98,18 @@ struct PairCfg {
 //
 // Packed prompts (PACKED): items are (unit, head); a unit is a query-tile
 // pair of one prompt, from the plan's list (heaviest first), and the prompt's
-// nP prefix tiles come ahead of its own key tiles.
+// nP prefix tiles come ahead of its own key tiles. A prompt's tiles are paired
+// from its end, so that where their number is odd the single one is the first,
+// which has one key tile, and not the last, which has all (17 tiles: 81 steps for
+// 89).
 template <bool PACKED>
 struct PairCursor {
     using Plan = typename PlanStorage<PACKED>::type;
     int item, it, i, b, h, g, nA, nB;
     bool valid;
-    // packed: the prompt's first row and length, the prefix's key tiles
-    int start_row, len, nP, prefix;
+    // packed: the prompt's first row and length, the prefix's key tiles; t0:
+    // query tile A (B is t0 + 1)
+    int start_row, len, nP, prefix, t0;
     __device__ __forceinline__ int item_of(int round) const {
         const int G = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
         return round * G + ((round & 1) ? G - 1 - c : c);
@@ -122,8 +126,10 @@ struct PairCursor {
             i = u.l;
             prefix = pack.prefix;
             nP = (prefix + kTK - 1) / kTK;
-            nA = nP + 2 * i + 1;
-            nB = (2 * i + 1) * kTQ < len ? nP + 2 * i + 2 : 0;
+            const bool odd = ((len + kTQ - 1) / kTQ) & 1;
+            t0 = odd ? max(2 * i - 1, 0) : 2 * i;
+            nA = nP + t0 + 1;
+            nB = odd && i == 0 ? 0 : nP + t0 + 2;
             return;
         }
         const int bh_count = a.B * a.H;
@@ -258,7 +264,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
                     for (int sub = 0; sub < Cfg::kSub; ++sub)
                         tma_load_3d_hint(sQ + (2 * qb + x) * Cfg::kQBytes + sub * kTQ * 128, &tmQ,
-                                    q_full(qb), sub * 64, (PACKED ? c.start_row : 0) + (2 * c.i + x) * kTQ,
+                                    q_full(qb), sub * 64, PACKED ? c.start_row + (c.t0 + x) * kTQ : (2 * c.i + x) * kTQ,
                                     c.b * a.H + c.h, pol_q);
                 }
                 const int nkv = c.n_kv();
@@ -454,7 +460,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 c.next(a, pack, plan, nq, np, n_items);
                 continue;
             }
-            const int qt = 2 * c.i + x;
+            const int qt = (PACKED ? c.t0 : 2 * c.i) + x;
             const int qpos = qt * kTQ + row;
             float m_used = -INFINITY;  // running max, log2 domain
             float l = 0.f;

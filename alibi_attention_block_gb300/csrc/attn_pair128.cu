@@ -78,7 +78,7 @@ struct PairCursor {
     using Plan = typename PlanStorage<PACKED>::type;
     int item, it, i, b, h, g, nA, nB;
     bool valid;
-    int start_row, len, nP, prefix, hc;
+    int start_row, len, nP, prefix, hc, t0;
     __device__ __forceinline__ int item_of(int round) const {
         const int G = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
         return round * G + ((round & 1) ? G - 1 - c : c);
@@ -98,9 +98,12 @@ struct PairCursor {
             i = u.l;
             prefix = pack.prefix;
             nP = (prefix + kTK - 1) / kTK;
-            const int endA = (2 * i + 1) * pack.R;  // one past tile A's last position
+            // tiles paired from the prompt's end (see attn_pair.cu)
+            const bool odd = ((len + pack.R - 1) / pack.R) & 1;
+            t0 = odd ? max(2 * i - 1, 0) : 2 * i;
+            const int endA = (t0 + 1) * pack.R;  // one past tile A's last position
             nA = nP + (min(endA, len) + kTK - 1) / kTK;
-            nB = endA < len ? nP + (min(endA + pack.R, len) + kTK - 1) / kTK : 0;
+            nB = odd && i == 0 ? 0 : nP + (min(endA + pack.R, len) + kTK - 1) / kTK;
             return;
         }
         const int bh_count = a.B * a.H;
@@ -239,7 +242,7 @@ __global__ void __launch_bounds__(kP128Threads, 1)
                             for (int sub = 0; sub < Cfg::kSub; ++sub)
                                 tma_load_3d_hint(sQ + x * Cfg::kQBytes + sub * kTQ * 128 + k * R * 128,
                                                  &tmQ, q_full(x), sub * 64,
-                                                 c.start_row + (2 * c.i + x) * R, c.h + k, pol_q);
+                                                 c.start_row + (c.t0 + x) * R, c.h + k, pol_q);
                     } else {
                         mbar_expect_tx(q_full(x), Cfg::kQBytes);
 #pragma unroll
@@ -471,7 +474,7 @@ __global__ void __launch_bounds__(kP128Threads, 1)
                 c.next(a, pack, plan, nq, np, n_items);
                 continue;
             }
-            const int qt = 2 * c.i + x;
+            const int qt = (PACKED ? c.t0 : 2 * c.i) + x;
             // packed: this row's head of the tile, and its position
             const int hl = PACKED ? row / tile_positions : 0;
             const int qfirst = qt * (PACKED ? tile_positions : kTQ);
