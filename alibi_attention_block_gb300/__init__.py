@@ -25,7 +25,7 @@ __all__ = ["layernorm_bias", "rmsnorm", "qkv_bias_rope_partial", "rope_inplace",
            "attn_prefill_packed", "attn_prefill_packed_workspace_size", "packed_desc",
            "attn_decode", "attn_decode_workspace_size", "decode_desc",
            "attn_decode_shared", "attn_decode_shared_workspace_size", "decode_shared_desc",
-           "linear", "mlp", "block_desc", "forward_workspace_size", "forward_q8_0_workspace_size", "forward", "forward_host", "ForwardGraph", "HostPipe", "model_desc",
+           "linear", "mlp", "block_desc", "forward_workspace_size", "forward_q8_0_workspace_size", "forward", "forward_packed", "forward_packed_workspace_size", "forward_host", "ForwardGraph", "HostPipe", "model_desc",
            "model_workspace_size", "model_forward",
            "check_device_status", "BlkError", "library_path"]
 
@@ -436,6 +436,45 @@ def forward(cfg, weights: dict, x, workspace=None, out=None):
     out = torch.empty_like(x) if out is None else out
     _abi.check(_lib().blk_forward(C.byref(desc), C.byref(w), _p(x), _p(out), _p(workspace),
                                   workspace.numel(), _dt(x), _stream()), "blk_forward")
+    return out
+
+
+def forward_packed_workspace_size(cfg, tokens: int, prompts: int) -> int:
+    desc = block_desc(cfg, 1, tokens)
+    need = C.c_size_t(0)
+    _abi.check(_lib().blk_forward_packed_workspace_size(C.byref(desc), prompts, C.byref(need)),
+               "blk_forward_packed_workspace_size")
+    return need.value
+
+
+def forward_packed(cfg, weights: dict, x, cu_seqlens, workspace=None, out=None):
+    """The block over packed prompts: x [T, D] holds them one behind the other,
+    prompt i in rows cu_seqlens[i] .. cu_seqlens[i+1] - 1 (int32 [prompts + 1]
+    on the device). Returns y [T, D]; rows outside every prompt hold
+    unspecified values. weights as for ``forward``."""
+    T, D = x.shape
+    if D != cfg.hidden:
+        raise ValueError(f"x has {D} columns, the block {cfg.hidden}")
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens has shape [prompts + 1]")
+    prompts = cu_seqlens.numel() - 1
+    unknown = set(weights) - set(_abi.WEIGHT_SLOTS)
+    if unknown:
+        raise KeyError(f"unknown weight slots: {sorted(unknown)}")
+    _same(x, out, *(t for name, t in weights.items() if name != "alibi_slopes"))
+    _shape(out, (T, D), "out")
+    desc = block_desc(cfg, 1, T)
+    if workspace is None:
+        workspace = torch.empty(forward_packed_workspace_size(cfg, T, prompts), dtype=torch.uint8,
+                                device=x.device)
+    w = _abi.BlockWeights(*[_p(weights.get(n)) for n in _abi.WEIGHT_SLOTS])
+    out = torch.empty_like(x) if out is None else out
+    dev = torch.cuda.current_device()
+    (cup,) = _pointers(torch.int32, dev, cu_seqlens)
+    wp, wn = _workspace(workspace, dev)
+    xp, op = _pointers(x.dtype, dev, x, out)
+    _abi.check(_lib().blk_forward_packed(C.byref(desc), C.byref(w), cup, prompts, xp, op, wp, wn,
+                                         _dt(x), _stream()), "blk_forward_packed")
     return out
 
 

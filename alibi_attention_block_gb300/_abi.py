@@ -117,6 +117,10 @@ _PROTOS = {
     "blk_forward_q8_0_workspace_size": (C.c_int, [C.POINTER(BlockDesc), C.POINTER(C.c_size_t)]),
     "blk_forward": (C.c_int, [C.POINTER(BlockDesc), C.POINTER(BlockWeights), vp, vp, vp,
                               C.c_size_t, C.c_int, vp]),
+    "blk_forward_packed_workspace_size": (C.c_int, [C.POINTER(BlockDesc), i64,
+                                                    C.POINTER(C.c_size_t)]),
+    "blk_forward_packed": (C.c_int, [C.POINTER(BlockDesc), C.POINTER(BlockWeights), vp, i64, vp,
+                                     vp, vp, C.c_size_t, C.c_int, vp]),
     "blk_attn_decode_workspace_size": (C.c_int, [C.POINTER(DecodeDesc), C.POINTER(C.c_size_t)]),
     "blk_attn_decode": (C.c_int, [C.POINTER(DecodeDesc), vp, vp, vp, vp, vp, vp, vp, C.c_size_t,
                                   C.c_int, vp]),

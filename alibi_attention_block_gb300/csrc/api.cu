@@ -702,10 +702,34 @@ blk_status run_attn_packed(const blk_packed_desc* d, const void* q, const void* 
     return e == cudaSuccess ? BLK_OK : cuda_fail(e, "packed attention launch");
 }
 
+// Packed prompts of a block (blk_forward_packed): batch 1, seq = all rows.
+struct PackedPrompts {
+    const int32_t* cu_seqlens;
+    int64_t prompts;
+};
+
 blk_status forward_impl(const blk_block_desc* d, const blk_block_weights* w,
                         const blk_q8_weights* q8, const void* x, void* y, void* workspace,
                         size_t ws_bytes, blk_dtype dt, blk_stream_t s, void* const* events,
-                        int n_events, int32_t* step_kinds, int* n_launches);
+                        int n_events, int32_t* step_kinds, int* n_launches,
+                        const PackedPrompts* packed = nullptr);
+
+// The attention of a packed block, and the whole workspace: the block's, then
+// the work list.
+blk_packed_desc packed_block_attn(const blk_block_desc* d, int64_t prompts) {
+    const auto& q = d->qkv;
+    return blk_packed_desc{q.seq, prompts, q.n_heads, q.n_kv_heads, q.head_dim, 0, 0.f, d->alibi};
+}
+blk_status validate_packed_block(const blk_block_desc* d, int64_t prompts) {
+    BLK_REQUIRE(d, "descriptor is NULL");
+    BLK_REQUIRE(d->qkv.batch == 1, "packed prompts are one batch entry: batch must be 1");
+    const blk_packed_desc pd = packed_block_attn(d, prompts);
+    return validate_packed_desc(&pd);
+}
+size_t packed_block_ws_bytes(const blk_block_desc* d, int64_t prompts) {
+    const blk_packed_desc pd = packed_block_attn(d, prompts);
+    return forward_layout(d).total + packed_ws_bytes(&pd);
+}
 
 }  // namespace
 
@@ -1186,6 +1210,33 @@ blk_status blk_forward_ex(const blk_block_desc* d, const blk_block_weights* w, c
                         step_kinds, n_launches);
 }
 
+blk_status blk_forward_packed_workspace_size(const blk_block_desc* d, int64_t prompts,
+                                             size_t* bytes) {
+    size_t block = 0;
+    blk_status st = blk_forward_workspace_size(d, &block);
+    if (st == BLK_OK) st = validate_packed_block(d, prompts);
+    if (st != BLK_OK) return st;
+    BLK_REQUIRE(bytes != nullptr, "bytes is NULL");
+    *bytes = packed_block_ws_bytes(d, prompts);
+    return BLK_OK;
+}
+
+blk_status blk_forward_packed(const blk_block_desc* d, const blk_block_weights* w,
+                              const int32_t* cu_seqlens, int64_t prompts, const void* x, void* y,
+                              void* workspace, size_t ws_bytes, blk_dtype dt, blk_stream_t s) {
+    blk_status st = validate_packed_block(d, prompts);
+    if (st != BLK_OK) return st;
+    BLK_REQUIRE(cu_seqlens != nullptr && (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) == 0,
+                "cu_seqlens must be a 4-byte aligned device pointer");
+    if ((st = validate_block(d, w)) != BLK_OK) return st;
+    const size_t need = packed_block_ws_bytes(d, prompts);
+    if (!workspace || ws_bytes < need || !aligned16(workspace))
+        return fail(BLK_EWORKSPACE, "workspace needs %zu bytes, 16-byte aligned", need);
+    const PackedPrompts packed{cu_seqlens, prompts};
+    return forward_impl(d, w, nullptr, x, y, workspace, ws_bytes, dt, s, nullptr, 0, nullptr,
+                        nullptr, &packed);
+}
+
 blk_status blk_forward_q8_0(const blk_block_desc* d, const blk_block_weights* w,
                             const blk_q8_weights* q8, const void* x, void* y, void* workspace,
                             size_t ws_bytes, blk_dtype dt, blk_stream_t s) {
@@ -1211,7 +1262,8 @@ namespace {
 blk_status forward_impl(const blk_block_desc* d, const blk_block_weights* w,
                         const blk_q8_weights* q8, const void* x, void* y, void* workspace,
                         size_t ws_bytes, blk_dtype dt, blk_stream_t s, void* const* events,
-                        int n_events, int32_t* step_kinds, int* n_launches) {
+                        int n_events, int32_t* step_kinds, int* n_launches,
+                        const PackedPrompts* packed) {
     BLK_REQUIRE(valid_dt(dt), "dtype must be BLK_F16 or BLK_BF16");
     blk_status st = validate_block(d, w, q8);
     if (st != BLK_OK) return st;
@@ -1325,9 +1377,15 @@ blk_status forward_impl(const blk_block_desc* d, const blk_block_weights* w,
     st = run_qkv(&q, attn_in, W_qkv, w->b_qkv, w->q_norm_w, w->k_norm_w, qb, kb, vb, t, cs, ds,
                  &log, split, pq_qkv);
     if (st != BLK_OK) return st;
-    // 3. causal attention (+ALiBi)
-    blk_attn_desc ad{q.batch, q.seq, q.n_heads, q.n_kv_heads, q.head_dim, 0.f, 1, d->alibi};
-    st = run_attn(&ad, qb, kb, vb, w->alibi_slopes, ob, t, cs, ds);
+    // 3. causal attention (+ALiBi), per sequence or per packed prompt
+    if (packed) {
+        const blk_packed_desc pd = packed_block_attn(d, packed->prompts);
+        st = run_attn_packed(&pd, qb, kb, vb, nullptr, nullptr, packed->cu_seqlens,
+                             w->alibi_slopes, ob, ws + L.total, t, cs, ds);
+    } else {
+        blk_attn_desc ad{q.batch, q.seq, q.n_heads, q.n_kv_heads, q.head_dim, 0.f, 1, d->alibi};
+        st = run_attn(&ad, qb, kb, vb, w->alibi_slopes, ob, t, cs, ds);
+    }
     if (st != BLK_OK) return st;
     BLK_STEP(BLK_STEP_ATTENTION);
     const int64_t Hd = q.n_heads * q.head_dim;

@@ -157,7 +157,7 @@ __device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t off) {
 template <int SLOTS>
 struct PrefixBars {
     uint32_t at;
-    static constexpr int kBytes = 56 + 16 * SLOTS;
+    static constexpr int kBytes = 64 + 16 * SLOTS;
     __device__ __forceinline__ uint32_t q_full() const { return at; }
     __device__ __forceinline__ uint32_t q_empty() const { return at + 8u; }
     __device__ __forceinline__ uint32_t s_full() const { return at + 16u; }
@@ -165,8 +165,9 @@ struct PrefixBars {
     __device__ __forceinline__ uint32_t p_full() const { return at + 32u; }
     __device__ __forceinline__ uint32_t pv_done() const { return at + 40u; }
     __device__ __forceinline__ uint32_t o_free() const { return at + 48u; }
-    __device__ __forceinline__ uint32_t full(int i) const { return at + 56u + 8u * i; }
-    __device__ __forceinline__ uint32_t empty(int i) const { return at + 56u + 8u * (SLOTS + i); }
+    __device__ __forceinline__ uint32_t drain() const { return at + 56u; }
+    __device__ __forceinline__ uint32_t full(int i) const { return at + 64u + 8u * i; }
+    __device__ __forceinline__ uint32_t empty(int i) const { return at + 64u + 8u * (SLOTS + i); }
     __device__ __forceinline__ void init() const {
         mbar_init(q_full(), 1);
         mbar_init(q_empty(), 1);
@@ -175,6 +176,7 @@ struct PrefixBars {
         mbar_init(p_full(), 4);
         mbar_init(pv_done(), 1);
         mbar_init(o_free(), 4);
+        mbar_init(drain(), 1);
         for (int i = 0; i < SLOTS; ++i) {
             mbar_init(full(i), 1);
             mbar_init(empty(i), 1);
@@ -185,7 +187,7 @@ struct PrefixBars {
 template <int SLOTS>
 struct OwnBars {
     uint32_t at;
-    static constexpr int kBytes = 128 + 16 * SLOTS;
+    static constexpr int kBytes = 136 + 16 * SLOTS;
     __device__ __forceinline__ uint32_t q_full(int i) const { return at + 8u * i; }
     __device__ __forceinline__ uint32_t q_empty(int i) const { return at + 16u + 8u * i; }
     __device__ __forceinline__ uint32_t s_full(int i) const { return at + 32u + 8u * i; }
@@ -195,8 +197,9 @@ struct OwnBars {
     __device__ __forceinline__ uint32_t o_free(int i) const { return at + 96u + 8u * i; }
     __device__ __forceinline__ uint32_t max_full() const { return at + 112u; }
     __device__ __forceinline__ uint32_t sum_full() const { return at + 120u; }
-    __device__ __forceinline__ uint32_t full(int i) const { return at + 128u + 8u * i; }
-    __device__ __forceinline__ uint32_t empty(int i) const { return at + 128u + 8u * (SLOTS + i); }
+    __device__ __forceinline__ uint32_t drain() const { return at + 128u; }
+    __device__ __forceinline__ uint32_t full(int i) const { return at + 136u + 8u * i; }
+    __device__ __forceinline__ uint32_t empty(int i) const { return at + 136u + 8u * (SLOTS + i); }
     __device__ __forceinline__ void init() const {
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full(i), 1);
@@ -209,6 +212,7 @@ struct OwnBars {
         }
         mbar_init(max_full(), 4);
         mbar_init(sum_full(), 4);
+        mbar_init(drain(), 1);
         for (int i = 0; i < SLOTS; ++i) {
             mbar_init(full(i), 1);
             mbar_init(empty(i), 1);
@@ -259,11 +263,12 @@ __device__ __forceinline__ bool prefix_phase(const SharedKernelArgs& a, const CU
         if (lane == 0) {
             // read again by the kv head's other row tiles, if it has any
             const uint64_t pol = a.nrt > 1 ? l2_evict_last_policy() : l2_evict_first_policy();
-            int r = 0;
+            int r = 0, nq = 0;  // tiles and query tiles on their way so far
             while (ok && c.valid) {
                 const int g = c.u / a.nrt, rt = c.u - g * a.nrt;
                 if (!(ok = mbar_wait(bar.q_empty(), (c.it & 1) ^ 1u, a.err))) break;
                 mbar_expect_tx(bar.q_full(), C::kTile);
+                ++nq;
 #pragma unroll
                 for (int sub = 0; sub < C::kSub; ++sub)
                     tma_load_4d(sQ + sub * kTQ * 128, &tmQ, bar.q_full(), sub * 64, 0, g,
@@ -284,6 +289,11 @@ __device__ __forceinline__ bool prefix_phase(const SharedKernelArgs& a, const CU
             for (int i = r > kSlots ? r - kSlots : 0; i < r && ok; ++i)
                 ok = mbar_wait(bar.empty(i % kSlots), (i / kSlots) & 1, a.err);
             if (ok && c.it > 0) ok = mbar_wait(bar.q_empty(), (c.it - 1) & 1, a.err);
+            if (!ok) {  // gave up: no copy may land behind this block's end
+                for (int i = r > kSlots ? r - kSlots : 0; i < r; ++i)
+                    mbar_wait(bar.full(i % kSlots), (i / kSlots) & 1, a.err);
+                if (nq > 0) mbar_wait(bar.q_full(), (nq - 1) & 1, a.err);
+            }
         }
     } else if (warp == 1) {
         if (lane == 0) {
@@ -347,6 +357,10 @@ __device__ __forceinline__ bool prefix_phase(const SharedKernelArgs& a, const CU
             // ... and the columns of S and P
             if (ok && t > 0) ok = mbar_wait(bar.pv_done(), (t - 1) & 1, a.err);
             tc_fence_after();
+            if (!ok) {  // gave up: nor any product
+                tc_commit(bar.drain());
+                mbar_wait(bar.drain(), 0, a.err);
+            }
         }
     } else {
         const int quarter = warp & 3;
@@ -564,11 +578,12 @@ __device__ __forceinline__ void own_phase(const SharedKernelArgs& a, const CUten
     if (warp == 0) {
         if (lane == 0) {
             const uint64_t pol = l2_evict_first_policy();
-            int r = 0;
+            int r = 0, nq = 0;  // tiles and query boxes on their way so far
             while (ok && c.valid) {
                 const int qb = c.it & 1;
                 if (!(ok = mbar_wait(bar.q_empty(qb), ((c.it >> 1) & 1) ^ 1u, a.err))) break;
                 mbar_expect_tx(bar.q_full(qb), G * 128 * C::kSub);
+                ++nq;
 #pragma unroll
                 for (int sub = 0; sub < C::kSub; ++sub)
                     tma_load_2d(sQ + qb * C::kQBytes + sub * 1024, &tmQ, bar.q_full(qb), sub * 64,
@@ -603,6 +618,11 @@ __device__ __forceinline__ void own_phase(const SharedKernelArgs& a, const CUten
                 }
                 c.next(a);
             }
+            // whatever the others met, no copy lands behind this block's end
+            for (int i = r > kSlots ? r - kSlots : 0; i < r; ++i)
+                mbar_wait(bar.full(i % kSlots), (i / kSlots) & 1, a.err);
+            for (int i = nq > 2 ? nq - 2 : 0; i < nq; ++i)
+                mbar_wait(bar.q_full(i & 1), (i >> 1) & 1, a.err);
         }
     } else if (warp == 1) {
         if (lane == 0) {
@@ -712,10 +732,12 @@ __device__ __forceinline__ void own_phase(const SharedKernelArgs& a, const CUten
                     t0 = globaltimer_ns();
                 } else if ((spin & 63u) == 0u && globaltimer_ns() - t0 > kWaitLimitNs) {
                     report_error(a.err, DEV_ERR_TIMEOUT);
-                    ok = false;
                     break;
                 }
             }
+            // ... and no product
+            tc_commit(bar.drain());
+            mbar_wait(bar.drain(), 0, a.err);
         }
     } else {
         const int quarter = warp & 3;

@@ -394,6 +394,21 @@ blk_status blk_forward_workspace_size(const blk_block_desc* d, size_t* bytes);
 blk_status blk_forward(const blk_block_desc* d, const blk_block_weights* w, const void* x,
                        void* y, void* workspace, size_t ws_bytes, blk_dtype dt, blk_stream_t s);
 
+/* blk_forward over prompts of different lengths packed in one token axis (no
+ * padding between them): d->qkv.batch is 1, d->qkv.seq the rows of x and y;
+ * prompt i is rows cu_seqlens[i] .. cu_seqlens[i+1] - 1 (device int32
+ * [prompts + 1], as for blk_attn_prefill_packed). Every step but the attention
+ * works row by row; the rotary turns by the packed row, which leaves the
+ * scores within a prompt what they are (they depend on position differences
+ * only). Rows of y outside every prompt hold unspecified values. The
+ * workspace has at least blk_forward_packed_workspace_size bytes. Errors as
+ * blk_forward and blk_attn_prefill_packed. */
+blk_status blk_forward_packed_workspace_size(const blk_block_desc* d, int64_t prompts,
+                                             size_t* bytes);
+blk_status blk_forward_packed(const blk_block_desc* d, const blk_block_weights* w,
+                              const int32_t* cu_seqlens, int64_t prompts, const void* x, void* y,
+                              void* workspace, size_t ws_bytes, blk_dtype dt, blk_stream_t s);
+
 /* Kinds of the kernel launches blk_forward enqueues, in the order they run. */
 typedef enum {
     BLK_STEP_INPUT_NORM = 0,   /* input LayerNorm/RMSNorm (pre-norm blocks) */

@@ -11,14 +11,18 @@ they add less than 2^-14 relative (the exponent's rounding 2^-18 ln 2, ex2's
 2^-22, a tile's accumulation). So
     |err| <= (u + 2^-14) sum_j p_j |v_j| + u |o| + n 2^-25 max |v|.
 """
+import dataclasses
+
 import numpy as np
 import pytest
 import torch
 
 import alibi_attention_block_gb300 as blk
 import oracle
-from tests.parity import f64, to_dev
-from workloads import draw
+import workloads
+from tests.parity import ABS_TOL, check, f64, to_dev
+from tests.test_storage_budget import POST_NORM_ABS_TOL
+from workloads import BLOCK_CONFIGS, draw, scaled
 
 pytestmark = pytest.mark.gpu
 
@@ -262,6 +266,54 @@ def test_graph_replay_and_other_stream():
         torch.cuda.synchronize()
         got = out.clone()
         assert torch.equal(got, blk.attn_prefill_packed(qd, kd, vd, cu, k_prefix=kpd, v_prefix=vpd))
+
+
+# ---- the block over packed prompts ------------------------------------
+
+BLOCKS = {
+    "stablelm": scaled(BLOCK_CONFIGS["stablelm2_1p6b"], batch=1, hidden=256, n_heads=4, n_kv_heads=4,
+                       intermediate=688),
+    "bloom": scaled(BLOCK_CONFIGS["bloom_560m"], batch=1, hidden=256, n_heads=4, n_kv_heads=4,
+                    intermediate=1024),
+    "olmo": scaled(BLOCK_CONFIGS["olmo2_1b"], batch=1, hidden=256, n_heads=2, n_kv_heads=2,
+                   intermediate=512),
+    "stablelm_12b": scaled(BLOCK_CONFIGS["stablelm2_12b"], batch=1, hidden=320, n_heads=8, n_kv_heads=2,
+                           intermediate=512),
+}
+
+
+@pytest.mark.parametrize("name", sorted(BLOCKS))
+@pytest.mark.parametrize("extra", [0, 300])
+def test_block_over_packed_prompts(name, extra):
+    """blk_forward_packed is the oracle's block on each prompt by itself (its
+    own positions from 0), at the gates of the block's dense tests, with the
+    work list in shared memory or (extra empty prompts) in the workspace."""
+    lens = [70, 1, 0, 200, 129]
+    cu = ends(lens)
+    T = cu[-1] + 5
+    cfg = dataclasses.replace(BLOCKS[name], seq=T)
+    x, w = workloads.block_inputs(cfg)
+    x = x.reshape(T, cfg.hidden)
+    wd = {k: to_dev(t) for k, t in w.items()}
+    y = blk.forward_packed(cfg, wd, to_dev(x), table(cu + [cu[-1]] * extra))
+    blk.check_device_status()
+    tol = POST_NORM_ABS_TOL if cfg.norm_place == "post" else ABS_TOL
+    for i, n in enumerate(lens):
+        if n:
+            one = dataclasses.replace(cfg, seq=n)
+            ref = oracle.block_forward(one, x[None, cu[i]:cu[i + 1]], w)["y"][0]
+            check(y[cu[i]:cu[i + 1]], ref, f"{name} prompt {i}", unit_scale=True, abs_tol=tol,
+                  storage=cfg.dtype)
+
+
+def test_block_over_one_prompt_equals_dense():
+    """One prompt that is all rows: the block's dense forward, bit for bit."""
+    cfg = dataclasses.replace(BLOCKS["stablelm"], seq=333)
+    x, w = workloads.block_inputs(cfg)
+    wd = {k: to_dev(t) for k, t in w.items()}
+    dense = blk.forward(cfg, wd, to_dev(x))
+    y = blk.forward_packed(cfg, wd, to_dev(x)[0], table([0, 333]))
+    assert torch.equal(y, dense[0])
 
 
 def test_binding_refuses():

@@ -90,6 +90,37 @@ def test_shared_matches_oracle(case):
     check(o, q, kp, vp, k, v, lens, dt, ref_slopes, name=str(case))
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+def test_every_kernel(dt, d, G):
+    """Each instantiation: several segments of prefix and own caches per CTA
+    and per unit, tails of every kind, with and without ALiBi."""
+    B, Hk, P, S = 21, 4, 1500, 300
+    q, kp, vp, k, v = inputs(B, Hk * G, Hk, d, P, S, dt, 400 + d + G)
+    lens = [(97 * i) % (S + 1) for i in range(B)]
+    args = [to_dev(t) for t in (q, kp, vp, k, v)] + [torch.tensor(lens, dtype=torch.int32, device="cuda")]
+    for alibi in (False, True):
+        ref_slopes, dev_slopes = slopes_of(Hk * G, alibi)
+        o = blk.attn_decode_shared(*args, alibi=alibi, slopes=dev_slopes)
+        blk.check_device_status()
+        check(o, q, kp, vp, k, v, lens, dt, ref_slopes, name=f"alibi {alibi}")
+
+
+def test_own_caches_beyond_32_bit_offsets():
+    """Caches of more than 2^31 elements: the last sequences' own keys lie
+    behind the range of 32-bit offsets."""
+    B, H, Hk, d, P, S = 9, 4, 2, 128, 150, (1 << 31) // (8 * 2 * 128) + 1000
+    q, kp, vp, k, v = inputs(B, H, Hk, d, P, 300, "bf16", 77)
+    kd, vd = (torch.zeros((B, Hk, S, d), dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    kd[:, :, :300], vd[:, :, :300] = to_dev(k), to_dev(v)
+    assert kd.numel() > 1 << 31 and (B - 1) * Hk * S * d > 1 << 31
+    lens = [300, 1, 2, 128, 129, 17, 255, 0, 300]
+    o = blk.attn_decode_shared(to_dev(q), to_dev(kp), to_dev(vp), kd, vd,
+                               torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    check(o, q, kp, vp, k, v, lens, "bf16", name="long caches")
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_growing_scores_rescale(d):
     """Scores that rise or fall along the prefix move the running maximum at

@@ -123,3 +123,41 @@ def test_shared_argument_refusals(lib):
     assert step(lib, d, ws=None) == _abi.BLK_EWORKSPACE
     assert step(lib, d, ws=FAKE + 8) == _abi.BLK_EWORKSPACE
     assert step(lib, d, n=need.value - 1) == _abi.BLK_EWORKSPACE
+
+
+# -------------------------------------------------- blk_forward_packed --
+
+def block(batch=1, seq=500, H=4, Hk=4, d=64):
+    q = _abi.QkvDesc(batch, seq, 256, H, Hk, d, _abi.BLK_QKV_STACKED, _abi.BLK_QKNORM_NONE, 1e-5, 16, 1e4)
+    return _abi.BlockDesc(q, _abi.BLK_NORM_LAYERNORM, _abi.BLK_NORM_PRE, _abi.BLK_RESIDUAL_SEQUENTIAL,
+                          1e-5, 0, 688, _abi.BLK_ACT_SWIGLU)
+
+
+def test_forward_packed_refusals(lib):
+    need, dense = C.c_size_t(0), C.c_size_t(0)
+    d = block()
+    assert lib.blk_forward_workspace_size(C.byref(d), C.byref(dense)) == _abi.BLK_OK
+    for prompts, extra in ((3, 0), (300, -(-16 * (1 + 1 + 300) // 256) * 256)):
+        assert lib.blk_forward_packed_workspace_size(C.byref(d), prompts, C.byref(need)) == _abi.BLK_OK
+        assert need.value == dense.value + extra
+    size = lib.blk_forward_packed_workspace_size
+    assert size(C.byref(d), 3, None) == _abi.BLK_EINVAL
+    assert size(C.byref(d), 0, C.byref(need)) == _abi.BLK_EINVAL
+    assert size(C.byref(block(batch=2)), 3, C.byref(need)) == _abi.BLK_EINVAL
+    assert size(C.byref(block(d=96)), 3, C.byref(need)) == _abi.BLK_EUNSUPPORTED
+    w = _abi.BlockWeights(**{n: FAKE for n in ("attn_norm_w", "mlp_norm_w", "w_qkv", "w_o", "w_gate", "w_up",
+                                               "w_down")})
+
+    def run(d=d, w=w, cu=FAKE, prompts=3, x=FAKE, y=FAKE * 2, ws=FAKE, n=BIG, dt=1):
+        return lib.blk_forward_packed(C.byref(d), C.byref(w), cu, prompts, x, y, ws, n, dt, None)
+
+    assert run(cu=None) == _abi.BLK_EINVAL
+    assert run(cu=FAKE + 2) == _abi.BLK_EINVAL
+    assert run(prompts=0) == _abi.BLK_EINVAL
+    assert run(d=block(batch=2)) == _abi.BLK_EINVAL
+    assert run(w=_abi.BlockWeights()) == _abi.BLK_EINVAL
+    assert run(x=None) == _abi.BLK_EINVAL
+    assert run(y=FAKE) == _abi.BLK_EINVAL                      # y aliases x
+    assert run(dt=5) == _abi.BLK_EINVAL
+    assert run(n=dense.value - 1) == _abi.BLK_EWORKSPACE
+    assert run(ws=None) == _abi.BLK_EWORKSPACE
