@@ -12,14 +12,15 @@ namespace {
 // ---- packed prompts: the work list -----------------------------------
 // The prompts' lengths are device data, so the list of work units is built on
 // the device: a short one by every CTA of the attention kernel for itself
-// (attn_plan.cuh), a long one by one block ahead of it: unit l of a prompt of n units attends to about l
-// key tiles more than unit 0, so a counting sort by l (in kPlanBins bins of
-// 2^shift units), largest first, orders the units heaviest first, as the
-// dense kernels order theirs. The order within a bin is whatever the shared
-// atomics give; every unit is computed alike wherever it stands, so results
-// do not depend on it. A table that is not nondecreasing within [0, tokens]
-// (it cannot be checked on the host) has its entries clamped, and units past
-// the list's room are dropped.
+// (attn_plan.cuh), a long one by one block ahead of it. Unit l of a prompt
+// attends to about l key tiles more than unit 0, so a counting sort by l (in
+// kPlanBins bins of 2^shift units), largest first, orders the units heaviest
+// first, as the dense kernels order theirs. The order within a bin is whatever
+// the shared atomics give; every unit is computed alike wherever it stands, so
+// results do not depend on it. The table cannot be checked on the host: its
+// entries are clamped to [0, tokens] and each raised to the greatest before it,
+// so that the prompts' lengths add up to at most tokens whatever it holds, and
+// the units to at most max_units.
 constexpr int kPlanThreads = 1024, kPlanBins = 2048;
 
 __global__ void __launch_bounds__(kPlanThreads)
@@ -27,6 +28,7 @@ __global__ void __launch_bounds__(kPlanThreads)
                 int4* plan, int pdl) {
     __shared__ int at[kPlanBins];
     __shared__ int warp_sum[kPlanThreads / 32];
+    __shared__ int first_of[kPlanThreads + 1];
     if (pdl) {
         pdl_wait();
         pdl_launch_dependents();
@@ -35,13 +37,35 @@ __global__ void __launch_bounds__(kPlanThreads)
     at[t] = 0;
     at[t + kPlanThreads] = 0;
     __syncthreads();
-    // one warp per prompt, one lane per unit
+    // the table in pieces of kPlanThreads prompts; of a piece one warp per
+    // prompt, one lane per unit
     auto each_unit = [&](auto&& f) {
-        for (int b = warp; b < prompts; b += kPlanThreads / 32) {
-            const int first = min(max(cu[b], 0), tokens);
-            const int len = min(max(cu[b + 1], first), tokens) - first;
-            const int n = len / unit + (len % unit != 0);
-            for (int l = lane; l < n; l += 32) f(first, len, l);
+        int before = 0;  // the greatest entry ahead of the piece
+        for (int base = 0; base < prompts; base += kPlanThreads) {
+            const int e = base + t;
+            int v = e <= prompts ? min(max(cu[e], 0), tokens) : 0;
+            const int behind = base + kPlanThreads <= prompts && t == kPlanThreads - 1
+                                   ? min(max(cu[base + kPlanThreads], 0), tokens)
+                                   : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v = max(v, u);
+            }
+            if (lane == 31) warp_sum[warp] = v;
+            __syncthreads();
+            v = max(max(v, before), __reduce_max_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0));
+            first_of[t] = v;
+            if (t == kPlanThreads - 1) first_of[kPlanThreads] = max(v, behind);
+            __syncthreads();
+            const int n_here = min(prompts - base, kPlanThreads);
+            for (int i = warp; i < n_here; i += kPlanThreads / 32) {
+                const int first = first_of[i], len = first_of[i + 1] - first;
+                const int n = len / unit + (len % unit != 0);
+                for (int l = lane; l < n; l += 32) f(first, len, l);
+            }
+            before = first_of[kPlanThreads - 1];
+            __syncthreads();
         }
     };
     each_unit([&](int, int, int l) { atomicAdd(&at[l >> shift], 1); });

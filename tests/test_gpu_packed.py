@@ -93,6 +93,9 @@ CASES = [
     (8, 2, 160, LENS, 0, False, "bf16"),
     (4, 1, 160, [200, 129, 1, 0, 64], 129, True, "fp16"),
     (2, 2, 160, [1, 260], 0, False, "fp16"),
+    (3, 1, 128, [45, 300, 0, 81], 5, True, "fp16"),
+    (5, 1, 160, [25, 24, 23, 150], 7, False, "bf16"),     # 24 positions a unit
+    (22, 1, 160, [9, 8, 0, 140], 130, True, "bf16"),      # 16 + 6 heads a group
 ]
 
 
@@ -207,6 +210,39 @@ def test_table_is_clamped():
     o = blk.attn_prefill_packed(*args, table([0, 300, 5, 5]))  # 300 > 5: an empty prompt
     blk.check_device_status()
     assert torch.equal(o, blk.attn_prefill_packed(*args, table([0, 300])))
+
+
+@pytest.mark.parametrize("prompts", [700, 5000])
+def test_long_table_that_overlaps(prompts):
+    """A long table that goes up and down between the ends, as if every other
+    prompt had all rows, makes no more work than the rows have: the list, in the
+    workspace, takes each entry as at least the greatest before it."""
+    T = 520
+    q, k, v, _, _ = inputs(2, 2, T, 64, 0, "bf16", 4)
+    args = to_dev(q), to_dev(k), to_dev(v)
+    bad = [(0, T, 0, 2 * T, -T)[i % 5] for i in range(prompts + 1)]
+    out = torch.full((T, 2, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    blk.attn_prefill_packed(*args, table(bad), out=out)
+    blk.check_device_status()
+    assert torch.equal(out, blk.attn_prefill_packed(*args, table([0, T])))
+    # and rising entries between falling ones: 0, 100, 50, 300, 200, 300, ...
+    want = blk.attn_prefill_packed(*args, table([0, 100, 300]), out=torch.full_like(out, 3.0))
+    got = blk.attn_prefill_packed(*args, table([0, 100, 50] + [300, 200] * (prompts // 2)),
+                                  out=torch.full_like(out, 3.0))
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("n", [1023, 1024, 1025, 2049])
+def test_list_in_pieces(n):
+    """Tables whose prompts end at and around the pieces the list is made of."""
+    lens = [1 + (i % 3 == 0) for i in range(n - 1)] + [260]
+    cu = ends(lens)
+    q, k, v, _, _ = inputs(1, 1, cu[-1], 64, 0, "fp16", 9)
+    o = blk.attn_prefill_packed(to_dev(q), to_dev(k), to_dev(v), table(cu))
+    assert torch.equal(o[0], to_dev(v)[0, :1])   # one visible key: its value row
+    for i in (1, 2, 1021, 1022, 1023, 1024, n - 2, n - 1):
+        if i < n:
+            check_rows(o[cu[i]:cu[i + 1]], reference(q, k, v, cu[i], lens[i]), "fp16", f"prompt {i}")
 
 
 @pytest.mark.parametrize("prompts", [255, 700])

@@ -70,6 +70,8 @@ CASES = [
     (3, 4, 1, 128, 0, 100, [100, 0, 1], True, "bf16"),                       # no prefix
     (2, 32, 8, 128, 20000, 64, [64, 1], False, "bf16"),
     (1, 6, 6, 64, 700, 10, [4], True, "bf16"),                               # given slopes
+    (1500, 2, 2, 64, 40, 3, [i % 4 for i in range(1500)], False, "bf16"),    # many sequences, some away
+    (1100, 8, 1, 128, 0, 2, [i % 3 for i in range(1100)], True, "fp16"),
 ]
 
 
