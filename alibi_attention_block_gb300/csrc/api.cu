@@ -723,6 +723,9 @@ blk_packed_desc packed_block_attn(const blk_block_desc* d, int64_t prompts) {
 blk_status validate_packed_block(const blk_block_desc* d, int64_t prompts) {
     BLK_REQUIRE(d, "descriptor is NULL");
     BLK_REQUIRE(d->qkv.batch == 1, "packed prompts are one batch entry: batch must be 1");
+    // the rotary turns by the packed row, in 32-bit floats
+    BLK_REQUIRE(d->qkv.rotary_span == 0 || d->qkv.seq <= (int64_t(1) << 24),
+                "a rotary block takes up to 2^24 packed rows");
     const blk_packed_desc pd = packed_block_attn(d, prompts);
     return validate_packed_desc(&pd);
 }

@@ -400,8 +400,9 @@ blk_status blk_forward(const blk_block_desc* d, const blk_block_weights* w, cons
  * [prompts + 1], as for blk_attn_prefill_packed). Every step but the attention
  * works row by row; the rotary turns by the packed row, which leaves the
  * scores within a prompt what they are (they depend on position differences
- * only). Rows of y outside every prompt hold unspecified values. The
- * workspace has at least blk_forward_packed_workspace_size bytes. Errors as
+ * only); a rotary block takes up to 2^24 rows. Rows of y outside every prompt
+ * hold unspecified values. The workspace has at least
+ * blk_forward_packed_workspace_size bytes. Errors as
  * blk_forward and blk_attn_prefill_packed. */
 blk_status blk_forward_packed_workspace_size(const blk_block_desc* d, int64_t prompts,
                                              size_t* bytes);

@@ -127,8 +127,8 @@ def test_shared_argument_refusals(lib):
 
 # -------------------------------------------------- blk_forward_packed --
 
-def block(batch=1, seq=500, H=4, Hk=4, d=64):
-    q = _abi.QkvDesc(batch, seq, 256, H, Hk, d, _abi.BLK_QKV_STACKED, _abi.BLK_QKNORM_NONE, 1e-5, 16, 1e4)
+def block(batch=1, seq=500, H=4, Hk=4, d=64, span=16):
+    q = _abi.QkvDesc(batch, seq, 256, H, Hk, d, _abi.BLK_QKV_STACKED, _abi.BLK_QKNORM_NONE, 1e-5, span, 1e4)
     return _abi.BlockDesc(q, _abi.BLK_NORM_LAYERNORM, _abi.BLK_NORM_PRE, _abi.BLK_RESIDUAL_SEQUENTIAL,
                           1e-5, 0, 688, _abi.BLK_ACT_SWIGLU)
 
@@ -145,6 +145,10 @@ def test_forward_packed_refusals(lib):
     assert size(C.byref(d), 0, C.byref(need)) == _abi.BLK_EINVAL
     assert size(C.byref(block(batch=2)), 3, C.byref(need)) == _abi.BLK_EINVAL
     assert size(C.byref(block(d=96)), 3, C.byref(need)) == _abi.BLK_EUNSUPPORTED
+    # positions of a rotary are held in 32-bit floats
+    assert size(C.byref(block(seq=2**24)), 3, C.byref(need)) == _abi.BLK_OK
+    assert size(C.byref(block(seq=2**24 + 1)), 3, C.byref(need)) == _abi.BLK_EINVAL
+    assert size(C.byref(block(seq=2**24 + 1, span=0)), 3, C.byref(need)) == _abi.BLK_OK
     w = _abi.BlockWeights(**{n: FAKE for n in ("attn_norm_w", "mlp_norm_w", "w_qkv", "w_o", "w_gate", "w_up",
                                                "w_down")})
 
