@@ -134,14 +134,16 @@ struct GqaCursor {
         nkv = (last + kTK - 1) / kTK;
     }
     __device__ __forceinline__ void start(const AttnArgs& a, const GqaPack& pk,
-                                          const AttnPack<PACKED>& pack, const Plan& plan, int nblk, int n_items) {
+                                         const AttnPack<PACKED>& pack, const Plan& plan, int nblk,
+                                         int n_items) {
         it = 0;
         item = item_of(0);
         valid = item < n_items;
         if (valid) decode(a, pk, pack, plan, nblk);
     }
     __device__ __forceinline__ void next(const AttnArgs& a, const GqaPack& pk,
-                                          const AttnPack<PACKED>& pack, const Plan& plan, int nblk, int n_items) {
+                                         const AttnPack<PACKED>& pack, const Plan& plan, int nblk,
+                                         int n_items) {
         ++it;
         item = item_of(it);
         valid = item < n_items;

@@ -101,7 +101,11 @@ struct PairCfg {
 // nP prefix tiles come ahead of its own key tiles. A prompt's tiles are paired
 // from its end, so that where their number is odd the single one is the first,
 // which has one key tile, and not the last, which has all (17 tiles: 81 steps for
-// 89).
+// 89). 32 x 64 heads: two prompts of 8192 and 5330 tokens 387 us, 1.01 PFLOP/s (the
+// dense kernel 1.04 at S = 8192); eight of 1273 on average 100 us, 0.65. As there, each
+// query tile's chain of scores, softmax and product is the bound. Shortening it did
+// not pay: a row's softmax in two halves on 16 warps, with an exchange of the maxima,
+// 487 us; P handed over in two halves of the tile, 397.
 template <bool PACKED>
 struct PairCursor {
     using Plan = typename PlanStorage<PACKED>::type;
@@ -114,8 +118,8 @@ struct PairCursor {
         const int G = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
         return round * G + ((round & 1) ? G - 1 - c : c);
     }
-    __device__ __forceinline__ void decode(const AttnArgs& a, const AttnPack<PACKED>& pack, const Plan& plan, int nq,
-                                           int np) {
+    __device__ __forceinline__ void decode(const AttnArgs& a, const AttnPack<PACKED>& pack,
+                                           const Plan& plan, int nq, int np) {
         if constexpr (PACKED) {
             const PlanUnit u = plan_unit(pack, plan, item / a.H);
             h = item % a.H;
@@ -141,15 +145,15 @@ struct PairCursor {
         nA = 2 * i + 1;                          // key tiles of query tile 2i
         nB = (2 * i + 1 < nq) ? 2 * i + 2 : 0;   // of query tile 2i+1, if present
     }
-    __device__ __forceinline__ void start(const AttnArgs& a, const AttnPack<PACKED>& pack, const Plan& plan, int nq, int np,
-                                          int n_items) {
+    __device__ __forceinline__ void start(const AttnArgs& a, const AttnPack<PACKED>& pack,
+                                         const Plan& plan, int nq, int np, int n_items) {
         it = 0;
         item = item_of(0);
         valid = item < n_items;
         if (valid) decode(a, pack, plan, nq, np);
     }
-    __device__ __forceinline__ void next(const AttnArgs& a, const AttnPack<PACKED>& pack, const Plan& plan, int nq, int np,
-                                          int n_items) {
+    __device__ __forceinline__ void next(const AttnArgs& a, const AttnPack<PACKED>& pack,
+                                         const Plan& plan, int nq, int np, int n_items) {
         ++it;
         item = item_of(it);
         valid = item < n_items;

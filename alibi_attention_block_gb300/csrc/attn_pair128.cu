@@ -83,8 +83,8 @@ struct PairCursor {
         const int G = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
         return round * G + ((round & 1) ? G - 1 - c : c);
     }
-    __device__ __forceinline__ void decode(const AttnArgs& a, const AttnPack<PACKED>& pack, const Plan& plan, int nq,
-                                           int np) {
+    __device__ __forceinline__ void decode(const AttnArgs& a, const AttnPack<PACKED>& pack,
+                                           const Plan& plan, int nq, int np) {
         if constexpr (PACKED) {
             const int per_unit = a.Hk * pack.nhc;
             const PlanUnit u = plan_unit(pack, plan, item / per_unit);
@@ -115,15 +115,15 @@ struct PairCursor {
         nA = 2 * i + 1;
         nB = (2 * i + 1 < nq) ? 2 * i + 2 : 0;
     }
-    __device__ __forceinline__ void start(const AttnArgs& a, const AttnPack<PACKED>& pack, const Plan& plan, int nq, int np,
-                                          int n_items) {
+    __device__ __forceinline__ void start(const AttnArgs& a, const AttnPack<PACKED>& pack,
+                                         const Plan& plan, int nq, int np, int n_items) {
         it = 0;
         item = item_of(0);
         valid = item < n_items;
         if (valid) decode(a, pack, plan, nq, np);
     }
-    __device__ __forceinline__ void next(const AttnArgs& a, const AttnPack<PACKED>& pack, const Plan& plan, int nq, int np,
-                                          int n_items) {
+    __device__ __forceinline__ void next(const AttnArgs& a, const AttnPack<PACKED>& pack,
+                                         const Plan& plan, int nq, int np, int n_items) {
         ++it;
         item = item_of(it);
         valid = item < n_items;

@@ -12,12 +12,12 @@ struct PlanUnit {
     int first, len, l;
 };
 
-// A small list is built by each CTA: the table's entries are in L2, and a
-// kernel that only builds the list costs 2.6 us, its launch and a workspace (a
-// call with 16 chat turns: 28 us with it, 15 without). Every CTA has to come to the same order, so no atomics:
-// prompts are ranked by their number of units (ties by index), and unit l of
-// the prompt of rank r comes behind all units above l, at place r among those
-// of level l.
+// A small list is built by each CTA: the table's entries are in L2, and a kernel
+// that only builds the list costs 2.6 us, its launch and a workspace (a call with
+// 16 chat turns: 28 us with it, 15 without). Every CTA has to come to the same
+// order, so no atomics: prompts are ranked by their number of units (ties by
+// index), and unit l of the prompt of rank r comes behind all units above l, at
+// place r among those of level l.
 struct PlanSmem {
     int first[kPlanCtaPrompts], len[kPlanCtaPrompts];
     int n[kPlanCtaPrompts], sorted_n[kPlanCtaPrompts];

@@ -38,7 +38,7 @@ struct CombineArgs {
 };
 
 // The CTA whose range [c * W / n, (c + 1) * W / n) holds tile t, n CTAs in all
-// (at most 512, W >= n): c * W < (t + 1) * n <= (c + 1) * W, from an estimate
+// (at most kSharedMaxGrid, W >= n): c * W < (t + 1) * n <= (c + 1) * W, from an estimate
 // in floating point that is off by one at most.
 __device__ __forceinline__ int cta_of(int64_t t, int64_t W, int n) {
     const int64_t x = (t + 1) * n;

@@ -38,12 +38,19 @@
 // result (max, sum, O) of its own. There are two CTAs per SM, so that one's
 // chain of scores, softmax and product fills the other's gaps; each does its
 // prefix range and then its own caches' range, whose loads begin as the
-// prefix's last tiles are consumed (in launches of their own,
-// 32 x 32 x 64 heads with 8192 shared and 279 own keys: 37.9 us, so 34.9; with one CTA of
-// an SM on the prefix and the other on the own caches the softmax of the prefix
-// took three times as long, and the whole half as long again).
+// prefix's last tiles are consumed (32 sequences of 32 x 64 heads, 8192 shared
+// and 279 own keys: in launches of their own 37.9 us, in one 34.9, 32.4 with the
+// ranges found beside the first loads; with one CTA of an SM on the prefix and
+// the other on the own caches the softmax of the prefix took three times as
+// long, and the whole half as long again).
 // Tiles go from the newest key down (with ALiBi the bias is largest there, so
 // the rescale of O stays rare).
+// Measured and bound: the bytes where rows are few (16 sequences of 16 x 128 heads,
+// 32771 shared keys: 67.2 us, 6.3 TB/s, 0.93 of the copy rate); else the tensor cores'
+// chain of scores, softmax and product per tile, and both parts' fixed ends: 64
+// sequences of 32/8 x 128 heads, 16384 shared keys, 44.8 us for 27.6 of bytes and
+// 9.4 of products. Tiles of 64 keys with two S buffers at head_dim 128, so that the
+// next scores come beside the softmax: 45.9; the SM's other CTA fills that gap.
 // 6 warps: TMA; MMA issue; four of softmax.
 #pragma once
 
