@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(gqa_threads(PACKED), 1)
         pdl_launch_dependents();
     }
     if constexpr (PACKED) {
-        if (!pack.plan) build_plan(plan, pack.cu_seqlens, pack.prompts, a.S, pk.R);
+        if (!pack.plan) build_plan(plan, pack.cu_seqlens, pack.prompts, a.S, pk.R, 0);
         n_items = plan_units(pack, plan) * a.Hk * pk.nhc;
     }
 

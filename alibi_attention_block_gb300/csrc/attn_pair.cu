@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         pdl_launch_dependents();
     }
     if constexpr (PACKED) {
-        if (!pack.plan) build_plan(plan, pack.cu_seqlens, pack.prompts, a.S, 2 * kTQ);
+        if (!pack.plan) build_plan(plan, pack.cu_seqlens, pack.prompts, a.S, 2 * kTQ, kTQ);
         n_items = plan_units(pack, plan) * a.H;
     }
     // registers: the launch gives every thread kLaunchRegs; warpgroup 0 (TMA,

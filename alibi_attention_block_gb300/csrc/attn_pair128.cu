@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kP128Threads, 1)
         pdl_launch_dependents();
     }
     if constexpr (PACKED) {
-        if (!pack.plan) build_plan(plan, pack.cu_seqlens, pack.prompts, a.S, 2 * pack.R);
+        if (!pack.plan) build_plan(plan, pack.cu_seqlens, pack.prompts, a.S, 2 * pack.R, pack.R);
         n_items = plan_units(pack, plan) * a.Hk * pack.nhc;
     }
     static_assert(4 * kRegsControl + 8 * kRegsSoftmax <= 12 * kLaunchRegs,
