@@ -3,6 +3,9 @@
 //   head_dim 128, MHA      attn_pair128.cu  (two query tiles, shared S buffer)
 //   head_dim 128, GQA      attn_gqa.cu      (the group's query heads packed
 //   head_dim 160, any      attn_gqa.cu       into one 128-row tile)
+// Packed prompts: head_dim 64 as above; 128 and 160 two query tiles of packed
+// heads (attn_pair128.cu, attn_pair160.cu), or one where ALiBi meets grouped heads
+// (attn_gqa.cu).
 #include "internal.h"
 
 namespace blk {
@@ -104,7 +107,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 
 // a query-tile pair per item, or one tile (attn_gqa.cu)
 bool packed_pairs(int H, int Hk, int d, bool alibi) {
-    return d == 64 || (d == 128 && (H == Hk || !alibi));
+    return d == 64 || H == Hk || !alibi;
 }
 // positions per unit
 int packed_unit(int H, int Hk, int d, bool alibi) {
@@ -141,9 +144,11 @@ cudaError_t launch_attention_packed(DType dt, const AttnArgs& a, const PackedArg
     const void* kp = p.prefix ? p.k_prefix : a.k;
     const void* vp = p.prefix ? p.v_prefix : a.v;
     const uint64_t rows = p.prefix ? p.prefix : a.S;
-    if (!make_tmap_3d(&pack.tmPK, dt, kp, a.Hk, rows, a.d, 128) ||
-        !make_tmap_3d(&pack.tmPK2, dt, kp, a.Hk, rows, a.d, 128, 32) ||
-        !make_tmap_3d(&pack.tmPV, dt, vp, a.Hk, rows, a.d, 128))
+    const bool pair160 = a.d == 160 && packed_pairs(a.H, a.Hk, a.d, a.alibi != 0);
+    const uint32_t tile = pair160 ? 64 : 128;  // keys per tile
+    if (!make_tmap_3d(&pack.tmPK, dt, kp, a.Hk, rows, a.d, tile) ||
+        !make_tmap_3d(&pack.tmPK2, dt, kp, a.Hk, rows, a.d, tile, 32) ||
+        !make_tmap_3d(&pack.tmPV, dt, vp, a.Hk, rows, a.d, tile))
         return cudaErrorInvalidValue;
     if (listed) {
         const bool pdl = pdl_allowed(s);
@@ -153,6 +158,7 @@ cudaError_t launch_attention_packed(DType dt, const AttnArgs& a, const PackedArg
         if (e != cudaSuccess) return e;
     }
     if (a.d == 64) return launch_attention_pair64_packed(dt, a, pack, max_units, s);
+    if (pair160) return launch_attention_pair160_packed(dt, a, pack, max_units, s);
     if (packed_pairs(a.H, a.Hk, a.d, a.alibi != 0))
         return launch_attention_pair128_packed(dt, a, pack, max_units, s);
     return launch_attention_gqa_packed(dt, a, pack, max_units, s);

@@ -65,8 +65,8 @@ struct GqaCfg {
     // descriptor for the whole row). Q and K tiles keep only the 32 columns of
     // head_dim 160's last slice, as a slice of 64-byte rows with the 64-byte
     // swizzle: what that saves makes room for a second V stage (with one, the
-    // next V was loaded only after the PV product; six packed prompts of 654
-    // tokens, 32/8 heads: 83.0 -> 74.7 us).
+    // next V was loaded only after the PV product; B2 S4096, 32/8 heads: 333 -> 308
+    // us).
     static constexpr bool kHalf = D % 64 != 0;
     static constexpr int kFull = D / 64;                 // whole slices
     static constexpr int kTileBytes = kSub * 128 * 128;
@@ -92,7 +92,8 @@ struct GqaPack {
 // This CTA's items: (position block pb, batch b, kv head g, head chunk hc).
 // Round r gives item r*Gd + blockIdx on even rounds and r*Gd + Gd-1-blockIdx
 // on odd ones (Gd = grid size); items are numbered latest block first.
-// Packed prompts (PACKED): a unit of the plan's list is a block of R
+// Packed prompts (PACKED; with ALiBi over grouped heads, a slope per row, as
+// attn_pair128.cu and attn_pair160.cu take the others): a unit is a block of R
 // positions of one prompt; the prefix's nP key tiles come ahead of the
 // prompt's own.
 template <bool PACKED>
@@ -653,8 +654,9 @@ cudaError_t launch_gqa_d(DType dt, const AttnArgs& a, const GqaPack& pk,
 template <typename T, int D, bool PACKED>
 cudaError_t launch_gqa_a(DType dt, const AttnArgs& a, const GqaPack& pk,
                          const AttnPack<PACKED>& pack, int64_t items, cudaStream_t s) {
-    return a.alibi ? launch_gqa_d<T, D, true>(dt, a, pk, pack, items, s)
-                   : launch_gqa_d<T, D, false>(dt, a, pk, pack, items, s);
+    if constexpr (!PACKED)  // packed prompts come here with ALiBi only
+        if (!a.alibi) return launch_gqa_d<T, D, false>(dt, a, pk, pack, items, s);
+    return launch_gqa_d<T, D, true>(dt, a, pk, pack, items, s);
 }
 
 template <bool PACKED>
@@ -696,7 +698,7 @@ cudaError_t launch_attention_gqa(DType dt, const AttnArgs& a, cudaStream_t s) {
 
 cudaError_t launch_attention_gqa_packed(DType dt, const AttnArgs& a, const AttnPack<true>& pack,
                                         int64_t max_units, cudaStream_t s) {
-    if (a.Hk <= 0 || a.H % a.Hk || (a.d != 128 && a.d != 160)) return cudaErrorInvalidValue;
+    if (a.Hk <= 0 || a.H % a.Hk || (a.d != 128 && a.d != 160) || !a.alibi) return cudaErrorInvalidValue;
     const GqaPack pk = gqa_pack(a.H, a.Hk);
     return launch_gqa(dt, a, pk, pack, max_units * a.Hk * pk.nhc, s);
 }

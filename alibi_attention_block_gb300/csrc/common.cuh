@@ -245,6 +245,21 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+// Whether two phases have completed: one round trip to shared memory for both.
+__device__ __forceinline__ bool mbar_test2(uint32_t bar0, uint32_t parity0, uint32_t bar1,
+                                           uint32_t parity1) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+        "and.pred p, p, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar0), "r"(parity0), "r"(bar1), "r"(parity1)
+        : "memory");
+    return ok != 0;
+}
 // Slow path of mbar_wait: keep trying until limit_ns has passed.
 static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, unsigned* err,
                                                    unsigned long long limit_ns = kWaitLimitNs) {
@@ -274,6 +289,12 @@ __device__ __forceinline__ bool mbar_wait_inl(uint32_t bar, uint32_t parity, uns
 // Wait for the phase with the given parity to complete. Gives up after
 // kWaitLimitNs: sets the error word and returns false. The first try is
 // inline so a completed phase costs one instruction.
+// Waits for two phases.
+__device__ __forceinline__ bool mbar_wait2_inl(uint32_t bar0, uint32_t parity0, uint32_t bar1,
+                                               uint32_t parity1, unsigned* err) {
+    if (mbar_test2(bar0, parity0, bar1, parity1)) return true;
+    return mbar_wait_inl(bar0, parity0, err) && mbar_wait_inl(bar1, parity1, err);
+}
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, unsigned* err) {
     if (mbar_try_wait(bar, parity)) return true;
     return mbar_wait_slow(bar, parity, err);

@@ -147,7 +147,7 @@ struct AttnPack<true> {
     const int4* plan;           // or nullptr: each CTA builds its own (attn_plan.cuh)
     const int32_t* cu_seqlens;
     int prompts, prefix;
-    int G, Gt, R, nhc;          // gqa_tile (attn_pair128.cu)
+    int G, Gt, R, nhc;          // gqa_tile (attn_pair128.cu, attn_pair160.cu)
 };
 // up to these sizes the list is built by each CTA, without a workspace
 constexpr int kPlanCtaPrompts = 256, kPlanCtaUnits = 1024;
@@ -167,6 +167,8 @@ cudaError_t launch_attention_packed(DType dt, const AttnArgs& a, const PackedArg
 cudaError_t launch_attention_pair64_packed(DType dt, const AttnArgs& a, const AttnPack<true>& pack,
                                            int64_t max_units, cudaStream_t s);
 cudaError_t launch_attention_pair128_packed(DType dt, const AttnArgs& a, const AttnPack<true>& pack,
+                                            int64_t max_units, cudaStream_t s);
+cudaError_t launch_attention_pair160_packed(DType dt, const AttnArgs& a, const AttnPack<true>& pack,
                                             int64_t max_units, cudaStream_t s);
 cudaError_t launch_attention_gqa_packed(DType dt, const AttnArgs& a, const AttnPack<true>& pack,
                                         int64_t max_units, cudaStream_t s);

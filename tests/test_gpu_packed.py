@@ -135,14 +135,20 @@ def test_packed_matches_oracle(case):
 
 @pytest.mark.parametrize("H,Hk,d", [(2, 2, 64), (2, 2, 128), (4, 1, 128), (4, 2, 160)])
 def test_equal_lengths_equal_the_dense_kernel(H, Hk, d):
-    """Prompts of one length are blk_attn_prefill's batch, bit for bit (the
-    same products in the same order)."""
+    """Prompts of one length are blk_attn_prefill's batch: at head_dim 64 bit for
+    bit (the same products in the same order); above, where the packed kernel's
+    key tiles are narrower, to the roundings of P and o on either side."""
     B, S = 3, 333
     q, k, v, _, _ = inputs(H, Hk, B * S, d, 0, "bf16", 71)
     qd, kd, vd = to_dev(q), to_dev(k), to_dev(v)
     o = blk.attn_prefill_packed(qd, kd, vd, table(ends([S] * B)))
     dense = blk.attn_prefill(*(t.view(t.shape[0], B, S, d).transpose(0, 1).contiguous() for t in (qd, kd, vd)))
-    assert torch.equal(o.view(B, S, H, d), dense)
+    if d == 64:
+        assert torch.equal(o.view(B, S, H, d), dense)
+    for b in range(B):
+        ref = reference(q, k, v, b * S, S)
+        check_rows(o[b * S:(b + 1) * S], ref, "bf16", f"packed, prompt {b}")
+        check_rows(dense[b], ref, "bf16", f"dense, prompt {b}")
 
 
 @pytest.mark.parametrize("H,Hk,d,P", [(2, 2, 64, 0), (2, 2, 128, 70), (4, 1, 128, 0), (4, 1, 160, 300)])

@@ -27,7 +27,7 @@ def call(lib, d, q=FAKE, k=FAKE, v=FAKE, kp=None, vp=None, cu=FAKE, slopes=None,
 
 @pytest.mark.parametrize("H,Hk,d,alibi,unit", [
     (32, 32, 64, 0, 256), (8, 2, 64, 1, 256), (16, 16, 128, 1, 256), (32, 8, 128, 0, 64),
-    (32, 8, 128, 1, 32), (32, 8, 160, 0, 32), (6, 2, 128, 0, 80), (32, 1, 160, 1, 8), (2, 2, 160, 0, 128)])
+    (32, 8, 128, 1, 32), (32, 8, 160, 0, 64), (6, 2, 128, 0, 80), (32, 1, 160, 1, 8), (2, 2, 160, 0, 256), (2, 2, 160, 1, 256), (32, 8, 160, 1, 32)])
 def test_workspace_size(lib, H, Hk, d, alibi, unit):
     """Nothing up to 256 prompts and 1024 units; above, one 16-byte entry for
     each unit that the prompts can have at most, and one for their count, in
