@@ -322,9 +322,9 @@ def attn_decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, lens, alibi=Fals
     qp, kpp, vpp, kp, vp, op = _pointers(q.dtype, dev, q, k_prefix, v_prefix, k_cache, v_cache, out)
     (lp,) = _pointers(torch.int32, dev, lens)
     sp = None if slopes is None else _pointers(torch.float32, dev, slopes)[0]
-    if workspace is None:
+    if workspace is None and need:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    wp, wn = _workspace(workspace, dev)
+    wp, wn = (None, 0) if workspace is None else _workspace(workspace, dev)
     o = out
     if o is None:
         o = torch.empty_like(q)

@@ -951,7 +951,11 @@ static blk_status validate_shared_desc(const blk_decode_shared_desc* d) {
     return BLK_OK;
 }
 
+static bool shared_is_small(const blk_decode_shared_desc* d) {
+    return shared_small(d->batch, d->n_heads, d->head_dim, d->prefix_len, d->max_seq);
+}
 static size_t shared_ws_bytes(const blk_decode_shared_desc* d) {
+    if (shared_is_small(d)) return 0;
     return static_cast<size_t>(shared_layout(d->batch, d->n_heads, d->n_kv_heads, d->head_dim,
                                              d->prefix_len).total);
 }
@@ -988,7 +992,7 @@ blk_status blk_attn_decode_shared(const blk_decode_shared_desc* d, const void* q
     BLK_REQUIRE(!alibi_slopes || (reinterpret_cast<uintptr_t>(alibi_slopes) & 3u) == 0,
                 "alibi_slopes must be 4-byte aligned");
     const size_t need = shared_ws_bytes(d);
-    if (!workspace || ws_bytes < need || !aligned16(workspace))
+    if (need && (!workspace || ws_bytes < need || !aligned16(workspace)))
         return fail(BLK_EWORKSPACE, "workspace needs %zu bytes, 16-byte aligned", need);
     DevState* ds = nullptr;
     if ((st = dev_state(&ds)) != BLK_OK) return st;
@@ -1013,8 +1017,9 @@ blk_status blk_attn_decode_shared(const blk_decode_shared_desc* d, const void* q
     a.ws = static_cast<uint8_t*>(workspace);
     a.err = ds->err;
     a.num_sms = ds->sms;
-    const cudaError_t e =
-        launch_attention_decode_shared(to_dt(dt), a, reinterpret_cast<cudaStream_t>(s));
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(s);
+    const cudaError_t e = shared_is_small(d) ? launch_attention_decode_shared_small(to_dt(dt), a, cs)
+                                             : launch_attention_decode_shared(to_dt(dt), a, cs);
     return e == cudaSuccess ? BLK_OK : cuda_fail(e, "shared-prefix decode attention launch");
 }
 

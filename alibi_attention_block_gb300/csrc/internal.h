@@ -250,6 +250,12 @@ cudaError_t launch_shared_bf16(int d, const SharedMaps& tm, const SharedKernelAr
 // (kv head, row tile, key tile) triples of the prefix pass
 int64_t shared_tiles(int64_t B, int64_t H, int64_t Hk, int64_t P);
 cudaError_t launch_attention_decode_shared(DType dt, const SharedArgs& s, cudaStream_t st);
+// few keys (attn_shared_small.cu), at most: (prefix_len + max_seq) * head_dim, blocks
+// (sequences * query heads), and their product
+constexpr int64_t kSharedSmallDims = 49152, kSharedSmallBlocks = 304,
+                  kSharedSmallWork = int64_t(7) << 20;
+bool shared_small(int64_t B, int64_t H, int64_t d, int64_t P, int64_t S_max);
+cudaError_t launch_attention_decode_shared_small(DType dt, const SharedArgs& s, cudaStream_t st);
 
 // ---- per-device state and error reporting shared with other entry points (api.cu)
 // SM count and device error word of the current device (set up on first use).

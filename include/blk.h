@@ -262,8 +262,9 @@ typedef struct {
  *     in front of each sequence's cache
  * GQA: kv head = h / (H / Hk), H / Hk in {1, 2, 4, 8}; head_dim 64 or 128.
  * The workspace holds partial results, at least
- * blk_attn_decode_shared_workspace_size bytes, 16-byte aligned; calls whose
- * kernels overlap on the GPU need a workspace each. */
+ * blk_attn_decode_shared_workspace_size bytes, 16-byte aligned (0 bytes, at a few
+ * hundred keys: none is needed, NULL will do); calls whose kernels overlap on the
+ * GPU need a workspace each. */
 blk_status blk_attn_decode_shared_workspace_size(const blk_decode_shared_desc* d, size_t* bytes);
 blk_status blk_attn_decode_shared(const blk_decode_shared_desc* d, const void* q,
                                   const void* k_prefix, const void* v_prefix, const void* k_cache,

@@ -75,12 +75,25 @@ CASES = [
 ]
 
 
+ROOM = 800  # more capacity than the kernel for few keys takes, at any head_dim
+
+
+def test_room_chooses_the_kernel():
+    """Few keys need no workspace; the same with ROOM more capacity do."""
+    for d in (64, 128):
+        assert blk.attn_decode_shared_workspace_size(blk.decode_shared_desc(2, 20, 4, 2, d, 100)) == 0
+        assert blk.attn_decode_shared_workspace_size(blk.decode_shared_desc(2, 20 + ROOM, 4, 2, d, 0)) > 0
+
+
+@pytest.mark.parametrize("room", [0, ROOM])
 @pytest.mark.parametrize("case", CASES, ids=lambda c: "B{}H{}Hk{}d{}P{}S{}{}_{}".format(
     *c[:6], "_alibi" if c[7] else "", c[8]))
-def test_shared_matches_oracle(case):
+def test_shared_matches_oracle(case, room):
+    """With capacity to spare, every case goes to the kernel for many keys."""
     B, H, Hk, d, P, S, lens, alibi, dt = case
     q, kp, vp, k, v = inputs(B, H, Hk, d, P, S, dt, 300 + B + H + d + P)
-    kd, vd = to_dev(k), to_dev(v)
+    kd, vd = (torch.zeros((B, Hk, S + room, d), dtype=t.dtype, device="cuda") for t in (k, v))
+    kd[:, :, :S], vd[:, :, :S] = to_dev(k), to_dev(v)
     for b, n in enumerate(lens):  # entries past each length are not part of the sequence
         kd[b, :, n:] = float("nan")
         vd[b, :, n:] = float("nan")
@@ -123,11 +136,11 @@ def test_own_caches_beyond_32_bit_offsets():
     check(o, q, kp, vp, k, v, lens, "bf16", name="long caches")
 
 
-@pytest.mark.parametrize("d", [64, 128])
-def test_growing_scores_rescale(d):
+@pytest.mark.parametrize("d,P", [(64, 1200), (128, 1200), (64, 600), (128, 300)])
+def test_growing_scores_rescale(d, P):
     """Scores that rise or fall along the prefix move the running maximum at
     every tile in one direction or the other."""
-    B, H, P, S = 3, 2, 1200, 40
+    B, H, S = 3, 2, 40
     q, kp, vp, k, v = inputs(B, H, H, d, P, S, "bf16", 8)
     q = torch.ones_like(q)
     for ramp in (torch.linspace(0, 3, P), torch.linspace(3, 0, P)):
@@ -156,8 +169,9 @@ def test_equals_decode_over_copied_prefix():
         check(o, q, kp, vp, k, v, lens, "bf16", oracle.alibi_slopes(H), name=f"cut at {cut}")
 
 
-def test_lengths_clamped_and_deterministic():
-    B, H, d, P, S = 3, 4, 64, 700, 32
+@pytest.mark.parametrize("P", [700, 1400])
+def test_lengths_clamped_and_deterministic(P):
+    B, H, d, S = 3, 4, 64, 32
     t = [to_dev(x) for x in inputs(B, H, H, d, P, S, "bf16", 31)]
 
     def call(lens):
@@ -202,8 +216,9 @@ def test_scale_and_workspace():
     check(o, q, kp, vp, k, v, lens, "fp16", scale=np.float32(0.2), name="scale")
 
 
-def test_graph_replay_and_other_stream():
-    B, H, Hk, d, P, S = 6, 8, 2, 128, 1000, 50
+@pytest.mark.parametrize("P", [100, 1000])
+def test_graph_replay_and_other_stream(P):
+    B, H, Hk, d, S = 6, 8, 2, 128, 50
     qd, kpd, vpd, kd, vd = (to_dev(t) for t in inputs(B, H, Hk, d, P, S, "bf16", 51))
     lens = torch.tensor([50, 1, 2, 0, 30, 7], dtype=torch.int32, device="cuda")
     ws = torch.empty(blk.attn_decode_shared_workspace_size(blk.decode_shared_desc(B, S, H, Hk, d, P)),
@@ -259,6 +274,26 @@ def test_prefill_then_decode():
     check(o, q[:, last.cpu()].transpose(0, 1), kp, vp, kc.cpu(), vc.cpu(), longer, dt, name="decode")
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("H,Hk,d,keys", [(38, 19, 64, 768), (8, 1, 64, 61), (2, 2, 128, 384), (16, 4, 128, 200),
+                                         (304, 304, 64, 30)])
+def test_few_keys(dt, H, Hk, d, keys):
+    """The kernel for few keys at its limits: batch 1 or more of many heads, a
+    prefix of all keys but one, of none, and in between."""
+    for B in (1, 3) if H <= 16 else (1,):
+        for P in (0, 1, keys // 3, keys - 1):
+            S = keys - P
+            assert blk.attn_decode_shared_workspace_size(blk.decode_shared_desc(B, S, H, Hk, d, P)) == 0
+            q, kp, vp, k, v = inputs(B, H, Hk, d, P, S, dt, 900 + P)
+            lens = [S, 1, 0][:B]
+            out = torch.full((B, H, d), 5.0, dtype=q.dtype, device="cuda")
+            ref_slopes, dev_slopes = slopes_of(H, P % 2 == 0)
+            blk.attn_decode_shared(*(None if t is None else to_dev(t) for t in (q, kp, vp, k, v)),
+                                   torch.tensor(lens, dtype=torch.int32, device="cuda"), alibi=P % 2 == 0,
+                                   slopes=dev_slopes, out=out)
+            check(out, q, kp, vp, k, v, lens, dt, ref_slopes, name=f"B {B} P {P}")
+
+
 def test_binding_refuses():
     q, kp, vp, k, v = (to_dev(t) for t in inputs(2, 4, 2, 64, 32, 16, "bf16", 71))
     n = torch.tensor([1, 2], dtype=torch.int32, device="cuda")
@@ -277,6 +312,8 @@ def test_binding_refuses():
     with pytest.raises(ValueError):
         blk.attn_decode_shared(q, kp.transpose(1, 2).contiguous().transpose(1, 2), vp, k, v, n)
     with pytest.raises(blk.BlkError):
-        blk.attn_decode_shared(q, kp, vp, k, v, n, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+        long = torch.zeros((2, 2, 16 + ROOM, 64), dtype=torch.bfloat16, device="cuda")
+        blk.attn_decode_shared(q, kp, vp, long, long, n,
+                               workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
     with pytest.raises(blk.BlkError):
         blk.attn_decode_shared(q, kp, vp, k, v, n, slopes=torch.ones(4, device="cuda"))

@@ -82,7 +82,7 @@ def test_argument_refusals(lib):
 
 # ---------------------------------------------- blk_attn_decode_shared --
 
-def shared(batch=4, max_seq=64, H=32, Hk=8, d=128, prefix=100, scale=-1.0, alibi=0):
+def shared(batch=4, max_seq=64, H=32, Hk=8, d=128, prefix=1000, scale=-1.0, alibi=0):
     return _abi.DecodeSharedDesc(batch, max_seq, H, Hk, d, prefix, scale, alibi)
 
 
@@ -123,6 +123,19 @@ def test_shared_argument_refusals(lib):
     assert step(lib, d, ws=None) == _abi.BLK_EWORKSPACE
     assert step(lib, d, ws=FAKE + 8) == _abi.BLK_EWORKSPACE
     assert step(lib, d, n=need.value - 1) == _abi.BLK_EWORKSPACE
+
+
+@pytest.mark.parametrize("few,many", [
+    (dict(prefix=300, max_seq=84), dict(prefix=300, max_seq=85)),                    # 384 keys of 128
+    (dict(d=64, Hk=32, prefix=0, max_seq=768, batch=1), dict(d=64, Hk=32, prefix=1, max_seq=768, batch=1)),
+    (dict(batch=19, H=16, Hk=16, prefix=20, max_seq=1), dict(batch=20, H=16, Hk=16, prefix=20, max_seq=1)),
+    (dict(batch=9, prefix=100, max_seq=99), dict(batch=9, prefix=100, max_seq=100)),  # 288 blocks
+])
+def test_shared_small_needs_no_workspace(lib, few, many):
+    need = C.c_size_t(1)
+    size = lib.blk_attn_decode_shared_workspace_size
+    assert size(C.byref(shared(**few)), C.byref(need)) == _abi.BLK_OK and need.value == 0
+    assert size(C.byref(shared(**many)), C.byref(need)) == _abi.BLK_OK and need.value > 0
 
 
 # -------------------------------------------------- blk_forward_packed --
