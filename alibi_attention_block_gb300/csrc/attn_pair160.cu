@@ -147,8 +147,9 @@ __global__ void __launch_bounds__(kPair160Threads, 1)
     // V tile i is ready once warp 3 has seen it land and cleared the rows
     // behind the prompt's end
     auto v_ready = [&](int i) { return bar0 + 112u + 8u * (4 * kStages + i); };
-    static_assert(112 + 40 * kStages + 4 <= 512, "barrier space");
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 112 + 40 * kStages);
+    auto drain = [&](int x) { return bar0 + 112u + 8u * (5 * kStages + x); };
+    static_assert(128 + 40 * kStages + 4 <= 512, "barrier space");
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 128 + 40 * kStages);
 
     const int warp = threadIdx.x / 32;
     const int lane = threadIdx.x & 31;
@@ -161,6 +162,7 @@ __global__ void __launch_bounds__(kPair160Threads, 1)
             mbar_init(o_free(x), 4);
             mbar_init(q_full(x), 1);
             mbar_init(q_empty(x), 1);
+            mbar_init(drain(x), 1);
         }
         if (ALIBI)
             for (int x = 0; x < 2; ++x) mbar_init(sQ + C::kOffTabBar + 8u * x, 4);
@@ -200,6 +202,7 @@ __global__ void __launch_bounds__(kPair160Threads, 1)
             Cursor c;
             c.start(a, pack, plan, n_items);
             int gkv = 0;           // K/V tiles loaded so far (ring position)
+            int nk = 0, nv = 0;    // K and V fills
             int itq[2] = {0, 0};   // Q fills per query tile
             bool ok = true;
             while (ok && c.valid) {
@@ -234,6 +237,7 @@ __global__ void __launch_bounds__(kPair160Threads, 1)
                     const int krow = own ? c.start_row + (kt - c.nP) * kTK : kt * kTK;
                     if (!(ok = mbar_wait_inl(k_empty(st), ph ^ 1u, a.err))) break;
                     mbar_expect_tx(k_full(st), C::kKBytes);
+                    ++nk;
 #pragma unroll
                     for (int sub = 0; sub < C::kFull; ++sub)
                         tma_load_3d_hint(sK + sub * kTK * 128, mK, k_full(st), sub * 64, krow, c.g, pol_kv);
@@ -241,6 +245,7 @@ __global__ void __launch_bounds__(kPair160Threads, 1)
                                      pol_kv);
                     if (!(ok = mbar_wait_inl(v_empty(st), ph ^ 1u, a.err))) break;
                     mbar_expect_tx(v_full(st), C::kVBytes);
+                    ++nv;
 #pragma unroll
                     for (int sub = 0; sub < C::kSub; ++sub)
                         tma_load_3d_hint(sK + C::kKBytes + sub * kTK * 128, mV, v_full(st), sub * 64, krow,
@@ -248,6 +253,13 @@ __global__ void __launch_bounds__(kPair160Threads, 1)
                 }
                 c.next(a, pack, plan, n_items);
             }
+            // whatever the others met, no copy lands behind this block's end
+            for (int i = max(nk - kStages, 0); i < nk; ++i)
+                mbar_wait(k_full(i % kStages), (i / kStages) & 1, a.err);
+            for (int i = max(nv - kStages, 0); i < nv; ++i)
+                mbar_wait(v_full(i % kStages), (i / kStages) & 1, a.err);
+            for (int x = 0; x < 2; ++x)
+                if (itq[x] > 0) mbar_wait(q_full(x), (itq[x] - 1) & 1, a.err);
         }
     } else if (warp == 1 || warp == 2) {
         if (lane == 0) {
@@ -350,6 +362,9 @@ __global__ void __launch_bounds__(kPair160Threads, 1)
                 if (nx > 0) ++itx;
                 c.next(a, pack, plan, n_items);
             }
+            // ... nor a product
+            tc_commit(drain(x));
+            mbar_wait(drain(x), 0, a.err);
         }
     } else {
         // warp 3: passes each V tile on once it has landed, the rows behind
