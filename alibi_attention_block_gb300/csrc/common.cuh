@@ -286,15 +286,15 @@ __device__ __forceinline__ bool mbar_wait_inl(uint32_t bar, uint32_t parity, uns
         }
     }
 }
-// Wait for the phase with the given parity to complete. Gives up after
-// kWaitLimitNs: sets the error word and returns false. The first try is
-// inline so a completed phase costs one instruction.
 // Waits for two phases.
 __device__ __forceinline__ bool mbar_wait2_inl(uint32_t bar0, uint32_t parity0, uint32_t bar1,
                                                uint32_t parity1, unsigned* err) {
     if (mbar_test2(bar0, parity0, bar1, parity1)) return true;
     return mbar_wait_inl(bar0, parity0, err) && mbar_wait_inl(bar1, parity1, err);
 }
+// Wait for the phase with the given parity to complete. Gives up after
+// kWaitLimitNs: sets the error word and returns false. The first try is
+// inline so a completed phase costs one instruction.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, unsigned* err) {
     if (mbar_try_wait(bar, parity)) return true;
     return mbar_wait_slow(bar, parity, err);
