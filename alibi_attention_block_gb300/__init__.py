@@ -160,6 +160,23 @@ def _workspace(t, dev):
     return _pointers(t.dtype, dev, t)[0], t.nbytes
 
 
+def _with_workspace(call, workspace, need, dev):
+    """call(pointer, bytes, stream) on the current stream of device dev, with
+    the caller's workspace, or one of `need` bytes from torch's allocator that
+    goes back as the call returns, to be used again in the stream's order (as a
+    tensor would be, in half its time)."""
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if workspace is not None:
+        return call(*_workspace(workspace, dev), stream)
+    if not need:
+        return call(None, 0, stream)
+    ptr = torch._C._cuda_cudaCachingAllocator_raw_alloc(need, stream)
+    try:
+        return call(ptr, need, stream)
+    finally:
+        torch._C._cuda_cudaCachingAllocator_raw_delete(ptr)
+
+
 def _refuse(t, dtype, dev):
     if t.dtype is not dtype:
         raise TypeError(f"expected a {dtype} tensor, got {t.dtype}")
@@ -231,16 +248,14 @@ def attn_prefill_packed(q, k, v, cu_seqlens, k_prefix=None, v_prefix=None, alibi
     qp, kp, vp, kpp, vpp, op = _pointers(q.dtype, dev, q, k, v, k_prefix, v_prefix, out)
     (cup,) = _pointers(torch.int32, dev, cu_seqlens)
     sp = None if slopes is None else _pointers(torch.float32, dev, slopes)[0]
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    wp, wn = (None, 0) if workspace is None else _workspace(workspace, dev)
     o = out
     if o is None:
         o = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
         op = o.data_ptr()
-    _abi.check(_lib().blk_attn_prefill_packed(
-        desc, qp, kp, vp, kpp, vpp, cup, sp, op, wp, wn, dt,
-        torch._C._cuda_getCurrentRawStream(dev)), "blk_attn_prefill_packed")
+    fn = _lib().blk_attn_prefill_packed
+    _abi.check(_with_workspace(
+        lambda wp, wn, st: fn(desc, qp, kp, vp, kpp, vpp, cup, sp, op, wp, wn, dt, st),
+        workspace, need, dev), "blk_attn_prefill_packed")
     return o
 
 
@@ -322,16 +337,14 @@ def attn_decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, lens, alibi=Fals
     qp, kpp, vpp, kp, vp, op = _pointers(q.dtype, dev, q, k_prefix, v_prefix, k_cache, v_cache, out)
     (lp,) = _pointers(torch.int32, dev, lens)
     sp = None if slopes is None else _pointers(torch.float32, dev, slopes)[0]
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    wp, wn = (None, 0) if workspace is None else _workspace(workspace, dev)
     o = out
     if o is None:
         o = torch.empty_like(q)
         op = o.data_ptr()
-    _abi.check(_lib().blk_attn_decode_shared(
-        desc, qp, kpp, vpp, kp, vp, lp, sp, op, wp, wn, dt,
-        torch._C._cuda_getCurrentRawStream(dev)), "blk_attn_decode_shared")
+    fn = _lib().blk_attn_decode_shared
+    _abi.check(_with_workspace(
+        lambda wp, wn, st: fn(desc, qp, kpp, vpp, kp, vp, lp, sp, op, wp, wn, dt, st),
+        workspace, need, dev), "blk_attn_decode_shared")
     return o
 
 

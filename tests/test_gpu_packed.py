@@ -358,6 +358,22 @@ def test_block_over_one_prompt_equals_dense():
     assert torch.equal(y, dense[0])
 
 
+def test_captured_without_a_workspace():
+    """A captured call with a long list keeps it in the graph's memory."""
+    cu = ends([3] * 300 + [200])
+    args = [to_dev(t) for t in inputs(2, 1, cu[-1], 64, 0, "bf16", 12)[:3]] + [table(cu)]
+    want = blk.attn_prefill_packed(*args)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o = blk.attn_prefill_packed(*args)
+    for _ in range(3):
+        o.zero_()
+        g.replay()
+        blk.attn_prefill_packed(args[0].flip(1).contiguous(), *args[1:])
+        torch.cuda.synchronize()
+        assert torch.equal(o, want)
+
+
 def test_binding_refuses():
     q, k, v, kp, vp = (to_dev(t) for t in inputs(4, 2, 64, 64, 32, "bf16", 13))
     cu = table([0, 64])

@@ -247,6 +247,28 @@ def test_graph_replay_and_other_stream(P):
         assert torch.equal(got, blk.attn_decode_shared(qd, kpd, vpd, kd, vd, lens))
 
 
+def test_captured_without_a_workspace():
+    """A captured call takes its workspace from the graph's memory: other calls
+    between its replays, and a second graph's, do not touch it."""
+    B, H, Hk, d, P, S = 6, 8, 2, 128, 1000, 50
+    args = [to_dev(t) for t in inputs(B, H, Hk, d, P, S, "bf16", 52)]
+    lens = torch.tensor([50, 1, 2, 0, 30, 7], dtype=torch.int32, device="cuda")
+    want = blk.attn_decode_shared(*args, lens)
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            o = blk.attn_decode_shared(*args, lens)
+        graphs.append((g, o))
+    for _ in range(3):
+        for g, o in graphs:
+            o.zero_()
+            g.replay()
+            blk.attn_decode_shared(args[0].flip(0), *args[1:], lens)
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, want) for _, o in graphs)
+
+
 def test_prefill_then_decode():
     """The two operators as a serving loop uses them: prompts prefilled behind
     a shared prefix, then one decode step over the prefix and the prompts' own
