@@ -205,9 +205,15 @@ def attn_prefill_packed_workspace_size(desc) -> int:
     return need.value
 
 
+def _values(alibi, scale):
+    """A call's switch and scale as plain values: a plan is kept by them, and a
+    0-dim tensor given for one hashes by identity, whatever it holds by now."""
+    return bool(alibi), None if scale is None else float(scale)
+
+
 @functools.lru_cache(maxsize=256)
 def _packed_plan(*args):
-    """(descriptor by reference, workspace bytes) of a call's sizes."""
+    """(descriptor by reference, workspace bytes) of a call's sizes and _values."""
     desc = packed_desc(*args)
     return C.byref(desc), attn_prefill_packed_workspace_size(desc)
 
@@ -243,7 +249,7 @@ def attn_prefill_packed(q, k, v, cu_seqlens, k_prefix=None, v_prefix=None, alibi
         raise ValueError("cu_seqlens has shape [prompts + 1]")
     _shape(slopes, (H,), "slopes")
     _shape(out, (T, H, d), "out")
-    desc, need = _packed_plan(T, cu_seqlens.numel() - 1, H, Hk, d, P, alibi, scale)
+    desc, need = _packed_plan(T, cu_seqlens.numel() - 1, H, Hk, d, P, *_values(alibi, scale))
     dev = torch.cuda.current_device()
     qp, kp, vp, kpp, vpp, op = _pointers(q.dtype, dev, q, k, v, k_prefix, v_prefix, out)
     (cup,) = _pointers(torch.int32, dev, cu_seqlens)
@@ -309,7 +315,7 @@ def attn_decode_shared_workspace_size(desc) -> int:
 
 @functools.lru_cache(maxsize=256)
 def _decode_shared_plan(*args):
-    """(descriptor by reference, workspace bytes) of a call's sizes."""
+    """(descriptor by reference, workspace bytes) of a call's sizes and _values."""
     desc = decode_shared_desc(*args)
     return C.byref(desc), attn_decode_shared_workspace_size(desc)
 
@@ -332,7 +338,7 @@ def attn_decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, lens, alibi=Fals
     _shape(lens, (B,), "lens")
     _shape(slopes, (H,), "slopes")
     _shape(out, (B, H, d), "out")
-    desc, need = _decode_shared_plan(B, S_max, H, Hk, d, P, alibi, scale)
+    desc, need = _decode_shared_plan(B, S_max, H, Hk, d, P, *_values(alibi, scale))
     dev = torch.cuda.current_device()
     qp, kpp, vpp, kp, vp, op = _pointers(q.dtype, dev, q, k_prefix, v_prefix, k_cache, v_cache, out)
     (lp,) = _pointers(torch.int32, dev, lens)
