@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kThreads) shared_small_kernel(const SmallArgs 
     constexpr int kStep = kWarps * (32 / L);  // keys per step of the block
     constexpr int U = 4;                      // steps in flight
     __shared__ float sc[kSharedSmallDims / D];
-    __shared__ float part[kWarps][D];
+    __shared__ __align__(16) float part[kWarps][D];  // written as float4, read as float2
     __shared__ float red_max[kWarps], red_sum[kWarps];
     if (a.pdl) {
         pdl_wait();
