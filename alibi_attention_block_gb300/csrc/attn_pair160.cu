@@ -255,11 +255,11 @@ __global__ void __launch_bounds__(kPair160Threads, 1)
             }
             // whatever the others met, no copy lands behind this block's end
             for (int i = max(nk - kStages, 0); i < nk; ++i)
-                mbar_wait(k_full(i % kStages), (i / kStages) & 1, a.err);
+                mbar_wait_inl(k_full(i % kStages), (i / kStages) & 1, a.err);
             for (int i = max(nv - kStages, 0); i < nv; ++i)
-                mbar_wait(v_full(i % kStages), (i / kStages) & 1, a.err);
+                mbar_wait_inl(v_full(i % kStages), (i / kStages) & 1, a.err);
             for (int x = 0; x < 2; ++x)
-                if (itq[x] > 0) mbar_wait(q_full(x), (itq[x] - 1) & 1, a.err);
+                if (itq[x] > 0) mbar_wait_inl(q_full(x), (itq[x] - 1) & 1, a.err);
         }
     } else if (warp == 1 || warp == 2) {
         if (lane == 0) {
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kPair160Threads, 1)
             }
             // ... nor a product
             tc_commit(drain(x));
-            mbar_wait(drain(x), 0, a.err);
+            mbar_wait_inl(drain(x), 0, a.err);
         }
     } else {
         // warp 3: passes each V tile on once it has landed, the rows behind
