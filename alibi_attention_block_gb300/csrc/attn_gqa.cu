@@ -187,6 +187,7 @@ __global__ void __launch_bounds__(gqa_threads(PACKED), 1)
     // packed: V tile i is ready once the last warp has seen it land and
     // cleared the rows behind the prompt's end
     auto v_ready = [&](int i) { return PACKED ? bar0 + 160u + 8u * i : v_full(i); };
+    const uint32_t drain = bar0 + 176u;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kOffBar + 152);
 
     const int warp = threadIdx.x / 32;
@@ -210,6 +211,7 @@ __global__ void __launch_bounds__(gqa_threads(PACKED), 1)
         mbar_init(p_full, 4);
         mbar_init(pv_done, 1);
         mbar_init(o_free, 4);
+        mbar_init(drain, 1);
         fence_barrier_init();
         tma_prefetch_desc(&tmQ);
         tma_prefetch_desc(&tmK);
@@ -317,6 +319,13 @@ __global__ void __launch_bounds__(gqa_threads(PACKED), 1)
                 }
                 c.next(a, pk, pack, plan, nblk, n_items);
             }
+            // whatever the others met, no copy lands behind this block's end
+            for (int i = max(gk - kKS, 0); i < gk; ++i)
+                mbar_wait(k_full(i % kKS), (i / kKS) & 1, a.err);
+            for (int i = max(gv - kVS, 0); i < gv; ++i)
+                mbar_wait(v_full(i % kVS), (i / kVS) & 1, a.err);
+            for (int i = max(c.it - kQB, 0); i < c.it; ++i)
+                mbar_wait(q_full(i % kQB), (i / kQB) & 1, a.err);
         }
     } else if (warp == 1) {
         if (lane == 0) {
@@ -397,6 +406,9 @@ __global__ void __launch_bounds__(gqa_threads(PACKED), 1)
                 ++itx;
                 c.next(a, pk, pack, plan, nblk, n_items);
             }
+            // ... nor a product
+            tc_commit(drain);
+            mbar_wait(drain, 0, a.err);
         }
     } else if (PACKED && warp == 6) {
         if constexpr (PACKED) {

@@ -83,9 +83,10 @@ struct PairCfg {
     // tile), one per item parity
     static constexpr int kOffTabBar = kOffBar + 256;
     static constexpr int kOffBias = kOffTabBar + 16;
-    // packed prompts: one more barrier per V stage
+    // packed prompts: one more barrier per V stage; and one for the end
     static constexpr int kOffVReady = kOffBias + 2 * 2 * kTK * 4;
-    static constexpr int kSmem = kOffVReady + 8 * kStages + 1024;  // + alignment slack
+    static constexpr int kOffDrain = kOffVReady + 8 * kStages;
+    static constexpr int kSmem = kOffDrain + 8 + 1024;  // + alignment slack
     static constexpr uint32_t kColP = 256;              // P_x at kColP + 64 x
     static constexpr uint32_t kColO = 384;              // O_x at kColO + D x
     static constexpr uint32_t kTmemCols = 512;
@@ -197,6 +198,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     // packed: V tile i is ready once warp 3 has seen it land and cleared the
     // rows behind the prompt's end
     auto v_ready = [&](int i) { return PACKED ? sQ + Cfg::kOffVReady + 8u * i : v_full(i); };
+    const uint32_t drain = sQ + Cfg::kOffDrain;
     uint32_t* tmem_slot =
         reinterpret_cast<uint32_t*>(smem + Cfg::kOffBar + 112 + 32 * kStages);
 
@@ -216,6 +218,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             mbar_init(q_full(x), 1);
             mbar_init(q_empty(x), 2);
         }
+        mbar_init(drain, 2);
         if (ALIBI)
             for (int x = 0; x < 2; ++x) mbar_init(sQ + Cfg::kOffTabBar + 8u * x, 4);
         for (int i = 0; i < kStages; ++i) {
@@ -258,7 +261,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const uint64_t pol_kv = l2_evict_last_policy(), pol_q = l2_evict_first_policy();
             PairCursor<PACKED> c;
             c.start(a, pack, plan, nq, np, n_items);
-            int gkv = 0;  // K/V tiles loaded so far (ring position)
+            int gkv = 0;   // K/V tiles loaded so far (ring position)
+            int half = 0;  // 1: and a K tile without its V
             bool ok = true;
             while (ok && c.valid) {
                 const int qb = c.it & 1;
@@ -297,6 +301,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         tma_load_3d_hint(sK + sub * kTK * 128, mK, k_full(st), sub * 64, krow,
                                     c.b * a.Hk + c.g, pol_kv);
                     if (!mbar_wait_inl(v_empty(st), ph ^ 1u, a.err)) {
+                        half = 1;
                         ok = false;
                         break;
                     }
@@ -307,6 +312,19 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                                     sub * 64, krow, c.b * a.Hk + c.g, pol_kv);
                 }
                 c.next(a, pack, plan, nq, np, n_items);
+            }
+            // whatever the others met, no copy lands behind this block's end:
+            // the last fill of each K, V and Q buffer. One wait in the code: with
+            // a loop for each kind, and the products' wait in their threads'
+            // branch, the whole kernel ran 0.5 to 2% longer
+#pragma unroll 1
+            for (int i = 0; i < 2 * kStages + 2; ++i) {
+                const bool q = i >= 2 * kStages;  // v_full(0) is k_full(kStages)
+                const int buf = i % kStages;
+                const int fills = q ? (c.it + 1 - (i & 1)) / 2
+                                    : (gkv + (i < kStages ? half : 0) + kStages - 1 - buf) / kStages;
+                if (fills > 0)
+                    mbar_wait_inl(q ? q_full(i & 1) : k_full(0) + 8u * i, (fills - 1) & 1, a.err);
             }
         }
     } else if (warp == 1 || warp == 2) {
@@ -408,6 +426,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 if (nx > 0) ++itx;
                 c.next(a, pack, plan, nq, np, n_items);
             }
+            tc_commit(drain);
         }
     } else if constexpr (PACKED) {
         // warp 3: passes each V tile on once it has landed, the rows behind
@@ -662,6 +681,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     __syncthreads();
     if (warp == 1) {
+        mbar_wait_inl(drain, 0, a.err);  // ... nor is a product still under way
         tc_fence_after();
         tmem_dealloc(tmem_base, Cfg::kTmemCols);
     }
