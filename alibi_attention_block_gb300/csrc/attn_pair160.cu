@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(kPair160Threads, 1)
             }
             ++n_done;
             for (int j = 0; j < nx; ++j, ++g) {
-                if (!mbar_wait_inl(s_full(x), g & 1, a.err)) {
+                if (!mbar_wait_inl(s_full(x), g & 1, a.err, idle_limit_ns(c.it, c.nP))) {
                     ok = false;
                     break;
                 }

@@ -86,6 +86,16 @@ __device__ __forceinline__ void build_plan(PlanSmem& p, const int32_t* cu, int p
     __syncthreads();
 }
 
+// Limit of a softmax warpgroup's wait for scores. A work item without a second
+// query tile leaves the second tile's warpgroup waiting through it, and a long
+// prefix behind many short prompts makes such items last seconds together (13200
+// prompts of one token, 4 heads of 64, behind 2^20 shared keys: 2.7 s). Such an
+// item has the prefix's key tiles and two of its own at most, and a tile takes 1 to
+// 2 us; this allows 10 for each item that the CTA has been through.
+__device__ __forceinline__ unsigned long long idle_limit_ns(int items, int prefix_tiles) {
+    return kWaitLimitNs + static_cast<unsigned long long>(items + 1) * (prefix_tiles + 2) * 10000ull;
+}
+
 template <typename Plan>
 __device__ __forceinline__ int plan_units(const AttnPack<true>& pack, const Plan& p) {
     return pack.plan ? pack.plan[0].x : p.total;

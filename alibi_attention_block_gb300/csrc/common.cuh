@@ -16,7 +16,8 @@ namespace blk {
 enum : unsigned { DEV_ERR_NONE = 0u, DEV_ERR_TIMEOUT = 1u };
 
 // Upper bound on any single wait inside a kernel. Legitimate waits in these
-// kernels last microseconds; a wait this long means a lost arrival.
+// kernels last microseconds; a wait this long means a lost arrival. (One may last
+// longer and has a limit that grows: idle_limit_ns in attn_plan.cuh.)
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;
 
 __device__ __forceinline__ uint64_t globaltimer_ns() {
@@ -275,12 +276,13 @@ static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity
 // The same wait with the slow path inlined: for kernels that change their
 // register budget per warpgroup (setmaxnreg), where a call to a function
 // compiled for the launch's register count is not allowed.
-__device__ __forceinline__ bool mbar_wait_inl(uint32_t bar, uint32_t parity, unsigned* err) {
+__device__ __forceinline__ bool mbar_wait_inl(uint32_t bar, uint32_t parity, unsigned* err,
+                                              unsigned long long limit_ns = kWaitLimitNs) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t i = 1;; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 63u) == 0u && globaltimer_ns() - t0 > kWaitLimitNs) {
+        if ((i & 63u) == 0u && globaltimer_ns() - t0 > limit_ns) {
             report_error(err, DEV_ERR_TIMEOUT);
             return false;
         }

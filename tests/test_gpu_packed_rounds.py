@@ -248,3 +248,24 @@ def test_scales_changed_in_place():
             assert torch.equal(blk.attn_decode_shared(*step, scale=t), blk.attn_decode_shared(*step, scale=value))
     ref = reference(q, k, v, 0, 100, scale=0.5)
     check_rows(blk.attn_prefill_packed(*args, scale=t), ref, "bf16", "scale 0.5")
+
+
+@pytest.mark.parametrize("H,Hk,d,n", [(4, 1, 64, 13200), (2, 2, 128, 16500), (2, 2, 160, 14000)])
+def test_a_long_idle_second_tile(H, Hk, d, n):
+    """Prompts of one token behind a prefix of 2^20, and one prompt of two query
+    tiles behind them: the second tile's softmax warps have nothing to do for
+    2.6 to 3 seconds, longer than a wait that has lost its arrival may last, and
+    then their part of the last prompt. It gets what it gets by itself."""
+    P, last = 1 << 20, 250
+    g = torch.Generator(device="cuda")
+    g.manual_seed(d)
+    q, k, v, kp, vp = (torch.randn(s, generator=g, device="cuda", dtype=torch.float32).to(torch.bfloat16)
+                       for s in ((H, n + last, d), (Hk, n + last, d), (Hk, n + last, d), (Hk, P, d), (Hk, P, d)))
+    pre = dict(k_prefix=kp, v_prefix=vp)
+    o = blk.attn_prefill_packed(q, k, v, table(list(range(n + 1)) + [n + last]), **pre)
+    blk.check_device_status()
+    alone = [t[:, n:].contiguous() for t in (q, k, v)]
+    assert torch.equal(o[n:], blk.attn_prefill_packed(*alone, table([0, last]), **pre))
+    first = [t[:, :100].contiguous() for t in (q, k, v)]
+    assert torch.equal(o[:100], blk.attn_prefill_packed(*first, table(list(range(101))), **pre))
+    blk.check_device_status()
