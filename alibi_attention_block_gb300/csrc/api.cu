@@ -954,10 +954,13 @@ static blk_status validate_shared_desc(const blk_decode_shared_desc* d) {
 static bool shared_is_small(const blk_decode_shared_desc* d) {
     return shared_small(d->batch, d->n_heads, d->head_dim, d->prefix_len, d->max_seq);
 }
+// The kernel writes partial results 32 bytes at a time, so the workspace, which
+// may be aligned to 16, is used from its first boundary of 32 on.
+constexpr uintptr_t kSharedWsAlign = 32;
 static size_t shared_ws_bytes(const blk_decode_shared_desc* d) {
     if (shared_is_small(d)) return 0;
     return static_cast<size_t>(shared_layout(d->batch, d->n_heads, d->n_kv_heads, d->head_dim,
-                                             d->prefix_len).total);
+                                             d->prefix_len).total) + (kSharedWsAlign - 16);
 }
 
 blk_status blk_attn_decode_shared_workspace_size(const blk_decode_shared_desc* d, size_t* bytes) {
@@ -1014,7 +1017,8 @@ blk_status blk_attn_decode_shared(const blk_decode_shared_desc* d, const void* q
     a.k_prefix = k_prefix;
     a.v_prefix = v_prefix;
     a.P = static_cast<int>(d->prefix_len);
-    a.ws = static_cast<uint8_t*>(workspace);
+    a.ws = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(workspace) + kSharedWsAlign - 1) &
+                                      ~(kSharedWsAlign - 1));
     a.err = ds->err;
     a.num_sms = ds->sms;
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(s);

@@ -205,7 +205,7 @@ struct SharedArgs {
     const void* k_prefix;  // [Hk, P, d]
     const void* v_prefix;
     int P;
-    uint8_t* ws;           // shared_layout(...).total bytes
+    uint8_t* ws;           // shared_layout(...).total bytes, 32-byte aligned
     unsigned* err;
     int num_sms;
 };
