@@ -325,8 +325,10 @@ def attn_decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, lens, alibi=Fals
     """One decode step of a batch that shares a prefix: q [B, H, d] (newest
     token of each sequence, at position P + lens[b] - 1) against k/v_prefix
     [Hk, P, d] (None: no prefix), stored once, and each sequence's own caches
-    [B, Hk, S_max, d] of lens[b] keys (int32 [B] on the device; 0: the
-    sequence takes no part, its row is zero). Returns o [B, H, d]."""
+    [B, Hk, S_max, d] of lens[b] keys (int32 [B] on the device, clamped to
+    [0, S_max]; 0: the sequence takes no part, its row is zero). Returns o
+    [B, H, d]; the softmax weights are rounded to q's type where a workspace is
+    needed, and held in 32 bits below (``attn_decode`` always does)."""
     dt = _dt(q)
     B, H, d = q.shape
     Hk, S_max = k_cache.shape[1], k_cache.shape[2]

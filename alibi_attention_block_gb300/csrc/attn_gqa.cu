@@ -526,7 +526,9 @@ __global__ void __launch_bounds__(gqa_threads(PACKED), 1)
                     m_used = mx;
                 }
                 // a row with no visible key in this tile and none before it
-                // (possible only for padding rows) keeps m = -inf: use 0
+                // keeps m = -inf: use 0. Padding rows, and, with packed ALiBi's
+                // walk down from the diagonal, the first rows of a block of
+                // positions that crosses a key tile's edge
                 const float m_eff = m_used == -INFINITY ? 0.f : m_used;
                 const uint64_t mul2 = f2_pack(ALIBI ? 1.f : scale_l2, ALIBI ? 1.f : scale_l2);
                 const uint64_t neg2 = f2_pack(-m_eff, -m_eff);

@@ -102,8 +102,8 @@ struct PairCfg {
 // nP prefix tiles come ahead of its own key tiles. A prompt's tiles are paired
 // from its end, so that where their number is odd the single one is the first,
 // which has one key tile, and not the last, which has all (17 tiles: 81 steps for
-// 89). 32 x 64 heads: two prompts of 8192 and 5330 tokens 387 us, 1.01 PFLOP/s (the
-// dense kernel 1.04 at S = 8192); eight of 1273 on average 100 us, 0.65. As there, each
+// 89). 32 x 64 heads: two prompts of 8192 and 5330 tokens 389 us, 1.01 PFLOP/s (the
+// dense kernel 1.04 at S = 8192); eight of 1273 on average 98.8 us, 0.66. As there, each
 // query tile's chain of scores, softmax and product is the bound. Shortening it did
 // not pay: a row's softmax in two halves on 16 warps, with an exchange of the maxima,
 // 487 us; P handed over in two halves of the tile, 397.
@@ -582,7 +582,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     m_used = mx;
                 }
                 // p = 2^(logit - m) in the storage type, and the row sum; P is
-                // held in registers until the previous PV has read P_x
+                // held in registers until the previous PV has read P_x. The
+                // product takes P from TMEM in 16 bits, with V's type: each
+                // weight is off by half a step at most, relative (2^-8 in bf16,
+                // 2^-11 in fp16), about what the output's own rounding costs. The
+                // sum takes the 32-bit weights
                 const uint64_t mul2 = f2_pack(ALIBI ? 1.f : scale_l2, ALIBI ? 1.f : scale_l2);
                 const float off = ALIBI ? sk - m_used : -m_used;
                 const uint64_t neg2 = f2_pack(off, off);

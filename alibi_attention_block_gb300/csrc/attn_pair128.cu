@@ -72,7 +72,7 @@ struct Cfg {
 // of tile x is head g * G + hc * Gt + r / R at position (2 i + x) R + r % R, so a
 // unit is 2 R positions of one prompt (R = 128 for MHA), and an item is (unit, kv
 // head, head chunk). 32/8 heads, 32 prompts of 145 tokens on average behind 2000
-// shared ones: 196 us with one tile per item (attn_gqa.cu), 176 with two.
+// shared ones: 196 us with one tile per item (attn_gqa.cu), 175 with two.
 template <bool PACKED>
 struct PairCursor {
     using Plan = typename PlanStorage<PACKED>::type;

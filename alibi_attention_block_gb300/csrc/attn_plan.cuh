@@ -13,8 +13,13 @@ struct PlanUnit {
 };
 
 // A small list is built by each CTA: the table's entries are in L2, and a kernel
-// that only builds the list costs 2.6 us, its launch and a workspace (a call with
-// 16 chat turns: 28 us with it, 15 without). Every CTA has to come to the same
+// that only builds the list costs 2.6 us, its launch and a workspace. In a graph, in
+// us, built by each CTA and in the workspace (16 x 64 heads, ALiBi, turns of 25
+// tokens):
+//    16 turns  11.7  15.7     64   30.7  31.2    128   57.2  51.9    255  106.3  90.3
+// (32 x 64 heads: 4 prompts of 2000 90.9 and 96.2, 8 of 1273 83.8 and 89.4). Where
+// all prompts are one unit there is one level, which one thread lists: above some
+// 64 such prompts that costs more than the launch. Every CTA has to come to the same
 // order, so no atomics: prompts are ranked by their number of units (ties by
 // index), and unit l of the prompt of rank r comes behind all units above l, in
 // the order of the ranks among those of level l. Where a unit is a pair of query

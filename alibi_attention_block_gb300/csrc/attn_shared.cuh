@@ -149,10 +149,11 @@ __device__ __forceinline__ float alibi_slope(const SharedKernelArgs& a, int h) {
 }
 
 // Descriptor of `off` (in 16 bytes) behind the one of d: the address is the
-// low word's field and does not carry out of it. In 32 bits on purpose: with
-// the unrolled 64-bit additions this kernel's O = P V products ran with other
-// descriptors than the source's (head_dim 64: keys 0, 16, 32, ... only; the
-// same loop not unrolled, or on this form, gives the products).
+// low word's field and does not carry out of it, so that 32 bits are enough. A
+// form of this kernel that added 64-bit offsets in unrolled loops gave wrong O =
+// P V at head_dim 64 (as if of keys 0, 16, 32, ... only) and right ones with the
+// loop not unrolled, or with this function. The cause is not known: the two
+// additions are equal for these addresses, and attn_pair.cu does the other one.
 __device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t off) {
     uint32_t lo, hi;
     asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(d));
@@ -446,6 +447,8 @@ __device__ __forceinline__ bool prefix_phase(const SharedKernelArgs& a, const CU
                     corr = ex2_approx(m_used - mx);
                     m_used = mx;
                 }
+                // weights in the storage type for the product (half a step each,
+                // see attn_pair.cu), in 32 bits for the sum
                 const uint64_t mul2 = f2_pack(mul, mul), neg2 = f2_pack(-m_used, -m_used);
                 uint64_t acc0 = f2_pack(0.f, 0.f), acc1 = acc0;
                 // P over S: nothing but this row's own scores is there, and they
@@ -914,6 +917,8 @@ __device__ __forceinline__ void own_phase(const SharedKernelArgs& a, const CUten
                 const uint32_t p_row = sP + (t & 1) * C::kPBytes + (key / 64) * 1024;
 #pragma unroll
                 for (int h = 0; h < G; ++h) {
+                    // in the storage type for the product, as the prefix's (on
+                    // the CUDA cores, in 32 bits, the pass was bound by them)
                     const float p = ex2_approx(s[h] - m[h]);
                     l[h] = fmaf(l[h], corr[h], p);
                     const uint32_t at =

@@ -7,7 +7,9 @@
 // attention of nnterp "stablelm" 03 Notes; ALiBi as in "Bloom in a sovereign
 // engine", Contribution.) Nothing is split over blocks, so there are no partial
 // results and no merge; the prefix comes from L2 for each sequence, a group's keys
-// for each of its heads. D / 8 lanes hold a key, 16 bytes each, on the CUDA cores.
+// for each of its heads. D / 8 lanes hold a key, 16 bytes each, on the CUDA cores,
+// with the weights in 32 bits throughout (the kernel for many keys rounds them for
+// its products).
 //
 // What bounds it is latency: the launch, and in a warp's two passes a load, products
 // and shuffles per 16 keys (head_dim 64). In a graph, in us, here and with the kernel

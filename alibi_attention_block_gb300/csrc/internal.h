@@ -149,7 +149,8 @@ struct AttnPack<true> {
     int prompts, prefix;
     int G, Gt, R, nhc;          // gqa_tile (attn_pair128.cu, attn_pair160.cu)
 };
-// up to these sizes the list is built by each CTA, without a workspace
+// up to these sizes the list is built by each CTA, without a workspace (both
+// sides' times: attn_plan.cuh)
 constexpr int kPlanCtaPrompts = 256, kPlanCtaUnits = 1024;
 struct PackedArgs {
     const void* k_prefix;  // [Hk, prefix, d]

@@ -194,7 +194,9 @@ typedef struct {
  * A prompt's results do not depend on the other prompts, nor on what rows
  * outside it hold (NaN included). As in blk_attn_prefill, a key that a row
  * does not see has weight 0, so a non-finite value (v) of a later token of
- * the same prompt and 128-key tile makes a NaN.
+ * the same prompt and 128-key tile makes a NaN. The softmax weights enter the
+ * products with V rounded to dt (half a step, relative), as there; their sums
+ * are of the 32-bit weights.
  * GQA: kv head = h / (H / Hk). head_dim in {64, 128, 160}. One launch; above
  * 256 prompts or some ten to hundred thousand tokens (by the head layout) a
  * second one ahead of it makes the work list in the workspace, which then has at
@@ -254,12 +256,17 @@ typedef struct {
  *     the prefix, entries 0 .. lens[b] - 1 at positions prefix_len ..
  *     prefix_len + lens[b] - 1 (the newest token's already written); later
  *     entries are not read
- *   lens: device int32 [batch], each in [1, max_seq]; read on the device, a
- *     value outside the range is clamped to it, and a length of 0 marks a
- *     sequence that takes no part: its output row is zero
+ *   lens: device int32 [batch], read on the device, each clamped to
+ *     [0, max_seq]; a length of 0 (or less) marks a sequence that takes no part:
+ *     its output row is zero
  *   alibi_slopes: as for blk_attn_prefill
- *   o [batch, H, d], as blk_attn_decode would give it with the prefix copied
- *     in front of each sequence's cache
+ *   o [batch, H, d]: the attention that blk_attn_decode computes with the prefix
+ *     copied in front of each sequence's cache, but not its bits. That call holds
+ *     the softmax weights in 32 bits throughout. Here they enter the products with
+ *     V rounded to dt (half a step, relative: 2^-8 in bf16, 2^-11 in fp16), as in
+ *     the prefill calls; their sums are of the 32-bit weights. With few keys (a
+ *     workspace size of 0: a matter of prefix_len, max_seq, heads and batch, not
+ *     of lens) they stay in 32 bits
  * GQA: kv head = h / (H / Hk), H / Hk in {1, 2, 4, 8}; head_dim 64 or 128.
  * The workspace holds partial results, at least
  * blk_attn_decode_shared_workspace_size bytes, 16-byte aligned (0 bytes, at a few
