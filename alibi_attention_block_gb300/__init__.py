@@ -25,6 +25,8 @@ __all__ = ["layernorm_bias", "rmsnorm", "qkv_bias_rope_partial", "rope_inplace",
            "attn_prefill_packed", "attn_prefill_packed_workspace_size", "packed_desc",
            "attn_decode", "attn_decode_workspace_size", "decode_desc",
            "attn_decode_shared", "attn_decode_shared_workspace_size", "decode_shared_desc",
+           "rope_plan", "rope_positions", "kv_append_paged", "attn_decode_paged",
+           "attn_decode_paged_workspace_size", "decode_paged_desc",
            "linear", "mlp", "block_desc", "forward_workspace_size", "forward_q8_0_workspace_size", "forward", "forward_packed", "forward_packed_workspace_size", "forward_host", "ForwardGraph", "HostPipe", "model_desc",
            "model_workspace_size", "model_forward",
            "check_device_status", "BlkError", "library_path"]
@@ -353,6 +355,200 @@ def attn_decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, lens, alibi=Fals
     _abi.check(_with_workspace(
         lambda wp, wn, st: fn(desc, qp, kpp, vpp, kp, vp, lp, sp, op, wp, wn, dt, st),
         workspace, need, dev), "blk_attn_decode_shared")
+    return o
+
+
+_SCALING = {"none": _abi.BLK_ROPE_PLAIN, "linear": _abi.BLK_ROPE_LINEAR,
+            "by_parts": _abi.BLK_ROPE_BY_PARTS}
+
+
+def rope_plan(span, base=10000.0, interleaved=False, scaling="none", factor=1.0, original_len=0.0,
+              beta_slow=1.0, beta_fast=32.0, amplitude=1.0):
+    """The plan of a rotary for ``rope_positions`` and ``kv_append_paged``, made
+    once: span dims of a head, in halves or interleaved pairs, with positions
+    scaled "linear" or "by_parts" (blk_rope_scaling in include/blk.h says
+    how), turned dims times amplitude. Plain host data."""
+    if scaling not in _SCALING:
+        raise ValueError(f"scaling must be one of {sorted(_SCALING)}")
+    plan = _abi.RopePlan()
+    desc = _abi.RopeDesc(span, 1 if interleaved else 0, base, _SCALING[scaling], amplitude, factor,
+                         original_len, beta_slow, beta_fast)
+    _abi.check(_lib().blk_rope_plan_init(C.byref(desc), C.byref(plan)), "blk_rope_plan_init")
+    return plan
+
+
+def _strided(t, dtype, dev):
+    """Pointer of a tensor [a, b, dim] with contiguous dims, as (pointer, stride
+    of a, stride of b)."""
+    if t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t, dtype, dev)
+    shape, stride = t.shape, t.stride()
+    if stride[2] != 1 and shape[2] != 1:
+        raise ValueError("a head's dims must be contiguous")
+    # the stride of an axis of length 1 is never used, whatever it is
+    return (t.data_ptr(), stride[0] if shape[0] > 1 else 0, stride[1] if shape[1] > 1 else 0)
+
+
+def rope_positions(q, positions, plan, k=None, inverse=False, q_out=None, k_out=None):
+    """Rotary of q [H, T, d] (and k [Hk, T, d]) at positions (int32 [T] on the
+    device) by a ``rope_plan``. Any strides with contiguous dims; a tensor
+    [T, H, d] goes in transposed. q_out / k_out: where to (q and k themselves
+    for in place; new tensors when None). Returns the result, or the two.
+    inverse=True turns back (the gradient's call)."""
+    dt, dtype, dev = _dt(q), q.dtype, torch.cuda.current_device()
+    H, T, d = q.shape
+    _shape(positions, (T,), "positions")
+    _shape(q_out, (H, T, d), "q_out")
+    o = torch.empty(q.shape, dtype=dtype, device=q.device) if q_out is None else q_out
+    qp, qh, qt = _strided(q, dtype, dev)
+    op, oh, ot = _strided(o, dtype, dev)
+    Hk = kp = kh = kt = lp = lh = lt = 0
+    if k is not None:
+        Hk = k.shape[0]
+        _shape(k, (Hk, T, d), "k")
+        _shape(k_out, (Hk, T, d), "k_out")
+        ko = torch.empty(k.shape, dtype=dtype, device=k.device) if k_out is None else k_out
+        kp, kh, kt = _strided(k, dtype, dev)
+        lp, lh, lt = _strided(ko, dtype, dev)
+    elif k_out is not None:
+        raise ValueError("k_out given without k")
+    (pp,) = _pointers(torch.int32, dev, positions)
+    desc = _abi.RopePosDesc(T, H, Hk, d, 1 if inverse else 0, qh, qt, oh, ot, kh, kt, lh, lt)
+    _abi.check(_lib().blk_rope_positions(desc, plan, qp, kp or None, pp, op, lp or None, dt,
+                                         torch._C._cuda_getCurrentRawStream(dev)),
+               "blk_rope_positions")
+    return o if k is None else (o, ko)
+
+
+def _paged(k_cache, v_cache, k_scale, v_scale, block_table, lens, dtype, dev):
+    """A paged cache's arguments checked: (descriptor's fields, pointers in the
+    calls' order: table, lens, caches, scales)."""
+    pages, Hk, n, d = k_cache.shape
+    B, max_pages = block_table.shape
+    stride = k_cache.stride()
+    if k_cache.dtype is torch.float8_e4m3fn:
+        kind = _abi.BLK_CACHE_E4M3
+        if k_scale is None or v_scale is None:
+            raise ValueError("a float8_e4m3fn cache has k_scale and v_scale")
+        _shape(k_scale, (pages, Hk), "k_scale")
+        _shape(v_scale, (pages, Hk), "v_scale")
+        ksp, vsp = _pointers(torch.float32, dev, k_scale, v_scale)
+    else:
+        kind, ksp, vsp = _abi.BLK_CACHE_16BIT, None, None
+        if k_cache.dtype is not dtype:
+            raise TypeError(f"caches are float8_e4m3fn or {dtype}, got {k_cache.dtype}")
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("a 16-bit cache has no scales")
+    _shape(v_cache, (pages, Hk, n, d), "v_cache")
+    for t in (k_cache, v_cache):
+        if t.dtype is not k_cache.dtype or t.get_device() != dev:
+            _refuse(t, k_cache.dtype, dev)
+    page = Hk * n * d
+    if pages == 1:
+        page_stride = page
+    else:
+        page_stride = stride[0]
+        if v_cache.stride(0) != page_stride:
+            raise ValueError("k_cache and v_cache must have the same page stride")
+    for t in (k_cache, v_cache):
+        if not (t.is_contiguous() or t[0].is_contiguous()):
+            raise ValueError("a page of the cache must be contiguous")
+    _shape(lens, (B,), "lens")
+    tp, lp = _pointers(torch.int32, dev, block_table, lens)
+    return (pages, n, Hk, d, B, max_pages, page_stride, kind), (tp, lp, k_cache.data_ptr(),
+                                                                v_cache.data_ptr(), ksp, vsp)
+
+
+def kv_append_paged(k, v, k_cache, v_cache, block_table, lens, cu_seqlens=None, k_scale=None,
+                    v_scale=None, rope=None, positions=None, q=None, q_out=None):
+    """Append new tokens' k and v [Hk, T, d] (any strides with contiguous dims; a
+    tensor [T, Hk, d] goes in transposed) to paged caches [pages, Hk,
+    page_tokens, d], in place: of the storage dtype, or float8_e4m3fn with
+    scales fp32 [pages, Hk]. Sequence b's new tokens are rows cu_seqlens[b] ..
+    cu_seqlens[b+1] - 1 (int32 [B + 1] on the device; None: row b) at the
+    positions up to lens[b] - 1 (lens int32 [B]: with the new tokens), in pages
+    block_table[b] (int32 [B, max_pages]). rope (a ``rope_plan``) turns k and q
+    [H, T, d] on the way, at the positions in the cache or at ``positions``
+    (int32 [T]). Returns q turned (q_out, or a new tensor; rows outside every
+    sequence are not written), None without q."""
+    dt, dtype, dev = _dt(k), k.dtype, torch.cuda.current_device()
+    Hk, T, d = k.shape
+    _shape(v, (Hk, T, d), "v")
+    fields, (tp, lp, kcp, vcp, ksp, vsp) = _paged(k_cache, v_cache, k_scale, v_scale, block_table,
+                                                  lens, dtype, dev)
+    if fields[2] != Hk or fields[3] != d:
+        raise ValueError(f"k has {Hk} heads of {d} dims, the cache {fields[2]} of {fields[3]}")
+    kp, kh, kt = _strided(k, dtype, dev)
+    vp, vh, vt = _strided(v, dtype, dev)
+    H, qp, qh, qt, op, oh, ot, o = 0, None, 0, 0, None, 0, 0, None
+    if q is not None:
+        H = q.shape[0]
+        _shape(q, (H, T, d), "q")
+        _shape(q_out, (H, T, d), "q_out")
+        o = torch.empty(q.shape, dtype=dtype, device=q.device) if q_out is None else q_out
+        qp, qh, qt = _strided(q, dtype, dev)
+        op, oh, ot = _strided(o, dtype, dev)
+    elif q_out is not None:
+        raise ValueError("q_out given without q")
+    _shape(cu_seqlens, (fields[4] + 1,), "cu_seqlens")
+    _shape(positions, (T,), "positions")
+    cup, pp = _pointers(torch.int32, dev, cu_seqlens, positions)
+    desc = _abi.AppendDesc(fields, T, H, kh, kt, vh, vt, qh, qt, oh, ot)
+    _abi.check(_lib().blk_kv_append_paged(desc, rope, kp, vp, qp, cup, pp, tp, lp, kcp, vcp, ksp, vsp,
+                                          op, dt, torch._C._cuda_getCurrentRawStream(dev)),
+               "blk_kv_append_paged")
+    return o
+
+
+def decode_paged_desc(fields, n_heads, q_batch_stride, q_head_stride, alibi=False, scale=None):
+    """fields: those of blk_paged_desc in their order."""
+    return _abi.DecodePagedDesc(fields, n_heads, q_batch_stride, q_head_stride,
+                                -1.0 if scale is None else scale, 1 if alibi else 0)
+
+
+def attn_decode_paged_workspace_size(desc) -> int:
+    need = C.c_size_t(0)
+    _abi.check(_lib().blk_attn_decode_paged_workspace_size(C.byref(desc), C.byref(need)),
+               "blk_attn_decode_paged_workspace_size")
+    return need.value
+
+
+@functools.lru_cache(maxsize=256)
+def _decode_paged_plan(*args):
+    """(descriptor by reference, workspace bytes) of a call's sizes and _values."""
+    desc = decode_paged_desc(*args)
+    return C.byref(desc), attn_decode_paged_workspace_size(desc)
+
+
+def attn_decode_paged(q, k_cache, v_cache, block_table, lens, k_scale=None, v_scale=None,
+                      alibi=False, slopes=None, scale=None, out=None, workspace=None):
+    """One decode step over a paged cache: q [B, H, d] (newest token of each
+    sequence, at position lens[b] - 1; any strides with contiguous dims)
+    against caches [pages, Hk, page_tokens, d], in the storage dtype or
+    float8_e4m3fn with scales fp32 [pages, Hk]; sequence b's keys 0 .. lens[b] -
+    1 lie in pages block_table[b] (int32 [B, max_pages], lens int32 [B], both
+    on the device). Length 0: a zero row. Returns o [B, H, d]."""
+    dt, dtype, dev = _dt(q), q.dtype, torch.cuda.current_device()
+    B, H, d = q.shape
+    fields, (tp, lp, kp, vp, ksp, vsp) = _paged(k_cache, v_cache, k_scale, v_scale, block_table,
+                                                lens, dtype, dev)
+    if fields[3] != d or fields[4] != B:
+        raise ValueError(f"q {tuple(q.shape)} does not fit the cache's head_dim {fields[3]} or "
+                         f"block_table's {fields[4]} sequences")
+    _shape(slopes, (H,), "slopes")
+    _shape(out, (B, H, d), "out")
+    qp, qb, qh = _strided(q, dtype, dev)
+    desc, need = _decode_paged_plan(fields, H, qb, qh, *_values(alibi, scale))
+    sp = None if slopes is None else _pointers(torch.float32, dev, slopes)[0]
+    if out is None:
+        o = torch.empty((B, H, d), dtype=dtype, device=q.device)
+        op = o.data_ptr()
+    else:
+        o, (op,) = out, _pointers(dtype, dev, out)
+    fn = _lib().blk_attn_decode_paged
+    _abi.check(_with_workspace(
+        lambda wp, wn, st: fn(desc, qp, kp, vp, ksp, vsp, tp, lp, sp, op, wp, wn, dt, st),
+        workspace, need, dev), "blk_attn_decode_paged")
     return o
 
 

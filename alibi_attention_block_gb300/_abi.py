@@ -54,6 +54,45 @@ class DecodeSharedDesc(C.Structure):
                 ("head_dim", i64), ("prefix_len", i64), ("softmax_scale", f32), ("alibi", i32)]
 
 
+BLK_ROPE_PLAIN, BLK_ROPE_LINEAR, BLK_ROPE_BY_PARTS = 0, 1, 2
+BLK_CACHE_16BIT, BLK_CACHE_E4M3 = 0, 1
+
+
+class RopeDesc(C.Structure):
+    _fields_ = [("span", i32), ("interleaved", i32), ("base", C.c_double), ("scaling", i32),
+                ("amplitude", f32), ("factor", C.c_double), ("original_len", C.c_double),
+                ("beta_slow", C.c_double), ("beta_fast", C.c_double)]
+
+
+class RopePlan(C.Structure):
+    _fields_ = [("turns", C.c_uint64 * 128), ("pairs", i32), ("interleaved", i32),
+                ("amplitude", f32), ("check", i32)]
+
+
+class RopePosDesc(C.Structure):
+    _fields_ = [("tokens", i64), ("n_heads", i64), ("n_k_heads", i64), ("head_dim", i64),
+                ("inverse", i32), ("q_head_stride", i64), ("q_token_stride", i64),
+                ("q_out_head_stride", i64), ("q_out_token_stride", i64), ("k_head_stride", i64),
+                ("k_token_stride", i64), ("k_out_head_stride", i64), ("k_out_token_stride", i64)]
+
+
+class PagedDesc(C.Structure):
+    _fields_ = [("pages", i64), ("page_tokens", i64), ("n_kv_heads", i64), ("head_dim", i64),
+                ("batch", i64), ("max_pages", i64), ("page_stride", i64), ("kind", i32)]
+
+
+class AppendDesc(C.Structure):
+    _fields_ = [("cache", PagedDesc), ("tokens", i64), ("n_heads", i64), ("k_head_stride", i64),
+                ("k_token_stride", i64), ("v_head_stride", i64), ("v_token_stride", i64),
+                ("q_head_stride", i64), ("q_token_stride", i64), ("q_out_head_stride", i64),
+                ("q_out_token_stride", i64)]
+
+
+class DecodePagedDesc(C.Structure):
+    _fields_ = [("cache", PagedDesc), ("n_heads", i64), ("q_batch_stride", i64),
+                ("q_head_stride", i64), ("softmax_scale", f32), ("alibi", i32)]
+
+
 class MlpDesc(C.Structure):
     _fields_ = [("tokens", i64), ("hidden", i64), ("intermediate", i64), ("act", i32)]
 
@@ -128,6 +167,15 @@ _PROTOS = {
                                                         C.POINTER(C.c_size_t)]),
     "blk_attn_decode_shared": (C.c_int, [C.POINTER(DecodeSharedDesc), vp, vp, vp, vp, vp, vp, vp,
                                          vp, vp, C.c_size_t, C.c_int, vp]),
+    "blk_rope_plan_init": (C.c_int, [C.POINTER(RopeDesc), C.POINTER(RopePlan)]),
+    "blk_rope_positions": (C.c_int, [C.POINTER(RopePosDesc), C.POINTER(RopePlan), vp, vp, vp, vp, vp,
+                                     C.c_int, vp]),
+    "blk_kv_append_paged": (C.c_int, [C.POINTER(AppendDesc), C.POINTER(RopePlan), vp, vp, vp, vp, vp,
+                                      vp, vp, vp, vp, vp, vp, vp, C.c_int, vp]),
+    "blk_attn_decode_paged_workspace_size": (C.c_int, [C.POINTER(DecodePagedDesc),
+                                                       C.POINTER(C.c_size_t)]),
+    "blk_attn_decode_paged": (C.c_int, [C.POINTER(DecodePagedDesc), vp, vp, vp, vp, vp, vp, vp, vp,
+                                        vp, vp, C.c_size_t, C.c_int, vp]),
     "blk_forward_graph_create": (C.c_int, [C.POINTER(BlockDesc), C.POINTER(BlockWeights), vp, vp,
                                            vp, C.c_size_t, C.c_int, C.POINTER(vp), C.c_int,
                                            C.POINTER(i32), C.POINTER(C.c_int), C.POINTER(vp)]),

@@ -248,6 +248,24 @@ bool make_tmap_queries(CUtensorMap* m, DType dt, const void* base, uint64_t batc
     return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_pages(CUtensorMap* m, uint32_t elem_bytes, const void* base, uint64_t pages,
+                     uint64_t heads, uint64_t tokens, uint64_t d, uint64_t page_stride,
+                     uint32_t box_rows, uint32_t swizzle) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {d, tokens, heads, pages};
+    const cuuint64_t strides[3] = {d * elem_bytes, tokens * d * elem_bytes, page_stride * elem_bytes};
+    const cuuint32_t box[4] = {swizzle / elem_bytes, box_rows, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUresult r = fn(m, elem_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                             : CU_TENSOR_MAP_DATA_TYPE_UINT16,
+                          4, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 }  // namespace blk
 
 using namespace blk;

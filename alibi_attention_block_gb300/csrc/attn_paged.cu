@@ -1,0 +1,224 @@
+// K8 host side and merge: one decode step of attention over a paged cache. The kernel
+// (attn_paged.cuh) leaves a partial result for each CTA's stay in a unit; the merge
+// joins them: o = sum_i w_i O_i / sum_i w_i l_i, w_i = 2^(m_i - max m).
+#include <cmath>
+
+#include "attn_paged.h"
+
+namespace blk {
+
+namespace {
+
+constexpr int kTK = 128;
+constexpr int kMergeThreads = 128;
+
+struct MergeArgs {
+    const float* po;
+    const float2* pm;
+    const int64_t* cum;
+    const int32_t* lens;
+    void* o;
+    int64_t rows;  // batch * H
+    int batch, H, G, GP, groups, units, capacity, grid, pdl;
+};
+
+// The CTA whose range [c * W / n, (c + 1) * W / n) holds tile t, n CTAs in all (W >= n):
+// c * W < (t + 1) * n <= (c + 1) * W.
+__device__ __forceinline__ int cta_of(int64_t t, int64_t W, int n) {
+    return static_cast<int>(((t + 1) * n - 1) / W);
+}
+
+// D / 8 threads per row of 8 columns each.
+template <typename T, int D>
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const MergeArgs a) {
+    constexpr int kPer = D / 8, kRows = kMergeThreads / kPer;
+    if (a.pdl) pdl_wait();
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kPer;
+    const int col = threadIdx.x % kPer * 8;
+    if (threadIdx.x >= kRows * kPer || row >= a.rows) return;
+    const int b = static_cast<int>(row / a.H), h = static_cast<int>(row - static_cast<int64_t>(b) * a.H);
+    const int g = h / a.G, in = h - g * a.G;  // kv head, and head of its group
+    const int u = g * a.groups + in / 8;
+    const int n = min(max(a.lens[b], 0), a.capacity);
+    float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (n > 0) {
+        const int64_t W = a.cum[a.batch] * a.units, nt = (n + kTK - 1) / kTK;
+        const int64_t t0 = a.cum[b] * a.units + u * nt;
+        const int ctas = static_cast<int>(min(static_cast<int64_t>(a.grid), W));
+        const int c0 = cta_of(t0, W, ctas), c1 = cta_of(t0 + nt - 1, W, ctas);
+        const int64_t rec = (c0 + static_cast<int64_t>(b) * a.units + u) * a.GP + in % 8;
+        const float* p = a.po + rec * D + col;
+        const float2* s = a.pm + rec;
+        float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+        for (int k = 0; k <= c1 - c0; ++k) {
+            const float4* q = reinterpret_cast<const float4*>(p + static_cast<int64_t>(k) * a.GP * D);
+            const float4 x = q[0], y = q[1];
+            const float2 ml = s[static_cast<int64_t>(k) * a.GP];
+            const float mn = fmaxf(m, ml.x);
+            const float keep = m == -INFINITY ? 0.f : exp2f(m - mn);
+            const float w = ml.x == -INFINITY && ml.y == 0.f ? 0.f : exp2f(ml.x - (mn == -INFINITY ? 0.f : mn));
+            m = mn;
+            l = fmaf(l, keep, w * ml.y);
+            const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = fmaf(f[e], keep, w * v[e]);
+        }
+        const float inv = l == 0.f ? 0.f : 1.0f / l;  // no key seen: a zero row
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] *= inv;
+    }
+    store8(static_cast<T*>(a.o) + row * D + col, f);
+}
+
+template <typename T>
+cudaError_t launch_merge(const MergeArgs& a, int d, cudaStream_t s) {
+    const int per = kMergeThreads / (d / 8);
+    const dim3 grid(static_cast<unsigned>((a.rows + per - 1) / per)), block(kMergeThreads);
+    switch (d) {
+        case 64: return launch_pdl(a.pdl != 0, paged_merge_kernel<T, 64>, grid, block, 0, s, a);
+        case 128: return launch_pdl(a.pdl != 0, paged_merge_kernel<T, 128>, grid, block, 0, s, a);
+        default: return launch_pdl(a.pdl != 0, paged_merge_kernel<T, 160>, grid, block, 0, s, a);
+    }
+}
+
+#define REQUIRE(cond, ...)                                                \
+    do {                                                                  \
+        if (!(cond)) return report_error_status(BLK_EINVAL, __VA_ARGS__); \
+    } while (0)
+
+blk_status check_desc(const blk_decode_paged_desc* d) {
+    REQUIRE(d, "desc is NULL");
+    const blk_status st = check_paged_desc(&d->cache);
+    if (st != BLK_OK) return st;
+    if (d->cache.head_dim != 64 && d->cache.head_dim != 128 && d->cache.head_dim != 160)
+        return report_error_status(BLK_EUNSUPPORTED, "head_dim must be 64, 128 or 160");
+    REQUIRE(d->n_heads >= 1 && d->n_heads <= 16384 && d->n_heads % d->cache.n_kv_heads == 0,
+            "n_heads must be a positive multiple of n_kv_heads");
+    REQUIRE(d->q_batch_stride >= 0 && d->q_head_stride >= 0 && d->q_batch_stride % 2 == 0 &&
+                d->q_head_stride % 2 == 0 && d->q_batch_stride <= (int64_t(1) << 40) &&
+                d->q_head_stride <= (int64_t(1) << 40),
+            "q's strides must be even");
+    REQUIRE(d->cache.batch * d->n_heads <= (int64_t(1) << 28), "batch and n_heads too large");
+    REQUIRE(std::isfinite(d->softmax_scale), "softmax_scale must be finite");
+    REQUIRE(d->alibi == 0 || d->alibi == 1, "alibi must be 0 or 1");
+    return BLK_OK;
+}
+
+// query heads of a kernel's unit, and units of a kv head
+int unit_heads(int64_t G) { return G == 1 ? 1 : G <= 4 ? 4 : 8; }
+int64_t unit_groups(int64_t G) { return (G + 7) / 8; }
+
+struct Layout {
+    size_t po, pm, cum, total;
+};
+Layout layout(const blk_decode_paged_desc* d) {
+    const int64_t G = d->n_heads / d->cache.n_kv_heads;
+    const size_t recs = static_cast<size_t>(kPagedMaxGrid + d->cache.batch * d->cache.n_kv_heads * unit_groups(G)) *
+                        unit_heads(G);
+    auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+    Layout L;
+    L.po = 0;
+    L.pm = up(recs * d->cache.head_dim * 4);
+    L.cum = L.pm + up(recs * 8);
+    L.total = L.cum + up((d->cache.batch + 1) * 8);
+    return L;
+}
+
+}  // namespace
+
+}  // namespace blk
+
+using namespace blk;
+
+extern "C" {
+
+blk_status blk_attn_decode_paged_workspace_size(const blk_decode_paged_desc* d, size_t* bytes) {
+    const blk_status st = check_desc(d);
+    if (st != BLK_OK) return st;
+    REQUIRE(bytes, "bytes is NULL");
+    *bytes = layout(d).total;
+    return BLK_OK;
+}
+
+blk_status blk_attn_decode_paged(const blk_decode_paged_desc* d, const void* q, const void* k_cache,
+                                 const void* v_cache, const float* k_scale, const float* v_scale,
+                                 const int32_t* block_table, const int32_t* lens,
+                                 const float* alibi_slopes, void* o, void* workspace,
+                                 size_t ws_bytes, blk_dtype dt, blk_stream_t s) {
+    REQUIRE(dt == BLK_F16 || dt == BLK_BF16, "dtype must be BLK_F16 or BLK_BF16");
+    blk_status st = check_desc(d);
+    if (st != BLK_OK) return st;
+    PagedArgs a{};
+    st = make_paged_cache(&d->cache, k_cache, v_cache, k_scale, v_scale, block_table, lens, &a.c);
+    if (st != BLK_OK) return st;
+    REQUIRE(q && (reinterpret_cast<uintptr_t>(q) & 15u) == 0 && o &&
+                (reinterpret_cast<uintptr_t>(o) & 15u) == 0,
+            "q and o must be 16-byte aligned device pointers");
+    REQUIRE(d->alibi || !alibi_slopes, "alibi_slopes given with alibi = 0");
+    REQUIRE((reinterpret_cast<uintptr_t>(alibi_slopes) & 3u) == 0, "alibi_slopes must be 4-byte aligned");
+    if (d->alibi && !alibi_slopes && (d->n_heads & (d->n_heads - 1)) != 0)
+        return report_error_status(BLK_EUNSUPPORTED,
+                                   "standard ALiBi slopes need a power-of-two head count");
+    const Layout L = layout(d);
+    if (!workspace || ws_bytes < L.total || (reinterpret_cast<uintptr_t>(workspace) & 15u) != 0)
+        return report_error_status(BLK_EWORKSPACE, "workspace needs %zu bytes, 16-byte aligned", L.total);
+    int sms = 0;
+    if ((st = current_device_info(&sms, &a.err)) != BLK_OK) return st;
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(s);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.q = q;
+    a.qs[0] = d->q_batch_stride;
+    a.qs[1] = d->q_head_stride;
+    a.po = reinterpret_cast<float*>(ws + L.po);
+    a.pm = reinterpret_cast<float2*>(ws + L.pm);
+    a.cum = reinterpret_cast<int64_t*>(ws + L.cum);
+    a.slopes = alibi_slopes;
+    a.H = static_cast<int>(d->n_heads);
+    a.G = a.H / a.c.Hk;
+    a.GP = unit_heads(a.G);
+    a.groups = static_cast<int>(unit_groups(a.G));
+    a.units = a.c.Hk * a.groups;
+    a.scale = d->softmax_scale > 0.f ? d->softmax_scale : 1.0f / std::sqrt(static_cast<float>(a.c.d));
+    a.alibi = d->alibi;
+    a.pdl = pdl_allowed(cs);
+    const bool e8 = d->cache.kind == BLK_CACHE_E4M3;
+    const uint32_t elem = e8 ? 1 : 2;
+    const bool wide = !e8 || a.c.d >= 128, narrow = e8 && a.c.d % 128 != 0;
+    PagedMapSet tm;
+    for (int kv = 0; kv < 2; ++kv)
+        for (int w = 0; w < 2; ++w)
+            for (int i = 0; i < 2; ++i) {
+                // (without a slice of a width its place holds the other's)
+                const bool sixty_four = i == 0 ? !wide : narrow;
+                if (!make_tmap_pages(&tm.m[kv][w][i], elem, kv ? v_cache : k_cache, a.c.pages, a.c.Hk,
+                                     d->cache.page_tokens, a.c.d, d->cache.page_stride,
+                                     w == 0 ? static_cast<uint32_t>(d->cache.page_tokens) : 16u,
+                                     sixty_four ? 64 : 128))
+                    return report_error_status(BLK_EINVAL, "no tensor map for this cache");
+            }
+    cudaError_t e = dt == BLK_F16 ? launch_paged_f16(e8, tm, a, sms, cs) : launch_paged_bf16(e8, tm, a, sms, cs);
+    if (e == cudaSuccess) {
+        MergeArgs m{};
+        m.po = a.po;
+        m.pm = a.pm;
+        m.cum = a.cum;
+        m.lens = lens;
+        m.o = o;
+        m.rows = d->cache.batch * d->n_heads;
+        m.batch = a.c.B;
+        m.H = a.H;
+        m.G = a.G;
+        m.GP = a.GP;
+        m.groups = a.groups;
+        m.units = a.units;
+        m.capacity = a.c.max_pages << a.c.page_log2;
+        m.grid = a.grid;
+        m.pdl = a.pdl;
+        e = dt == BLK_F16 ? launch_merge<__half>(m, a.c.d, cs) : launch_merge<__nv_bfloat16>(m, a.c.d, cs);
+    }
+    return e == cudaSuccess ? BLK_OK
+                            : report_error_status(BLK_ECUDA, "paged decode launch: %s", cudaGetErrorString(e));
+}
+
+}  // extern "C"

@@ -1,0 +1,957 @@
+// K8: one decode step of attention over a paged cache of 16-bit values or e4m3 codes: the
+// kernel (its instantiations: attn_paged_*.cu; plan and merge: attn_paged.cu).
+//
+//   o[b, h] = sum_j p_j v_j,  p = softmax_j(scale q[b, h] . k_j - slope_h (lens[b] - 1 - j))
+//
+// over the keys j < lens[b] that page table[b][j / page] holds (the attention of
+// nnterp "stablelm" 03 Notes; ALiBi as in "Bloom in a sovereign engine", Contribution). A step
+// reads each key and value once for the 4 d flops of each of the group's few heads, so
+// it is bound by the cache's bytes, if the products cost little enough. On the CUDA cores
+// an 8-bit cache leaves 23 elements per clock and SM to be unpacked and multiplied G times
+// each, which is all that they can do at G = 4. So keys are the rows of a tensor-core product
+// and heads its few columns,
+//     S^T [128 keys, N] = K Q^T,   O^T [d, N] = V^T P^T,
+// and the codes go from the cache to the tensor core as they are: K and V tiles come by TMA
+// and are operands without any conversion.
+//
+// 8 bits: a product of kind f8f6f4 takes 8-bit operands on both sides, so the queries and the
+// weights are written as sums of e4m3 numbers, in columns of their own:
+//     q = 2^e (q1 + 2^-5 q2 + 2^-10 q3),   q1 = e4m3(2^-e q), q2 = e4m3(2^5 (2^-e q - q1)), ...
+// with 2^e such that the row's largest is in [128, 256). Each e4m3 holds 4 significant bits, a
+// remainder is at most 2^-5 of its number, so two parts hold a bf16 number and three an fp16
+// number exactly, down to 2^-23 and 2^-28 of the row's largest. (The columns are there
+// anyway: N is at least 16.) Weights, likewise: two parts (bf16) are at most 2^-9 off, relative, three
+// (fp16) 2^-14, which is less than the output's own rounding; their sums are of the 32-bit
+// weights. Where a weight is far below the largest, the error is absolute, 2^-22 and
+// 2^-27 of that one.
+// A page's scales are factors of its keys: that of K multiplies the score, that of V
+// the weight ahead of its rounding. So that the weight times scale stays in e4m3's range whatever the
+// scales are, the running reference that is subtracted is of score + log2(scale of V), not of the score.
+// The sum of the weights has the same reference; scales of V below 2^-40 count as 2^-40 in it.
+//
+// 16 bits: the operands in the storage type, weights rounded to it (as in the prefill kernels).
+//
+// Work: a unit is (sequence, kv head, up to eight of its query heads) of ceil(len / 128) key tiles. The tiles of all
+// units, in one line, are cut into equal ranges, one per CTA, whatever the lengths are; a CTA's
+// stay in a unit is a segment with a partial result (reference, sum, O), joined by the merge.
+// The lengths are device data: each CTA sums them itself. Tiles go from the newest key down.
+// A tile is 128 keys from up to eight pages: a lane of the loading warp for each 16 of them finds
+// the page one tile ahead, copies its rows by TMA and its scales by cp.async. A page id outside
+// the pool becomes a coordinate outside the tensor map, which fills with zeros; its keys are
+// masked. The last tile is copied in boxes of 16 keys, up to the product's step; rows behind
+// its end that the cache holds are cleared: 0 times what an unused entry holds need not be 0.
+// 7 warps: loading; MMA issue; four of softmax, a thread per key; queries.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "attn_paged.h"
+
+namespace blk {
+
+namespace {
+
+constexpr int kThreads = 224;
+constexpr int kTK = 128;
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <typename T, bool E8, int D, int GP>
+struct Cfg {
+    static constexpr int kElem = E8 ? 1 : 2;
+    // slices of a row: 128 bytes each (128-byte swizzle), then one of 64 (64-byte swizzle).
+    // head_dim 160: its last slice is part zeros, which TMA writes
+    static constexpr int kWide = E8 ? D / 128 : (D + 63) / 64;
+    static constexpr int kNarrow = E8 && D % 128 ? 1 : 0;
+    static constexpr int kRow = 128 * kWide + 64 * kNarrow;
+    static constexpr int kTile = kTK * kRow;
+    static constexpr int kStepKeys = 32 / kElem;  // keys of a product's step: 32 bytes of P
+    static constexpr int kParts = !E8 ? 1 : dt_traits<T>::mma_fmt == 0 ? 3 : 2;
+    static constexpr int kUsed = kParts * GP;  // columns with something in them
+    static constexpr int kN = kUsed <= 16 ? 16 : 32;
+    // ... and the operands' rows for them in groups of 8; what follows in shared
+    // memory makes up the rest (columns do not mix, and none of the rest is read)
+    static constexpr int kRows = (kUsed + 7) / 8 * 8;
+    static constexpr int kLd = kUsed == 3 ? 4 : kUsed == 12 ? 16 : kUsed == 24 ? 32 : kUsed;
+    static constexpr int kBlocks = D > 128 ? 2 : 1;  // of O's rows: 128 and 64
+    // two CTAs per SM, so that one's chain of scores, softmax and product fills the
+    // other's gaps; four where tiles are short, one where they are long
+    static constexpr int kCtas = E8 && D == 64 && kN == 16 ? 4 : kTile > 32768 ? 1 : 2;
+    static constexpr int kQBytes = kRows * kRow, kPBytes = kRows * 128 * kElem;
+    static constexpr int kFixed = 2 * kQBytes + 2 * kPBytes + 8 * 2 * 8 * 4 + 4 * 8 * 4 * 4 + 2 * 8 * 4 + 512 + 16;
+    static constexpr int kFit = (228 * 1024 / kCtas - 2048 - 64 - kFixed) / kTile;
+    static constexpr int kSlots = kFit < 6 ? kFit : 6;
+    static_assert(kSlots >= 3, "a ring of tiles");
+    static constexpr int kOffQ = kSlots * kTile;
+    static constexpr int kOffP = kOffQ + 2 * kQBytes;
+    static constexpr int kOffScale = kOffP + 2 * kPBytes;    // [8 tiles][K, V][8 groups of 16 keys]
+    static constexpr int kOffMax = kOffScale + 8 * 2 * 8 * 4;  // [2][8][4]
+    static constexpr int kOffSum = kOffMax + 2 * 8 * 4 * 4;    // [2][8][4]
+    static constexpr int kOffMul = kOffSum + 2 * 8 * 4 * 4;    // [2][8]
+    static constexpr int kOffBar = kOffMul + 2 * 8 * 4;
+    static constexpr int kOffSlot = kOffBar + 512;
+    static constexpr int kSmem = kOffSlot + 16 + 1024;  // + alignment slack
+    static_assert(kCtas * (kSmem + 1024 + 64) <= 228 * 1024, "shared memory of an SM");
+    // TMEM: S^T twice (by tile), O^T twice (by segment)
+    static constexpr uint32_t kColO = 2 * kN;
+    static constexpr uint32_t kCols = kN == 16 ? 128 : 256;
+    static_assert(2 * kN + 2 * kBlocks * kN <= static_cast<int>(kCols) && kCtas * kCols <= 512, "TMEM");
+    // weights are at most 2 (threshold below) times 128; 16 bits: as they are
+    static constexpr float kTop = E8 ? 128.f : 1.f;
+    static constexpr float kThreshold = E8 ? 1.f : 8.f;  // log2 of the largest weight before a rescale
+};
+
+template <int N>
+__device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&r)[N]) {
+    if constexpr (N == 1)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\t"
+                     "tcgen05.wait::ld.sync.aligned;" : "=r"(r[0]) : "r"(taddr) : "memory");
+    else if constexpr (N == 2)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];\n\t"
+                     "tcgen05.wait::ld.sync.aligned;"
+                     : "=r"(r[0]), "=r"(r[1]) : "r"(taddr) : "memory");
+    else if constexpr (N == 4)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\t"
+                     "tcgen05.wait::ld.sync.aligned;"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(taddr) : "memory");
+    else if constexpr (N == 8)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+                     "tcgen05.wait::ld.sync.aligned;"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                       "=r"(r[6]), "=r"(r[7]) : "r"(taddr) : "memory");
+    else if constexpr (N == 16)
+        tmem_ld16(taddr, r);
+    else
+        tmem_ld32(taddr, r);
+}
+template <int N>
+__device__ __forceinline__ void st_cols(uint32_t taddr, const uint32_t (&r)[N]) {
+    if constexpr (N == 1)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(r[0])
+                     : "memory");
+    else if constexpr (N == 2)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(taddr), "r"(r[0]),
+                     "r"(r[1]) : "memory");
+    else if constexpr (N == 4)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
+                     "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+    else if constexpr (N == 8)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                     ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+                     "r"(r[6]), "r"(r[7]) : "memory");
+    else if constexpr (N == 16)
+        tmem_st16_nowait(taddr, r);
+    else
+        tmem_st32_nowait(taddr, r);
+    tmem_st_wait();
+}
+
+// max over the warp's lanes: floats as integers of the same order
+__device__ __forceinline__ float warp_max(float v) {
+    int i = __float_as_int(v);
+    i = i < 0 ? i ^ 0x7fffffff : i;
+    i = __reduce_max_sync(0xffffffffu, i);
+    return __int_as_float(i < 0 ? i ^ 0x7fffffff : i);
+}
+
+// Descriptor of `off` (in 16 bytes) behind the one of d, added in the low word (the
+// address is its field and does not carry out of it).
+__device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t off) {
+    uint32_t lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(d));
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo + off), "r"(hi));
+    return r;
+}
+
+// Two numbers to e4m3 codes and back.
+__device__ __forceinline__ uint32_t to_codes(float x, float y) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float2 of_codes(uint32_t c) {
+    return __half22float2(
+        __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c), __NV_E4M3)));
+}
+// ... and the numbers' parts: c[i] holds the codes of part i of both.
+template <int PARTS>
+__device__ __forceinline__ void split_parts(float x, float y, uint32_t (&c)[PARTS]) {
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) {
+        c[i] = to_codes(x, y);
+        if (i + 1 < PARTS) {
+            const float2 f = of_codes(c[i]);
+            x = (x - f.x) * 32.f;
+            y = (y - f.y) * 32.f;
+        }
+    }
+}
+__device__ __forceinline__ void st_byte(uint32_t at, uint32_t v) {
+    asm volatile("st.shared.b8 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+
+// 4 bytes to shared memory, with nothing waited for ...
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// ... and an arrival once this thread's copies so far are there.
+__device__ __forceinline__ void arrive_behind_copies(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+template <int SLOTS>
+struct Bars {
+    uint32_t at;
+    static constexpr int kBytes = 208 + 16 * SLOTS;
+    __device__ __forceinline__ uint32_t q_full(int i) const { return at + 8u * i; }
+    __device__ __forceinline__ uint32_t q_empty(int i) const { return at + 16u + 8u * i; }
+    __device__ __forceinline__ uint32_t s_full(int i) const { return at + 32u + 8u * i; }
+    __device__ __forceinline__ uint32_t s_free(int i) const { return at + 48u + 8u * i; }
+    __device__ __forceinline__ uint32_t p_full(int i) const { return at + 64u + 8u * i; }
+    __device__ __forceinline__ uint32_t pv_done(int i) const { return at + 80u + 8u * i; }
+    __device__ __forceinline__ uint32_t o_free(int i) const { return at + 96u + 8u * i; }
+    __device__ __forceinline__ uint32_t max_full() const { return at + 112u; }
+    __device__ __forceinline__ uint32_t sum_full() const { return at + 120u; }
+    __device__ __forceinline__ uint32_t drain() const { return at + 128u; }
+    __device__ __forceinline__ uint32_t range_full() const { return at + 136u; }
+    __device__ __forceinline__ uint32_t scale_full(int i) const { return at + 144u + 8u * i; }
+    __device__ __forceinline__ uint32_t full(int i) const { return at + 208u + 8u * i; }
+    __device__ __forceinline__ uint32_t empty(int i) const { return at + 208u + 8u * (SLOTS + i); }
+    __device__ __forceinline__ void init() const {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(q_full(i), 1);
+            mbar_init(q_empty(i), 1 + 4);  // the products', and the softmax warps' with the factors
+            mbar_init(s_full(i), 1);
+            mbar_init(s_free(i), 4);
+            mbar_init(p_full(i), 4);
+            mbar_init(pv_done(i), 1);
+            mbar_init(o_free(i), 4);
+        }
+        mbar_init(max_full(), 4);
+        mbar_init(sum_full(), 4);
+        mbar_init(drain(), 1);
+        mbar_init(range_full(), 4);
+        for (int i = 0; i < 8; ++i) mbar_init(scale_full(i), 8);
+        for (int i = 0; i < SLOTS; ++i) {
+            mbar_init(full(i), 1);
+            mbar_init(empty(i), 1);
+        }
+    }
+};
+
+__device__ __forceinline__ int len_of(const PagedArgs& a, int b) {
+    return min(max(a.c.lens[b], 0), a.c.max_pages << a.c.page_log2);
+}
+
+// A CTA's segments: tiles [t, t + n) of unit (b, u), key tiles first ..
+// first + n - 1 of the unit; t counts all units' tiles.
+struct Segments {
+    int64_t t, end;
+    int b, u, first, n, len, it;
+    bool valid;
+    __device__ __forceinline__ void set() {
+        valid = t < end;
+        if (!valid) return;
+        const int left = (len + kTK - 1) / kTK - first;
+        n = static_cast<int>(min(static_cast<int64_t>(left), end - t));
+    }
+    // base: tiles ahead of sequence b0's first unit; the range starts in b0
+    __device__ __forceinline__ void start(const PagedArgs& a, int64_t lo, int64_t hi, int b0,
+                                          int64_t base) {
+        t = lo;
+        end = hi;
+        it = 0;
+        b = b0;
+        valid = t < end;
+        if (!valid) return;
+        len = len_of(a, b);
+        const int nt = (len + kTK - 1) / kTK;
+        u = static_cast<int>((t - base) / nt);
+        first = static_cast<int>((t - base) % nt);
+        set();
+    }
+    __device__ __forceinline__ void next(const PagedArgs& a) {
+        t += n;
+        ++it;
+        first = 0;
+        if (t < end && ++u == a.units) {
+            u = 0;
+            do {
+                len = len_of(a, ++b);
+            } while (len == 0);
+        }
+        set();
+    }
+};
+
+// The tiles of a CTA's segments in turn.
+struct Tile {
+    int t, it, b, u, row, keys;  // running number, segment; first key, keys from there on
+    bool first, last;            // of its segment
+};
+struct Tiles {
+    Segments c;
+    int t = 0, i = 0;
+    __device__ __forceinline__ bool next(const PagedArgs& a, Tile& x) {
+        if (!c.valid) return false;
+        x.t = t++;
+        x.it = c.it;
+        x.b = c.b;
+        x.u = c.u;
+        x.row = (c.first + c.n - 1 - i) * kTK;
+        x.keys = c.len - x.row;
+        x.first = i == 0;
+        x.last = ++i == c.n;
+        if (x.last) {
+            c.next(a);
+            i = 0;
+        }
+        return true;
+    }
+};
+
+// This CTA's range of tiles, by the four softmax warps: tiles [lo, hi), the first in sequence
+// b0, `base` tiles ahead of that sequence.
+struct Range {
+    int64_t lo, hi, base;
+    int b0;
+    int64_t sum[4];
+};
+__device__ __forceinline__ void find_range(const PagedArgs& a, Range& out, uint32_t range_full) {
+    const int t = static_cast<int>(threadIdx.x) - 64, lane = t & 31, w = t / 32;
+    // thread t sums the tiles of a run of sequences
+    const int per = (a.c.B + 127) / 128;
+    const int b_lo = min(t * per, a.c.B), b_hi = min(b_lo + per, a.c.B);
+    int64_t mine = 0;
+    for (int b = b_lo; b < b_hi; ++b) mine += (len_of(a, b) + kTK - 1) / kTK;
+    int64_t upto = mine;  // inclusive sum over the warp's threads, then over all
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (lane == 31) out.sum[w] = upto;
+    // (all four warps come here before any wait that can give up)
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    int64_t before = upto - mine, total = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (i < w) before += out.sum[i];
+        total += out.sum[i];
+    }
+    // with fewer tiles than CTAs, one for each of the first W (the merge counts
+    // on every CTA of a unit's span having some of it)
+    const int64_t W = total * a.units;
+    const int64_t ctas = min(static_cast<int64_t>(gridDim.x), W), me = blockIdx.x;
+    const int64_t lo = me < ctas ? me * W / ctas : 0, hi = me < ctas ? (me + 1) * W / ctas : 0;
+    if (t == 0) {
+        out.lo = lo;
+        out.hi = hi;
+    }
+    // the thread whose run holds the first tile finds its sequence
+    if (lo < hi && before * a.units <= lo && lo < (before + mine) * a.units) {
+        int64_t base = before * a.units;
+        int b = b_lo;
+        for (;; ++b) {
+            const int64_t nt = (len_of(a, b) + kTK - 1) / kTK * static_cast<int64_t>(a.units);
+            if (lo < base + nt) break;
+            base += nt;
+        }
+        out.b0 = b;
+        out.base = base;
+    }
+    if (me == 0) {
+        int64_t c = before;
+        for (int b = b_lo; b < b_hi; ++b) {
+            a.cum[b] = c;
+            c += (len_of(a, b) + kTK - 1) / kTK;
+        }
+        if (t == 0) a.cum[a.c.B] = total;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(range_full);
+}
+
+template <typename T, bool E8, int D, int GP>
+__device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& tm, Tiles tiles,
+                                           uint8_t* smem, uint32_t tmem, int warp, int lane) {
+    using C = Cfg<T, E8, D, GP>;
+    constexpr int kSlots = C::kSlots, N = C::kN;
+    const uint32_t sKV = smem_u32(smem);
+    const uint32_t sQ = sKV + C::kOffQ, sP = sKV + C::kOffP;
+    const Bars<kSlots> bar{sKV + C::kOffBar};
+    float* scales = reinterpret_cast<float*>(smem + C::kOffScale);
+    float* red_max = reinterpret_cast<float*>(smem + C::kOffMax);
+    float* red_sum = reinterpret_cast<float*>(smem + C::kOffSum);
+    float* factors = reinterpret_cast<float*>(smem + C::kOffMul);
+    const int lg = a.c.page_log2;
+    bool ok = true;
+    if (warp == 0) {
+        const uint64_t pol = l2_evict_first_policy();
+        int r = 0;  // tiles of K and V on their way so far
+        Tile x, y;
+        // the page of this lane's 16 keys, -1: none
+        auto find_page = [&](const Tile& z) -> int {
+            const int at = z.row + 16 * lane;
+            if (lane >= 8 || 16 * lane >= z.keys) return -1;
+            const int p = a.c.table[static_cast<int64_t>(z.b) * a.c.max_pages + (at >> lg)];
+            return p >= 0 && p < a.c.pages ? p : -1;
+        };
+        bool have = tiles.next(a, x), more = false;
+        int page = have ? find_page(x) : -1, page_next = -1;
+        while (have) {
+            more = tiles.next(a, y);
+            if (more) page_next = find_page(y);
+            const int g = x.u / a.groups;
+            const bool whole = x.keys >= kTK;
+            const int rows = whole ? kTK : (x.keys + C::kStepKeys - 1) / C::kStepKeys * C::kStepKeys;
+            // boxes of a page's rows, or of 16
+            const int box = whole ? min(kTK, 1 << lg) : 16;
+            const bool mine = lane < 8 && (16 * lane) % box == 0 && 16 * lane < rows;
+            const int from = (x.row + 16 * lane) & ((1 << lg) - 1);
+            for (int kv = 0; kv < 2; ++kv, ++r) {
+                const int sl = r % kSlots;
+                ok = __all_sync(0xffffffffu, mbar_wait(bar.empty(sl), ((r / kSlots) & 1) ^ 1u, a.err));
+                if (!ok) break;
+                if (kv == 0 && lane < 8) {
+                    // the scales of these 16 keys; negative: they are masked. The ring's
+                    // entry was read ahead of the product that has freed this slot
+                    float* dst = scales + (x.t & 7) * 16 + lane;
+                    if (E8 && page >= 0) {
+                        const int64_t at = static_cast<int64_t>(page) * a.c.Hk + g;
+                        cp_async4(smem_u32(dst), a.c.k_scale + at);
+                        cp_async4(smem_u32(dst + 8), a.c.v_scale + at);
+                        arrive_behind_copies(bar.scale_full(x.t & 7));
+                    } else {
+                        dst[0] = page >= 0 ? 1.f : -1.f;
+                        dst[8] = 1.f;
+                        mbar_arrive(bar.scale_full(x.t & 7));
+                    }
+                }
+                if (lane == 0) mbar_expect_tx(bar.full(sl), rows * C::kRow);
+                __syncwarp();
+                if (mine) {
+                    const uint32_t dst = sKV + sl * C::kTile;
+                    const CUtensorMap* m = tm.m[kv][whole ? 0 : 1];
+                    const int p = page >= 0 ? page : a.c.pages;  // outside: zeros
+#pragma unroll
+                    for (int s = 0; s < C::kWide; ++s)
+                        tma_load_4d_hint(dst + s * kTK * 128 + lane * 16 * 128, m, bar.full(sl),
+                                         s * 128 / C::kElem, from, g, p, pol);
+                    if (C::kNarrow)
+                        tma_load_4d_hint(dst + C::kWide * kTK * 128 + lane * 16 * 64, m + 1, bar.full(sl),
+                                         C::kWide * 128, from, g, p, pol);
+                }
+            }
+            if (!ok) break;
+            x = y;
+            page = page_next;
+            have = more;
+        }
+        // whatever the others met, no copy lands behind this block's end
+        cp_async_commit();
+        cp_async_wait<0>();
+        for (int i = r > kSlots ? r - kSlots : 0; i < r; ++i)
+            mbar_wait(bar.full(i % kSlots), (i / kSlots) & 1, a.err);
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t fmt = E8 ? 0 : dt_traits<T>::mma_fmt;  // e4m3 is 0 too
+            constexpr uint32_t idesc_s = make_idesc_f16(fmt, kTK, N, false);
+            // A MN-major
+            constexpr uint32_t idesc_o = make_idesc_f16(fmt, D == 64 ? 64 : 128, N, false) | (1u << 15);
+            constexpr uint32_t idesc_o2 = make_idesc_f16(fmt, 64, N, false) | (1u << 15);
+            constexpr uint32_t kSlotStep = C::kTile >> 4;
+            // offsets in 16 bytes of the narrow slices, and of V's second block of rows
+            constexpr uint32_t kNarrowK = (C::kWide * kTK * 128) >> 4;
+            constexpr uint32_t kNarrowQ = (C::kWide * C::kRows * 128) >> 4;
+            constexpr uint32_t kSecond = (D > 128 ? (E8 ? 1 : 2) * kTK * 128 : 0) >> 4;
+            const uint64_t dk0 = make_sdesc_sw128(sKV, 16, 1024), dk0n = make_sdesc_sw64(sKV, 16, 512);
+            const uint64_t dv0 = make_sdesc_sw128(sKV, kTK * 128, 1024);
+            const uint64_t dq0 = make_sdesc_sw128(sQ, 16, 1024), dq0n = make_sdesc_sw64(sQ, 16, 512);
+            const uint64_t dp0 = make_sdesc_sw128(sP, 16, 1024);
+            auto mma = [&](uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t acc) {
+                if (E8) tc_mma_f8_ss(d, da, db, idesc, acc);
+                else tc_mma_ss(d, da, db, idesc, acc);
+            };
+            // S^T = K Q^T: the keys and (first tile) queries are there, and the
+            // softmax has read the S buffer's last tile
+            auto s_ready = [&](const Tile& x) {
+                const int r = 2 * x.t;
+                return mbar_test(bar.full(r % kSlots), (r / kSlots) & 1) &&
+                       (!x.first || mbar_test(bar.q_full(x.it & 1), (x.it >> 1) & 1)) &&
+                       (x.t < 2 || mbar_test(bar.s_free(x.t & 1), ((x.t >> 1) - 1) & 1));
+            };
+            auto issue_s = [&](const Tile& x) {
+                tc_fence_after();
+                const int sl = 2 * x.t % kSlots;
+                const uint32_t k = sl * kSlotStep, q = (x.it & 1) * (C::kQBytes >> 4);
+#pragma unroll
+                for (int ks = 0; ks < D * C::kElem / 32; ++ks) {
+                    const uint32_t in = (ks % 4) * 2;
+                    if (ks / 4 < C::kWide)
+                        mma(tmem + N * (x.t & 1), desc_at(dk0, k + (ks / 4) * ((kTK * 128) >> 4) + in),
+                            desc_at(dq0, q + (ks / 4) * ((C::kRows * 128) >> 4) + in), idesc_s, ks > 0 ? 1u : 0u);
+                    else
+                        mma(tmem + N * (x.t & 1), desc_at(dk0n, k + kNarrowK + in),
+                            desc_at(dq0n, q + kNarrowQ + in), idesc_s, ks > 0 ? 1u : 0u);
+                }
+                tc_commit(bar.s_full(x.t & 1));
+                tc_commit(bar.empty(sl));
+                if (x.last) tc_commit(bar.q_empty(x.it & 1));
+            };
+            // O^T += V^T P^T: the values and P are there, and (first tile) the O
+            // buffer's last segment has been read out
+            auto pv_ready = [&](const Tile& x) {
+                const int r = 2 * x.t + 1;
+                return mbar_test(bar.full(r % kSlots), (r / kSlots) & 1) &&
+                       mbar_test(bar.p_full(x.t & 1), (x.t >> 1) & 1) &&
+                       (!x.first || x.it < 2 || mbar_test(bar.o_free(x.it & 1), ((x.it >> 1) - 1) & 1));
+            };
+            auto issue_pv = [&](const Tile& x) {
+                tc_fence_after();
+                const int sl = (2 * x.t + 1) % kSlots;
+                const uint32_t v = sl * kSlotStep, p = (x.t & 1) * (C::kPBytes >> 4);
+                const uint32_t o = tmem + C::kColO + C::kBlocks * N * (x.it & 1);
+                const int steps = (min(x.keys, kTK) + C::kStepKeys - 1) / C::kStepKeys;
+#pragma unroll
+                for (int ks = 0; ks < kTK / C::kStepKeys; ++ks) {
+                    if (ks >= steps) continue;
+                    const uint64_t dp = desc_at(dp0, p + (ks / 4) * ((C::kRows * 128) >> 4) + (ks % 4) * 2);
+                    const uint32_t acc = !x.first || ks > 0 ? 1u : 0u;
+                    constexpr uint32_t kStep = (C::kStepKeys * 128) >> 4;
+                    if (C::kWide > 0)
+                        mma(o, desc_at(dv0, v + ks * kStep), dp, idesc_o, acc);
+                    else  // 64-byte rows
+                        mma(o, desc_at(dk0n, v + ks * (kStep / 2)), dp, idesc_o, acc);
+                    if (C::kBlocks > 1) {
+                        if (C::kNarrow)
+                            mma(o + N, desc_at(dk0n, v + kSecond + ks * (kStep / 2)), dp, idesc_o2, acc);
+                        else
+                            mma(o + N, desc_at(dv0, v + kSecond + ks * kStep), dp, idesc_o2, acc);
+                    }
+                }
+                tc_commit(bar.pv_done(x.t & 1));
+                tc_commit(bar.empty(sl));
+            };
+            Tile now, nxt;
+            bool have = tiles.next(a, now), more = true, s_out = false, pv_out = false;
+            bool ahead = false;  // S of nxt is out
+            if (have) more = tiles.next(a, nxt);
+            uint64_t t0 = globaltimer_ns();
+            for (uint32_t spin = 1; have; ++spin) {
+                bool did = false;
+                if (!s_out) {
+                    if (s_ready(now)) {
+                        issue_s(now);
+                        s_out = did = true;
+                    }
+                } else if (more && !ahead && s_ready(nxt)) {
+                    issue_s(nxt);
+                    ahead = did = true;
+                }
+                if (s_out && !pv_out && pv_ready(now)) {
+                    issue_pv(now);
+                    pv_out = did = true;
+                }
+                if (pv_out) {  // on to the next tile
+                    have = more;
+                    now = nxt;
+                    s_out = ahead;
+                    pv_out = ahead = false;
+                    if (more) more = tiles.next(a, nxt);
+                }
+                if (did) {
+                    spin = 0;
+                } else if (spin == 1) {
+                    t0 = globaltimer_ns();
+                } else if ((spin & 63u) == 0u && globaltimer_ns() - t0 > kWaitLimitNs) {
+                    report_error(a.err, DEV_ERR_TIMEOUT);
+                    break;
+                }
+            }
+            // ... and no product
+            tc_commit(bar.drain());
+            mbar_wait(bar.drain(), 0, a.err);
+        }
+    } else if (warp == 6) {
+        // queries: rows of the operand are part * GP + head
+        Segments& c = tiles.c;
+        constexpr int kPairs = (D + 63) / 64;  // of neighbouring dims, per lane
+        while (ok && c.valid) {
+            const int qb = c.it & 1;
+            const int g = c.u / a.groups, h0 = g * a.G + (c.u - g * a.groups) * 8;
+            const int heads = min(GP, (g + 1) * a.G - h0);
+            float2 f[GP][kPairs];
+#pragma unroll
+            for (int h = 0; h < GP; ++h) {
+                const T* q = static_cast<const T*>(a.q) + c.b * a.qs[0] + (h0 + h) * a.qs[1];
+#pragma unroll
+                for (int i = 0; i < kPairs; ++i) {
+                    const int p = lane + 32 * i;
+                    f[h][i] = h < heads && 2 * p < D
+                                  ? dt_traits<T>::unpack2(*reinterpret_cast<const uint32_t*>(q + 2 * p))
+                                  : make_float2(0.f, 0.f);
+                }
+            }
+            ok = __all_sync(0xffffffffu, mbar_wait(bar.q_empty(qb), ((c.it >> 1) & 1) ^ 1u, a.err));
+            if (!ok) break;
+            const uint32_t dst = sQ + qb * C::kQBytes;
+#pragma unroll
+            for (int h = 0; h < GP; ++h) {
+                float down = 1.f, up = 1.f;
+                if (E8) {
+                    uint32_t most = 0;
+#pragma unroll
+                    for (int i = 0; i < kPairs; ++i) {
+                        const uint32_t x = __float_as_uint(f[h][i].x) & 0x7fffffffu;
+                        const uint32_t y = __float_as_uint(f[h][i].y) & 0x7fffffffu;
+                        if (x < 0x7f800000u) most = max(most, x);
+                        if (y < 0x7f800000u) most = max(most, y);
+                    }
+                    most = __reduce_max_sync(0xffffffffu, most);
+                    const int e = most ? max(static_cast<int>(most >> 23) - 127 - 7, -100) : 0;
+                    down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                    up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+                }
+                if (lane == 0) factors[qb * 8 + h] = up * a.scale * kLog2e;
+#pragma unroll
+                for (int i = 0; i < kPairs; ++i) {
+                    const int col = 2 * (lane + 32 * i) * C::kElem;  // byte of the row
+                    if (2 * (lane + 32 * i) >= D) continue;
+                    uint32_t c8[C::kParts];
+                    if (E8) {
+                        split_parts<C::kParts>(f[h][i].x * down, f[h][i].y * down, c8);
+                        // an infinity is no code: a NaN, as its scores' softmax is
+                        if (isinf(f[h][i].x)) c8[0] |= 0x7fu;
+                        if (isinf(f[h][i].y)) c8[0] |= 0x7f00u;
+                    } else {
+                        c8[0] = dt_traits<T>::pack2(f[h][i].x, f[h][i].y);
+                    }
+#pragma unroll
+                    for (int s = 0; s < C::kParts; ++s) {
+                        const int n = s * GP + h;
+                        uint32_t at;
+                        if (col < 128 * C::kWide)
+                            at = dst + (col / 128) * C::kRows * 128 + n * 128 + ((col & 127) ^ ((n & 7) << 4));
+                        else
+                            at = dst + C::kWide * C::kRows * 128 + n * 64 +
+                                 ((col - 128 * C::kWide) ^ (((n >> 1) & 3) << 4));
+                        if (E8)
+                            asm volatile("st.shared.b16 [%0], %1;" ::"r"(at),
+                                         "h"(static_cast<uint16_t>(c8[s])) : "memory");
+                        else
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(c8[s]) : "memory");
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar.q_full(qb));
+            c.next(a);
+        }
+    } else {
+        Segments& c = tiles.c;
+        const int quarter = warp & 3;
+        const int key = quarter * 32 + lane;  // TMEM lane: key of a tile
+        const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+        const uint32_t tS = tmem + lane_off, tO = tmem + lane_off + C::kColO;
+        int t = 0;
+        // a segment's O is in TMEM until its last PV has completed: read out
+        // behind the next segment's first tile
+        bool pend = false;
+        int pend_t = 0, pend_buf = 0;
+        int64_t pend_rec = 0;
+        auto read_out = [&]() -> bool {
+            if (!mbar_wait(bar.pv_done(pend_t & 1), (pend_t >> 1) & 1, a.err)) return false;
+            tc_fence_after();
+            uint32_t o[C::kBlocks][C::kLd];
+#pragma unroll
+            for (int mb = 0; mb < C::kBlocks; ++mb)
+                ld_cols<C::kLd>(tO + N * (C::kBlocks * pend_buf + mb), o[mb]);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar.o_free(pend_buf));
+#pragma unroll
+            for (int mb = 0; mb < C::kBlocks; ++mb) {
+                // a block of 64 rows takes 16 lanes of each quarter
+                const bool half = D == 64 || mb == 1;
+                const int dim = half ? mb * 128 + quarter * 16 + lane : key;
+                if ((!half || lane < 16) && dim < D) {
+#pragma unroll
+                    for (int h = 0; h < GP; ++h) {
+                        float v = __uint_as_float(o[mb][h]);
+                        if (C::kParts > 1) v = fmaf(__uint_as_float(o[mb][GP + h]), 1.f / 32, v);
+                        if (C::kParts > 2)
+                            v = fmaf(__uint_as_float(o[mb][(C::kParts - 1) * GP + h]), 1.f / 1024, v);
+                        a.po[(pend_rec * GP + h) * D + dim] = v * (1.f / C::kTop);
+                    }
+                }
+                __syncwarp();
+            }
+            return true;
+        };
+        while (ok && c.valid) {
+            float m[GP], l[GP], slope[GP], mul[GP];
+            if (!(ok = mbar_wait(bar.q_full(c.it & 1), (c.it >> 1) & 1, a.err))) break;
+            const int g = c.u / a.groups, h0 = g * a.G + (c.u - g * a.groups) * 8;
+#pragma unroll
+            for (int h = 0; h < GP; ++h) {
+                m[h] = -INFINITY;
+                l[h] = 0.f;
+                mul[h] = factors[(c.it & 1) * 8 + h];
+                slope[h] = 0.f;
+                if (a.alibi) {
+                    const int hq = min(h0 + h, a.H - 1);
+                    slope[h] = kLog2e * (a.slopes ? a.slopes[hq]
+                                                  : exp2f(-8.0f * static_cast<float>(hq + 1) /
+                                                          static_cast<float>(a.H)));
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar.q_empty(c.it & 1));
+            for (int i = 0; i < c.n; ++i, ++t) {
+                const int row = (c.first + c.n - 1 - i) * kTK;
+                const int keys = c.len - row;
+                if (!mbar_wait(bar.scale_full(t & 7), (t >> 3) & 1, a.err) ||
+                    !mbar_wait(bar.s_full(t & 1), (t >> 1) & 1, a.err)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                uint32_t r[C::kLd];
+                ld_cols<C::kLd>(tS + N * (t & 1), r);
+                const float ks = scales[(t & 7) * 16 + key / 16];
+                const float vs = scales[(t & 7) * 16 + 8 + key / 16];
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar.s_free(t & 1));
+                const bool seen = key < keys && !(ks < 0.f);
+                const float back = static_cast<float>(row + key - (c.len - 1));
+                // the scale of V is at most 2^up
+                const int up = static_cast<int>((__float_as_uint(vs) + 0x7fffffu) >> 23) - 127;
+                const float shift = E8 ? static_cast<float>(max(up, -40)) : 0.f;
+                float s[GP];
+                float* rm = red_max + (t & 1) * 32;
+#pragma unroll
+                for (int h = 0; h < GP; ++h) {
+                    float v = __uint_as_float(r[h]);
+                    if (C::kParts > 1) v = fmaf(__uint_as_float(r[GP + h]), 1.f / 32, v);
+                    if (C::kParts > 2)
+                        v = fmaf(__uint_as_float(r[(C::kParts - 1) * GP + h]), 1.f / 1024, v);
+                    s[h] = seen ? fmaf(v, E8 ? mul[h] * ks : mul[h], slope[h] * back) : -INFINITY;
+                    const float w = warp_max(s[h] + shift);
+                    if (lane == h) rm[h * 4 + quarter] = w;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar.max_full());
+                if (!mbar_wait(bar.max_full(), t & 1, a.err)) {
+                    ok = false;
+                    break;
+                }
+                // the same decision in every thread
+                float corr[GP];
+                bool moved = false;
+#pragma unroll
+                for (int h = 0; h < GP; ++h) {
+                    const float4 w = *reinterpret_cast<const float4*>(rm + h * 4);
+                    const float mx = fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w));
+                    corr[h] = 1.f;
+                    if (mx > m[h] + C::kThreshold) {
+                        corr[h] = ex2_approx(m[h] - mx);
+                        m[h] = mx;
+                        moved = true;
+                    }
+                }
+                // P^T buffer t & 1 was read by the PV of tile t - 2
+                if (t > 1 && !mbar_wait(bar.pv_done(t & 1), ((t >> 1) - 1) & 1, a.err)) {
+                    ok = false;
+                    break;
+                }
+                float p[GP];
+#pragma unroll
+                for (int h = 0; h < GP; ++h) {
+                    // (nothing seen so far: 0, not a NaN)
+                    p[h] = ex2_approx(s[h] - (m[h] == -INFINITY ? 0.f : m[h]));
+                    l[h] = fmaf(l[h], corr[h], p[h]);
+                }
+                const uint32_t p_buf = sP + (t & 1) * C::kPBytes;
+                if constexpr (E8) {
+                    const float top = vs * C::kTop;
+                    constexpr int kStep = GP > 1 ? 2 : 1;
+#pragma unroll
+                    for (int h = 0; h < GP; h += kStep) {
+                        uint32_t c8[C::kParts];
+                        split_parts<C::kParts>(p[h] * top, GP > 1 ? p[h + kStep - 1] * top : 0.f, c8);
+#pragma unroll
+                        for (int q = 0; q < C::kParts; ++q)
+#pragma unroll
+                            for (int e = 0; e < kStep; ++e) {
+                                const int n = q * GP + h + e;
+                                st_byte(p_buf + n * 128 + (key ^ ((n & 7) << 4)), c8[q] >> (8 * e));
+                            }
+                    }
+                } else {
+                    const uint32_t p_row = p_buf + (key / 64) * C::kRows * 128;
+#pragma unroll
+                    for (int h = 0; h < GP; ++h) {
+                        const uint32_t at =
+                            p_row + h * 128 + (((key & 63) * 2) ^ (static_cast<uint32_t>(h & 7) << 4));
+                        const uint16_t bits = static_cast<uint16_t>(dt_traits<T>::pack2(p[h], 0.f));
+                        asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(bits) : "memory");
+                    }
+                }
+                if (keys < kTK && (keys & 15) && quarter == 0) {
+                    // values behind the tile's end, up to the next copied box
+                    const int rv = 2 * t + 1, sl = rv % kSlots;
+                    if (!mbar_wait(bar.full(sl), (rv / kSlots) & 1, a.err)) {
+                        ok = false;
+                        break;
+                    }
+                    const int n = 16 - (keys & 15);
+                    const uint32_t at = sKV + sl * C::kTile;
+#pragma unroll
+                    for (int w = 0; w < C::kWide; ++w)
+                        for (int x = lane; x < 8 * n; x += 32)
+                            st_shared_v4(at + w * kTK * 128 + keys * 128 + x * 16, 0u, 0u, 0u, 0u);
+                    if (C::kNarrow)
+                        for (int x = lane; x < 4 * n; x += 32)
+                            st_shared_v4(at + C::kWide * kTK * 128 + keys * 64 + x * 16, 0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+                if (i > 0 && moved) {
+                    if (!mbar_wait(bar.pv_done((t - 1) & 1), ((t - 1) >> 1) & 1, a.err)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int mb = 0; mb < C::kBlocks; ++mb) {
+                        uint32_t o[C::kLd];
+                        const uint32_t col = tO + N * (C::kBlocks * (c.it & 1) + mb);
+                        ld_cols<C::kLd>(col, o);
+#pragma unroll
+                        for (int n = 0; n < C::kUsed; ++n)
+                            o[n] = __float_as_uint(__uint_as_float(o[n]) * corr[n % GP]);
+                        st_cols<C::kLd>(col, o);
+                    }
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar.p_full(t & 1));
+                if (pend) {
+                    ok = read_out();
+                    pend = false;
+                    if (!ok) break;
+                }
+            }
+            if (!ok) break;
+            // the segment's result
+#pragma unroll
+            for (int h = 0; h < GP; ++h) {
+                float v = l[h];
+#pragma unroll
+                for (int x = 16; x > 0; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
+                if (lane == h) red_sum[(c.it & 1) * 32 + h * 4 + quarter] = v;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar.sum_full());
+            if (!mbar_wait(bar.sum_full(), c.it & 1, a.err)) {
+                ok = false;
+                break;
+            }
+            const int64_t rec = static_cast<int64_t>(blockIdx.x) +
+                                (static_cast<int64_t>(c.b) * a.units + c.u);
+            pend = true;
+            pend_t = t - 1;
+            pend_buf = c.it & 1;
+            pend_rec = rec;
+            if (quarter == 0 && lane < GP) {
+                const float4 w = *reinterpret_cast<const float4*>(red_sum + (c.it & 1) * 32 + lane * 4);
+                float mh = m[0];
+#pragma unroll
+                for (int h = 1; h < GP; ++h)
+                    if (lane == h) mh = m[h];
+                a.pm[rec * GP + lane] = make_float2(mh, (w.x + w.y) + (w.z + w.w));
+            }
+            c.next(a);
+        }
+        if (ok && pend) ok = read_out();
+    }
+}
+
+template <typename T, bool E8, int D, int GP>
+__global__ void __launch_bounds__(kThreads, (Cfg<T, E8, D, GP>::kCtas))
+    paged_kernel(const __grid_constant__ PagedMapSet tm, const __grid_constant__ PagedArgs a) {
+    using C = Cfg<T, E8, D, GP>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Range range;
+    uint8_t* smem = align_1024(smem_raw);
+    const Bars<C::kSlots> bar{smem_u32(smem) + C::kOffBar};
+    static_assert(Bars<C::kSlots>::kBytes <= 512, "barrier space");
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffSlot);
+    const int warp = threadIdx.x / 32;
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        bar.init();
+        fence_barrier_init();
+        for (int i = 0; i < 4; ++i) tma_prefetch_desc(&tm.m[i / 2][i % 2][0]);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), C::kCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    if (a.pdl) pdl_wait();
+    if (warp >= 2 && warp < 6) find_range(a, range, bar.range_full());
+    if (mbar_wait(bar.range_full(), 0, a.err)) {
+        Tiles tiles;
+        tiles.c.start(a, range.lo, range.hi, range.b0, range.base);
+        const PagedMaps maps{{{tm.m[0][0], tm.m[0][1]}, {tm.m[1][0], tm.m[1][1]}}};
+        paged_body<T, E8, D, GP>(a, maps, tiles, smem, tmem, warp, lane);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, C::kCols);
+    if (a.pdl) pdl_launch_dependents();
+}
+
+template <typename T, bool E8, int D, int GP>
+cudaError_t launch_paged_g(const PagedMapSet& tm, PagedArgs& a, int sms, cudaStream_t s) {
+    using C = Cfg<T, E8, D, GP>;
+    auto kern = paged_kernel<T, E8, D, GP>;
+    const cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(kern), C::kSmem);
+    if (e != cudaSuccess) return e;
+    const int64_t room = static_cast<int64_t>(a.c.max_pages) << a.c.page_log2;
+    const int64_t most = static_cast<int64_t>(a.c.B) * a.units * ((room + kTK - 1) / kTK);
+    int64_t grid = C::kCtas * sms;
+    grid = grid < kPagedMaxGrid ? grid : kPagedMaxGrid;
+    a.grid = static_cast<int>(grid < most ? grid : most);
+    return launch_pdl(a.pdl != 0, kern, dim3(a.grid), dim3(kThreads), C::kSmem, s, tm,
+                      static_cast<const PagedArgs&>(a));
+}
+
+template <typename T, bool E8, int D>
+cudaError_t launch_paged_d(const PagedMapSet& tm, PagedArgs& a, int sms, cudaStream_t s) {
+    switch (a.GP) {
+        case 1: return launch_paged_g<T, E8, D, 1>(tm, a, sms, s);
+        case 4: return launch_paged_g<T, E8, D, 4>(tm, a, sms, s);
+        case 8: return launch_paged_g<T, E8, D, 8>(tm, a, sms, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+template <typename T, bool E8>
+cudaError_t launch_paged_t(const PagedMapSet& tm, PagedArgs& a, int sms, cudaStream_t s) {
+    switch (a.c.d) {
+        case 64: return launch_paged_d<T, E8, 64>(tm, a, sms, s);
+        case 128: return launch_paged_d<T, E8, 128>(tm, a, sms, s);
+        case 160: return launch_paged_d<T, E8, 160>(tm, a, sms, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+}  // namespace blk

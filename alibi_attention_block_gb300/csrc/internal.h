@@ -313,5 +313,11 @@ bool make_tmap_3d(CUtensorMap* m, DType dt, const void* base, uint64_t planes, u
 // one kv head, a row of 64 columns each, group index fastest.
 bool make_tmap_queries(CUtensorMap* m, DType dt, const void* base, uint64_t batch,
                        uint64_t kv_heads, uint64_t group, uint64_t d, uint32_t box_batch);
+// 4D map of a paged cache [pages, heads, tokens, d] of elem_bytes (1 or 2; pages page_stride
+// elements apart) with a {swizzle / elem_bytes, box_rows, 1, 1} box: swizzle 128 or 64, the bytes
+// of a box's rows.
+bool make_tmap_pages(CUtensorMap* m, uint32_t elem_bytes, const void* base, uint64_t pages,
+                     uint64_t heads, uint64_t tokens, uint64_t d, uint64_t page_stride,
+                     uint32_t box_rows, uint32_t swizzle);
 
 }  // namespace blk

@@ -279,6 +279,151 @@ blk_status blk_attn_decode_shared(const blk_decode_shared_desc* d, const void* q
                                   const float* alibi_slopes, void* o, void* workspace,
                                   size_t ws_bytes, blk_dtype dt, blk_stream_t s);
 
+/* ---- rotary at given positions ---------------------------------------- */
+
+typedef enum {
+    BLK_ROPE_PLAIN = 0,    /* theta_j = base^(-2j/span), radians per position */
+    BLK_ROPE_LINEAR = 1,   /* theta_j / factor (positions interpolated) */
+    BLK_ROPE_BY_PARTS = 2  /* by a pair's turns in the original context, r_j = original_len theta_j /
+                              (2 pi): g theta_j + (1 - g) theta_j / factor with
+                              g = clamp((r_j - beta_slow) / (beta_fast - beta_slow), 0, 1) */
+} blk_rope_scaling;
+
+typedef struct {
+    int32_t span;         /* 2..256, even: the first span dims of a head are turned */
+    int32_t interleaved;  /* 0: pair j is dims (j, j + span/2); 1: dims (2j, 2j + 1) */
+    double base;          /* >= 1 */
+    int32_t scaling;      /* blk_rope_scaling */
+    float amplitude;      /* > 0: turned dims are multiplied by it (1: a rotation) */
+    double factor;        /* LINEAR and BY_PARTS: >= 1 */
+    double original_len, beta_slow, beta_fast; /* BY_PARTS; beta_fast > beta_slow */
+} blk_rope_desc;
+
+/* What the calls below take, made once per rotary by blk_rope_plan_init (host
+ * memory of the caller's; nothing to free, may be copied). */
+typedef struct {
+    uint64_t turns[128];  /* angle of pair j per position, in 2^-64 turns */
+    int32_t pairs, interleaved;
+    float amplitude;
+    int32_t check;
+} blk_rope_plan;
+
+/* Host arithmetic in 64 bits only. An angle is position * turns modulo 2^64, so
+ * it is as good at position 2^31 - 1 as at 1 (2^-24 of a turn). */
+blk_status blk_rope_plan_init(const blk_rope_desc* d, blk_rope_plan* plan);
+
+typedef struct {
+    int64_t tokens;               /* 1 .. 2^30 */
+    int64_t n_heads, n_k_heads;   /* of q, of k (0: no k) */
+    int64_t head_dim;             /* a multiple of 16, at most 256, at least the plan's span */
+    int32_t inverse;              /* 1: turn back (the transposed matrix, so the gradient's call) */
+    /* elements from head to head and from token to token, multiples of 8; a
+     * head's dims are contiguous */
+    int64_t q_head_stride, q_token_stride, q_out_head_stride, q_out_token_stride;
+    int64_t k_head_stride, k_token_stride, k_out_head_stride, k_out_token_stride;
+} blk_rope_pos_desc;
+
+/* The rotary of the QKV call (nnterp "stablelm" 03 Notes) at positions from
+ * device memory, on queries and keys of packed tokens in one launch:
+ *   q [n_heads, tokens, head_dim], k [n_k_heads, tokens, head_dim] by the strides;
+ *   positions: device int32 [tokens], any values (negative ones turn back)
+ *   q_out, k_out: the same shapes; may be q and k (with the same strides), else
+ *     they must not overlap q, k or themselves. Dims behind the span are copied.
+ * k and k_out NULL: no k. One rounding, to dt. */
+blk_status blk_rope_positions(const blk_rope_pos_desc* d, const blk_rope_plan* plan, const void* q,
+                              const void* k, const int32_t* positions, void* q_out, void* k_out,
+                              blk_dtype dt, blk_stream_t s);
+
+/* ---- paged key/value cache -------------------------------------------- */
+
+typedef enum {
+    BLK_CACHE_16BIT = 0,  /* values in the call's storage dtype */
+    BLK_CACHE_E4M3 = 1    /* 8-bit codes (4 exponent, 3 mantissa bits), value = code * scale */
+} blk_cache_kind;
+
+typedef struct {
+    int64_t pages;        /* of the pool */
+    int64_t page_tokens;  /* 16, 32, 64 or 128 */
+    int64_t n_kv_heads, head_dim;
+    int64_t batch;        /* sequences */
+    int64_t max_pages;    /* columns of the block table */
+    int64_t page_stride;  /* elements from page to page of k_cache and v_cache: a multiple of 16, at least
+                             n_kv_heads * page_tokens * head_dim */
+    int32_t kind;         /* blk_cache_kind */
+} blk_paged_desc;
+
+typedef struct {
+    blk_paged_desc cache; /* head_dim a multiple of 16, at most 256 */
+    int64_t tokens;       /* rows of k, v and q (1 .. 2^30) */
+    int64_t n_heads;      /* of q (0: no q) */
+    /* elements from head to head and from token to token, multiples of 8 */
+    int64_t k_head_stride, k_token_stride, v_head_stride, v_token_stride;
+    int64_t q_head_stride, q_token_stride, q_out_head_stride, q_out_token_stride;
+} blk_append_desc;
+
+/* Write new tokens' keys and values into a paged cache, the keys turned on the
+ * way, and turn their queries, in one launch:
+ *   k, v [n_kv_heads, tokens, head_dim], q [n_heads, tokens, head_dim] by the strides
+ *   cu_seqlens: device int32 [batch + 1]: sequence b's new tokens are rows
+ *     cu_seqlens[b] .. cu_seqlens[b+1] - 1 (none: allowed); NULL: row b, one each
+ *   lens: device int32 [batch]: each sequence's tokens WITH the new ones, which
+ *     take the positions up to lens[b] - 1 (so the same array serves the step's
+ *     blk_attn_decode_paged)
+ *   block_table: device int32 [batch, max_pages]: position p of sequence b is
+ *     row p % page_tokens of page block_table[b][p / page_tokens]
+ *   k_cache, v_cache [pages, n_kv_heads, page_tokens, head_dim] by page_stride;
+ *     k_scale, v_scale: fp32 [pages, n_kv_heads] for BLK_CACHE_E4M3, else NULL
+ *   rope: the rotary of k and q, or NULL; positions: device int32 [tokens] for
+ *     it, or NULL for the positions in the cache
+ *   q_out [n_heads, tokens, head_dim]: q turned; may be q. q and q_out NULL: no q
+ * BLK_CACHE_E4M3: a page's scale, one for each kv head, K and V apart, is the
+ * smallest power of two of at least 2^-60 with which no finite value of the
+ * page needs a code above 448. It is set as the page's first row is written, and only
+ * grows behind that; codes that the page holds are then divided by the
+ * same power of two (exactly, but for codes that fall below 2^-6). Values are
+ * rounded once, from 32 bits; an infinity becomes the largest code, a NaN stays one.
+ * Rows behind the new ones, and tokens that were there at an unchanged scale, keep their bits.
+ * A page that takes tokens belongs to one sequence in the call. The three arrays
+ * are read on the device and cannot be checked here: cu_seqlens' entries are
+ * clamped to the rows; a token with a negative position takes no part; one
+ * whose page is behind the table or outside the pool leaves the cache as it is. */
+blk_status blk_kv_append_paged(const blk_append_desc* d, const blk_rope_plan* rope, const void* k,
+                               const void* v, const void* q, const int32_t* cu_seqlens,
+                               const int32_t* positions, const int32_t* block_table,
+                               const int32_t* lens, void* k_cache, void* v_cache, float* k_scale,
+                               float* v_scale, void* q_out, blk_dtype dt, blk_stream_t s);
+
+typedef struct {
+    blk_paged_desc cache; /* head_dim 64, 128 or 160 */
+    int64_t n_heads;      /* a multiple of n_kv_heads */
+    int64_t q_batch_stride, q_head_stride; /* elements; even */
+    float softmax_scale;  /* <= 0 -> head_dim^-0.5 */
+    int32_t alibi;        /* 0 off; 1: score -= slope_h * (query_pos - key_pos) */
+} blk_decode_paged_desc;
+
+/* One decode step of attention over a paged cache:
+ *   q [batch, n_heads, head_dim] by the strides: each sequence's newest token, at position
+ *     lens[b] - 1
+ *   the cache, its scales, block_table and lens as above (scales finite and >= 0; any, not powers of two only).
+ *     lens is clamped to [0, max_pages * page_tokens]; 0: a zero row. Keys in a
+ *     page outside the pool take no part (a row without any key is zero).
+ *     Pages may be shared by sequences, or occur twice.
+ *   alibi_slopes: as for blk_attn_prefill
+ *   o [batch, n_heads, head_dim], contiguous
+ * GQA: kv head = h / (n_heads / n_kv_heads), any ratio; above 8 the cache is read
+ * once for every 8 query heads of a kv head. Sums and statistics are in 32 bits; softmax weights enter the product
+ * with V rounded: to dt over a 16-bit cache; over e4m3, to sums of two (bf16) or three
+ * (fp16) e4m3 numbers, at most 2^-9 or 2^-14 off, relative, or 2^-22 and 2^-27 of the largest.
+ * Two launches. The workspace holds partial results, at least
+ * blk_attn_decode_paged_workspace_size bytes, 16-byte aligned; calls whose
+ * kernels overlap on the GPU need a workspace each. */
+blk_status blk_attn_decode_paged_workspace_size(const blk_decode_paged_desc* d, size_t* bytes);
+blk_status blk_attn_decode_paged(const blk_decode_paged_desc* d, const void* q, const void* k_cache,
+                                 const void* v_cache, const float* k_scale, const float* v_scale,
+                                 const int32_t* block_table, const int32_t* lens,
+                                 const float* alibi_slopes, void* o, void* workspace,
+                                 size_t ws_bytes, blk_dtype dt, blk_stream_t s);
+
 /* ---- linear and MLP --------------------------------------------------- */
 
 /* y = x W^T [+ bias] [+ res1] [+ res2] on tcgen05 tensor cores.
