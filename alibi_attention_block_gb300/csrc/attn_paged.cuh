@@ -76,7 +76,8 @@ struct Cfg {
     // two CTAs per SM, so that one's chain of scores, softmax and product fills the
     // other's gaps; four where tiles are short, one where they are long
     static constexpr int kCtas = E8 && D == 64 && kN == 16 ? 4 : kTile > 32768 ? 1 : 2;
-    static constexpr int kQBytes = kRows * kRow, kPBytes = kRows * 128 * kElem;
+    // (each buffer at a multiple of the swizzle's 1024 bytes)
+    static constexpr int kQBytes = (kRows * kRow + 1023) / 1024 * 1024, kPBytes = kRows * 128 * kElem;
     static constexpr int kFixed = 2 * kQBytes + 2 * kPBytes + 8 * 2 * 8 * 4 + 4 * 8 * 4 * 4 + 2 * 8 * 4 + 512 + 16;
     static constexpr int kFit = (228 * 1024 / kCtas - 2048 - 64 - kFixed) / kTile;
     static constexpr int kSlots = kFit < 6 ? kFit : 6;

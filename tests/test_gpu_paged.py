@@ -132,6 +132,18 @@ CASES = [
 
 @pytest.mark.parametrize("bits", [8, 16])
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("d", [64, 128, 160])
+@pytest.mark.parametrize("G", [1, 4, 8])
+def test_every_kernel(G, d, dt, bits):
+    """Each instantiation with more tiles than CTAs: several segments each, of several tiles,
+    and tails of every kind; with ALiBi too."""
+    lens = [(211 * i) % 1700 for i in range(27)]
+    for alibi in (False, True):
+        run(27, 4 * G, 4, d, 32, lens, dt, bits, alibi, seed=G + d, spread=6.0 if alibi else 0.0)
+
+
+@pytest.mark.parametrize("bits", [8, 16])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
 @pytest.mark.parametrize("case", CASES, ids=lambda c: "B{}H{}Hk{}d{}p{}".format(*c[:5]))
 def test_matches_definition(case, dt, bits):
     B, H, Hk, d, page, lens, alibi = case
