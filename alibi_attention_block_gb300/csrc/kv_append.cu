@@ -15,7 +15,7 @@
 // which is exact down to e4m3's subnormals (only codes of below 2^-6 after the division
 // are rounded a second time). A page's scale never falls while the page fills.
 //
-// Work: a block takes one page's new rows of one head of K or V, so that the page's
+// Work: a team of threads takes one page's new rows of one head of K or V, so that the page's
 // largest value is found and used in one place, without atomics: each thread holds
 // its turned values in registers between the two. Blocks of queries take a
 // group of heads and reuse the angles. The number of pages that a sequence
@@ -24,6 +24,8 @@
 // offset; surplus blocks end at once. Bound by bytes: the new rows read once, their
 // codes and scales written once.
 #include <cuda_fp8.h>
+
+#include <algorithm>
 
 #include <cmath>
 
@@ -42,7 +44,10 @@ struct AppendArgs {
     int64_t xs[3][2], qs[2];  // strides of heads and tokens, in elements
     const int32_t* cu;         // or nullptr: one token per sequence
     const int32_t* positions;  // of the rotary, or nullptr: the cache's
-    int tokens, H, per;        // query heads, and of them per block
+    int tokens, H;             // query heads
+    int team;                  // threads of a page and head
+    int kv_per, kv_groups;     // heads of K and V per block (K's, then V's), and blocks of them
+    int q_per;                 // query heads per block
     int pdl;
 };
 
@@ -97,14 +102,14 @@ __device__ __forceinline__ bool rows_of(const AppendArgs& a, int64_t i, int lane
     return true;
 }
 
-__device__ __forceinline__ uint32_t finite_bits(float x) {
-    const uint32_t u = __float_as_uint(x) & 0x7fffffffu;
-    return u < 0x7f800000u ? u : 0u;
+__device__ __forceinline__ float if_finite(float x) {
+    x = fabsf(x);
+    return x < INFINITY ? x : 0.f;
 }
 
-// The smallest power of two of at least 2^-60 with which |x| (its bits) takes at most 448 = 1.75 * 2^8.
-__device__ __forceinline__ float scale_for(uint32_t bits) {
-    const int e = static_cast<int>((bits + 0x1fffffu) >> 23) - 127 - 8;
+// The smallest power of two of at least 2^-60 with which a number takes at most 448 = 1.75 * 2^8.
+__device__ __forceinline__ float scale_for(float most) {
+    const int e = static_cast<int>((__float_as_uint(most) + 0x1fffffu) >> 23) - 127 - 8;
     return __uint_as_float(static_cast<uint32_t>(max(e, -60) + 127) << 23);
 }
 
@@ -138,44 +143,63 @@ __device__ __forceinline__ uint32_t rescaled(uint32_t codes, float by) {
     return out;
 }
 
-// Threads: so many that IT rounds of them take a whole page (threads_for).
+// A block has teams of threads: a team takes one page and head at a time, its threads so
+// many that IT rounds of them hold the page (32 values each). What a block needs to know of its page (the search, the
+// length, the table) is a chain of dependent loads that its teams and heads share:
+// with a block of one warp for each page and head, 5000 tokens of 32 x 64 heads took 47 us.
 template <typename T, bool E8, int VP, int IT>
-__global__ void __launch_bounds__(512) kv_append_kernel(const __grid_constant__ AppendArgs a) {
-    __shared__ uint32_t most[16];
+__global__ void __launch_bounds__(IT * VP > 16 ? 512 : 768) kv_append_kernel(const __grid_constant__ AppendArgs a) {
+    __shared__ float most[2][32];
+    extern __shared__ float4 angles[];
+    __shared__ uint64_t plan[kMaxRotaryPairs];
     const int d = a.c.d, units = d / (2 * VP);
-    const int rows = blockDim.x / units;  // of a round
-    const int u = threadIdx.x % units, r0 = threadIdx.x / units;
     const int lane = threadIdx.x & 31;
-    const bool mine = r0 < rows;
-    // heads of K, then of V, then groups of query heads
-    const int what = blockIdx.y < a.c.Hk ? 0 : blockIdx.y < 2 * a.c.Hk ? 1 : 2;
-    const int head = blockIdx.y - what * a.c.Hk;
-    const Unit<VP> at(u, what == 1 ? 0 : a.turn.plan.pairs, a.turn.plan.interleaved);
-    uint64_t turns[VP];
-#pragma unroll
-    for (int i = 0; i < VP; ++i) turns[i] = at.turned ? a.turn.plan.turns[u * VP + i] : 0;
+    const bool is_q = static_cast<int>(blockIdx.y) >= a.kv_groups;
+    // queries: threads by head, token and unit; else by team, token and unit
+    const int threads = is_q ? blockDim.x : a.team;
+    const int team = is_q ? 0 : threadIdx.x / a.team;
+    const int tid = is_q ? threadIdx.x : threadIdx.x % a.team;
+    const int u = tid % units, place = tid / units;
+    const int rows = threads / units;
+    const Unit<VP> at(u, a.turn.plan.pairs, a.turn.plan.interleaved);
+    for (int i = threadIdx.x; i < a.turn.plan.pairs; i += blockDim.x) plan[i] = a.turn.plan.turns[i];
     const float m = a.turn.plan.amplitude;
+    __syncthreads();
     if (a.pdl) pdl_wait();
     PageRows r;
     if (!rows_of(a, blockIdx.x, lane, r)) return;
-    const T* x = static_cast<const T*>(a.x[what]) + r.row * a.xs[what][1];
+    using Raw = typename RawPiece<VP>::type;
 
-    if (what == 2) {
-        const int h1 = min((head + 1) * a.per, a.H);
-        for (int k = mine ? r0 : r.n; k < r.n; k += rows) {
+    if (is_q) {
+        const int side = min(rows, 1 << a.c.page_log2);  // tokens side by side
+        const int step = rows / side;                    // and heads
+        const int h0 = (blockIdx.y - a.kv_groups) * a.q_per, h1 = min(h0 + a.q_per, a.H);
+        if (place >= side * step) return;
+        for (int k = place % side; k < r.n; k += side) {
             Angles<VP> ang;
             if (at.turned)
-                ang.set(turns, a.positions ? a.positions[r.row + k] : static_cast<int>(r.pos + k), m, m);
-#pragma unroll 4
-            for (int h = head * a.per; h < h1; ++h) {
-                const T* src = x + h * a.xs[2][0] + k * a.xs[2][1];
-                T* dst = static_cast<T*>(a.q_out) + h * a.qs[0] + (r.row + k) * a.qs[1];
-                float p[VP], q[VP];
-                load_piece(src + at.a, p);
-                load_piece(src + at.b, q);
-                if (at.turned) ang.turn(p, q, a.turn.plan.interleaved);
-                store_piece(dst + at.a, p);
-                store_piece(dst + at.b, q);
+                ang.set(plan + u * VP, a.positions ? a.positions[r.row + k] : static_cast<int>(r.pos + k), m, m);
+            const T* x = static_cast<const T*>(a.x[2]) + (r.row + k) * a.xs[2][1];
+            T* y = static_cast<T*>(a.q_out) + (r.row + k) * a.qs[1];
+            // four heads' loads on their way at a time
+            for (int h = h0 + place / side; h < h1; h += 4 * step) {
+                Raw raw[4][2];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (h + i * step < h1) {
+                        raw[i][0] = load_raw<T, VP>(x + (h + i * step) * a.xs[2][0] + at.a);
+                        raw[i][1] = load_raw<T, VP>(x + (h + i * step) * a.xs[2][0] + at.b);
+                    }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (h + i * step < h1) {
+                        float p[VP], q[VP];
+                        unpack_raw<T, VP>(raw[i][0], p);
+                        unpack_raw<T, VP>(raw[i][1], q);
+                        if (at.turned) ang.turn(p, q, a.turn.plan.interleaved);
+                        store_piece(y + (h + i * step) * a.qs[0] + at.a, p);
+                        store_piece(y + (h + i * step) * a.qs[0] + at.b, q);
+                    }
             }
         }
         return;
@@ -185,96 +209,200 @@ __global__ void __launch_bounds__(512) kv_append_kernel(const __grid_constant__ 
     if (r.page >= a.c.max_pages) return;
     const int page = a.c.table[static_cast<int64_t>(r.b) * a.c.max_pages + r.page];
     if (page < 0 || page >= a.c.pages) return;
-    const int64_t base = page * a.c.page_stride + (static_cast<int64_t>(head) << a.c.page_log2) * d;
-    x += head * a.xs[what][0];
-    float v[IT][2][VP];
-    uint32_t top = 0;
+    const bool mine = place < rows;
+    const int slots = 2 * a.c.Hk, teams = blockDim.x / a.team;
+    const int end = min(static_cast<int>(blockIdx.y + 1) * a.kv_per, slots);
+    Raw raw[IT][2];
+    // the values' pieces lie side by side wherever the keys' do
+    auto fetch = [&](int slot) {
+        const int what = slot >= a.c.Hk;
+        const T* x = static_cast<const T*>(a.x[what]) + (slot - what * a.c.Hk) * a.xs[what][0] +
+                     r.row * a.xs[what][1];
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        const int k = r0 + i * rows;
-        if (mine && k < r.n) {
-            load_piece(x + k * a.xs[what][1] + at.a, v[i][0]);
-            load_piece(x + k * a.xs[what][1] + at.b, v[i][1]);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        const int k = r0 + i * rows;
-        if (mine && k < r.n) {
-            if (at.turned) {
-                Angles<VP> ang;
-                ang.set(turns, a.positions ? a.positions[r.row + k] : static_cast<int>(r.pos + k), m, m);
-                ang.turn(v[i][0], v[i][1], a.turn.plan.interleaved);
-            }
-            if constexpr (E8) {
-#pragma unroll
-                for (int e = 0; e < VP; ++e)
-                    top = max(top, max(finite_bits(v[i][0][e]), finite_bits(v[i][1][e])));
+        for (int i = 0; i < IT; ++i) {
+            const int k = place + i * rows;
+            if (mine && k < r.n) {
+                raw[i][0] = load_raw<T, VP>(x + k * a.xs[what][1] + at.a);
+                raw[i][1] = load_raw<T, VP>(x + k * a.xs[what][1] + at.b);
             }
         }
-    }
-    if constexpr (E8) {
-        float* scales = what ? a.c.v_scale : a.c.k_scale;
-        float* scale = scales + static_cast<int64_t>(page) * a.c.Hk + head;
-        uint8_t* codes = static_cast<uint8_t*>(what ? a.c.v : a.c.k) + base;
-        // a page's first row begins its scale anew
-        const float held = r.first > 0 ? *scale : 0.f;
-        top = __reduce_max_sync(0xffffffffu, top);
-        if (lane == 0) most[threadIdx.x / 32] = top;
+    };
+    int odd = 0, slot = blockIdx.y * a.kv_per + team;
+    constexpr bool kAhead = VP > 1;  // (single elements: too many registers)
+    if (kAhead && slot < end) fetch(slot);
+    // cosines and sines of the rows, for all the block's heads of K: plane j of a unit's
+    // pairs 2 j and 2 j + 1 (VP 1: of its pair)
+    const int turned_units = a.turn.plan.pairs / VP, cells = r.n * turned_units;
+    constexpr int kPlanes = VP > 1 ? VP / 2 : 1;
+    if (static_cast<int>(blockIdx.y) * a.kv_per < a.c.Hk && cells > 0) {
+        for (int i = threadIdx.x; i < cells * kPlanes; i += blockDim.x) {
+            const int cell = i / kPlanes, j = i - cell * kPlanes;
+            const int k = cell / turned_units, pair = (cell - k * turned_units) * VP + 2 * j;
+            const int pos = a.positions ? a.positions[r.row + k] : static_cast<int>(r.pos + k);
+            float c0, s0, c1, s1;
+            turn_cos_sin(plan[pair], pos, c0, s0);
+            if constexpr (VP > 1) {
+                turn_cos_sin(plan[pair + 1], pos, c1, s1);
+                angles[j * cells + cell] = make_float4(c0 * m, s0 * m, c1 * m, s1 * m);
+            } else {
+                reinterpret_cast<float2*>(angles)[cell] = make_float2(c0 * m, s0 * m);
+            }
+        }
         __syncthreads();
-        for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) top = max(top, most[w]);
-        const float now = fmaxf(scale_for(top), held);
-        if (threadIdx.x == 0) *scale = now;
-        if (r.first > 0 && held < now) {
-            const float by = held / now;
-            uint4* old = reinterpret_cast<uint4*>(codes);
-            for (int i = threadIdx.x; i < r.first * (d / 16); i += blockDim.x) {
-                uint4 o = old[i];
-                o.x = rescaled(o.x, by);
-                o.y = rescaled(o.y, by);
-                o.z = rescaled(o.z, by);
-                o.w = rescaled(o.w, by);
-                old[i] = o;
-            }
-        }
-        const float inv = 1.0f / now;
+    }
+    for (; slot < end; slot += teams) {
+        const int what = slot >= a.c.Hk, head = slot - what * a.c.Hk;
+        const bool turned = at.turned && what == 0;
+        const int64_t base = page * a.c.page_stride + (static_cast<int64_t>(head) << a.c.page_log2) * d;
+        if (!kAhead) fetch(slot);
+        float v[IT][2][VP];
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            const int k = r0 + i * rows;
-            if (mine && k < r.n) {
-                uint8_t* dst = codes + (r.first + k) * d;
-                store_codes<VP>(dst + at.a, v[i][0], inv);
-                store_codes<VP>(dst + at.b, v[i][1], inv);
-            }
+            unpack_raw<T, VP>(raw[i][0], v[i][0]);
+            unpack_raw<T, VP>(raw[i][1], v[i][1]);
         }
-    } else {
-        T* cache = static_cast<T*>(what ? a.c.v : a.c.k) + base;
+        if (kAhead && slot + teams < end) fetch(slot + teams);  // on their way behind these
+        float held = 0.f;
+        float* scale = nullptr;
+        if constexpr (E8) {
+            scale = (what ? a.c.v_scale : a.c.k_scale) + static_cast<int64_t>(page) * a.c.Hk + head;
+            if (r.first > 0) held = *scale;  // (a page's first row begins its scale anew)
+        }
+        float top = 0.f;
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            const int k = r0 + i * rows;
+            const int k = place + i * rows;
             if (mine && k < r.n) {
-                T* dst = cache + (r.first + k) * d;
-                store_piece(dst + at.a, v[i][0]);
-                store_piece(dst + at.b, v[i][1]);
+                if (turned) {
+#pragma unroll
+                    for (int j = 0; j < kPlanes; ++j) {
+                        const int cell = k * turned_units + u;
+                        if constexpr (VP > 1) {
+                            const float4 f = angles[j * cells + cell];
+                            turn_in_unit<VP>(v[i][0], v[i][1], 2 * j, a.turn.plan.interleaved, f.x, f.y);
+                            turn_in_unit<VP>(v[i][0], v[i][1], 2 * j + 1, a.turn.plan.interleaved, f.z, f.w);
+                        } else {
+                            const float2 f = reinterpret_cast<const float2*>(angles)[cell];
+                            turn_in_unit<VP>(v[i][0], v[i][1], 0, a.turn.plan.interleaved, f.x, f.y);
+                        }
+                    }
+                }
+                if constexpr (E8) {
+#pragma unroll
+                    for (int e = 0; e < VP; ++e)
+                        top = fmaxf(top, fmaxf(fabsf(v[i][0][e]), fabsf(v[i][1][e])));  // (NaN: passed over)
+                }
+            }
+        }
+        if constexpr (E8) {
+            uint8_t* codes = static_cast<uint8_t*>(what ? a.c.v : a.c.k) + base;
+            // the team's largest (a round of its own barrier; entries alternate between rounds)
+            auto of_team = [&](float x) {
+                x = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
+                if (a.team > 32) {
+                    const int w0 = team * (a.team / 32);
+                    if (lane == 0) most[odd][threadIdx.x / 32] = x;
+                    asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(a.team) : "memory");
+                    for (int w = 0; w < a.team / 32; ++w) x = fmaxf(x, most[odd][w0 + w]);
+                    odd ^= 1;
+                } else {
+                    __syncwarp();  // every lane has read the scale
+                }
+                return x;
+            };
+            top = of_team(top);
+            if (top == INFINITY) {  // the largest finite one, then
+                top = 0.f;
+#pragma unroll
+                for (int i = 0; i < IT; ++i) {
+                    if (!mine || place + i * rows >= r.n) continue;
+#pragma unroll
+                    for (int e = 0; e < VP; ++e)
+                        top = fmaxf(top, fmaxf(if_finite(v[i][0][e]), if_finite(v[i][1][e])));
+                }
+                top = of_team(top);
+            }
+            const float now = fmaxf(scale_for(top), held);
+            if (tid == 0) *scale = now;
+            if (r.first > 0 && held < now) {
+                const float by = held / now;
+                uint4* old = reinterpret_cast<uint4*>(codes);
+                for (int i = tid; i < r.first * (d / 16); i += a.team) {
+                    uint4 o = old[i];
+                    o.x = rescaled(o.x, by);
+                    o.y = rescaled(o.y, by);
+                    o.z = rescaled(o.z, by);
+                    o.w = rescaled(o.w, by);
+                    old[i] = o;
+                }
+            }
+            const float inv = 1.0f / now;
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                const int k = place + i * rows;
+                if (mine && k < r.n) {
+                    uint8_t* dst = codes + (r.first + k) * d;
+                    store_codes<VP>(dst + at.a, v[i][0], inv);
+                    store_codes<VP>(dst + at.b, v[i][1], inv);
+                }
+            }
+        } else {
+            T* cache = static_cast<T*>(what ? a.c.v : a.c.k) + base;
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                const int k = place + i * rows;
+                if (mine && k < r.n) {
+                    T* dst = cache + (r.first + k) * d;
+                    store_piece(dst + at.a, v[i][0]);
+                    store_piece(dst + at.b, v[i][1]);
+                }
             }
         }
     }
 }
 
 template <typename T, bool E8, int VP, int IT>
-cudaError_t launch_append(const AppendArgs& a, int64_t items, int slots, cudaStream_t s) {
+cudaError_t launch_append(AppendArgs& a, int64_t items, int sms, cudaStream_t s) {
     const int units = a.c.d / (2 * VP), page = 1 << a.c.page_log2;
-    const int threads = (units * ((page + IT - 1) / IT) + 31) / 32 * 32;
+    a.team = (units * ((page + IT - 1) / IT) + 31) / 32 * 32;
+    const int teams = a.team >= 256 ? 1 : 256 / a.team;
+    // heads of a block: as many as make about a round of blocks each of keys and values and of
+    // queries (768 threads per SM), since what is ahead of a block's first load is a chain of
+    // latencies; eight in turn at most for a team, sixteen for a thread of queries
+    const int64_t blocks = static_cast<int64_t>(sms) * std::max(1, 768 / (teams * a.team)), slots = 2 * a.c.Hk;
+    int64_t loops = items * slots / (teams * blocks);
+    loops = loops < 1 ? 1 : loops > 8 ? 8 : loops;
+    a.kv_per = static_cast<int>(teams * loops);
+    a.kv_groups = static_cast<int>((slots + a.kv_per - 1) / a.kv_per);
+    const int64_t side = teams * a.team / units / page > 1 ? teams * a.team / units / page : 1;
+    int64_t per = items * a.H / (side * blocks);
+    per = side * (per < 1 ? 1 : per > 16 ? 16 : per);
+    a.q_per = static_cast<int>(per);
+    const int64_t groups = a.kv_groups + (a.H + per - 1) / per;
+    const int table = page * a.turn.plan.pairs * 8;
+    if (table > 48 * 1024) {
+        const cudaError_t e =
+            set_smem_attr_once(reinterpret_cast<const void*>(kv_append_kernel<T, E8, VP, IT>), 128 * 1024);
+        if (e != cudaSuccess) return e;
+    }
     return launch_pdl(a.pdl != 0, kv_append_kernel<T, E8, VP, IT>,
-                      dim3(static_cast<unsigned>(items), static_cast<unsigned>(slots)), dim3(threads), 0,
-                      s, a);
+                      dim3(static_cast<unsigned>(items), static_cast<unsigned>(groups)),
+                      dim3(teams * a.team), table, s, a);
 }
 template <typename T, bool E8>
-cudaError_t launch_append_w(const AppendArgs& a, int64_t items, int slots, cudaStream_t s) {
-    switch (turn_width(a.turn.plan.pairs)) {  // 64 values held per thread
-        case 8: return launch_append<T, E8, 8, 4>(a, items, slots, s);
-        case 4: return launch_append<T, E8, 4, 8>(a, items, slots, s);
-        default: return launch_append<T, E8, 1, 32>(a, items, slots, s);
+cudaError_t launch_append_w(AppendArgs& a, int64_t items, int sms, cudaStream_t s) {
+    const int values = a.c.d << a.c.page_log2;  // of a page and head
+    switch (turn_width(a.turn.plan.pairs)) {
+        // 32 values per thread, 64 where a page would take more than 512 threads
+        case 8:
+            return values > 512 * 32 ? launch_append<T, E8, 8, 4>(a, items, sms, s)
+                                     : launch_append<T, E8, 8, 2>(a, items, sms, s);
+        case 4:
+            return values > 512 * 32 ? launch_append<T, E8, 4, 8>(a, items, sms, s)
+                                     : launch_append<T, E8, 4, 4>(a, items, sms, s);
+        default:
+            return values > 512 * 32 ? launch_append<T, E8, 1, 32>(a, items, sms, s)
+                                     : launch_append<T, E8, 1, 16>(a, items, sms, s);
     }
 }
 
@@ -397,18 +525,12 @@ extern "C" blk_status blk_kv_append_paged(const blk_append_desc* d, const blk_ro
     a.pdl = pdl_allowed(cs);
     const int64_t items = cu_seqlens ? (d->tokens >> a.c.page_log2) + 2 * d->cache.batch : d->tokens;
     REQUIRE(items <= 0x7fffffff, "tokens and batch too large");
-    // query heads per block: fewer where there are few tokens
-    const int64_t rows = d->tokens * d->n_heads / (1 << a.c.page_log2);
-    int64_t per = rows / (8 * sms);
-    per = per < 1 ? 1 : per > 8 ? 8 : per;
-    a.per = static_cast<int>(per);
-    const int slots = static_cast<int>(2 * d->cache.n_kv_heads + (d->n_heads + per - 1) / per);
     const bool e8 = d->cache.kind == BLK_CACHE_E4M3;
     const cudaError_t e =
-        dt == BLK_F16 ? (e8 ? launch_append_w<__half, true>(a, items, slots, cs)
-                            : launch_append_w<__half, false>(a, items, slots, cs))
-                      : (e8 ? launch_append_w<__nv_bfloat16, true>(a, items, slots, cs)
-                            : launch_append_w<__nv_bfloat16, false>(a, items, slots, cs));
+        dt == BLK_F16 ? (e8 ? launch_append_w<__half, true>(a, items, sms, cs)
+                            : launch_append_w<__half, false>(a, items, sms, cs))
+                      : (e8 ? launch_append_w<__nv_bfloat16, true>(a, items, sms, cs)
+                            : launch_append_w<__nv_bfloat16, false>(a, items, sms, cs));
     return e == cudaSuccess ? BLK_OK
                             : report_error_status(BLK_ECUDA, "append launch: %s", cudaGetErrorString(e));
 }

@@ -28,20 +28,39 @@ struct TurnArgs {
     int inverse;
 };
 
+// A piece as it lies in memory, and its numbers.
+template <int VP> struct RawPiece;
+template <> struct RawPiece<8> { using type = uint4; };
+template <> struct RawPiece<4> { using type = uint2; };
+template <> struct RawPiece<1> { using type = uint16_t; };
+
+template <typename T, int VP>
+__device__ __forceinline__ typename RawPiece<VP>::type load_raw(const T* p) {
+    return *reinterpret_cast<const typename RawPiece<VP>::type*>(p);
+}
+template <typename T, int VP>
+__device__ __forceinline__ void unpack_raw(const typename RawPiece<VP>::type& r, float (&f)[VP]) {
+    if constexpr (VP == 1) {
+        f[0] = dt_traits<T>::unpack2(r).x;
+    } else {
+        uint32_t w[VP / 2];
+        w[0] = r.x;
+        w[1] = r.y;
+        if constexpr (VP == 8) {
+            w[2] = r.z;
+            w[3] = r.w;
+        }
+#pragma unroll
+        for (int i = 0; i < VP / 2; ++i) {
+            const float2 x = dt_traits<T>::unpack2(w[i]);
+            f[2 * i] = x.x;
+            f[2 * i + 1] = x.y;
+        }
+    }
+}
 template <typename T, int VP>
 __device__ __forceinline__ void load_piece(const T* p, float (&f)[VP]) {
-    if constexpr (VP == 8) {
-        load8(p, f);
-    } else if constexpr (VP == 4) {
-        const uint2 u = *reinterpret_cast<const uint2*>(p);
-        const float2 x = dt_traits<T>::unpack2(u.x), y = dt_traits<T>::unpack2(u.y);
-        f[0] = x.x;
-        f[1] = x.y;
-        f[2] = y.x;
-        f[3] = y.y;
-    } else {
-        f[0] = dt_traits<T>::to_f(p[0]);
-    }
+    unpack_raw<T, VP>(load_raw<T, VP>(p), f);
 }
 
 template <typename T, int VP>
@@ -74,54 +93,64 @@ struct Unit {
     }
 };
 
-// Cosines and sines of a unit's pairs at a position, times the amplitude.
+// Cosine and sine of one pair's angle at a position.
+__device__ __forceinline__ void turn_cos_sin(uint64_t turns, int pos, float& c, float& s) {
+    const uint32_t t = static_cast<uint32_t>(
+        (turns * static_cast<uint64_t>(static_cast<int64_t>(pos)) + 0x80000000ull) >> 32);
+    const uint32_t quarter = (t + 0x20000000u) >> 30;
+    const float x = static_cast<float>(static_cast<int32_t>(t - (quarter << 30))) *
+                    (6.28318530717958648f / 4294967296.0f);
+    const float z = x * x;
+    float u = fmaf(z, 1.f / 362880, -1.f / 5040);
+    u = fmaf(z, u, 1.f / 120);
+    u = fmaf(z, u, -1.f / 6);
+    u = fmaf(z * x, u, x);  // sine
+    float w = fmaf(z, 1.f / 40320, -1.f / 720);
+    w = fmaf(z, w, 1.f / 24);
+    w = fmaf(z, w, -0.5f);
+    w = fmaf(z, w, 1.f);  // cosine
+    // a quarter turn on: (c, s) -> (-s, c)
+    c = quarter & 1 ? u : w;
+    s = quarter & 1 ? w : u;
+    if ((quarter + 1) & 2) c = -c;
+    if (quarter & 2) s = -s;
+}
+
+__device__ __forceinline__ void turn_pair(float& x, float& y, float c, float s) {
+    const float x0 = x;
+    x = fmaf(x0, c, -(y * s));
+    y = fmaf(y, c, x0 * s);
+}
+
+// Where pair i of a unit lies in its pieces a and b.
+template <int VP>
+__device__ __forceinline__ void turn_in_unit(float (&a)[VP], float (&b)[VP], int i, int interleaved,
+                                             float c, float s) {
+    if (VP > 1 && interleaved) {
+        if (i < VP / 2) turn_pair(a[(2 * i) % VP], a[(2 * i + 1) % VP], c, s);
+        else turn_pair(b[(2 * i) % VP], b[(2 * i + 1) % VP], c, s);
+    } else {
+        turn_pair(a[i], b[i], c, s);
+    }
+}
+
+// A unit's cosines and sines at a position, times the amplitude (sign: the same, or its
+// negative to turn back), for several heads.
 template <int VP>
 struct Angles {
     float c[VP], s[VP];
-    __device__ __forceinline__ void set(const uint64_t (&turns)[VP], int pos, float amplitude,
-                                        float sign) {
+    __device__ __forceinline__ void set(const uint64_t* turns, int pos, float amplitude, float sign) {
 #pragma unroll
         for (int i = 0; i < VP; ++i) {
-            const uint32_t t = static_cast<uint32_t>(
-                (turns[i] * static_cast<uint64_t>(static_cast<int64_t>(pos)) + 0x80000000ull) >> 32);
-            const uint32_t quarter = (t + 0x20000000u) >> 30;
-            const float x = static_cast<float>(static_cast<int32_t>(t - (quarter << 30))) *
-                            (6.28318530717958648f / 4294967296.0f);
-            const float z = x * x;
-            float u = fmaf(z, 1.f / 362880, -1.f / 5040);
-            u = fmaf(z, u, 1.f / 120);
-            u = fmaf(z, u, -1.f / 6);
-            u = fmaf(z * x, u, x);  // sine
-            float w = fmaf(z, 1.f / 40320, -1.f / 720);
-            w = fmaf(z, w, 1.f / 24);
-            w = fmaf(z, w, -0.5f);
-            w = fmaf(z, w, 1.f);  // cosine
-            // a quarter turn on: (c, s) -> (-s, c)
-            float cs = quarter & 1 ? u : w, sn = quarter & 1 ? w : u;
-            if ((quarter + 1) & 2) cs = -cs;
-            if (quarter & 2) sn = -sn;
+            float cs, sn;
+            turn_cos_sin(turns[i], pos, cs, sn);
             c[i] = cs * amplitude;
-            s[i] = sn * sign;  // sign: +- amplitude
+            s[i] = sn * sign;
         }
     }
     __device__ __forceinline__ void turn(float (&a)[VP], float (&b)[VP], int interleaved) const {
-        if (VP > 1 && interleaved) {
 #pragma unroll
-            for (int i = 0; i < VP / 2; ++i) {
-                pair(a[2 * i], a[2 * i + 1], i);
-                pair(b[2 * i], b[2 * i + 1], VP / 2 + i);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < VP; ++i) pair(a[i], b[i], i);
-        }
-    }
-
-private:
-    __device__ __forceinline__ void pair(float& x, float& y, int i) const {
-        const float x0 = x;
-        x = fmaf(x0, c[i], -(y * s[i]));
-        y = fmaf(y, c[i], x0 * s[i]);
+        for (int i = 0; i < VP; ++i) turn_in_unit<VP>(a, b, i, interleaved, c[i], s[i]);
     }
 };
 
