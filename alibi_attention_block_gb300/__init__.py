@@ -377,16 +377,87 @@ def rope_plan(span, base=10000.0, interleaved=False, scaling="none", factor=1.0,
     return plan
 
 
-def _strided(t, dtype, dev):
-    """Pointer of a tensor [a, b, dim] with contiguous dims, as (pointer, stride
-    of a, stride of b)."""
-    if t.dtype is not dtype or t.get_device() != dev:
-        _refuse(t, dtype, dev)
-    shape, stride = t.shape, t.stride()
-    if stride[2] != 1 and shape[2] != 1:
-        raise ValueError("a head's dims must be contiguous")
-    # the stride of an axis of length 1 is never used, whatever it is
-    return (t.data_ptr(), stride[0] if shape[0] > 1 else 0, stride[1] if shape[1] > 1 else 0)
+def _sig(*ts):
+    """What a plan is kept by of a call's tensors: type, shape and strides."""
+    try:
+        return tuple([None if t is None else (t.dtype, t.shape, t.stride()) for t in ts])
+    except AttributeError:
+        raise TypeError("expected a torch.Tensor") from None
+
+
+def _addresses(dev, *ts):
+    """Device pointers of tensors on device dev (None stays None)."""
+    out = []
+    for t in ts:
+        if t is None:
+            out.append(None)
+        elif t.get_device() == dev:
+            out.append(t.data_ptr())
+        else:
+            _refuse(t, t.dtype, dev)
+    return out
+
+
+_DT = {torch.float16: _abi.BLK_F16, torch.bfloat16: _abi.BLK_BF16}
+
+
+def _storage(dtype):
+    if dtype not in _DT:
+        raise TypeError(f"storage dtype must be float16 or bfloat16, got {dtype}")
+    return _DT[dtype]
+
+
+def _want(sig, dtype, shape, what):
+    """A tensor of this type and shape, its axes one behind the other (None: no tensor)."""
+    if sig is None:
+        return
+    if sig[0] is not dtype:
+        raise TypeError(f"{what}: expected a {dtype} tensor, got {sig[0]}")
+    if sig[1] != shape:
+        raise ValueError(f"{what} has shape {tuple(sig[1])}, expected {shape}")
+    _dense(sig, what)
+
+
+def _dense(sig, what):
+    n = 1
+    for size, stride in zip(reversed(sig[1]), reversed(sig[2])):
+        if size != 1 and stride != n:
+            raise ValueError(f"{what} must be contiguous")
+        n *= size
+
+
+def _heads(sig, dtype, shape, what):
+    """(stride of the first axis, of the second) of a tensor [a, b, dim] with
+    contiguous dims. The stride of an axis of length 1 is never used, whatever
+    it is."""
+    if sig is None:
+        return 0, 0
+    if sig[0] is not dtype:
+        raise TypeError(f"{what}: expected a {dtype} tensor, got {sig[0]}")
+    if sig[1] != shape:
+        raise ValueError(f"{what} has shape {tuple(sig[1])}, expected {shape}")
+    if sig[2][2] != 1 and sig[1][2] != 1:
+        raise ValueError(f"{what}: a head's dims must be contiguous")
+    return tuple(sig[2][i] if sig[1][i] > 1 else 0 for i in (0, 1))
+
+
+@functools.lru_cache(maxsize=256)
+def _rope_pos_plan(sig, inverse):
+    """(descriptor by reference, storage type) of a call's tensors."""
+    q, positions, k, q_out, k_out = sig
+    if len(q[1]) != 3:
+        raise ValueError("q has shape [heads, tokens, head_dim]")
+    H, T, d = q[1]
+    dt = _storage(q[0])
+    _want(positions, torch.int32, (T,), "positions")
+    Hk = 0
+    if k is not None:
+        if len(k[1]) != 3:
+            raise ValueError("k has shape [heads, tokens, head_dim]")
+        Hk = k[1][0]
+    strides = (*_heads(q, q[0], (H, T, d), "q"), *_heads(q_out, q[0], (H, T, d), "q_out"),
+               *_heads(k, q[0], (Hk, T, d), "k"), *_heads(k_out, q[0], (Hk, T, d), "k_out"))
+    return C.byref(_abi.RopePosDesc(T, H, Hk, d, inverse, *strides)), dt
 
 
 def rope_positions(q, positions, plan, k=None, inverse=False, q_out=None, k_out=None):
@@ -395,68 +466,70 @@ def rope_positions(q, positions, plan, k=None, inverse=False, q_out=None, k_out=
     [T, H, d] goes in transposed. q_out / k_out: where to (q and k themselves
     for in place; new tensors when None). Returns the result, or the two.
     inverse=True turns back (the gradient's call)."""
-    dt, dtype, dev = _dt(q), q.dtype, torch.cuda.current_device()
-    H, T, d = q.shape
-    _shape(positions, (T,), "positions")
-    _shape(q_out, (H, T, d), "q_out")
-    o = torch.empty(q.shape, dtype=dtype, device=q.device) if q_out is None else q_out
-    qp, qh, qt = _strided(q, dtype, dev)
-    op, oh, ot = _strided(o, dtype, dev)
-    Hk = kp = kh = kt = lp = lh = lt = 0
-    if k is not None:
-        Hk = k.shape[0]
-        _shape(k, (Hk, T, d), "k")
-        _shape(k_out, (Hk, T, d), "k_out")
-        ko = torch.empty(k.shape, dtype=dtype, device=k.device) if k_out is None else k_out
-        kp, kh, kt = _strided(k, dtype, dev)
-        lp, lh, lt = _strided(ko, dtype, dev)
-    elif k_out is not None:
+    if k is None and k_out is not None:
         raise ValueError("k_out given without k")
-    (pp,) = _pointers(torch.int32, dev, positions)
-    desc = _abi.RopePosDesc(T, H, Hk, d, 1 if inverse else 0, qh, qt, oh, ot, kh, kt, lh, lt)
-    _abi.check(_lib().blk_rope_positions(desc, plan, qp, kp or None, pp, op, lp or None, dt,
-                                         torch._C._cuda_getCurrentRawStream(dev)),
-               "blk_rope_positions")
+    o = torch.empty_like(q) if q_out is None else q_out
+    ko = torch.empty_like(k) if k_out is None and k is not None else k_out
+    desc, dt = _rope_pos_plan(_sig(q, positions, k, o, ko), 1 if inverse else 0)
+    dev = torch._C._cuda_getDevice()
+    qp, pp, kp, op, lp = _addresses(dev, q, positions, k, o, ko)
+    status = _lib().blk_rope_positions(desc, plan, qp, kp, pp, op, lp, dt,
+                                       torch._C._cuda_getCurrentRawStream(dev))
+    if status:
+        _abi.check(status, "blk_rope_positions")
     return o if k is None else (o, ko)
 
 
-def _paged(k_cache, v_cache, k_scale, v_scale, block_table, lens, dtype, dev):
-    """A paged cache's arguments checked: (descriptor's fields, pointers in the
-    calls' order: table, lens, caches, scales)."""
-    pages, Hk, n, d = k_cache.shape
-    B, max_pages = block_table.shape
-    stride = k_cache.stride()
-    if k_cache.dtype is torch.float8_e4m3fn:
-        kind = _abi.BLK_CACHE_E4M3
-        if k_scale is None or v_scale is None:
-            raise ValueError("a float8_e4m3fn cache has k_scale and v_scale")
-        _shape(k_scale, (pages, Hk), "k_scale")
-        _shape(v_scale, (pages, Hk), "v_scale")
-        ksp, vsp = _pointers(torch.float32, dev, k_scale, v_scale)
-    else:
-        kind, ksp, vsp = _abi.BLK_CACHE_16BIT, None, None
-        if k_cache.dtype is not dtype:
-            raise TypeError(f"caches are float8_e4m3fn or {dtype}, got {k_cache.dtype}")
-        if k_scale is not None or v_scale is not None:
-            raise ValueError("a 16-bit cache has no scales")
-    _shape(v_cache, (pages, Hk, n, d), "v_cache")
-    for t in (k_cache, v_cache):
-        if t.dtype is not k_cache.dtype or t.get_device() != dev:
-            _refuse(t, k_cache.dtype, dev)
-    page = Hk * n * d
-    if pages == 1:
-        page_stride = page
-    else:
-        page_stride = stride[0]
-        if v_cache.stride(0) != page_stride:
+def _paged(dtype, k_cache, v_cache, k_scale, v_scale, block_table, lens):
+    """Fields of blk_paged_desc, from the tensors' _sig."""
+    if len(k_cache[1]) != 4:
+        raise ValueError("k_cache has shape [pages, kv_heads, page_tokens, head_dim]")
+    if len(block_table[1]) != 2:
+        raise ValueError("block_table has shape [batch, max_pages]")
+    pages, Hk, n, d = k_cache[1]
+    B, max_pages = block_table[1]
+    kind = _abi.BLK_CACHE_E4M3 if k_cache[0] is torch.float8_e4m3fn else _abi.BLK_CACHE_16BIT
+    if kind == _abi.BLK_CACHE_16BIT and k_cache[0] is not dtype:
+        raise TypeError(f"caches are float8_e4m3fn or {dtype}, got {k_cache[0]}")
+    if (k_scale is None) != (kind == _abi.BLK_CACHE_16BIT) or (k_scale is None) != (v_scale is None):
+        raise ValueError("a float8_e4m3fn cache has k_scale and v_scale, a 16-bit cache has none")
+    _want(k_scale, torch.float32, (pages, Hk), "k_scale")
+    _want(v_scale, torch.float32, (pages, Hk), "v_scale")
+    if v_cache[0] is not k_cache[0] or v_cache[1] != k_cache[1]:
+        raise ValueError("v_cache must be as k_cache")
+    for c, what in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _dense((c[0], c[1][1:], c[2][1:]), f"a page of {what}")
+    page_stride = Hk * n * d
+    if pages > 1:
+        page_stride = k_cache[2][0]
+        if v_cache[2][0] != page_stride:
             raise ValueError("k_cache and v_cache must have the same page stride")
-    for t in (k_cache, v_cache):
-        if not (t.is_contiguous() or t[0].is_contiguous()):
-            raise ValueError("a page of the cache must be contiguous")
-    _shape(lens, (B,), "lens")
-    tp, lp = _pointers(torch.int32, dev, block_table, lens)
-    return (pages, n, Hk, d, B, max_pages, page_stride, kind), (tp, lp, k_cache.data_ptr(),
-                                                                v_cache.data_ptr(), ksp, vsp)
+    _want(block_table, torch.int32, (B, max_pages), "block_table")
+    _want(lens, torch.int32, (B,), "lens")
+    return pages, n, Hk, d, B, max_pages, page_stride, kind
+
+
+@functools.lru_cache(maxsize=256)
+def _append_plan(sig):
+    """(descriptor by reference, storage type) of a call's tensors."""
+    k, v, q, q_out, cu_seqlens, positions, k_cache, v_cache, k_scale, v_scale, table, lens = sig
+    if len(k[1]) != 3:
+        raise ValueError("k has shape [kv_heads, tokens, head_dim]")
+    Hk, T, d = k[1]
+    dt = _storage(k[0])
+    fields = _paged(k[0], k_cache, v_cache, k_scale, v_scale, table, lens)
+    if fields[2] != Hk or fields[3] != d:
+        raise ValueError(f"k has {Hk} heads of {d} dims, the cache {fields[2]} of {fields[3]}")
+    _want(cu_seqlens, torch.int32, (fields[4] + 1,), "cu_seqlens")
+    _want(positions, torch.int32, (T,), "positions")
+    H = 0
+    if q is not None:
+        if len(q[1]) != 3:
+            raise ValueError("q has shape [heads, tokens, head_dim]")
+        H = q[1][0]
+    strides = (*_heads(k, k[0], (Hk, T, d), "k"), *_heads(v, k[0], (Hk, T, d), "v"),
+               *_heads(q, k[0], (H, T, d), "q"), *_heads(q_out, k[0], (H, T, d), "q_out"))
+    return C.byref(_abi.AppendDesc(fields, T, H, *strides)), dt
 
 
 def kv_append_paged(k, v, k_cache, v_cache, block_table, lens, cu_seqlens=None, k_scale=None,
@@ -471,32 +544,17 @@ def kv_append_paged(k, v, k_cache, v_cache, block_table, lens, cu_seqlens=None, 
     [H, T, d] on the way, at the positions in the cache or at ``positions``
     (int32 [T]). Returns q turned (q_out, or a new tensor; rows outside every
     sequence are not written), None without q."""
-    dt, dtype, dev = _dt(k), k.dtype, torch.cuda.current_device()
-    Hk, T, d = k.shape
-    _shape(v, (Hk, T, d), "v")
-    fields, (tp, lp, kcp, vcp, ksp, vsp) = _paged(k_cache, v_cache, k_scale, v_scale, block_table,
-                                                  lens, dtype, dev)
-    if fields[2] != Hk or fields[3] != d:
-        raise ValueError(f"k has {Hk} heads of {d} dims, the cache {fields[2]} of {fields[3]}")
-    kp, kh, kt = _strided(k, dtype, dev)
-    vp, vh, vt = _strided(v, dtype, dev)
-    H, qp, qh, qt, op, oh, ot, o = 0, None, 0, 0, None, 0, 0, None
-    if q is not None:
-        H = q.shape[0]
-        _shape(q, (H, T, d), "q")
-        _shape(q_out, (H, T, d), "q_out")
-        o = torch.empty(q.shape, dtype=dtype, device=q.device) if q_out is None else q_out
-        qp, qh, qt = _strided(q, dtype, dev)
-        op, oh, ot = _strided(o, dtype, dev)
-    elif q_out is not None:
+    if q is None and q_out is not None:
         raise ValueError("q_out given without q")
-    _shape(cu_seqlens, (fields[4] + 1,), "cu_seqlens")
-    _shape(positions, (T,), "positions")
-    cup, pp = _pointers(torch.int32, dev, cu_seqlens, positions)
-    desc = _abi.AppendDesc(fields, T, H, kh, kt, vh, vt, qh, qt, oh, ot)
-    _abi.check(_lib().blk_kv_append_paged(desc, rope, kp, vp, qp, cup, pp, tp, lp, kcp, vcp, ksp, vsp,
-                                          op, dt, torch._C._cuda_getCurrentRawStream(dev)),
-               "blk_kv_append_paged")
+    o = torch.empty_like(q) if q_out is None and q is not None else q_out
+    ts = (k, v, q, o, cu_seqlens, positions, k_cache, v_cache, k_scale, v_scale, block_table, lens)
+    desc, dt = _append_plan(_sig(*ts))
+    dev = torch._C._cuda_getDevice()
+    kp, vp, qp, op, cup, pp, kcp, vcp, ksp, vsp, tp, lp = _addresses(dev, *ts)
+    status = _lib().blk_kv_append_paged(desc, rope, kp, vp, qp, cup, pp, tp, lp, kcp, vcp, ksp, vsp,
+                                        op, dt, torch._C._cuda_getCurrentRawStream(dev))
+    if status:
+        _abi.check(status, "blk_kv_append_paged")
     return o
 
 
@@ -514,10 +572,22 @@ def attn_decode_paged_workspace_size(desc) -> int:
 
 
 @functools.lru_cache(maxsize=256)
-def _decode_paged_plan(*args):
-    """(descriptor by reference, workspace bytes) of a call's sizes and _values."""
-    desc = decode_paged_desc(*args)
-    return C.byref(desc), attn_decode_paged_workspace_size(desc)
+def _decode_paged_plan(sig, alibi, scale):
+    """(descriptor by reference, workspace bytes, storage type) of a call's
+    tensors and _values."""
+    q, out, slopes, k_cache, v_cache, k_scale, v_scale, table, lens = sig
+    if len(q[1]) != 3:
+        raise ValueError("q has shape [batch, heads, head_dim]")
+    B, H, d = q[1]
+    dt = _storage(q[0])
+    fields = _paged(q[0], k_cache, v_cache, k_scale, v_scale, table, lens)
+    if fields[3] != d or fields[4] != B:
+        raise ValueError(f"q {tuple(q[1])} does not fit the cache's head_dim {fields[3]} or "
+                         f"block_table's {fields[4]} sequences")
+    _want(slopes, torch.float32, (H,), "slopes")
+    _want(out, q[0], (B, H, d), "out")
+    desc = decode_paged_desc(fields, H, *_heads(q, q[0], (B, H, d), "q"), alibi, scale)
+    return C.byref(desc), attn_decode_paged_workspace_size(desc), dt
 
 
 def attn_decode_paged(q, k_cache, v_cache, block_table, lens, k_scale=None, v_scale=None,
@@ -528,27 +598,20 @@ def attn_decode_paged(q, k_cache, v_cache, block_table, lens, k_scale=None, v_sc
     float8_e4m3fn with scales fp32 [pages, Hk]; sequence b's keys 0 .. lens[b] -
     1 lie in pages block_table[b] (int32 [B, max_pages], lens int32 [B], both
     on the device). Length 0: a zero row. Returns o [B, H, d]."""
-    dt, dtype, dev = _dt(q), q.dtype, torch.cuda.current_device()
-    B, H, d = q.shape
-    fields, (tp, lp, kp, vp, ksp, vsp) = _paged(k_cache, v_cache, k_scale, v_scale, block_table,
-                                                lens, dtype, dev)
-    if fields[3] != d or fields[4] != B:
-        raise ValueError(f"q {tuple(q.shape)} does not fit the cache's head_dim {fields[3]} or "
-                         f"block_table's {fields[4]} sequences")
-    _shape(slopes, (H,), "slopes")
-    _shape(out, (B, H, d), "out")
-    qp, qb, qh = _strided(q, dtype, dev)
-    desc, need = _decode_paged_plan(fields, H, qb, qh, *_values(alibi, scale))
-    sp = None if slopes is None else _pointers(torch.float32, dev, slopes)[0]
-    if out is None:
-        o = torch.empty((B, H, d), dtype=dtype, device=q.device)
+    ts = (q, out, slopes, k_cache, v_cache, k_scale, v_scale, block_table, lens)
+    desc, need, dt = _decode_paged_plan(_sig(*ts), *_values(alibi, scale))
+    dev = torch._C._cuda_getDevice()
+    qp, op, sp, kp, vp, ksp, vsp, tp, lp = _addresses(dev, *ts)
+    o = out
+    if o is None:
+        o = torch.empty_like(q) if q.is_contiguous() else torch.empty(q.shape, dtype=q.dtype, device=q.device)
         op = o.data_ptr()
-    else:
-        o, (op,) = out, _pointers(dtype, dev, out)
     fn = _lib().blk_attn_decode_paged
-    _abi.check(_with_workspace(
+    status = _with_workspace(
         lambda wp, wn, st: fn(desc, qp, kp, vp, ksp, vsp, tp, lp, sp, op, wp, wn, dt, st),
-        workspace, need, dev), "blk_attn_decode_paged")
+        workspace, need, dev)
+    if status:
+        _abi.check(status, "blk_attn_decode_paged")
     return o
 
 

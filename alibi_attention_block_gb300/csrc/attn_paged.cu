@@ -109,6 +109,13 @@ blk_status check_desc(const blk_decode_paged_desc* d) {
 int unit_heads(int64_t G) { return G == 1 ? 1 : G <= 4 ? 4 : 8; }
 int64_t unit_groups(int64_t G) { return (G + 7) / 8; }
 
+// Whether a sequence's tiles are so few that a CTA takes each unit whole.
+constexpr int64_t kDirectTiles = 4;
+bool is_direct(const blk_paged_desc& c) {
+    return c.max_pages * c.page_tokens <= kDirectTiles * kTK &&
+           c.batch * c.n_kv_heads <= (int64_t(1) << 24);
+}
+
 struct Layout {
     size_t po, pm, cum, total;
 };
@@ -117,7 +124,8 @@ Layout layout(const blk_decode_paged_desc* d) {
     const size_t recs = static_cast<size_t>(kPagedMaxGrid + d->cache.batch * d->cache.n_kv_heads * unit_groups(G)) *
                         unit_heads(G);
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
-    Layout L;
+    Layout L{};
+    if (is_direct(d->cache)) return L;
     L.po = 0;
     L.pm = up(recs * d->cache.head_dim * 4);
     L.cum = L.pm + up(recs * 8);
@@ -161,7 +169,7 @@ blk_status blk_attn_decode_paged(const blk_decode_paged_desc* d, const void* q, 
         return report_error_status(BLK_EUNSUPPORTED,
                                    "standard ALiBi slopes need a power-of-two head count");
     const Layout L = layout(d);
-    if (!workspace || ws_bytes < L.total || (reinterpret_cast<uintptr_t>(workspace) & 15u) != 0)
+    if (L.total && (!workspace || ws_bytes < L.total || (reinterpret_cast<uintptr_t>(workspace) & 15u) != 0))
         return report_error_status(BLK_EWORKSPACE, "workspace needs %zu bytes, 16-byte aligned", L.total);
     int sms = 0;
     if ((st = current_device_info(&sms, &a.err)) != BLK_OK) return st;
@@ -173,6 +181,8 @@ blk_status blk_attn_decode_paged(const blk_decode_paged_desc* d, const void* q, 
     a.po = reinterpret_cast<float*>(ws + L.po);
     a.pm = reinterpret_cast<float2*>(ws + L.pm);
     a.cum = reinterpret_cast<int64_t*>(ws + L.cum);
+    a.direct = L.total == 0;
+    a.o = o;
     a.slopes = alibi_slopes;
     a.H = static_cast<int>(d->n_heads);
     a.G = a.H / a.c.Hk;
@@ -185,20 +195,20 @@ blk_status blk_attn_decode_paged(const blk_decode_paged_desc* d, const void* q, 
     const bool e8 = d->cache.kind == BLK_CACHE_E4M3;
     const uint32_t elem = e8 ? 1 : 2;
     const bool wide = !e8 || a.c.d >= 128, narrow = e8 && a.c.d % 128 != 0;
-    PagedMapSet tm;
+    PagedMapSet tm;  // (a slice of a width that a head does not have: never used)
     for (int kv = 0; kv < 2; ++kv)
-        for (int w = 0; w < 2; ++w)
-            for (int i = 0; i < 2; ++i) {
-                // (without a slice of a width its place holds the other's)
-                const bool sixty_four = i == 0 ? !wide : narrow;
-                if (!make_tmap_pages(&tm.m[kv][w][i], elem, kv ? v_cache : k_cache, a.c.pages, a.c.Hk,
-                                     d->cache.page_tokens, a.c.d, d->cache.page_stride,
-                                     w == 0 ? static_cast<uint32_t>(d->cache.page_tokens) : 16u,
-                                     sixty_four ? 64 : 128))
-                    return report_error_status(BLK_EINVAL, "no tensor map for this cache");
-            }
+        for (int i = wide ? 0 : 1; i <= (narrow ? 1 : 0); ++i) {
+            const void* base = kv ? v_cache : k_cache;
+            const uint32_t page = static_cast<uint32_t>(d->cache.page_tokens);
+            bool ok = make_tmap_pages(&tm.m[kv][0][i], elem, base, a.c.pages, a.c.Hk, page, a.c.d,
+                                      d->cache.page_stride, page, i ? 64 : 128);
+            if (page == 16) tm.m[kv][1][i] = tm.m[kv][0][i];
+            else ok = ok && make_tmap_pages(&tm.m[kv][1][i], elem, base, a.c.pages, a.c.Hk, page, a.c.d,
+                                            d->cache.page_stride, 16, i ? 64 : 128);
+            if (!ok) return report_error_status(BLK_EINVAL, "no tensor map for this cache");
+        }
     cudaError_t e = dt == BLK_F16 ? launch_paged_f16(e8, tm, a, sms, cs) : launch_paged_bf16(e8, tm, a, sms, cs);
-    if (e == cudaSuccess) {
+    if (e == cudaSuccess && !a.direct) {
         MergeArgs m{};
         m.po = a.po;
         m.pm = a.pm;

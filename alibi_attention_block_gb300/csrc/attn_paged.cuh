@@ -34,6 +34,8 @@
 // Work: a unit is (sequence, kv head, up to eight of its query heads) of ceil(len / 128) key tiles. The tiles of all
 // units, in one line, are cut into equal ranges, one per CTA, whatever the lengths are; a CTA's
 // stay in a unit is a segment with a partial result (reference, sum, O), joined by the merge.
+// Where the cache has few tiles per sequence (is_direct in attn_paged.cu) a CTA takes a whole unit and
+// writes its rows: no range to find, no partial results, one launch.
 // The lengths are device data: each CTA sums them itself. Tiles go from the newest key down.
 // A tile is 128 keys from up to eight pages: a lane of the loading warp for each 16 of them finds
 // the page one tile ahead, copies its rows by TMA and its scales by cp.async. A page id outside
@@ -658,7 +660,7 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
         // a segment's O is in TMEM until its last PV has completed: read out
         // behind the next segment's first tile
         bool pend = false;
-        int pend_t = 0, pend_buf = 0;
+        int pend_t = 0, pend_buf = 0, pend_heads = 0;
         int64_t pend_rec = 0;
         auto read_out = [&]() -> bool {
             if (!mbar_wait(bar.pv_done(pend_t & 1), (pend_t >> 1) & 1, a.err)) return false;
@@ -670,6 +672,15 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar.o_free(pend_buf));
+            float inv[GP];
+            if (a.direct) {  // (the only segment: its sums are the first)
+#pragma unroll
+                for (int h = 0; h < GP; ++h) {
+                    const float4 w = *reinterpret_cast<const float4*>(red_sum + h * 4);
+                    const float sum = (w.x + w.y) + (w.z + w.w);
+                    inv[h] = sum == 0.f ? 0.f : 1.f / (sum * C::kTop);
+                }
+            }
 #pragma unroll
             for (int mb = 0; mb < C::kBlocks; ++mb) {
                 // a block of 64 rows takes 16 lanes of each quarter
@@ -682,7 +693,13 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
                         if (C::kParts > 1) v = fmaf(__uint_as_float(o[mb][GP + h]), 1.f / 32, v);
                         if (C::kParts > 2)
                             v = fmaf(__uint_as_float(o[mb][(C::kParts - 1) * GP + h]), 1.f / 1024, v);
-                        a.po[(pend_rec * GP + h) * D + dim] = v * (1.f / C::kTop);
+                        if (!a.direct) {
+                            a.po[(pend_rec * GP + h) * D + dim] = v * (1.f / C::kTop);
+                        } else if (h < pend_heads) {
+                            const uint16_t bits =
+                                static_cast<uint16_t>(dt_traits<T>::pack2(v * inv[h], 0.f));
+                            static_cast<uint16_t*>(a.o)[(pend_rec + h) * D + dim] = bits;
+                        }
                     }
                 }
                 __syncwarp();
@@ -863,8 +880,9 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
             pend = true;
             pend_t = t - 1;
             pend_buf = c.it & 1;
-            pend_rec = rec;
-            if (quarter == 0 && lane < GP) {
+            pend_rec = a.direct ? static_cast<int64_t>(c.b) * a.H + h0 : rec;
+            pend_heads = (g + 1) * a.G - h0;
+            if (!a.direct && quarter == 0 && lane < GP) {
                 const float4 w = *reinterpret_cast<const float4*>(red_sum + (c.it & 1) * 32 + lane * 4);
                 float mh = m[0];
 #pragma unroll
@@ -893,7 +911,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<T, E8, D, GP>::kCtas))
     if (threadIdx.x == 0) {
         bar.init();
         fence_barrier_init();
-        for (int i = 0; i < 4; ++i) tma_prefetch_desc(&tm.m[i / 2][i % 2][0]);
+        for (int i = 0; i < 4; ++i) tma_prefetch_desc(&tm.m[i / 2][i % 2][C::kWide ? 0 : 1]);
     }
     if (warp == 1) {
         tmem_alloc(smem_u32(tmem_slot), C::kCols);
@@ -904,10 +922,25 @@ __global__ void __launch_bounds__(kThreads, (Cfg<T, E8, D, GP>::kCtas))
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     if (a.pdl) pdl_wait();
-    if (warp >= 2 && warp < 6) find_range(a, range, bar.range_full());
-    if (mbar_wait(bar.range_full(), 0, a.err)) {
-        Tiles tiles;
-        tiles.c.start(a, range.lo, range.hi, range.b0, range.base);
+    Tiles tiles;
+    bool ok = true;
+    if (a.direct) {
+        // a unit per CTA, whole
+        const int b = static_cast<int>(blockIdx.x) / a.units, u = static_cast<int>(blockIdx.x) - b * a.units;
+        const int nt = (len_of(a, b) + kTK - 1) / kTK;
+        tiles.c.start(a, static_cast<int64_t>(u) * nt, static_cast<int64_t>(u + 1) * nt, b, 0);
+        if (nt == 0) {  // no key: zero rows
+            const int g = u / a.groups, h0 = g * a.G + (u - g * a.groups) * 8;
+            const int n = min(GP, (g + 1) * a.G - h0) * (D / 8);
+            uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.o) + (static_cast<int64_t>(b) * a.H + h0) * D);
+            for (int i = threadIdx.x; i < n; i += kThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+    } else {
+        if (warp >= 2 && warp < 6) find_range(a, range, bar.range_full());
+        ok = mbar_wait(bar.range_full(), 0, a.err);
+        if (ok) tiles.c.start(a, range.lo, range.hi, range.b0, range.base);
+    }
+    if (ok) {
         const PagedMaps maps{{{tm.m[0][0], tm.m[0][1]}, {tm.m[1][0], tm.m[1][1]}}};
         paged_body<T, E8, D, GP>(a, maps, tiles, smem, tmem, warp, lane);
     }
@@ -928,7 +961,8 @@ cudaError_t launch_paged_g(const PagedMapSet& tm, PagedArgs& a, int sms, cudaStr
     const int64_t most = static_cast<int64_t>(a.c.B) * a.units * ((room + kTK - 1) / kTK);
     int64_t grid = C::kCtas * sms;
     grid = grid < kPagedMaxGrid ? grid : kPagedMaxGrid;
-    a.grid = static_cast<int>(grid < most ? grid : most);
+    grid = a.direct ? static_cast<int64_t>(a.c.B) * a.units : grid < most ? grid : most;
+    a.grid = static_cast<int>(grid);
     return launch_pdl(a.pdl != 0, kern, dim3(a.grid), dim3(kThreads), C::kSmem, s, tm,
                       static_cast<const PagedArgs&>(a));
 }

@@ -32,6 +32,8 @@ struct PagedArgs {
     int grid;
     float scale;
     int alibi, pdl;
+    int direct;  // a unit per CTA, rows to o
+    void* o;
 };
 
 cudaError_t launch_paged_f16(bool e8, const PagedMapSet& tm, PagedArgs& a, int sms, cudaStream_t s);

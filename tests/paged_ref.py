@@ -56,16 +56,16 @@ def values(cache, scale):
 
 def rows(cache, scale, table, n, page):
     """The first n positions of a sequence: ([Hk, n, d], seen [n], scale [Hk, n])."""
-    x = values(cache, scale)
-    pages, Hk, _, d = x.shape
-    out, seen, sc = np.zeros((Hk, n, d)), np.zeros(n, bool), np.ones((Hk, n))
-    for p in range(n):
-        at = int(table[p // page])
-        if 0 <= at < pages:
-            out[:, p], seen[p] = x[at, :, p % page], True
-            if scale is not None:
-                sc[:, p] = scale[at].cpu().double().numpy()
-    return out, seen, sc
+    at = torch.as_tensor(table[:-(-n // page)], dtype=torch.long, device=cache.device)
+    ok = (at >= 0) & (at < cache.shape[0])
+    x = cache[at.clamp(0, cache.shape[0] - 1)].float().double()
+    s = torch.ones(x.shape[:2], dtype=torch.float64, device=x.device)
+    if scale is not None:
+        s = scale[at.clamp(0, cache.shape[0] - 1)].double()
+        x = x * s[..., None, None]
+    x = x.transpose(0, 1).flatten(1, 2)[:, :n].cpu().numpy()
+    seen = ok.repeat_interleave(page)[:n].cpu().numpy()
+    return np.where(seen[None, :, None], x, 0.0), seen, s.t().repeat_interleave(page, 1)[:, :n].cpu().numpy()
 
 
 def decode(q, k, v, seen, slopes=None, scale=None):

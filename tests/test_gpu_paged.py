@@ -83,13 +83,13 @@ def check(got, q, k, v, ks, vs, table, lens, page, dt, slopes=None, scale=None, 
             f"{name} row {b}: error {err.max():.3e}, {float((err / bound).max()):.2f} of the bound"
 
 
-def run(B, H, Hk, d, page, lens, dt, bits, alibi=False, seed=0, spread=0.0, scale=None):
+def run(B, H, Hk, d, page, lens, dt, bits, alibi=False, seed=0, spread=0.0, scale=None, room=1):
     g = torch.Generator(device="cuda")
     g.manual_seed(seed)
     need = [-(-n // page) for n in lens]
     pages = sum(need) + 2
     k, v, ks, vs = pool(pages, Hk, page, d, dt, bits, g, spread)
-    table = torch.full((B, max(need) + 1), -1, dtype=torch.int32)
+    table = torch.full((B, max(need) + room), -1, dtype=torch.int32)
     order = np.random.RandomState(seed).permutation(pages)
     at = 0
     for b, m in enumerate(need):
@@ -146,5 +146,14 @@ def test_every_kernel(G, d, dt, bits):
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
 @pytest.mark.parametrize("case", CASES, ids=lambda c: "B{}H{}Hk{}d{}p{}".format(*c[:5]))
 def test_matches_definition(case, dt, bits):
+    """With room to spare in the block table, every case takes the two launches."""
     B, H, Hk, d, page, lens, alibi = case
-    run(B, H, Hk, d, page, lens, dt, bits, alibi, seed=B + H + d)
+    for room in (0, 2000):
+        run(B, H, Hk, d, page, lens, dt, bits, alibi, seed=B + H + d, room=room)
+
+
+def test_room_chooses_the_form():
+    def need(max_pages, page):
+        return blk.attn_decode_paged_workspace_size(blk.decode_paged_desc(
+            (9, page, 2, 64, 3, max_pages, 2 * page * 64, 1), 4, 256, 64))
+    assert need(32, 16) == 0 and need(4, 128) == 0 and need(33, 16) > 0 and need(5, 128) > 0
