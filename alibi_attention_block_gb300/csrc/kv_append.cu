@@ -26,6 +26,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include <cmath>
 
@@ -102,6 +103,11 @@ __device__ __forceinline__ bool rows_of(const AppendArgs& a, int64_t i, int lane
     return true;
 }
 
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+    float r;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 __device__ __forceinline__ float if_finite(float x) {
     x = fabsf(x);
     return x < INFINITY ? x : 0.f;
@@ -148,13 +154,14 @@ __device__ __forceinline__ uint32_t rescaled(uint32_t codes, float by) {
 // length, the table) is a chain of dependent loads that its teams and heads share:
 // with a block of one warp for each page and head, 5000 tokens of 32 x 64 heads took 47 us.
 template <typename T, bool E8, int VP, int IT>
-__global__ void __launch_bounds__(IT * VP > 16 ? 512 : 768) kv_append_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(IT * VP > 16 ? 512 : IT * VP > 8 ? 768 : 1024) kv_append_kernel(const __grid_constant__ AppendArgs a) {
     __shared__ float most[2][32];
     extern __shared__ float4 angles[];
     __shared__ uint64_t plan[kMaxRotaryPairs];
     const int d = a.c.d, units = d / (2 * VP);
     const int lane = threadIdx.x & 31;
-    const bool is_q = static_cast<int>(blockIdx.y) >= a.kv_groups;
+    const int group = blockIdx.y;
+    const bool is_q = group >= a.kv_groups;
     // queries: threads by head, token and unit; else by team, token and unit
     const int threads = is_q ? blockDim.x : a.team;
     const int team = is_q ? 0 : threadIdx.x / a.team;
@@ -170,28 +177,92 @@ __global__ void __launch_bounds__(IT * VP > 16 ? 512 : 768) kv_append_kernel(con
     if (!rows_of(a, blockIdx.x, lane, r)) return;
     using Raw = typename RawPiece<VP>::type;
 
+    // cosines and sines of the rows, for all the block's heads: plane j of a unit's pairs
+    // 2 j and 2 j + 1 (VP 1: of its pair)
+    const int turned_units = a.turn.plan.pairs / VP, cells = r.n * turned_units;
+    constexpr int kPlanes = VP > 1 ? VP / 2 : 1;
+    auto make_table = [&]() {
+        for (int i = threadIdx.x; i < cells * kPlanes; i += blockDim.x) {
+            const int cell = i / kPlanes, j = i - cell * kPlanes;
+            const int k = cell / turned_units, pair = (cell - k * turned_units) * VP + 2 * j;
+            const int pos = a.positions ? a.positions[r.row + k] : static_cast<int>(r.pos + k);
+            float c0, s0, c1, s1;
+            turn_cos_sin(plan[pair], pos, c0, s0);
+            if constexpr (VP > 1) {
+                turn_cos_sin(plan[pair + 1], pos, c1, s1);
+                angles[j * cells + cell] = make_float4(c0 * m, s0 * m, c1 * m, s1 * m);
+            } else {
+                reinterpret_cast<float2*>(angles)[cell] = make_float2(c0 * m, s0 * m);
+            }
+        }
+        __syncthreads();
+    };
+    auto look_up = [&](int k, Angles<VP>& ang) {
+        const int cell = k * turned_units + u;
+        if constexpr (VP > 1) {
+#pragma unroll
+            for (int j = 0; j < kPlanes; ++j) {
+                const float4 f = angles[j * cells + cell];
+                ang.c[2 * j] = f.x;
+                ang.s[2 * j] = f.y;
+                ang.c[2 * j + 1] = f.z;
+                ang.s[2 * j + 1] = f.w;
+            }
+        } else {
+            const float2 f = reinterpret_cast<const float2*>(angles)[cell];
+            ang.c[0] = f.x;
+            ang.s[0] = f.y;
+        }
+    };
+
+    // ... two pairs at a time, for a unit turned once (fewer registers than look_up)
+    auto turn_by_table = [&](int k, float (&x)[VP], float (&y)[VP]) {
+        const int cell = k * turned_units + u;
+        if constexpr (VP > 1) {
+            if (a.turn.plan.interleaved) {
+#pragma unroll
+                for (int j = 0; j < kPlanes; ++j) {
+                    const float4 f = angles[j * cells + cell];
+                    float(&z)[VP] = j < kPlanes / 2 ? x : y;
+                    turn_pair(z[4 * j % VP], z[4 * j % VP + 1], f.x, f.y);
+                    turn_pair(z[4 * j % VP + 2], z[4 * j % VP + 3], f.z, f.w);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < kPlanes; ++j) {
+                    const float4 f = angles[j * cells + cell];
+                    turn_pair(x[2 * j], y[2 * j], f.x, f.y);
+                    turn_pair(x[2 * j + 1], y[2 * j + 1], f.z, f.w);
+                }
+            }
+        } else {
+            const float2 f = reinterpret_cast<const float2*>(angles)[cell];
+            turn_pair(x[0], y[0], f.x, f.y);
+        }
+    };
+
     if (is_q) {
+        make_table();
         const int side = min(rows, 1 << a.c.page_log2);  // tokens side by side
         const int step = rows / side;                    // and heads
-        const int h0 = (blockIdx.y - a.kv_groups) * a.q_per, h1 = min(h0 + a.q_per, a.H);
+        const int h0 = (group - a.kv_groups) * a.q_per, h1 = min(h0 + a.q_per, a.H);
         if (place >= side * step) return;
         for (int k = place % side; k < r.n; k += side) {
             Angles<VP> ang;
-            if (at.turned)
-                ang.set(plan + u * VP, a.positions ? a.positions[r.row + k] : static_cast<int>(r.pos + k), m, m);
+            if (at.turned) look_up(k, ang);
             const T* x = static_cast<const T*>(a.x[2]) + (r.row + k) * a.xs[2][1];
             T* y = static_cast<T*>(a.q_out) + (r.row + k) * a.qs[1];
             // four heads' loads on their way at a time
-            for (int h = h0 + place / side; h < h1; h += 4 * step) {
-                Raw raw[4][2];
+            for (int h = h0 + place / side; h < h1; h += 2 * step) {
+                Raw raw[2][2];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 2; ++i)
                     if (h + i * step < h1) {
                         raw[i][0] = load_raw<T, VP>(x + (h + i * step) * a.xs[2][0] + at.a);
                         raw[i][1] = load_raw<T, VP>(x + (h + i * step) * a.xs[2][0] + at.b);
                     }
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 2; ++i)
                     if (h + i * step < h1) {
                         float p[VP], q[VP];
                         unpack_raw<T, VP>(raw[i][0], p);
@@ -209,156 +280,126 @@ __global__ void __launch_bounds__(IT * VP > 16 ? 512 : 768) kv_append_kernel(con
     if (r.page >= a.c.max_pages) return;
     const int page = a.c.table[static_cast<int64_t>(r.b) * a.c.max_pages + r.page];
     if (page < 0 || page >= a.c.pages) return;
-    const bool mine = place < rows;
-    const int slots = 2 * a.c.Hk, teams = blockDim.x / a.team;
-    const int end = min(static_cast<int>(blockIdx.y + 1) * a.kv_per, slots);
-    Raw raw[IT][2];
-    // the values' pieces lie side by side wherever the keys' do
-    auto fetch = [&](int slot) {
-        const int what = slot >= a.c.Hk;
-        const T* x = static_cast<const T*>(a.x[what]) + (slot - what * a.c.Hk) * a.xs[what][0] +
-                     r.row * a.xs[what][1];
+    const int teams = blockDim.x / a.team, team_warps = a.team / 32;
+    const int first = group * a.kv_per, end = min(first + a.kv_per, 2 * a.c.Hk);
+    const int64_t head_size = static_cast<int64_t>(d) << a.c.page_log2;
+    bool on[IT];  // this thread's rows
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const int k = place + i * rows;
-            if (mine && k < r.n) {
-                raw[i][0] = load_raw<T, VP>(x + k * a.xs[what][1] + at.a);
-                raw[i][1] = load_raw<T, VP>(x + k * a.xs[what][1] + at.b);
+    for (int i = 0; i < IT; ++i) on[i] = place < rows && place + i * rows < r.n;
+    // The largest of x over the team (a round of its own barrier; entries alternate between rounds).
+    int odd = 0;
+    auto of_team = [&](float x) {
+        x = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
+        if (team_warps > 1) {
+            if (lane == 0) most[odd][threadIdx.x / 32] = x;
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(a.team) : "memory");
+            x = most[odd][team * team_warps + (lane < team_warps ? lane : 0)];
+            x = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
+            odd ^= 1;
+        } else {
+            __syncwarp();  // every lane has read the scale
+        }
+        return x;
+    };
+    // Heads s0 + team, s0 + team + teams, ... < s1 of K or of V.
+    auto append = [&](auto values, int s0, int s1) {
+        constexpr bool kValues = decltype(values)::value;
+        s0 += team;
+        if (s0 >= s1) return;
+        // (the values' pieces lie where the keys' do)
+        const bool turned = at.turned && !kValues;
+        const int64_t hs = a.xs[kValues][0], ts = a.xs[kValues][1];
+        const T* x = static_cast<const T*>(a.x[kValues]) + s0 * hs + (r.row + place) * ts;
+        const int64_t base = page * a.c.page_stride + s0 * head_size + (r.first + place) * d;
+        const int64_t head_step = teams * head_size;
+        uint8_t* codes = static_cast<uint8_t*>(kValues ? a.c.v : a.c.k) + base;
+        T* cache = static_cast<T*>(kValues ? a.c.v : a.c.k) + base;
+        float* scale = (kValues ? a.c.v_scale : a.c.k_scale) + static_cast<int64_t>(page) * a.c.Hk + s0;
+        constexpr bool kAhead = VP > 1;  // the next head's loads behind this one's (VP 1: too many registers)
+        Raw raw[IT][2];
+        auto fetch = [&]() {
+#pragma unroll
+            for (int i = 0; i < IT; ++i)
+                if (on[i]) {
+                    raw[i][0] = load_raw<T, VP>(x + i * rows * ts + at.a);
+                    raw[i][1] = load_raw<T, VP>(x + i * rows * ts + at.b);
+                }
+            x += teams * hs;
+        };
+        if (kAhead) fetch();
+        for (int s = s0; s < s1; s += teams) {
+            if (!kAhead) fetch();
+            float v[IT][2][VP];
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                unpack_raw<T, VP>(raw[i][0], v[i][0]);
+                unpack_raw<T, VP>(raw[i][1], v[i][1]);
+            }
+            if (kAhead && s + teams < s1) fetch();
+            float held = 0.f;
+            if (E8 && r.first > 0) held = *scale;  // (a page's first row begins its scale anew)
+            float top = 0.f;
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                if (!on[i]) continue;
+                if (turned) turn_by_table(place + i * rows, v[i][0], v[i][1]);
+                if constexpr (E8) {
+#pragma unroll
+                    for (int e = 0; e < VP; ++e) top = max_abs(top, v[i][0][e], v[i][1][e]);  // (NaN: passed over)
+                }
+            }
+            if constexpr (E8) {
+                top = of_team(top);
+                if (top == INFINITY) {  // the largest finite one, then
+                    top = 0.f;
+#pragma unroll
+                    for (int i = 0; i < IT; ++i) {
+                        if (!on[i]) continue;
+#pragma unroll
+                        for (int e = 0; e < VP; ++e)
+                            top = fmaxf(top, fmaxf(if_finite(v[i][0][e]), if_finite(v[i][1][e])));
+                    }
+                    top = of_team(top);
+                }
+                const float now = fmaxf(scale_for(top), held);
+                if (tid == 0) *scale = now;
+                if (r.first > 0 && held < now) {
+                    const float by = held / now;
+                    uint4* old = reinterpret_cast<uint4*>(codes - (r.first + place) * d);
+                    for (int i = tid; i < r.first * (d / 16); i += a.team) {
+                        uint4 o = old[i];
+                        o.x = rescaled(o.x, by);
+                        o.y = rescaled(o.y, by);
+                        o.z = rescaled(o.z, by);
+                        o.w = rescaled(o.w, by);
+                        old[i] = o;
+                    }
+                }
+                const float inv = 1.0f / now;
+#pragma unroll
+                for (int i = 0; i < IT; ++i)
+                    if (on[i]) {
+                        store_codes<VP>(codes + i * rows * d + at.a, v[i][0], inv);
+                        store_codes<VP>(codes + i * rows * d + at.b, v[i][1], inv);
+                    }
+                codes += head_step;
+                scale += teams;
+            } else {
+#pragma unroll
+                for (int i = 0; i < IT; ++i)
+                    if (on[i]) {
+                        store_piece(cache + i * rows * d + at.a, v[i][0]);
+                        store_piece(cache + i * rows * d + at.b, v[i][1]);
+                    }
+                cache += head_step;
             }
         }
     };
-    int odd = 0, slot = blockIdx.y * a.kv_per + team;
-    constexpr bool kAhead = VP > 1;  // (single elements: too many registers)
-    if (kAhead && slot < end) fetch(slot);
-    // cosines and sines of the rows, for all the block's heads of K: plane j of a unit's
-    // pairs 2 j and 2 j + 1 (VP 1: of its pair)
-    const int turned_units = a.turn.plan.pairs / VP, cells = r.n * turned_units;
-    constexpr int kPlanes = VP > 1 ? VP / 2 : 1;
-    if (static_cast<int>(blockIdx.y) * a.kv_per < a.c.Hk && cells > 0) {
-        for (int i = threadIdx.x; i < cells * kPlanes; i += blockDim.x) {
-            const int cell = i / kPlanes, j = i - cell * kPlanes;
-            const int k = cell / turned_units, pair = (cell - k * turned_units) * VP + 2 * j;
-            const int pos = a.positions ? a.positions[r.row + k] : static_cast<int>(r.pos + k);
-            float c0, s0, c1, s1;
-            turn_cos_sin(plan[pair], pos, c0, s0);
-            if constexpr (VP > 1) {
-                turn_cos_sin(plan[pair + 1], pos, c1, s1);
-                angles[j * cells + cell] = make_float4(c0 * m, s0 * m, c1 * m, s1 * m);
-            } else {
-                reinterpret_cast<float2*>(angles)[cell] = make_float2(c0 * m, s0 * m);
-            }
-        }
-        __syncthreads();
+    if (first < a.c.Hk) {
+        make_table();
+        append(std::false_type{}, first, min(end, a.c.Hk));
     }
-    for (; slot < end; slot += teams) {
-        const int what = slot >= a.c.Hk, head = slot - what * a.c.Hk;
-        const bool turned = at.turned && what == 0;
-        const int64_t base = page * a.c.page_stride + (static_cast<int64_t>(head) << a.c.page_log2) * d;
-        if (!kAhead) fetch(slot);
-        float v[IT][2][VP];
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            unpack_raw<T, VP>(raw[i][0], v[i][0]);
-            unpack_raw<T, VP>(raw[i][1], v[i][1]);
-        }
-        if (kAhead && slot + teams < end) fetch(slot + teams);  // on their way behind these
-        float held = 0.f;
-        float* scale = nullptr;
-        if constexpr (E8) {
-            scale = (what ? a.c.v_scale : a.c.k_scale) + static_cast<int64_t>(page) * a.c.Hk + head;
-            if (r.first > 0) held = *scale;  // (a page's first row begins its scale anew)
-        }
-        float top = 0.f;
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const int k = place + i * rows;
-            if (mine && k < r.n) {
-                if (turned) {
-#pragma unroll
-                    for (int j = 0; j < kPlanes; ++j) {
-                        const int cell = k * turned_units + u;
-                        if constexpr (VP > 1) {
-                            const float4 f = angles[j * cells + cell];
-                            turn_in_unit<VP>(v[i][0], v[i][1], 2 * j, a.turn.plan.interleaved, f.x, f.y);
-                            turn_in_unit<VP>(v[i][0], v[i][1], 2 * j + 1, a.turn.plan.interleaved, f.z, f.w);
-                        } else {
-                            const float2 f = reinterpret_cast<const float2*>(angles)[cell];
-                            turn_in_unit<VP>(v[i][0], v[i][1], 0, a.turn.plan.interleaved, f.x, f.y);
-                        }
-                    }
-                }
-                if constexpr (E8) {
-#pragma unroll
-                    for (int e = 0; e < VP; ++e)
-                        top = fmaxf(top, fmaxf(fabsf(v[i][0][e]), fabsf(v[i][1][e])));  // (NaN: passed over)
-                }
-            }
-        }
-        if constexpr (E8) {
-            uint8_t* codes = static_cast<uint8_t*>(what ? a.c.v : a.c.k) + base;
-            // the team's largest (a round of its own barrier; entries alternate between rounds)
-            auto of_team = [&](float x) {
-                x = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
-                if (a.team > 32) {
-                    const int w0 = team * (a.team / 32);
-                    if (lane == 0) most[odd][threadIdx.x / 32] = x;
-                    asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(a.team) : "memory");
-                    for (int w = 0; w < a.team / 32; ++w) x = fmaxf(x, most[odd][w0 + w]);
-                    odd ^= 1;
-                } else {
-                    __syncwarp();  // every lane has read the scale
-                }
-                return x;
-            };
-            top = of_team(top);
-            if (top == INFINITY) {  // the largest finite one, then
-                top = 0.f;
-#pragma unroll
-                for (int i = 0; i < IT; ++i) {
-                    if (!mine || place + i * rows >= r.n) continue;
-#pragma unroll
-                    for (int e = 0; e < VP; ++e)
-                        top = fmaxf(top, fmaxf(if_finite(v[i][0][e]), if_finite(v[i][1][e])));
-                }
-                top = of_team(top);
-            }
-            const float now = fmaxf(scale_for(top), held);
-            if (tid == 0) *scale = now;
-            if (r.first > 0 && held < now) {
-                const float by = held / now;
-                uint4* old = reinterpret_cast<uint4*>(codes);
-                for (int i = tid; i < r.first * (d / 16); i += a.team) {
-                    uint4 o = old[i];
-                    o.x = rescaled(o.x, by);
-                    o.y = rescaled(o.y, by);
-                    o.z = rescaled(o.z, by);
-                    o.w = rescaled(o.w, by);
-                    old[i] = o;
-                }
-            }
-            const float inv = 1.0f / now;
-#pragma unroll
-            for (int i = 0; i < IT; ++i) {
-                const int k = place + i * rows;
-                if (mine && k < r.n) {
-                    uint8_t* dst = codes + (r.first + k) * d;
-                    store_codes<VP>(dst + at.a, v[i][0], inv);
-                    store_codes<VP>(dst + at.b, v[i][1], inv);
-                }
-            }
-        } else {
-            T* cache = static_cast<T*>(what ? a.c.v : a.c.k) + base;
-#pragma unroll
-            for (int i = 0; i < IT; ++i) {
-                const int k = place + i * rows;
-                if (mine && k < r.n) {
-                    T* dst = cache + (r.first + k) * d;
-                    store_piece(dst + at.a, v[i][0]);
-                    store_piece(dst + at.b, v[i][1]);
-                }
-            }
-        }
-    }
+    if (end > a.c.Hk) append(std::true_type{}, max(first - a.c.Hk, 0), end - a.c.Hk);
 }
 
 template <typename T, bool E8, int VP, int IT>
@@ -367,9 +408,9 @@ cudaError_t launch_append(AppendArgs& a, int64_t items, int sms, cudaStream_t s)
     a.team = (units * ((page + IT - 1) / IT) + 31) / 32 * 32;
     const int teams = a.team >= 256 ? 1 : 256 / a.team;
     // heads of a block: as many as make about a round of blocks each of keys and values and of
-    // queries (768 threads per SM), since what is ahead of a block's first load is a chain of
+    // queries, since what is ahead of a block's first load is a chain of
     // latencies; eight in turn at most for a team, sixteen for a thread of queries
-    const int64_t blocks = static_cast<int64_t>(sms) * std::max(1, 768 / (teams * a.team)), slots = 2 * a.c.Hk;
+    const int64_t blocks = static_cast<int64_t>(sms) * std::max(1, (IT * VP > 8 ? 768 : 1024) / (teams * a.team)), slots = 2 * a.c.Hk;
     int64_t loops = items * slots / (teams * blocks);
     loops = loops < 1 ? 1 : loops > 8 ? 8 : loops;
     a.kv_per = static_cast<int>(teams * loops);
@@ -378,9 +419,11 @@ cudaError_t launch_append(AppendArgs& a, int64_t items, int sms, cudaStream_t s)
     int64_t per = items * a.H / (side * blocks);
     per = side * (per < 1 ? 1 : per > 16 ? 16 : per);
     a.q_per = static_cast<int>(per);
+    // (K's groups, the longest, first: side by side with the queries' in the grid they were last, and
+    // the whole slower, 112 -> 118 us in the large case)
     const int64_t groups = a.kv_groups + (a.H + per - 1) / per;
     const int table = page * a.turn.plan.pairs * 8;
-    if (table > 48 * 1024) {
+    if (table > 46 * 1024) {  // (with the static 1.3 KB, more than a launch has without asking)
         const cudaError_t e =
             set_smem_attr_once(reinterpret_cast<const void*>(kv_append_kernel<T, E8, VP, IT>), 128 * 1024);
         if (e != cudaSuccess) return e;
@@ -393,8 +436,10 @@ template <typename T, bool E8>
 cudaError_t launch_append_w(AppendArgs& a, int64_t items, int sms, cudaStream_t s) {
     const int values = a.c.d << a.c.page_log2;  // of a page and head
     switch (turn_width(a.turn.plan.pairs)) {
-        // 32 values per thread, 64 where a page would take more than 512 threads
+        // 32 values per thread, 64 where a page would take more than 512 threads; in 16 bits, where no
+        // value waits for the page's largest, 16 (10.6 -> 9.4 us for 3020 tokens of 16 x 64)
         case 8:
+            if (!E8 && values <= 512 * 16) return launch_append<T, E8, 8, 1>(a, items, sms, s);
             return values > 512 * 32 ? launch_append<T, E8, 8, 4>(a, items, sms, s)
                                      : launch_append<T, E8, 8, 2>(a, items, sms, s);
         case 4:

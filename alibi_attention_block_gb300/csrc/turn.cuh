@@ -122,15 +122,19 @@ __device__ __forceinline__ void turn_pair(float& x, float& y, float c, float s) 
     y = fmaf(y, c, x0 * s);
 }
 
-// Where pair i of a unit lies in its pieces a and b.
+// Turns a unit's pieces a and b: pair i by (c[i], s[i]).
 template <int VP>
-__device__ __forceinline__ void turn_in_unit(float (&a)[VP], float (&b)[VP], int i, int interleaved,
-                                             float c, float s) {
+__device__ __forceinline__ void turn_unit(float (&a)[VP], float (&b)[VP], int interleaved,
+                                          const float (&c)[VP], const float (&s)[VP]) {
     if (VP > 1 && interleaved) {
-        if (i < VP / 2) turn_pair(a[(2 * i) % VP], a[(2 * i + 1) % VP], c, s);
-        else turn_pair(b[(2 * i) % VP], b[(2 * i + 1) % VP], c, s);
+#pragma unroll
+        for (int i = 0; i < VP / 2; ++i) {
+            turn_pair(a[2 * i], a[2 * i + 1], c[i], s[i]);
+            turn_pair(b[2 * i], b[2 * i + 1], c[VP / 2 + i], s[VP / 2 + i]);
+        }
     } else {
-        turn_pair(a[i], b[i], c, s);
+#pragma unroll
+        for (int i = 0; i < VP; ++i) turn_pair(a[i], b[i], c[i], s[i]);
     }
 }
 
@@ -149,8 +153,7 @@ struct Angles {
         }
     }
     __device__ __forceinline__ void turn(float (&a)[VP], float (&b)[VP], int interleaved) const {
-#pragma unroll
-        for (int i = 0; i < VP; ++i) turn_in_unit<VP>(a, b, i, interleaved, c[i], s[i]);
+        turn_unit<VP>(a, b, interleaved, c, s);
     }
 };
 
