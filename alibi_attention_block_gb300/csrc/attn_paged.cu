@@ -23,9 +23,14 @@ struct MergeArgs {
 };
 
 // The CTA whose range [c * W / n, (c + 1) * W / n) holds tile t, n CTAs in all (W >= n):
-// c * W < (t + 1) * n <= (c + 1) * W.
+// c * W < (t + 1) * n <= (c + 1) * W, from an estimate in floating point that is off by
+// one at most (n is at most kPagedMaxGrid).
 __device__ __forceinline__ int cta_of(int64_t t, int64_t W, int n) {
-    return static_cast<int>(((t + 1) * n - 1) / W);
+    const int64_t x = (t + 1) * n;
+    int c = static_cast<int>(static_cast<float>(t) * (static_cast<float>(n) / static_cast<float>(W)));
+    while (c * W >= x) --c;
+    while ((c + 1) * W < x) ++c;
+    return c;
 }
 
 // D / 8 threads per row of 8 columns each.

@@ -19,11 +19,11 @@
 //     q = 2^e (q1 + 2^-5 q2 + 2^-10 q3),   q1 = e4m3(2^-e q), q2 = e4m3(2^5 (2^-e q - q1)), ...
 // with 2^e such that the row's largest is in [128, 256). Each e4m3 holds 4 significant bits, a
 // remainder is at most 2^-5 of its number, so two parts hold a bf16 number and three an fp16
-// number exactly, down to 2^-23 and 2^-28 of the row's largest. (The columns are there
+// number exactly, down to 2^-22 and 2^-27 of the row's largest. (The columns are there
 // anyway: N is at least 16.) Weights, likewise: two parts (bf16) are at most 2^-9 off, relative, three
 // (fp16) 2^-14, which is less than the output's own rounding; their sums are of the 32-bit
-// weights. Where a weight is far below the largest, the error is absolute, 2^-22 and
-// 2^-27 of that one.
+// weights. Where a weight is far below the largest, the error is absolute, 2^-21 and
+// 2^-26 of that one.
 // A page's scales are factors of its keys: that of K multiplies the score, that of V
 // the weight ahead of its rounding. So that the weight times scale stays in e4m3's range whatever the
 // scales are, the running reference that is subtracted is of score + log2(scale of V), not of the score.
@@ -267,8 +267,11 @@ struct Segments {
         if (!valid) return;
         len = len_of(a, b);
         const int nt = (len + kTK - 1) / kTK;
-        u = static_cast<int>((t - base) / nt);
-        first = static_cast<int>((t - base) % nt);
+        // (from its sequence's first tile: units * 2^24 tiles at most, by lengths in 31 bits)
+        const int64_t in = t - base;
+        u = in < (int64_t(1) << 31) ? static_cast<int>(static_cast<uint32_t>(in) / static_cast<uint32_t>(nt))
+                                    : static_cast<int>(in / nt);
+        first = static_cast<int>(in - static_cast<int64_t>(u) * nt);
         set();
     }
     __device__ __forceinline__ void next(const PagedArgs& a) {

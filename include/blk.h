@@ -413,7 +413,7 @@ typedef struct {
  * GQA: kv head = h / (n_heads / n_kv_heads), any ratio; above 8 the cache is read
  * once for every 8 query heads of a kv head. Sums and statistics are in 32 bits; softmax weights enter the product
  * with V rounded: to dt over a 16-bit cache; over e4m3, to sums of two (bf16) or three
- * (fp16) e4m3 numbers, at most 2^-9 or 2^-14 off, relative, or 2^-22 and 2^-27 of the largest.
+ * (fp16) e4m3 numbers, at most 2^-9 or 2^-14 off, relative, or 2^-21 and 2^-26 of the largest.
  * Two launches. The workspace holds partial results, at least
  * blk_attn_decode_paged_workspace_size bytes, 16-byte aligned; calls whose
  * kernels overlap on the GPU need a workspace each. Where block_table has room for a

@@ -203,3 +203,185 @@ def test_append(c, dt, bits):
     for i, layout in enumerate(("heads", "tokens")):
         case(*c, dt, bits, interleaved=i == 1, seed=c[2] + c[3] + i, layout=layout, loud=1.0 + 3 * i,
              with_q=c[3] > 0)
+
+
+def test_positions_and_room():
+    """Given positions; single tokens without cu_seqlens; pages behind the table and outside the pool."""
+    case(4, 2, 128, 128, 32, [0, 40, 7], [33, 30, 0], "bf16", 8, positions=True, seed=1)
+    case(4, 2, 64, 64, 16, [0, 15, 16, 100], [1, 1, 1, 1], "fp16", 8, one_each=True, seed=2)
+    case(4, 2, 64, 64, 16, [0, 15, 16, 100], [1, 1, 1, 1], "bf16", 16, one_each=True, seed=3)
+    case(2, 2, 128, 64, 16, [0, 40], [70, 30], "bf16", 8, capacity=3, seed=4)   # 48 positions of room
+    case(2, 2, 128, 64, 16, [0, 40], [70, 30], "bf16", 16, capacity=3, seed=5)
+
+
+def blank(pages, Hk, page, d, kind):
+    dt = torch.float8_e4m3fn if kind == 8 else torch.bfloat16
+    caches = [torch.zeros((pages, Hk, page, d), device="cuda").to(dt) for _ in "kv"]
+    scales = [torch.full((pages, Hk), 2.0 ** -60, device="cuda") for _ in "kv"] if kind == 8 else [None, None]
+    return (*caches, *scales)
+
+
+def same(a, b):
+    return torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("page", [16, 64])
+def test_tokens_one_by_one(page):
+    """100 single tokens leave the scales of one call with all of them, and its codes but for those
+    that a growing scale has rounded twice (below 2^-6 of it)."""
+    Hk, d, n = 3, 64, 100
+    g = gen(11)
+    k, v = (torch.randn((Hk, n, d), generator=g, device="cuda") * torch.exp2(torch.arange(n, device="cuda") / 9 - 6)[:, None]
+            for _ in "kv")
+    k, v = k.bfloat16(), v.bfloat16()
+    plan = blk.rope_plan(32, 10000.0)
+    pages = -(-n // page)
+    table = i32([list(range(pages))])
+    whole, steps = blank(pages, Hk, page, d, 8), blank(pages, Hk, page, d, 8)
+    blk.kv_append_paged(k, v, *whole[:2], table, i32([n]), cu_seqlens=i32([0, n]), k_scale=whole[2], v_scale=whole[3],
+                        rope=plan)
+    for t in range(n):
+        blk.kv_append_paged(k[:, t:t + 1], v[:, t:t + 1], *steps[:2], table, i32([t + 1]), k_scale=steps[2],
+                            v_scale=steps[3], rope=plan)
+    for i in range(2):
+        assert torch.equal(whole[2 + i], steps[2 + i])
+        a, b = whole[i].float(), steps[i].float()
+        big = a.abs() >= 2.0 ** -6
+        assert torch.equal(a[big], b[big])
+        assert float((a - b).abs().max()) <= 2.0 ** -9
+
+
+def test_not_finite_values():
+    """NaN stays NaN, an infinity becomes the largest code; the scale is that of the finite values."""
+    Hk, d, page = 2, 64, 16
+    k = torch.randn((Hk, 20, d), generator=gen(5), device="cuda").bfloat16()
+    v = k.clone()
+    v[0, 3, 5], v[0, 4, 6], v[0, 5, 7] = float("inf"), -float("inf"), float("nan")
+    v[1, 17] = float("inf")  # a page of which ...
+    v[1, 16], v[1, 18:] = float("nan"), float("inf")  # ... nothing is finite
+    c = blank(2, Hk, page, d, 8)
+    blk.kv_append_paged(k, v, *c[:2], i32([[0, 1]]), i32([20]), cu_seqlens=i32([0, 20]), k_scale=c[2], v_scale=c[3])
+    got, s = c[1].float(), c[3]
+    assert got[0, 0, 3, 5] == 448 and got[0, 0, 4, 6] == -448 and torch.isnan(got[0, 0, 5, 7])
+    fin = v[0, :16].float()
+    assert float(s[0, 0]) == ref.page_scale(float(fin[torch.isfinite(fin)].abs().max()))
+    assert float(s[1, 1]) == 2.0 ** -60 and torch.isnan(got[1, 1, 0]).all() and (got[1, 1, 1:4] == 448).all()
+    assert torch.isfinite(got[0, 1]).all() and torch.isfinite(c[0].float()).all()
+
+
+def test_bits_of_a_call():
+    """Twice the same bits; with views of one pool, on another stream, in place, as a graph replayed."""
+    Hk, H, d, page, B = 2, 4, 128, 32, 5
+    g = gen(6)
+    new, before = [40, 1, 0, 70, 33], [0, 31, 5, 10, 64]
+    T = sum(new)
+    cu, lens = i32(np.concatenate([[0], np.cumsum(new)]).tolist()), i32([a + b for a, b in zip(new, before)])
+    table = i32([[5 * j + b for j in range(4)] for b in range(B)])
+    k, v, q = (randn((n, T, d), "bf16", g) for n in (Hk, Hk, H))
+    plan = blk.rope_plan(128, 500000.0, interleaved=True)
+
+    def run(c, q=q, **kw):
+        return blk.kv_append_paged(k, v, c[0], c[1], table, lens, cu_seqlens=cu, k_scale=c[2], v_scale=c[3], rope=plan,
+                                   q=q, **kw)
+    a, b = blank(20, Hk, page, d, 8), blank(20, Hk, page, d, 8)
+    qa, qb = run(a), run(b)
+    run(b)  # over again: the same tokens at the same scales
+    assert torch.equal(qa, qb) and all(same(x, y) for x, y in zip(a, b))
+    both = torch.zeros((20, 2, Hk, page, d), device="cuda").to(torch.float8_e4m3fn)
+    c = (both[:, 0], both[:, 1], torch.zeros((20, Hk), device="cuda"), torch.zeros((20, Hk), device="cuda"))
+    run(c)
+    held = table.view(-1).long()[[b * 4 + j for b in range(B) for j in range(-(-int(lens[b]) // page))]]
+    for i in range(2):
+        x, y = c[i].contiguous().view(torch.uint8), a[i].view(torch.uint8)
+        assert torch.equal(x[held], y[held])
+    s = torch.cuda.Stream()
+    e = blank(20, Hk, page, d, 8)
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        qe = q.clone()
+        assert run(e, qe, q_out=qe) is qe
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(qe, qa) and all(same(x, y) for x, y in zip(a, e))
+    f = blank(20, Hk, page, d, 8)
+    qf = torch.empty_like(q)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(f, q_out=qf)
+    for x in f[:2]:
+        x.view(torch.uint8).zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(qf, qa) and all(same(x, y) for x, y in zip(a, f))
+    # a fused projection's rows [T, H + 2 Hk, d]
+    fused = torch.cat((q, k, v)).transpose(0, 1).contiguous().transpose(0, 1)
+    h = blank(20, Hk, page, d, 8)
+    qh = blk.kv_append_paged(fused[H:H + Hk], fused[H + Hk:], h[0], h[1], table, lens, cu_seqlens=cu, k_scale=h[2],
+                             v_scale=h[3], rope=plan, q=fused[:H])
+    assert torch.equal(qh, qa) and all(same(x, y) for x, y in zip(a, h))
+
+
+def test_lengths_and_tables_that_do_not_fit():
+    """Tokens with negative positions, and those whose page is not there, take no part; falling
+    offsets are clamped: nothing is written outside what the table names."""
+    Hk, d, page = 2, 64, 16
+    k, v = (randn((Hk, 40, d), "bf16", gen(i)) for i in (1, 2))
+    c = blank(6, Hk, page, d, 16)
+    # sequence 0: ten of 20 tokens have negative positions; 1: its second page is outside the pool; 2: length 0
+    table = i32([[1, 2], [3, 77], [4, -1]])
+    blk.kv_append_paged(k, v, *c[:2], table, i32([10, 20, 0]), cu_seqlens=i32([0, 20, 40, 40]))
+    assert torch.equal(c[0][1, :, :10], k[:, 10:20]) and torch.equal(c[1][3, :, :16], v[:, 20:36])
+    rest = c[0].float()
+    rest[1, :, :10] = 0
+    rest[3] = 0
+    assert not rest.any()
+    for cu in ([0, 50, 20, 40], [-7, 10, 5, 1000], [40, 0, 40, 0], [2 ** 31 - 1, -2 ** 31, 3, 9]):
+        c = blank(6, Hk, page, d, 8)
+        blk.kv_append_paged(k, v, *c[:2], table, i32([32, 2 ** 31 - 1, 31]), cu_seqlens=i32(cu), k_scale=c[2], v_scale=c[3])
+        torch.cuda.synchronize()
+        for x in c[:2]:
+            assert not x.float()[[0, 5]].any()
+    blk.check_device_status()
+
+
+def test_pool_beyond_32_bit_offsets():
+    Hk, page, d = 2, 128, 128
+    pages = (1 << 32) // (Hk * page * d) + 3
+    c = [torch.zeros((pages, Hk, page, d), dtype=torch.float8_e4m3fn, device="cuda") for _ in "kv"]
+    s = [torch.zeros((pages, Hk), device="cuda") for _ in "kv"]
+    k, v = (randn((Hk, 200, d), "bf16", gen(i)) for i in (3, 4))
+    table = i32([[pages - 1, pages - 2], [0, 1]])
+    blk.kv_append_paged(k, v, *c, table, i32([200, 0]), cu_seqlens=i32([0, 200, 200]), k_scale=s[0], v_scale=s[1])
+    got = (c[1][pages - 1].float() * s[1][pages - 1][:, None, None])
+    assert float((got - v[:, :128].float()).abs().max()) <= 2.0 ** -4 * float(v.float().abs().max())
+    assert not c[1][:2].view(torch.uint8).any()
+    # ... and the decode step over it: keys and values there, by 64-bit offsets
+    q = randn((2, 4, d), "bf16", gen(9))
+    o = blk.attn_decode_paged(q, *c, table, i32([200, 0]), k_scale=s[0], v_scale=s[1])
+    kr, seen, _ = ref.rows(c[0], s[0], [pages - 1, pages - 2], 200, page)
+    vr, _, _ = ref.rows(c[1], s[1], [pages - 1, pages - 2], 200, page)
+    want, mag, _ = ref.decode(f64(q[0].float()), kr, vr, seen)
+    assert (np.abs(f64(o[0].float()) - want) <= 2.0 ** -7 * mag + 2.0 ** -8 * np.abs(want)).all() and not o[1].any()
+
+
+def test_rope_strides_and_gradient():
+    """[T, H, d] transposed, and a slice; the inverse is the gradient of a rotation's call."""
+    g = gen(8)
+    x = randn((50, 6, 128), "fp16", g)
+    pos = torch.randint(-1000, 1000, (50,), generator=g, device="cuda", dtype=torch.int32)  # negative ones too
+    plan = blk.rope_plan(64, 10000.0, amplitude=0.75)
+    a = blk.rope_positions(x.transpose(0, 1), pos, plan)
+    assert torch.equal(a, blk.rope_positions(x.transpose(0, 1).contiguous(), pos, plan))
+    q, k = blk.rope_positions(x.transpose(0, 1)[:4], pos, plan, k=x.transpose(0, 1)[4:])
+    assert torch.equal(torch.cat((q, k)), a)
+    want, mag = ref.turn(f64(x.transpose(0, 1).float()), f64(pos), ref.thetas(64), False, 0.75)
+    close(a, want, mag, "fp16")
+    # <turn(x), y> = <x, turn back(y)>, each product rounded: u of the terms' magnitudes
+    y = randn((6, 50, 128), "fp16", g)
+    b = blk.rope_positions(y, pos, plan, inverse=True)
+    left, right = (a.double() * y.double()).sum(), (x.transpose(0, 1).double() * b.double()).sum()
+    terms = (a.double() * y.double()).abs().sum() + (x.transpose(0, 1).double() * b.double()).abs().sum()
+    assert abs(float(left - right)) <= 2.0 ** -10 * float(terms)
+    # differences of the turn along y: it is linear, so they are the turn of y
+    one = blk.rope_positions((x.transpose(0, 1).double() + y.double()).half(), pos, plan).double()
+    two, far = ref.turn(f64((x.transpose(0, 1).double() + y.double()).half()), f64(pos), ref.thetas(64), False, 0.75)
+    assert (np.abs(f64(one) - two) <= far * 2.0 ** -20 + 2.0 ** -11 * np.abs(two) * (1 + 2.0 ** -10) + 2.0 ** -25).all()
