@@ -356,7 +356,7 @@ typedef struct {
     blk_paged_desc cache; /* head_dim a multiple of 16, at most 256 */
     int64_t tokens;       /* rows of k, v and q (1 .. 2^30) */
     int64_t n_heads;      /* of q (0: no q) */
-    /* elements from head to head and from token to token, multiples of 8 */
+    /* elements from head to head and from token to token, multiples of 8 (k and v: tokens below 2^24) */
     int64_t k_head_stride, k_token_stride, v_head_stride, v_token_stride;
     int64_t q_head_stride, q_token_stride, q_out_head_stride, q_out_token_stride;
 } blk_append_desc;
