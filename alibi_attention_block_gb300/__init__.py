@@ -374,13 +374,21 @@ def rope_plan(span, base=10000.0, interleaved=False, scaling="none", factor=1.0,
     desc = _abi.RopeDesc(span, 1 if interleaved else 0, base, _SCALING[scaling], amplitude, factor,
                          original_len, beta_slow, beta_fast)
     _abi.check(_lib().blk_rope_plan_init(C.byref(desc), C.byref(plan)), "blk_rope_plan_init")
+    plan.ref = C.byref(plan)
     return plan
+
+
+def _plan_ref(plan):
+    try:
+        return plan.ref
+    except AttributeError:
+        raise TypeError("a rotary is given as a rope_plan") from None
 
 
 def _sig(*ts):
     """What a plan is kept by of a call's tensors: type, shape and strides."""
     try:
-        return tuple([None if t is None else (t.dtype, t.shape, t.stride()) for t in ts])
+        return tuple([t if t is None else (t.dtype, t.shape, t.stride()) for t in ts])
     except AttributeError:
         raise TypeError("expected a torch.Tensor") from None
 
@@ -468,12 +476,13 @@ def rope_positions(q, positions, plan, k=None, inverse=False, q_out=None, k_out=
     inverse=True turns back (the gradient's call)."""
     if k is None and k_out is not None:
         raise ValueError("k_out given without k")
+    ref = _plan_ref(plan)
     o = torch.empty_like(q) if q_out is None else q_out
     ko = torch.empty_like(k) if k_out is None and k is not None else k_out
     desc, dt = _rope_pos_plan(_sig(q, positions, k, o, ko), 1 if inverse else 0)
     dev = torch._C._cuda_getDevice()
     qp, pp, kp, op, lp = _addresses(dev, q, positions, k, o, ko)
-    status = _lib().blk_rope_positions(desc, plan, qp, kp, pp, op, lp, dt,
+    status = _lib().blk_rope_positions(desc, ref, qp, kp, pp, op, lp, dt,
                                        torch._C._cuda_getCurrentRawStream(dev))
     if status:
         _abi.check(status, "blk_rope_positions")
@@ -546,12 +555,13 @@ def kv_append_paged(k, v, k_cache, v_cache, block_table, lens, cu_seqlens=None, 
     sequence are not written), None without q."""
     if q is None and q_out is not None:
         raise ValueError("q_out given without q")
+    ref = None if rope is None else _plan_ref(rope)
     o = torch.empty_like(q) if q_out is None and q is not None else q_out
     ts = (k, v, q, o, cu_seqlens, positions, k_cache, v_cache, k_scale, v_scale, block_table, lens)
     desc, dt = _append_plan(_sig(*ts))
     dev = torch._C._cuda_getDevice()
     kp, vp, qp, op, cup, pp, kcp, vcp, ksp, vsp, tp, lp = _addresses(dev, *ts)
-    status = _lib().blk_kv_append_paged(desc, rope, kp, vp, qp, cup, pp, tp, lp, kcp, vcp, ksp, vsp,
+    status = _lib().blk_kv_append_paged(desc, ref, kp, vp, qp, cup, pp, tp, lp, kcp, vcp, ksp, vsp,
                                         op, dt, torch._C._cuda_getCurrentRawStream(dev))
     if status:
         _abi.check(status, "blk_kv_append_paged")

@@ -126,7 +126,8 @@ def test_cache_refusals(lib, bad, status):
     dict(k=FAKE + 4), dict(table=None), dict(table=FAKE + 2), dict(lens=None), dict(kc=None), dict(vc=FAKE + 8),
     dict(ks=None), dict(vs=FAKE + 2), dict(n_heads=4), dict(q=FAKE), dict(q=FAKE, qo=FAKE), dict(n_heads=4, q=FAKE),
     dict(n_heads=20000, q=FAKE, qo=FAKE), dict(pos=FAKE), dict(plan=_abi.RopePlan()), dict(k_head_stride=12),
-    dict(v_token_stride=-8), dict(n_heads=4, q=FAKE, qo=FAKE, q_head_stride=64), dict(dt=3)])
+    dict(v_token_stride=-8),
+    dict(k_token_stride=1 << 24), dict(n_heads=4, q=FAKE, qo=FAKE, q_head_stride=64), dict(dt=3)])
 def test_append_refusals(lib, bad):
     assert append(lib, **bad) == EINVAL
 
@@ -221,6 +222,6 @@ def test_binding_rope_refusals(lib):
                        (dict(positions=pos[:4]), ValueError), (dict(k=q[:, :4]), ValueError),
                        (dict(k=q.half()), TypeError), (dict(k_out=q), ValueError), (dict(q_out=q[:3]), ValueError),
                        (dict(q=q[0]), ValueError), (dict(q=q.transpose(1, 2).contiguous().transpose(1, 2)), ValueError),
-                       (dict(positions=[1] * 5), TypeError)):
+                       (dict(positions=[1] * 5), TypeError), (dict(plan=None), TypeError), (dict(plan=64), TypeError)):
         with pytest.raises(error):
             blk.rope_positions(**{"q": q, "positions": pos, "plan": plan, **bad})
