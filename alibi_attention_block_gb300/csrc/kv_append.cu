@@ -19,8 +19,8 @@
 // largest value is found and used in one place, without atomics: each thread holds
 // its turned values in registers between the two. Blocks of queries take a
 // group of heads and reuse the angles. The number of pages that a sequence
-// touches is device data: sequence b's blocks are numbers floor(cu[b] / page) + 2 b and
-// up, which leaves room for floor(n / page) + 2 pages, enough for n tokens from any
+// touches is device data: sequence b's items are numbers floor(cu[b] / size) + 2 b and
+// up, which leaves room for floor(n / size) + 2 items, enough for n tokens from any
 // offset; surplus blocks end at once. Bound by bytes: the new rows read once, their
 // codes and scales written once.
 #include <cuda_fp8.h>
@@ -46,16 +46,17 @@ struct AppendArgs {
     const int32_t* cu;         // or nullptr: one token per sequence
     const int32_t* positions;  // of the rotary, or nullptr: the cache's
     int tokens, H;             // query heads
-    int team;                  // threads of a page and head
+    int kv_log2, q_log2;       // tokens of an item, of keys and values and of queries
+    unsigned kv_items, q_items;
+    int team;                  // threads of an item of keys or values and head
     int kv_per, kv_groups;     // heads of K and V per block (K's, then V's), and blocks of them
     int q_per;                 // query heads per block
     int pdl;
 };
 
-// The new rows of one page of one sequence.
-struct PageRows {
-    int b, first, n;   // sequence; first row in the page, rows
-    int page;          // column of the table
+// The new rows of one item: of a sequence's positions j 2^lg .. (j + 1) 2^lg - 1 for some j.
+struct ItemRows {
+    int b, n;          // sequence, rows
     int64_t row, pos;  // of the first: row of k, v and q, position
 };
 
@@ -64,8 +65,7 @@ __device__ __forceinline__ int start_of(const AppendArgs& a, int b) {
 }
 
 // Rows of item i, in every thread of a warp alike; false: none.
-__device__ __forceinline__ bool rows_of(const AppendArgs& a, int64_t i, int lane, PageRows& r) {
-    const int lg = a.c.page_log2;
+__device__ __forceinline__ bool rows_of(const AppendArgs& a, int64_t i, int lg, int lane, ItemRows& r) {
     int64_t c0, n, at;
     if (a.cu) {
         // the last sequence whose numbers begin at or ahead of i
@@ -92,12 +92,10 @@ __device__ __forceinline__ bool rows_of(const AppendArgs& a, int64_t i, int lane
     int64_t p0 = end - n;  // of the sequence's first new row
     c0 -= p0;              // row of position 0
     p0 = p0 < 0 ? 0 : p0;
-    const int64_t page = (p0 >> lg) + at;
-    const int64_t lo = max(p0, page << lg), hi = min(end, (page + 1) << lg);
+    const int64_t j = (p0 >> lg) + at;
+    const int64_t lo = max(p0, j << lg), hi = min(end, (j + 1) << lg);
     if (at < 0 || lo >= hi) return false;
-    r.first = static_cast<int>(lo - (page << lg));
     r.n = static_cast<int>(hi - lo);
-    r.page = static_cast<int>(page);
     r.row = c0 + lo;
     r.pos = lo;
     return true;
@@ -149,42 +147,94 @@ __device__ __forceinline__ uint32_t rescaled(uint32_t codes, float by) {
     return out;
 }
 
+// A block's heads of queries of an item: threads by head, token and unit.
+template <typename T, int VP>
+__device__ __forceinline__ void turn_queries(const AppendArgs& a, const ItemRows& r, const Unit<VP>& at,
+                                             const uint64_t* plan, int group, int place, int rows) {
+    using Raw = typename RawPiece<VP>::type;
+    const float m = a.turn.plan.amplitude;
+    const int side = min(rows, 1 << a.q_log2);       // tokens side by side
+    const int step = rows / side;                    // and heads
+    const int h0 = group * a.q_per, h1 = min(h0 + a.q_per, a.H);
+    if (place >= side * step) return;
+    for (int k = place % side; k < r.n; k += side) {
+        Angles<VP> ang;
+        if (at.turned) {
+            uint64_t turns[VP];
+#pragma unroll
+            for (int i = 0; i < VP; ++i)
+                turns[i] = VP == 1 || i < VP / 2 ? plan[at.p0 + i] : plan[at.p1 + i - VP / 2];
+            ang.set(turns, a.positions ? a.positions[r.row + k] : static_cast<int>(r.pos + k), m, m);
+        }
+        const T* x = static_cast<const T*>(a.x[2]) + (r.row + k) * a.xs[2][1];
+        T* y = static_cast<T*>(a.q_out) + (r.row + k) * a.qs[1];
+        // several heads' loads on their way at a time
+        constexpr int kHeads = VP == 8 ? 2 : 4;
+        for (int h = h0 + place / side; h < h1; h += kHeads * step) {
+            Raw raw[kHeads][2];
+#pragma unroll
+            for (int i = 0; i < kHeads; ++i)
+                if (h + i * step < h1) {
+                    raw[i][0] = load_raw<T, VP>(x + (h + i * step) * a.xs[2][0] + at.a);
+                    raw[i][1] = load_raw<T, VP>(x + (h + i * step) * a.xs[2][0] + at.b);
+                }
+#pragma unroll
+            for (int i = 0; i < kHeads; ++i)
+                if (h + i * step < h1) {
+                    float p[VP], q[VP];
+                    unpack_raw<T, VP>(raw[i][0], p);
+                    unpack_raw<T, VP>(raw[i][1], q);
+                    if (at.turned) ang.turn(p, q, a.turn.plan.interleaved);
+                    store_piece(y + (h + i * step) * a.qs[0] + at.a, p);
+                    store_piece(y + (h + i * step) * a.qs[0] + at.b, q);
+                }
+        }
+    }
+}
+
 // A block has teams of threads: a team takes one page and head at a time, its threads so
-// many that IT rounds of them hold the page (32 values each). What a block needs to know of its page (the search, the
+// many that IT rounds of them hold the page (32 values each), or 256, and the page is read twice. What a block needs to know of its page (the search, the
 // length, the table) is a chain of dependent loads that its teams and heads share:
 // with a block of one warp for each page and head, 5000 tokens of 32 x 64 heads took 47 us.
-template <typename T, bool E8, int VP, int IT>
-__global__ void __launch_bounds__(IT * VP > 16 ? 512 : IT * VP > 8 ? 768 : 1024) kv_append_kernel(const __grid_constant__ AppendArgs a) {
+// ROUNDS: for pages larger than a team's IT rounds (a variant, since its registers are the others' spills).
+template <typename T, bool E8, int VP, int IT, bool ROUNDS>
+__global__ void __launch_bounds__(IT * VP > 8 ? 768 : 1024) kv_append_kernel(const __grid_constant__ AppendArgs a) {
     __shared__ float most[2][32];
     extern __shared__ float4 angles[];
     __shared__ uint64_t plan[kMaxRotaryPairs];
     const int d = a.c.d, units = d / (2 * VP);
     const int lane = threadIdx.x & 31;
-    const int group = blockIdx.y;
-    const bool is_q = group >= a.kv_groups;
+    // blocks of keys and values, the longest, come first, then those of queries (side by side:
+    // 118 us for 112 in the large case, the tail being one of the former)
+    const unsigned kv_blocks = a.kv_items * a.kv_groups;
+    const bool is_q = blockIdx.x >= kv_blocks;
+    const unsigned of = is_q ? a.q_items : a.kv_items, nth = is_q ? blockIdx.x - kv_blocks : blockIdx.x;
+    const int group = nth / of, item = nth - group * of;
     // queries: threads by head, token and unit; else by team, token and unit
     const int threads = is_q ? blockDim.x : a.team;
     const int team = is_q ? 0 : threadIdx.x / a.team;
     const int tid = is_q ? threadIdx.x : threadIdx.x % a.team;
     const int u = tid % units, place = tid / units;
     const int rows = threads / units;
-    const Unit<VP> at(u, a.turn.plan.pairs, a.turn.plan.interleaved);
+    const Unit<VP> at(u, d, a.turn.plan.pairs, a.turn.plan.interleaved);
     for (int i = threadIdx.x; i < a.turn.plan.pairs; i += blockDim.x) plan[i] = a.turn.plan.turns[i];
     const float m = a.turn.plan.amplitude;
     __syncthreads();
     if (a.pdl) pdl_wait();
-    PageRows r;
-    if (!rows_of(a, blockIdx.x, lane, r)) return;
+    ItemRows r;
+    if (!rows_of(a, item, is_q ? a.q_log2 : a.kv_log2, lane, r)) return;
     using Raw = typename RawPiece<VP>::type;
 
-    // cosines and sines of the rows, for all the block's heads: plane j of a unit's pairs
+    // cosines and sines of the rows, for all the block's heads of keys: plane j of a unit's pairs
     // 2 j and 2 j + 1 (VP 1: of its pair)
     const int turned_units = a.turn.plan.pairs / VP, cells = r.n * turned_units;
     constexpr int kPlanes = VP > 1 ? VP / 2 : 1;
     auto make_table = [&]() {
         for (int i = threadIdx.x; i < cells * kPlanes; i += blockDim.x) {
             const int cell = i / kPlanes, j = i - cell * kPlanes;
-            const int k = cell / turned_units, pair = (cell - k * turned_units) * VP + 2 * j;
+            const int k = cell / turned_units;
+            const Unit<VP> of(cell - k * turned_units, d, a.turn.plan.pairs, a.turn.plan.interleaved);
+            const int pair = VP == 1 ? of.p0 : 2 * j < VP / 2 ? of.p0 + 2 * j : of.p1 + 2 * j - VP / 2;
             const int pos = a.positions ? a.positions[r.row + k] : static_cast<int>(r.pos + k);
             float c0, s0, c1, s1;
             turn_cos_sin(plan[pair], pos, c0, s0);
@@ -197,25 +247,7 @@ __global__ void __launch_bounds__(IT * VP > 16 ? 512 : IT * VP > 8 ? 768 : 1024)
         }
         __syncthreads();
     };
-    auto look_up = [&](int k, Angles<VP>& ang) {
-        const int cell = k * turned_units + u;
-        if constexpr (VP > 1) {
-#pragma unroll
-            for (int j = 0; j < kPlanes; ++j) {
-                const float4 f = angles[j * cells + cell];
-                ang.c[2 * j] = f.x;
-                ang.s[2 * j] = f.y;
-                ang.c[2 * j + 1] = f.z;
-                ang.s[2 * j + 1] = f.w;
-            }
-        } else {
-            const float2 f = reinterpret_cast<const float2*>(angles)[cell];
-            ang.c[0] = f.x;
-            ang.s[0] = f.y;
-        }
-    };
-
-    // ... two pairs at a time, for a unit turned once (fewer registers than look_up)
+    // ... two pairs at a time
     auto turn_by_table = [&](int cell, float (&x)[VP], float (&y)[VP]) {
         if constexpr (VP > 1) {
             if (a.turn.plan.interleaved) {
@@ -241,44 +273,16 @@ __global__ void __launch_bounds__(IT * VP > 16 ? 512 : IT * VP > 8 ? 768 : 1024)
     };
 
     if (is_q) {
-        make_table();
-        const int side = min(rows, 1 << a.c.page_log2);  // tokens side by side
-        const int step = rows / side;                    // and heads
-        const int h0 = (group - a.kv_groups) * a.q_per, h1 = min(h0 + a.q_per, a.H);
-        if (place >= side * step) return;
-        for (int k = place % side; k < r.n; k += side) {
-            Angles<VP> ang;
-            if (at.turned) look_up(k, ang);
-            const T* x = static_cast<const T*>(a.x[2]) + (r.row + k) * a.xs[2][1];
-            T* y = static_cast<T*>(a.q_out) + (r.row + k) * a.qs[1];
-            // four heads' loads on their way at a time
-            for (int h = h0 + place / side; h < h1; h += 2 * step) {
-                Raw raw[2][2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (h + i * step < h1) {
-                        raw[i][0] = load_raw<T, VP>(x + (h + i * step) * a.xs[2][0] + at.a);
-                        raw[i][1] = load_raw<T, VP>(x + (h + i * step) * a.xs[2][0] + at.b);
-                    }
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (h + i * step < h1) {
-                        float p[VP], q[VP];
-                        unpack_raw<T, VP>(raw[i][0], p);
-                        unpack_raw<T, VP>(raw[i][1], q);
-                        if (at.turned) ang.turn(p, q, a.turn.plan.interleaved);
-                        store_piece(y + (h + i * step) * a.qs[0] + at.a, p);
-                        store_piece(y + (h + i * step) * a.qs[0] + at.b, q);
-                    }
-            }
-        }
+        turn_queries<T, VP>(a, r, at, plan, group, place, rows);
         return;
     }
 
     // a page of the sequence's that is not there takes nothing
-    if (r.page >= a.c.max_pages) return;
-    const int page = a.c.table[static_cast<int64_t>(r.b) * a.c.max_pages + r.page];
+    const int64_t column = r.pos >> a.c.page_log2;
+    if (column >= a.c.max_pages) return;
+    const int page = a.c.table[static_cast<int64_t>(r.b) * a.c.max_pages + column];
     if (page < 0 || page >= a.c.pages) return;
+    const int in_page = static_cast<int>(r.pos & ((1 << a.c.page_log2) - 1));  // the first row's place
     const int teams = blockDim.x / a.team, team_warps = a.team / 32;
     const int first = group * a.kv_per, end = min(first + a.kv_per, 2 * a.c.Hk);
     const int64_t head_size = static_cast<int64_t>(d) << a.c.page_log2;
@@ -293,6 +297,7 @@ __global__ void __launch_bounds__(IT * VP > 16 ? 512 : IT * VP > 8 ? 768 : 1024)
         cell[i] = min(k, r.n - 1) * turned_units + u;
     }
     const int gap = at.b - at.a;
+    const int chunks = (r.n + rows * IT - 1) / (rows * IT);
     // The largest of x over the team (a round of its own barrier; entries alternate between rounds).
     int odd = 0;
     auto of_team = [&](float x) {
@@ -318,7 +323,7 @@ __global__ void __launch_bounds__(IT * VP > 16 ? 512 : IT * VP > 8 ? 768 : 1024)
         // (offsets in a head fit 32 bits: token strides are below 2^24)
         const int64_t hs = a.xs[kValues][0] * teams;
         const T* x = static_cast<const T*>(a.x[kValues]) + s0 * a.xs[kValues][0] + r.row * a.xs[kValues][1];
-        const int64_t base = page * a.c.page_stride + s0 * head_size + r.first * d;
+        const int64_t base = page * a.c.page_stride + s0 * head_size + in_page * d;
         const int64_t head_step = teams * head_size;
         uint8_t* codes = static_cast<uint8_t*>(kValues ? a.c.v : a.c.k) + base;
         T* cache = static_cast<T*>(kValues ? a.c.v : a.c.k) + base;
@@ -351,6 +356,92 @@ __global__ void __launch_bounds__(IT * VP > 16 ? 512 : IT * VP > 8 ? 768 : 1024)
                     asm volatile("prefetch.global.L2 [%0];" ::"l"(x + from[i] + gap));
                 }
         };
+        // Values of rounds c IT .. of a head, for pages of more rows than IT rounds take.
+        auto rounds = [&](int c, float (&v)[IT][2][VP], bool (&in)[IT]) {
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                const int k = place + (c * IT + i) * rows;
+                in[i] = place < rows && k < r.n;
+                raw[i][0] = Raw{};
+                raw[i][1] = Raw{};
+                if (in[i]) {
+                    raw[i][0] = load_raw<T, VP>(x + k * static_cast<int>(a.xs[kValues][1]) + at.a);
+                    raw[i][1] = load_raw<T, VP>(x + k * static_cast<int>(a.xs[kValues][1]) + at.b);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                unpack_raw<T, VP>(raw[i][0], v[i][0]);
+                unpack_raw<T, VP>(raw[i][1], v[i][1]);
+                const int k = min(place + (c * IT + i) * rows, r.n - 1);
+                if (turned) turn_by_table(k * turned_units + u, v[i][0], v[i][1]);
+            }
+        };
+        // The page's scale, set by its largest value; what it holds at another one is brought to it.
+        auto set_scale = [&](float top, float held) {
+            const float now = fmaxf(scale_for(top), held);
+            if (tid == 0) *scale = now;
+            if (in_page > 0 && held < now) {
+                const float by = held / now;
+                uint4* old = reinterpret_cast<uint4*>(codes - in_page * d);
+                for (int i = tid; i < in_page * (d / 16); i += a.team) {
+                    uint4 o = old[i];
+                    o.x = rescaled(o.x, by);
+                    o.y = rescaled(o.y, by);
+                    o.z = rescaled(o.z, by);
+                    o.w = rescaled(o.w, by);
+                    old[i] = o;
+                }
+            }
+            return 1.0f / now;
+        };
+        if (ROUNDS) {
+            // the largest first, then the rows again (from the L2 cache), turned again
+            for (int s = s0; s < s1; s += teams) {
+                float v[IT][2][VP];
+                bool in[IT];
+                float inv = 1.f;
+                if constexpr (E8) {
+                    const float held = in_page > 0 ? *scale : 0.f;
+                    float top = 0.f;
+                    for (int finite = 0; finite < 2; ++finite) {
+                        for (int c = 0; c < chunks; ++c) {
+                            rounds(c, v, in);
+#pragma unroll
+                            for (int i = 0; i < IT; ++i)
+#pragma unroll
+                                for (int e = 0; e < VP; ++e)
+                                    top = finite ? fmaxf(top, fmaxf(if_finite(v[i][0][e]), if_finite(v[i][1][e])))
+                                                 : max_abs(top, v[i][0][e], v[i][1][e]);
+                        }
+                        top = of_team(top);
+                        if (top < INFINITY) break;
+                        top = 0.f;
+                    }
+                    inv = set_scale(top, held);
+                }
+                for (int c = 0; c < chunks; ++c) {
+                    rounds(c, v, in);
+#pragma unroll
+                    for (int i = 0; i < IT; ++i) {
+                        if (!in[i]) continue;
+                        const int at_row = (place + (c * IT + i) * rows) * d;
+                        if constexpr (E8) {
+                            store_codes<VP>(codes + at_row + at.a, v[i][0], inv);
+                            store_codes<VP>(codes + at_row + at.b, v[i][1], inv);
+                        } else {
+                            store_piece(cache + at_row + at.a, v[i][0]);
+                            store_piece(cache + at_row + at.b, v[i][1]);
+                        }
+                    }
+                }
+                x += hs;
+                codes += head_step;
+                cache += head_step;
+                scale += teams;
+            }
+            return;
+        }
         if (kAhead) fetch(s1 - s0 - teams);
         for (int s = s0; s < s1; s += teams) {
             if (!kAhead) fetch(0);
@@ -362,7 +453,7 @@ __global__ void __launch_bounds__(IT * VP > 16 ? 512 : IT * VP > 8 ? 768 : 1024)
             }
             if (kAhead && s + teams < s1) fetch(s1 - s - 2 * teams);
             float held = 0.f;
-            if (E8 && r.first > 0) held = *scale;  // (a page's first row begins its scale anew)
+            if (E8 && in_page > 0) held = *scale;  // (a page's first row begins its scale anew)
             float top = 0.f;
 #pragma unroll
             for (int i = 0; i < IT; ++i) {
@@ -384,21 +475,7 @@ __global__ void __launch_bounds__(IT * VP > 16 ? 512 : IT * VP > 8 ? 768 : 1024)
                     }
                     top = of_team(top);
                 }
-                const float now = fmaxf(scale_for(top), held);
-                if (tid == 0) *scale = now;
-                if (r.first > 0 && held < now) {
-                    const float by = held / now;
-                    uint4* old = reinterpret_cast<uint4*>(codes - r.first * d);
-                    for (int i = tid; i < r.first * (d / 16); i += a.team) {
-                        uint4 o = old[i];
-                        o.x = rescaled(o.x, by);
-                        o.y = rescaled(o.y, by);
-                        o.z = rescaled(o.z, by);
-                        o.w = rescaled(o.w, by);
-                        old[i] = o;
-                    }
-                }
-                const float inv = 1.0f / now;
+                const float inv = set_scale(top, held);
 #pragma unroll
                 for (int i = 0; i < IT; ++i)
                     if (on[i]) {
@@ -425,52 +502,63 @@ __global__ void __launch_bounds__(IT * VP > 16 ? 512 : IT * VP > 8 ? 768 : 1024)
     if (end > a.c.Hk) append(std::true_type{}, max(first - a.c.Hk, 0), end - a.c.Hk);
 }
 
-template <typename T, bool E8, int VP, int IT>
-cudaError_t launch_append(AppendArgs& a, int64_t items, int sms, cudaStream_t s) {
-    const int units = a.c.d / (2 * VP), page = 1 << a.c.page_log2;
-    a.team = (units * ((page + IT - 1) / IT) + 31) / 32 * 32;
-    const int teams = a.team >= 256 ? 1 : 256 / a.team;
-    // heads of a block: as many as make about a round of blocks each of keys and values and of
-    // queries, since what is ahead of a block's first load is a chain of
-    // latencies; sixteen at most in turn
-    const int64_t blocks = static_cast<int64_t>(sms) * std::max(1, (IT * VP > 8 ? 768 : 1024) / (teams * a.team)), slots = 2 * a.c.Hk;
-    int64_t loops = items * slots / (teams * blocks);
-    loops = loops < 1 ? 1 : loops > 16 ? 16 : loops;
-    a.kv_per = static_cast<int>(teams * loops);
-    a.kv_groups = static_cast<int>((slots + a.kv_per - 1) / a.kv_per);
-    const int64_t side = teams * a.team / units / page > 1 ? teams * a.team / units / page : 1;
-    int64_t per = items * a.H / (side * blocks);
-    per = side * (per < 1 ? 1 : per > 16 ? 16 : per);
-    a.q_per = static_cast<int>(per);
-    // (K's groups, the longest, first: side by side with the queries' in the grid they were last, and
-    // the whole slower, 112 -> 118 us in the large case)
-    const int64_t groups = a.kv_groups + (a.H + per - 1) / per;
-    const int table = page * a.turn.plan.pairs * 8;
+template <typename T, bool E8, int VP, int IT, bool ROUNDS>
+cudaError_t launch_variant(const AppendArgs& a, unsigned blocks, int threads, cudaStream_t s) {
+    auto kern = kv_append_kernel<T, E8, VP, IT, ROUNDS>;
+    const int table = (1 << a.kv_log2) * a.turn.plan.pairs * 8;
     if (table > 46 * 1024) {  // (with the static 1.3 KB, more than a launch has without asking)
-        const cudaError_t e =
-            set_smem_attr_once(reinterpret_cast<const void*>(kv_append_kernel<T, E8, VP, IT>), 128 * 1024);
+        const cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(kern), 128 * 1024);
         if (e != cudaSuccess) return e;
     }
-    return launch_pdl(a.pdl != 0, kv_append_kernel<T, E8, VP, IT>,
-                      dim3(static_cast<unsigned>(items), static_cast<unsigned>(groups)),
-                      dim3(teams * a.team), table, s, a);
+    return launch_pdl(a.pdl != 0, kern, dim3(blocks), dim3(threads), table, s, a);
+}
+
+template <typename T, bool E8, int VP>
+cudaError_t launch_append(AppendArgs& a, int sms, cudaStream_t s) {
+    // 32 values per thread at a time; in 16 bits, where no value waits for the page's largest,
+    // 16 (10.6 -> 9.4 us for 3020 tokens of 16 x 64)
+    constexpr int IT = E8 ? (VP == 8 ? 2 : VP == 4 ? 4 : 16) : VP == 8 ? 1 : VP == 4 ? 4 : 16;
+    const int units = a.c.d / (2 * VP);
+    // An item of keys and values is a page, whose largest value is one; in 16 bits at most 32 tokens
+    // (16 prompts of 994 tokens, 16 x 128, pages of 128: 76 us with items of a page, 64 with these)
+    a.kv_log2 = E8 ? a.c.page_log2 : std::min(a.c.page_log2, 5);
+    a.team = (units * (((1 << a.kv_log2) + IT - 1) / IT) + 31) / 32 * 32;
+    const bool rounds = a.team > 512;
+    if (rounds) a.team = 256;
+    const int teams = a.team >= 256 ? 1 : 256 / a.team, threads = teams * a.team;
+    const int64_t B = a.c.B;
+    const int64_t kv_items = a.cu ? (a.tokens >> a.kv_log2) + 2 * B : B;
+    // Heads of a block: as many as make about a round of blocks, since what is ahead of a block's
+    // first load is a chain of latencies; sixteen at most in turn.
+    const int64_t blocks = static_cast<int64_t>(sms) * std::max(1, (IT * VP > 8 ? 768 : 1024) / threads);
+    const int64_t slots = 2 * a.c.Hk;
+    const int64_t loops = std::min<int64_t>(16, std::max<int64_t>(1, kv_items * slots / (teams * blocks)));
+    a.kv_per = static_cast<int>(teams * loops);
+    a.kv_groups = static_cast<int>((slots + a.kv_per - 1) / a.kv_per);
+    const int64_t kv_blocks = kv_items * a.kv_groups;
+    // Queries, an item: as many tokens as a block has threads for; heads: four at least for a thread
+    // (its loads on their way), so that there are six blocks per SM or so, 32 at most. (In a launch of
+    // their own, with fewer registers, they no longer fill what the others leave: 16 prompts of 994
+    // tokens, 32 x 64: 69 us for 55.)
+    for (a.q_log2 = 3; units << (a.q_log2 + 1) <= threads && a.q_log2 < 7;) ++a.q_log2;
+    const int64_t q_items = a.cu ? (a.tokens >> a.q_log2) + 2 * B : B;
+    const int64_t step = std::max(1, threads / units >> a.q_log2);  // heads side by side
+    const int64_t heads = q_items * a.H / step;
+    const int64_t per = heads < 4 * sms ? 1 : std::min<int64_t>(32, (heads / (6 * sms) + 4) / 4 * 4);
+    a.q_per = static_cast<int>(step * per);
+    const int64_t all = kv_blocks + q_items * ((a.H + a.q_per - 1) / a.q_per);
+    if (all > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    a.kv_items = static_cast<unsigned>(kv_items);
+    a.q_items = static_cast<unsigned>(q_items);
+    return rounds ? launch_variant<T, E8, VP, IT, E8>(a, static_cast<unsigned>(all), threads, s)
+                  : launch_variant<T, E8, VP, IT, false>(a, static_cast<unsigned>(all), threads, s);
 }
 template <typename T, bool E8>
-cudaError_t launch_append_w(AppendArgs& a, int64_t items, int sms, cudaStream_t s) {
-    const int values = a.c.d << a.c.page_log2;  // of a page and head
+cudaError_t launch_append_w(AppendArgs& a, int sms, cudaStream_t s) {
     switch (turn_width(a.turn.plan.pairs)) {
-        // 32 values per thread, 64 where a page would take more than 512 threads; in 16 bits, where no
-        // value waits for the page's largest, 16 (10.6 -> 9.4 us for 3020 tokens of 16 x 64)
-        case 8:
-            if (!E8 && values <= 512 * 16) return launch_append<T, E8, 8, 1>(a, items, sms, s);
-            return values > 512 * 32 ? launch_append<T, E8, 8, 4>(a, items, sms, s)
-                                     : launch_append<T, E8, 8, 2>(a, items, sms, s);
-        case 4:
-            return values > 512 * 32 ? launch_append<T, E8, 4, 8>(a, items, sms, s)
-                                     : launch_append<T, E8, 4, 4>(a, items, sms, s);
-        default:
-            return values > 512 * 32 ? launch_append<T, E8, 1, 32>(a, items, sms, s)
-                                     : launch_append<T, E8, 1, 16>(a, items, sms, s);
+        case 8: return launch_append<T, E8, 8>(a, sms, s);
+        case 4: return launch_append<T, E8, 4>(a, sms, s);
+        default: return launch_append<T, E8, 1>(a, sms, s);
     }
 }
 
@@ -592,14 +680,12 @@ extern "C" blk_status blk_kv_append_paged(const blk_append_desc* d, const blk_ro
     if ((st = current_device_info(&sms, &err)) != BLK_OK) return st;
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(s);
     a.pdl = pdl_allowed(cs);
-    const int64_t items = cu_seqlens ? (d->tokens >> a.c.page_log2) + 2 * d->cache.batch : d->tokens;
-    REQUIRE(items <= 0x7fffffff, "tokens and batch too large");
     const bool e8 = d->cache.kind == BLK_CACHE_E4M3;
     const cudaError_t e =
-        dt == BLK_F16 ? (e8 ? launch_append_w<__half, true>(a, items, sms, cs)
-                            : launch_append_w<__half, false>(a, items, sms, cs))
-                      : (e8 ? launch_append_w<__nv_bfloat16, true>(a, items, sms, cs)
-                            : launch_append_w<__nv_bfloat16, false>(a, items, sms, cs));
+        dt == BLK_F16 ? (e8 ? launch_append_w<__half, true>(a, sms, cs)
+                            : launch_append_w<__half, false>(a, sms, cs))
+                      : (e8 ? launch_append_w<__nv_bfloat16, true>(a, sms, cs)
+                            : launch_append_w<__nv_bfloat16, false>(a, sms, cs));
     return e == cudaSuccess ? BLK_OK
                             : report_error_status(BLK_ECUDA, "append launch: %s", cudaGetErrorString(e));
 }

@@ -38,10 +38,13 @@ __global__ void __launch_bounds__(kThreads) rope_pos_kernel(const __grid_constan
     const int u = threadIdx.x % units;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * rows + threadIdx.x / units;
     if (threadIdx.x >= rows * units || t >= a.tokens) return;
-    const Unit<VP> at(u, a.turn.plan.pairs, a.turn.plan.interleaved);
+    const Unit<VP> at(u, a.d, a.turn.plan.pairs, a.turn.plan.interleaved);
     uint64_t turns[VP];
 #pragma unroll
-    for (int i = 0; i < VP; ++i) turns[i] = at.turned ? a.turn.plan.turns[u * VP + i] : 0;
+    for (int i = 0; i < VP; ++i)
+        turns[i] = !at.turned                 ? 0
+                   : VP == 1 || i < VP / 2 ? a.turn.plan.turns[at.p0 + i]
+                                              : a.turn.plan.turns[at.p1 + i - VP / 2];
     if (a.pdl) pdl_wait();
     Angles<VP> ang;
     if (at.turned) {
@@ -177,8 +180,11 @@ blk_status blk_rope_positions(const blk_rope_pos_desc* d, const blk_rope_plan* p
     const int vp = turn_width(plan->pairs);
     const int64_t rows = kThreads / (a.d / (2 * vp));
     const int64_t tiles = (d->tokens + rows - 1) / rows, heads = d->n_heads + d->n_k_heads;
-    // as many heads per block as leave about 16 blocks per SM
-    int64_t per = tiles * heads / (16 * sms);
+    // heads per block: so many that there are about 32 blocks per SM, in whole fours, a thread's
+    // loads in flight (4093 tokens of 32 + 32 x 64: one each 20.0 us, four 14.3; 16000 of 32 + 8 x
+    // 160: forty 84, eight to twelve 72); one where tokens are few
+    int64_t per = (tiles * heads / (32 * sms) + 3) / 4 * 4;
+    if (tiles * heads >= 4 * sms) per = per < 4 ? 4 : per;
     per = per < 1 ? 1 : per > heads ? heads : per;
     a.per = static_cast<int>(per);
     const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>((heads + per - 1) / per));

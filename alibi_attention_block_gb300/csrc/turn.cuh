@@ -12,9 +12,12 @@
 // were no faster, and moved codes of an 8-bit cache to their neighbours).
 //
 // A thread works on a unit: VP pairs of one token, read as two pieces of VP
-// elements. Half layout: pair j is (j, j + pairs); the pieces are VP dims
-// of the first half and their partners. Interleaved: pair j is (2j, 2j + 1); the
-// pieces lie side by side. Units behind the turned part pass two pieces on.
+// elements. The pieces of neighbouring units lie side by side, so that a warp's access is
+// whole lines of memory. Half layout: pair j is (j, j + pairs); a unit's pieces are VP dims
+// of the first half and their partners. Interleaved: pair j is (2j, 2j + 1); a unit has a piece
+// (VP / 2 pairs) in each half of the span. Units behind the turned part have one in each half of
+// the rest, which they pass on. (Two pieces next to each other, 32 bytes per thread: half sectors
+// at a time.)
 // VP is 8 (16-byte accesses) where the span is a multiple of 16, 4 where it is one of
 // 8 (40 of 160 dims), else 1.
 #pragma once
@@ -76,19 +79,28 @@ __device__ __forceinline__ void store_piece(T* p, const float (&f)[VP]) {
     }
 }
 
-// Unit u of a head: where its two pieces lie, and whether it is turned.
+// Unit u of a head of d dims: where its two pieces lie, and whether it is turned; the first
+// pair of the first and of the second half of its pairs.
 template <int VP>
 struct Unit {
-    int a, b;
+    int a, b, p0, p1;
     bool turned;
-    __device__ __forceinline__ Unit(int u, int pairs, int interleaved) {
+    __device__ __forceinline__ Unit(int u, int d, int pairs, int interleaved) {
         turned = u * VP < pairs;
-        if (interleaved || !turned) {
-            a = 2 * u * VP;  // (behind the span: 2 pairs + 2 VP (u - pairs / VP))
-            b = a + VP;
-        } else {
+        if (turned) {
             a = u * VP;
             b = pairs + a;
+            p0 = interleaved ? u * (VP / 2) : u * VP;
+            p1 = interleaved ? (pairs + u * VP) / 2 : u * VP + VP / 2;
+            if (VP == 1 && interleaved) {  // a pair by itself
+                a = 2 * u;
+                b = a + 1;
+                p0 = u;
+            }
+        } else {
+            a = pairs + u * VP;  // span + (u - pairs / VP) VP
+            b = a + (d / 2 - pairs);
+            p0 = p1 = 0;
         }
     }
 };
@@ -143,7 +155,7 @@ __device__ __forceinline__ void turn_unit(float (&a)[VP], float (&b)[VP], int in
 template <int VP>
 struct Angles {
     float c[VP], s[VP];
-    __device__ __forceinline__ void set(const uint64_t* turns, int pos, float amplitude, float sign) {
+    __device__ __forceinline__ void set(const uint64_t (&turns)[VP], int pos, float amplitude, float sign) {
 #pragma unroll
         for (int i = 0; i < VP; ++i) {
             float cs, sn;
