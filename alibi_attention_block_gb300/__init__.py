@@ -367,12 +367,18 @@ def rope_plan(span, base=10000.0, interleaved=False, scaling="none", factor=1.0,
     """The plan of a rotary for ``rope_positions`` and ``kv_append_paged``, made
     once: span dims of a head, in halves or interleaved pairs, with positions
     scaled "linear" or "by_parts" (blk_rope_scaling in include/blk.h says
-    how), turned dims times amplitude. Plain host data."""
+    how), turned dims times amplitude. Plain host data, not to be changed: calls
+    with the same values share it."""
     if scaling not in _SCALING:
         raise ValueError(f"scaling must be one of {sorted(_SCALING)}")
+    return _rope_plan(int(span), 1 if interleaved else 0, float(base), _SCALING[scaling], float(amplitude),
+                      float(factor), float(original_len), float(beta_slow), float(beta_fast))
+
+
+@functools.lru_cache(maxsize=64)
+def _rope_plan(*fields):
     plan = _abi.RopePlan()
-    desc = _abi.RopeDesc(span, 1 if interleaved else 0, base, _SCALING[scaling], amplitude, factor,
-                         original_len, beta_slow, beta_fast)
+    desc = _abi.RopeDesc(*fields)
     _abi.check(_lib().blk_rope_plan_init(C.byref(desc), C.byref(plan)), "blk_rope_plan_init")
     plan.ref = C.byref(plan)
     return plan

@@ -346,7 +346,7 @@ typedef struct {
     int64_t page_tokens;  /* 16, 32, 64 or 128 */
     int64_t n_kv_heads, head_dim;
     int64_t batch;        /* sequences */
-    int64_t max_pages;    /* columns of the block table */
+    int64_t max_pages;    /* columns of the block table; max_pages * page_tokens at most 2^26 */
     int64_t page_stride;  /* elements from page to page of k_cache and v_cache: a multiple of 16, at least
                              n_kv_heads * page_tokens * head_dim */
     int32_t kind;         /* blk_cache_kind */

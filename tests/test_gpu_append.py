@@ -385,3 +385,30 @@ def test_rope_strides_and_gradient():
     one = blk.rope_positions((x.transpose(0, 1).double() + y.double()).half(), pos, plan).double()
     two, far = ref.turn(f64((x.transpose(0, 1).double() + y.double()).half()), f64(pos), ref.thetas(64), False, 0.75)
     assert (np.abs(f64(one) - two) <= far * 2.0 ** -20 + 2.0 ** -11 * np.abs(two) * (1 + 2.0 ** -10) + 2.0 ** -25).all()
+
+
+@pytest.mark.parametrize("d,span", [(256, 256), (160, 40), (256, 250), (160, 0)])
+def test_pages_in_rounds(d, span):
+    """8-bit pages of more values than a block holds at a time are read twice: whole pages, part-full ones that
+    are gone on with, and an infinity in one."""
+    for layout in ("heads", "tokens"):
+        case(2, 2, d, span, 128, [0, 100, 127, 5], [300, 156, 1, 20], "bf16", 8, seed=d + span, layout=layout,
+             with_q=span > 0, loud=2.0)
+    k = randn((1, 128, d), "bf16", gen(d)) * 3
+    v = k.clone()
+    v[0, 77, d - 1] = -float("inf")
+    c = blank(2, 1, 128, d, 8)
+    blk.kv_append_paged(k, v, *c[:2], i32([[1]]), i32([128]), cu_seqlens=i32([0, 128]), k_scale=c[2], v_scale=c[3])
+    fin = v[torch.isfinite(v)].float()
+    s = float(c[3][1, 0])
+    assert s == ref.page_scale(float(fin.abs().max())) and c[1][1, 0, 77, d - 1].float() == -448
+    want = ref.e4m3(np.clip(f64(v[0].float()) / s, -448, 448))
+    assert np.array_equal(f64(c[1][1, 0].float()), want)
+    assert torch.equal(c[2][1], torch.tensor([ref.page_scale(float(k.float().abs().max()))], device="cuda"))
+
+
+def test_many_tokens_and_heads():
+    """Blocks that take several heads of keys, of values and of queries in turn, the last of each part-filled."""
+    for H, Hk, d, span, page, bits in ((40, 10, 64, 32, 16, 8), (23, 23, 64, 64, 32, 8), (40, 10, 128, 128, 64, 8),
+                                       (9, 3, 160, 40, 64, 16), (5, 5, 128, 128, 128, 8), (23, 23, 64, 16, 128, 16)):
+        case(H, Hk, d, span, page, [0, 33, 0, 700], [1200, 1500, 9, 800], "bf16", bits, interleaved=H == 40, seed=H)

@@ -98,6 +98,7 @@ BAD_CACHES = [
     (dict(page=8), EUNSUPPORTED), (dict(page=256), EUNSUPPORTED), (dict(Hk=0), EINVAL), (dict(Hk=5000), EINVAL),
     (dict(d=136), EUNSUPPORTED), (dict(d=0), EUNSUPPORTED), (dict(d=272), EUNSUPPORTED), (dict(B=0), EINVAL),
     (dict(B=(1 << 24) + 1), EINVAL), (dict(max_pages=0), EINVAL), (dict(max_pages=1 << 28), EINVAL),
+    (dict(max_pages=(1 << 22) + 1), EINVAL),
     (dict(stride=2 * 16 * 128 - 16), EINVAL), (dict(stride=2 * 16 * 128 + 8), EINVAL), (dict(stride=1 << 40), EINVAL),
     (dict(pages=1 << 30, stride=1 << 30), EINVAL), (dict(kind=2), EINVAL), (dict(kind=-1), EINVAL)]
 
