@@ -22,10 +22,11 @@
  *     (griddepcontrol.wait) before its first global access. A kernel the
  *     caller enqueues after a call is ordered as usual, unless the caller
  *     launches it with the same attribute.
- *   - Row-major, contiguous, 16-byte-aligned tensors. Linear weights follow the
+ *   - Row-major, contiguous, 16-byte-aligned tensors (the rotary at given
+ *     positions and the paged cache take strides). Linear weights follow the
  *     torch convention W[out, in], y = x W^T + b (nnterp "stablelm" Printout).
  *   - Storage dtype `dt` is fp16 or bf16 for every tensor of a call, except
- *     ALiBi slopes (fp32). All accumulation and statistics are fp32. K/V are
+ *     ALiBi slopes (fp32), Q8_0 weights and e4m3 caches with their scales. All accumulation and statistics are fp32. K/V are
  *     read at the stated dtype: nothing is silently converted.
  *   - Every call validates its arguments before any launch and returns a
  *     blk_status; a rejected call has no side effects. blk_last_error() gives a
