@@ -45,8 +45,8 @@
 // 7 warps: loading; MMA issue; four of softmax, a thread per key; queries.
 // Measured and bound: 96 sequences of up to 16384 keys, 32/8 x 128 heads, e4m3: 153-156 us (6.5 TB/s, 0.95-0.97 of
 // the copy rate); 8 of up to 32771, 16 x 128, 16 bits: 150 us (6.7 TB/s). Below some 100 MB the fixed
-// parts show: launch 2.4 us, the first tile's chain (lengths, table, tile, scores, softmax, product) 3.5,
-// merge 3 (32 of up to 4099 keys, 32/8 x 128: 22.9 us for 14.1 of bytes). Three CTAs per SM at head_dim 128: 24.3.
+// parts show: launch 2.4 us, the first tile's chain (lengths, table, tile, scores, softmax, product) 3, the
+// CTAs' ends apart 2, merge 3 (32 of up to 4099 keys, 32/8 x 128: 22.4 us for 14.1 of bytes). Three CTAs per SM at head_dim 128: 24.3.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -260,16 +260,15 @@ struct Segments {
         const int left = (len + kTK - 1) / kTK - first;
         n = static_cast<int>(min(static_cast<int64_t>(left), end - t));
     }
-    // base: tiles ahead of sequence b0's first unit; the range starts in b0
-    __device__ __forceinline__ void start(const PagedArgs& a, int64_t lo, int64_t hi, int b0,
-                                          int64_t base) {
+    // base: tiles ahead of sequence b0's first unit; the range starts in b0, of length l0
+    __device__ __forceinline__ void start(int64_t lo, int64_t hi, int b0, int64_t base, int l0) {
         t = lo;
         end = hi;
         it = 0;
         b = b0;
         valid = t < end;
         if (!valid) return;
-        len = len_of(a, b);
+        len = l0;
         const int nt = (len + kTK - 1) / kTK;
         // (from its sequence's first tile: units * 2^24 tiles at most, by lengths in 31 bits)
         const int64_t in = t - base;
@@ -318,6 +317,22 @@ struct Tiles {
     }
 };
 
+// The range of CTA `me` among W tiles: as many CTAs as there are tiles, if those are fewer (the merge
+// counts on every CTA of a unit's span having some of it).
+__device__ __forceinline__ void cut(int64_t W, int64_t& lo, int64_t& hi) {
+    const int64_t ctas = min(static_cast<int64_t>(gridDim.x), W), me = blockIdx.x;
+    if (me >= ctas) {
+        lo = hi = 0;
+    } else if (W < (1 << 21)) {  // (me + 1 is at most 2^10: 32 bits)
+        const uint32_t n = static_cast<uint32_t>(ctas), w = static_cast<uint32_t>(W);
+        lo = static_cast<uint32_t>(me) * w / n;
+        hi = (static_cast<uint32_t>(me) + 1) * w / n;
+    } else {
+        lo = me * W / ctas;
+        hi = (me + 1) * W / ctas;
+    }
+}
+
 // This CTA's range of tiles, by the four softmax warps: tiles [lo, hi), the first in sequence
 // b0, `base` tiles ahead of that sequence.
 struct Range {
@@ -347,11 +362,9 @@ __device__ __forceinline__ void find_range(const PagedArgs& a, Range& out, uint3
         if (i < w) before += out.sum[i];
         total += out.sum[i];
     }
-    // with fewer tiles than CTAs, one for each of the first W (the merge counts
-    // on every CTA of a unit's span having some of it)
-    const int64_t W = total * a.units;
-    const int64_t ctas = min(static_cast<int64_t>(gridDim.x), W), me = blockIdx.x;
-    const int64_t lo = me < ctas ? me * W / ctas : 0, hi = me < ctas ? (me + 1) * W / ctas : 0;
+    const int64_t W = total * a.units, me = blockIdx.x;
+    int64_t lo, hi;
+    cut(W, lo, hi);
     if (t == 0) {
         out.lo = lo;
         out.hi = hi;
@@ -378,6 +391,61 @@ __device__ __forceinline__ void find_range(const PagedArgs& a, Range& out, uint3
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(range_full);
+}
+
+// The same for up to 128 sequences, by each warp for itself: four lengths a lane, read once and passed
+// between lanes, no barrier and no shared memory (with find_range a CTA has its range 1.45 us behind its
+// start and its first copies out 3.2 us behind it; with this a call of 23.0 us takes 22.4).
+constexpr int kFewSequences = 128;
+__device__ __forceinline__ void warp_range(const PagedArgs& a, int lane, bool first_warp, Segments& c) {
+    const int per = (a.c.B + 31) / 32, b0 = lane * per;
+    int len[4], mine = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        len[k] = k < per && b0 + k < a.c.B ? len_of(a, b0 + k) : 0;
+        mine += (len[k] + kTK - 1) / kTK;
+    }
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    const int before = upto - mine, total = __shfl_sync(0xffffffffu, upto, 31);
+    int64_t lo, hi;
+    cut(static_cast<int64_t>(total) * a.units, lo, hi);
+    if (blockIdx.x == 0 && first_warp) {
+        int64_t sum = before;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < per && b0 + k < a.c.B) {
+                a.cum[b0 + k] = sum;
+                sum += (len[k] + kTK - 1) / kTK;
+            }
+        if (lane == 0) a.cum[a.c.B] = total;
+    }
+    // the lane whose sequences hold the first tile, and which of them
+    const int64_t mul = a.units;
+    const bool here = lo < hi && before * mul <= lo && lo < upto * mul;
+    int b = 0, l = 0;
+    int64_t base = before * mul;
+    bool found = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int64_t nt = (len[k] + kTK - 1) / kTK * mul;
+        if (!found && lo < base + nt) {
+            found = true;
+            b = b0 + k;
+            l = len[k];
+        }
+        if (!found) base += nt;
+    }
+    const unsigned who = __ballot_sync(0xffffffffu, here);
+    const int src = who ? __ffs(who) - 1 : 0;
+    b = __shfl_sync(0xffffffffu, b, src);
+    l = __shfl_sync(0xffffffffu, l, src);
+    base = __shfl_sync(0xffffffffu, base, src);
+    c.start(lo, hi, b, base, l);
 }
 
 template <typename T, bool E8, int D, int GP>
@@ -934,18 +1002,21 @@ __global__ void __launch_bounds__(kThreads, (Cfg<T, E8, D, GP>::kCtas))
     if (a.direct) {
         // a unit per CTA, whole
         const int b = static_cast<int>(blockIdx.x) / a.units, u = static_cast<int>(blockIdx.x) - b * a.units;
-        const int nt = (len_of(a, b) + kTK - 1) / kTK;
-        tiles.c.start(a, static_cast<int64_t>(u) * nt, static_cast<int64_t>(u + 1) * nt, b, 0);
+        const int len = len_of(a, b), nt = (len + kTK - 1) / kTK;
+        tiles.c.start(static_cast<int64_t>(u) * nt, static_cast<int64_t>(u + 1) * nt, b, 0, len);
         if (nt == 0) {  // no key: zero rows
             const int g = u / a.groups, h0 = g * a.G + (u - g * a.groups) * 8;
             const int n = min(GP, (g + 1) * a.G - h0) * (D / 8);
             uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.o) + (static_cast<int64_t>(b) * a.H + h0) * D);
             for (int i = threadIdx.x; i < n; i += kThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
         }
+    } else if (a.c.B <= kFewSequences) {
+        warp_range(a, lane, warp == 2, tiles.c);
     } else {
         if (warp >= 2 && warp < 6) find_range(a, range, bar.range_full());
         ok = mbar_wait(bar.range_full(), 0, a.err);
-        if (ok) tiles.c.start(a, range.lo, range.hi, range.b0, range.base);
+        if (ok) tiles.c.start(range.lo, range.hi, range.b0, range.base,
+                              range.lo < range.hi ? len_of(a, range.b0) : 0);
     }
     if (ok) {
         const PagedMaps maps{{{tm.m[0][0], tm.m[0][1]}, {tm.m[1][0], tm.m[1][1]}}};
