@@ -623,9 +623,13 @@ def attn_decode_paged(q, k_cache, v_cache, block_table, lens, k_scale=None, v_sc
         o = torch.empty_like(q) if q.is_contiguous() else torch.empty(q.shape, dtype=q.dtype, device=q.device)
         op = o.data_ptr()
     fn = _lib().blk_attn_decode_paged
-    status = _with_workspace(
-        lambda wp, wn, st: fn(desc, qp, kp, vp, ksp, vsp, tp, lp, sp, op, wp, wn, dt, st),
-        workspace, need, dev)
+    if need == 0 and workspace is None:
+        status = fn(desc, qp, kp, vp, ksp, vsp, tp, lp, sp, op, None, 0, dt,
+                    torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        status = _with_workspace(
+            lambda wp, wn, st: fn(desc, qp, kp, vp, ksp, vsp, tp, lp, sp, op, wp, wn, dt, st),
+            workspace, need, dev)
     if status:
         _abi.check(status, "blk_attn_decode_paged")
     return o
