@@ -24,7 +24,7 @@
 // offset; surplus blocks end at once.
 // To read and write: the new rows, their codes and scales, once. Measured and bound: the queries' part
 // by those bytes, the keys' and values' in 8 bits by instructions and latency per row at 0.6 of the copy
-// rate; 27595 tokens of 32/8 x 128 heads with queries 101 us (6.1 TB/s), 5713 of 32 x 64 24.6 us (4.7
+// rate; 27595 tokens of 32/8 x 128 heads with queries 100 us (6.2 TB/s), 5713 of 32 x 64 24.5 us (4.7
 // TB/s); a step of 16 sequences 4 us.
 #include <cuda_fp8.h>
 
@@ -50,7 +50,9 @@ struct AppendArgs {
     int tokens, H;             // query heads
     int kv_log2, q_log2;       // tokens of an item, of keys and values and of queries
     unsigned kv_items, q_items;
-    int team;                  // threads of an item of keys or values and head
+    int team, teams;           // threads of an item of keys or values and head, and such teams
+    int kv_rows;               // rows that a team takes in a round
+    int64_t head_hop[2], cache_hop;  // elements from a team's head to its next one, of k, v and the cache
     int kv_per, kv_groups;     // heads of K and V per block (K's, then V's), and blocks of them
     int q_per;                 // query heads per block
     int pdl;
@@ -197,7 +199,7 @@ __device__ __forceinline__ void turn_queries(const AppendArgs& a, const ItemRows
 // A block has teams of threads: a team takes one item and head at a time, its threads so many that IT
 // rounds of them hold the rows. What a block needs to know of its item (the search, the length, the
 // table) is a chain of dependent loads, which its teams and heads share: with a block of one warp for
-// each page and head, 5713 tokens of 32 x 64 heads took 47 us, with teams 34, and 24.6 with the steps
+// each page and head, 5713 tokens of 32 x 64 heads took 47 us, with teams 34, and 24.5 with the steps
 // below.
 // ROUNDS: for pages of more values than 512 threads hold: 256 read the rows twice (a variant of its own,
 // since its registers would be the other's spills).
@@ -287,7 +289,9 @@ __global__ void __launch_bounds__(IT * VP > 8 ? 768 : 1024) kv_append_kernel(con
     const int page = a.c.table[static_cast<int64_t>(r.b) * a.c.max_pages + column];
     if (page < 0 || page >= a.c.pages) return;
     const int in_page = static_cast<int>(r.pos & ((1 << a.c.page_log2) - 1));  // the first row's place
-    const int teams = blockDim.x / a.team, team_warps = a.team / 32;
+    const int team_warps = a.team / 32;
+    // (What is the same for all blocks is read from the arguments at each use: registers hold less, fewer
+    // are spilled. 27595 tokens of 32/8 x 128: 101.4 -> 100.3 us; 3020 of 16 x 64, 16 bits: 9.41 -> 9.33.)
     const int first = group * a.kv_per, end = min(first + a.kv_per, 2 * a.c.Hk);
     const int64_t head_size = static_cast<int64_t>(d) << a.c.page_log2;
     // This thread's rows: the others' values are zeros, which change no largest one, and are not
@@ -296,12 +300,12 @@ __global__ void __launch_bounds__(IT * VP > 8 ? 768 : 1024) kv_append_kernel(con
     int cell[IT];
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-        const int k = place + i * rows;
-        on[i] = place < rows && k < r.n;
+        const int k = place + i * a.kv_rows;
+        on[i] = place < a.kv_rows && k < r.n;
         cell[i] = min(k, r.n - 1) * turned_units + u;
     }
     const int gap = at.b - at.a;
-    const int chunks = (r.n + rows * IT - 1) / (rows * IT);
+    const int chunks = (r.n + a.kv_rows * IT - 1) / (a.kv_rows * IT);
     // The largest of x over the team (a round of its own barrier; entries alternate between rounds).
     int odd = 0;
     auto of_team = [&](float x) {
@@ -325,10 +329,8 @@ __global__ void __launch_bounds__(IT * VP > 8 ? 768 : 1024) kv_append_kernel(con
         // (the values' pieces lie where the keys' do)
         const bool turned = at.turned && !kValues;
         // (offsets in a head fit 32 bits: token strides are below 2^24)
-        const int64_t hs = a.xs[kValues][0] * teams;
         const T* x = static_cast<const T*>(a.x[kValues]) + s0 * a.xs[kValues][0] + r.row * a.xs[kValues][1];
         const int64_t base = page * a.c.page_stride + s0 * head_size + in_page * d;
-        const int64_t head_step = teams * head_size;
         uint8_t* codes = static_cast<uint8_t*>(kValues ? a.c.v : a.c.k) + base;
         T* cache = static_cast<T*>(kValues ? a.c.v : a.c.k) + base;
         float* scale = (kValues ? a.c.v_scale : a.c.k_scale) + static_cast<int64_t>(page) * a.c.Hk + s0;
@@ -337,7 +339,7 @@ __global__ void __launch_bounds__(IT * VP > 8 ? 768 : 1024) kv_append_kernel(con
         int from[IT], to[IT];
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            const int k = place + i * rows;  // (where there is no such row: a number that is not used)
+            const int k = place + i * a.kv_rows;  // (where there is no such row: a number that is not used)
             from[i] = static_cast<int>(static_cast<uint32_t>(k) * static_cast<uint32_t>(a.xs[kValues][1])) + at.a;
             to[i] = k * d + at.a;
             raw[i][0] = Raw{};
@@ -350,7 +352,7 @@ __global__ void __launch_bounds__(IT * VP > 8 ? 768 : 1024) kv_append_kernel(con
                     raw[i][0] = load_raw<T, VP>(x + from[i]);
                     raw[i][1] = load_raw<T, VP>(x + from[i] + gap);
                 }
-            x += hs;
+            x += a.head_hop[kValues];
             // ... and the head after it to the L2 cache (25.2 -> 24.0 us, 109.5 -> 106.9; in 16
             // bits, where blocks are more, it gains nothing)
 #pragma unroll
@@ -364,8 +366,8 @@ __global__ void __launch_bounds__(IT * VP > 8 ? 768 : 1024) kv_append_kernel(con
         auto rounds = [&](int c, float (&v)[IT][2][VP], bool (&in)[IT]) {
 #pragma unroll
             for (int i = 0; i < IT; ++i) {
-                const int k = place + (c * IT + i) * rows;
-                in[i] = place < rows && k < r.n;
+                const int k = place + (c * IT + i) * a.kv_rows;
+                in[i] = place < a.kv_rows && k < r.n;
                 raw[i][0] = Raw{};
                 raw[i][1] = Raw{};
                 if (in[i]) {
@@ -377,7 +379,7 @@ __global__ void __launch_bounds__(IT * VP > 8 ? 768 : 1024) kv_append_kernel(con
             for (int i = 0; i < IT; ++i) {
                 unpack_raw<T, VP>(raw[i][0], v[i][0]);
                 unpack_raw<T, VP>(raw[i][1], v[i][1]);
-                const int k = min(place + (c * IT + i) * rows, r.n - 1);
+                const int k = min(place + (c * IT + i) * a.kv_rows, r.n - 1);
                 if (turned) turn_by_table(k * turned_units + u, v[i][0], v[i][1]);
             }
         };
@@ -401,7 +403,7 @@ __global__ void __launch_bounds__(IT * VP > 8 ? 768 : 1024) kv_append_kernel(con
         };
         if (ROUNDS) {
             // the largest first, then the rows again (from the L2 cache), turned again
-            for (int s = s0; s < s1; s += teams) {
+            for (int s = s0; s < s1; s += a.teams) {
                 float v[IT][2][VP];
                 bool in[IT];
                 float inv = 1.f;
@@ -429,7 +431,7 @@ __global__ void __launch_bounds__(IT * VP > 8 ? 768 : 1024) kv_append_kernel(con
 #pragma unroll
                     for (int i = 0; i < IT; ++i) {
                         if (!in[i]) continue;
-                        const int at_row = (place + (c * IT + i) * rows) * d;
+                        const int at_row = (place + (c * IT + i) * a.kv_rows) * d;
                         if constexpr (E8) {
                             store_codes<VP>(codes + at_row + at.a, v[i][0], inv);
                             store_codes<VP>(codes + at_row + at.b, v[i][1], inv);
@@ -439,15 +441,15 @@ __global__ void __launch_bounds__(IT * VP > 8 ? 768 : 1024) kv_append_kernel(con
                         }
                     }
                 }
-                x += hs;
-                codes += head_step;
-                cache += head_step;
-                scale += teams;
+                x += a.head_hop[kValues];
+                codes += a.cache_hop;
+                cache += a.cache_hop;
+                scale += a.teams;
             }
             return;
         }
-        if (kAhead) fetch(s1 - s0 - teams);
-        for (int s = s0; s < s1; s += teams) {
+        if (kAhead) fetch(s1 - s0 - a.teams);
+        for (int s = s0; s < s1; s += a.teams) {
             if (!kAhead) fetch(0);
             float v[IT][2][VP];
 #pragma unroll
@@ -455,7 +457,7 @@ __global__ void __launch_bounds__(IT * VP > 8 ? 768 : 1024) kv_append_kernel(con
                 unpack_raw<T, VP>(raw[i][0], v[i][0]);
                 unpack_raw<T, VP>(raw[i][1], v[i][1]);
             }
-            if (kAhead && s + teams < s1) fetch(s1 - s - 2 * teams);
+            if (kAhead && s + a.teams < s1) fetch(s1 - s - 2 * a.teams);
             float held = 0.f;
             if (E8 && in_page > 0) held = *scale;  // (a page's first row begins its scale anew)
             float top = 0.f;
@@ -486,8 +488,8 @@ __global__ void __launch_bounds__(IT * VP > 8 ? 768 : 1024) kv_append_kernel(con
                         store_codes<VP>(codes + to[i], v[i][0], inv);
                         store_codes<VP>(codes + to[i] + gap, v[i][1], inv);
                     }
-                codes += head_step;
-                scale += teams;
+                codes += a.cache_hop;
+                scale += a.teams;
             } else {
 #pragma unroll
                 for (int i = 0; i < IT; ++i)
@@ -495,7 +497,7 @@ __global__ void __launch_bounds__(IT * VP > 8 ? 768 : 1024) kv_append_kernel(con
                         store_piece(cache + to[i], v[i][0]);
                         store_piece(cache + to[i] + gap, v[i][1]);
                     }
-                cache += head_step;
+                cache += a.cache_hop;
             }
         }
     };
@@ -530,6 +532,10 @@ cudaError_t launch_append(AppendArgs& a, int sms, cudaStream_t s) {
     const bool rounds = a.team > 512;
     if (rounds) a.team = 256;
     const int teams = a.team >= 256 ? 1 : 256 / a.team, threads = teams * a.team;
+    a.teams = teams;
+    a.kv_rows = a.team / units;
+    for (int i = 0; i < 2; ++i) a.head_hop[i] = teams * a.xs[i][0];
+    a.cache_hop = static_cast<int64_t>(teams) * a.c.d << a.c.page_log2;
     const int64_t B = a.c.B;
     const int64_t kv_items = a.cu ? (a.tokens >> a.kv_log2) + 2 * B : B;
     // Heads of a block: about so many as make one round of blocks, since what is ahead of a block's
