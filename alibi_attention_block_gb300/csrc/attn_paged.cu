@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const MergeA
     if (threadIdx.x >= kRows * kPer || row >= a.rows) return;
     const int b = static_cast<int>(row / a.H), h = static_cast<int>(row - static_cast<int64_t>(b) * a.H);
     const int g = h / a.G, in = h - g * a.G;  // kv head, and head of its group
-    const int u = g * a.groups + in / 8;
+    const int u = g * a.groups + in / a.GP;
     const int n = min(max(a.lens[b], 0), a.capacity);
     float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (n > 0) {
@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const MergeA
         const int64_t t0 = a.cum[b] * a.units + u * nt;
         const int ctas = static_cast<int>(min(static_cast<int64_t>(a.grid), W));
         const int c0 = cta_of(t0, W, ctas), c1 = cta_of(t0 + nt - 1, W, ctas);
-        const int64_t rec = (c0 + static_cast<int64_t>(b) * a.units + u) * a.GP + in % 8;
+        const int64_t rec = (c0 + static_cast<int64_t>(b) * a.units + u) * a.GP + in % a.GP;
         const float* p = a.po + rec * D + col;
         const float2* s = a.pm + rec;
         float m = -INFINITY, l = 0.f;
@@ -110,10 +110,6 @@ blk_status check_desc(const blk_decode_paged_desc* d) {
     return BLK_OK;
 }
 
-// query heads of a kernel's unit, and units of a kv head
-int unit_heads(int64_t G) { return G == 1 ? 1 : G <= 4 ? 4 : 8; }
-int64_t unit_groups(int64_t G) { return (G + 7) / 8; }
-
 // Whether a sequence's tiles are so few that a CTA takes each unit whole.
 constexpr int64_t kDirectTiles = 4;
 bool is_direct(const blk_paged_desc& c) {
@@ -121,13 +117,28 @@ bool is_direct(const blk_paged_desc& c) {
            c.batch * c.n_kv_heads <= (int64_t(1) << 24);
 }
 
+// Query heads of a unit. Sixteen, each reading of the cache for twice the heads, where the bytes bound
+// (256 sequences of up to 8192 keys, 16 heads on one, 16 bits: 93 -> 65 us at head_dim 128, 144 -> 87 at 160;
+// 32 on one: 178 -> 115, 280 -> 161); not at 64 (59 -> 57, but a call of 32 sequences 16.7 -> 17.6), not over e4m3,
+// where the softmax of each head costs more than its bytes (64 -> 77), and not where a CTA takes a unit
+// whole, which halves the CTAs (4 sequences of 500 keys, 32/2: 9.0 -> 9.8).
+int unit_heads(const blk_decode_paged_desc* d) {
+    const int64_t G = d->n_heads / d->cache.n_kv_heads;
+    if (G <= 8) return G == 1 ? 1 : G <= 4 ? 4 : 8;
+    return d->cache.kind == BLK_CACHE_16BIT && d->cache.head_dim >= 128 && !is_direct(d->cache) ? 16 : 8;
+}
+// ... and units of a kv head
+int64_t unit_groups(const blk_decode_paged_desc* d) {
+    const int n = unit_heads(d);
+    return (d->n_heads / d->cache.n_kv_heads + n - 1) / n;
+}
+
 struct Layout {
     size_t po, pm, cum, total;
 };
 Layout layout(const blk_decode_paged_desc* d) {
-    const int64_t G = d->n_heads / d->cache.n_kv_heads;
-    const size_t recs = static_cast<size_t>(kPagedMaxGrid + d->cache.batch * d->cache.n_kv_heads * unit_groups(G)) *
-                        unit_heads(G);
+    const size_t recs = static_cast<size_t>(kPagedMaxGrid + d->cache.batch * d->cache.n_kv_heads * unit_groups(d)) *
+                        unit_heads(d);
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
     Layout L{};
     if (is_direct(d->cache)) return L;
@@ -191,8 +202,8 @@ blk_status blk_attn_decode_paged(const blk_decode_paged_desc* d, const void* q, 
     a.slopes = alibi_slopes;
     a.H = static_cast<int>(d->n_heads);
     a.G = a.H / a.c.Hk;
-    a.GP = unit_heads(a.G);
-    a.groups = static_cast<int>(unit_groups(a.G));
+    a.GP = unit_heads(d);
+    a.groups = static_cast<int>(unit_groups(d));
     a.units = a.c.Hk * a.groups;
     a.scale = d->softmax_scale > 0.f ? d->softmax_scale : 1.0f / std::sqrt(static_cast<float>(a.c.d));
     a.alibi = d->alibi;

@@ -31,8 +31,9 @@
 //
 // 16 bits: the operands in the storage type, weights rounded to it (as in the prefill kernels).
 //
-// Work: a unit is (sequence, kv head, up to eight of its query heads) of ceil(len / 128) key tiles. The tiles of all
-// units, in one line, are cut into equal ranges, one per CTA, whatever the lengths are; a CTA's
+// Work: a unit is (sequence, kv head, up to eight of its query heads, sixteen over wide 16-bit
+// rows: unit_heads in attn_paged.cu) of ceil(len / 128) key tiles. The tiles of all units, in one
+// line, are cut into equal ranges, one per CTA, whatever the lengths are; a CTA's
 // stay in a unit is a segment with a partial result (reference, sum, O), joined by the merge.
 // Where the cache has few tiles per sequence (is_direct in attn_paged.cu) a CTA takes a whole unit and
 // writes its rows: no range to find, no partial results, one launch.
@@ -79,22 +80,25 @@ struct Cfg {
     static constexpr int kRows = (kUsed + 7) / 8 * 8;
     static constexpr int kLd = kUsed == 3 ? 4 : kUsed == 12 ? 16 : kUsed == 24 ? 32 : kUsed;
     static constexpr int kBlocks = D > 128 ? 2 : 1;  // of O's rows: 128 and 64
-    // two CTAs per SM, so that one's chain of scores, softmax and product fills the
-    // other's gaps; four where tiles are short, one where they are long
-    static constexpr int kCtas = E8 && D == 64 && kN == 16 ? 4 : kTile > 32768 ? 1 : 2;
     // (each buffer at a multiple of the swizzle's 1024 bytes)
     static constexpr int kQBytes = (kRows * kRow + 1023) / 1024 * 1024, kPBytes = kRows * 128 * kElem;
-    static constexpr int kFixed = 2 * kQBytes + 2 * kPBytes + 8 * 2 * 8 * 4 + 4 * 8 * 4 * 4 + 2 * 8 * 4 + 512 + 16;
-    static constexpr int kFit = (228 * 1024 / kCtas - 2048 - 64 - kFixed) / kTile;
+    static constexpr int kHeads = GP > 8 ? GP : 8;  // that the small arrays have room for
+    static constexpr int kFixed =
+        2 * kQBytes + 2 * kPBytes + 8 * 2 * 8 * 4 + 4 * kHeads * 4 * 4 + 2 * kHeads * 4 + 512 + 16;
+    // two CTAs per SM, so that one's chain of scores, softmax and product fills the
+    // other's gaps; four where tiles are short, one where three of them do not fit twice
+    static constexpr int fit(int ctas) { return (228 * 1024 / ctas - 2048 - 64 - kFixed) / kTile; }
+    static constexpr int kCtas = E8 && D == 64 && kN == 16 ? 4 : fit(2) < 3 ? 1 : 2;
+    static constexpr int kFit = fit(kCtas);
     static constexpr int kSlots = kFit < 6 ? kFit : 6;
     static_assert(kSlots >= 3 && kSlots <= 6, "a ring of tiles, and the scales' ring of eight");
     static constexpr int kOffQ = kSlots * kTile;
     static constexpr int kOffP = kOffQ + 2 * kQBytes;
     static constexpr int kOffScale = kOffP + 2 * kPBytes;    // [8 tiles][K, V][8 groups of 16 keys]
-    static constexpr int kOffMax = kOffScale + 8 * 2 * 8 * 4;  // [2][8][4]
-    static constexpr int kOffSum = kOffMax + 2 * 8 * 4 * 4;    // [2][8][4]
-    static constexpr int kOffMul = kOffSum + 2 * 8 * 4 * 4;    // [2][8]
-    static constexpr int kOffBar = kOffMul + 2 * 8 * 4;
+    static constexpr int kOffMax = kOffScale + 8 * 2 * 8 * 4;    // [2][kHeads][4]
+    static constexpr int kOffSum = kOffMax + 2 * kHeads * 4 * 4;  // [2][kHeads][4]
+    static constexpr int kOffMul = kOffSum + 2 * kHeads * 4 * 4;  // [2][kHeads]
+    static constexpr int kOffBar = kOffMul + 2 * kHeads * 4;
     static constexpr int kOffSlot = kOffBar + 512;
     static constexpr int kSmem = kOffSlot + 16 + 1024;  // + alignment slack
     static_assert(kCtas * (kSmem + 1024 + 64) <= 228 * 1024, "shared memory of an SM");
@@ -655,7 +659,7 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
         constexpr int kPairs = (D + 63) / 64;  // of neighbouring dims, per lane
         while (ok && c.valid) {
             const int qb = c.it & 1;
-            const int g = c.u / a.groups, h0 = g * a.G + (c.u - g * a.groups) * 8;
+            const int g = c.u / a.groups, h0 = g * a.G + (c.u - g * a.groups) * GP;
             const int heads = min(GP, (g + 1) * a.G - h0);
             float2 f[GP][kPairs];
 #pragma unroll
@@ -689,7 +693,7 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
                     down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
                     up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
                 }
-                if (lane == 0) factors[qb * 8 + h] = up * a.scale * kLog2e;
+                if (lane == 0) factors[qb * C::kHeads + h] = up * a.scale * kLog2e;
 #pragma unroll
                 for (int i = 0; i < kPairs; ++i) {
                     const int col = 2 * (lane + 32 * i) * C::kElem;  // byte of the row
@@ -784,12 +788,12 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
         while (ok && c.valid) {
             float m[GP], l[GP], slope[GP], mul[GP];
             if (!(ok = mbar_wait(bar.q_full(c.it & 1), (c.it >> 1) & 1, a.err))) break;
-            const int g = c.u / a.groups, h0 = g * a.G + (c.u - g * a.groups) * 8;
+            const int g = c.u / a.groups, h0 = g * a.G + (c.u - g * a.groups) * GP;
 #pragma unroll
             for (int h = 0; h < GP; ++h) {
                 m[h] = -INFINITY;
                 l[h] = 0.f;
-                mul[h] = factors[(c.it & 1) * 8 + h];
+                mul[h] = factors[(c.it & 1) * C::kHeads + h];
                 slope[h] = 0.f;
                 if (a.alibi) {
                     const int hq = min(h0 + h, a.H - 1);
@@ -822,7 +826,7 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
                 const int up = static_cast<int>((__float_as_uint(vs) + 0x7fffffu) >> 23) - 127;
                 const float shift = E8 ? static_cast<float>(max(up, -40)) : 0.f;
                 float s[GP];
-                float* rm = red_max + (t & 1) * 32;
+                float* rm = red_max + (t & 1) * 4 * C::kHeads;
 #pragma unroll
                 for (int h = 0; h < GP; ++h) {
                     float v = __uint_as_float(r[h]);
@@ -942,7 +946,7 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
                 float v = l[h];
 #pragma unroll
                 for (int x = 16; x > 0; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
-                if (lane == h) red_sum[(c.it & 1) * 32 + h * 4 + quarter] = v;
+                if (lane == h) red_sum[((c.it & 1) * C::kHeads + h) * 4 + quarter] = v;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar.sum_full());
@@ -958,7 +962,7 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
             pend_rec = a.direct ? static_cast<int64_t>(c.b) * a.H + h0 : rec;
             pend_heads = (g + 1) * a.G - h0;
             if (!a.direct && quarter == 0 && lane < GP) {
-                const float4 w = *reinterpret_cast<const float4*>(red_sum + (c.it & 1) * 32 + lane * 4);
+                const float4 w = *reinterpret_cast<const float4*>(red_sum + ((c.it & 1) * C::kHeads + lane) * 4);
                 float mh = m[0];
 #pragma unroll
                 for (int h = 1; h < GP; ++h)
@@ -1005,7 +1009,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<T, E8, D, GP>::kCtas))
         const int len = len_of(a, b), nt = (len + kTK - 1) / kTK;
         tiles.c.start(static_cast<int64_t>(u) * nt, static_cast<int64_t>(u + 1) * nt, b, 0, len);
         if (nt == 0) {  // no key: zero rows
-            const int g = u / a.groups, h0 = g * a.G + (u - g * a.groups) * 8;
+            const int g = u / a.groups, h0 = g * a.G + (u - g * a.groups) * GP;
             const int n = min(GP, (g + 1) * a.G - h0) * (D / 8);
             uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.o) + (static_cast<int64_t>(b) * a.H + h0) * D);
             for (int i = threadIdx.x; i < n; i += kThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -1051,7 +1055,10 @@ cudaError_t launch_paged_d(const PagedMapSet& tm, PagedArgs& a, int sms, cudaStr
         case 1: return launch_paged_g<T, E8, D, 1>(tm, a, sms, s);
         case 4: return launch_paged_g<T, E8, D, 4>(tm, a, sms, s);
         case 8: return launch_paged_g<T, E8, D, 8>(tm, a, sms, s);
-        default: return cudaErrorInvalidValue;
+        default:
+            if constexpr (!E8 && D >= 128)
+                if (a.GP == 16) return launch_paged_g<T, E8, D, 16>(tm, a, sms, s);
+            return cudaErrorInvalidValue;
     }
 }
 

@@ -27,7 +27,7 @@ struct PagedArgs {
     const float* slopes;
     unsigned* err;
     int H, G, GP;   // query heads; of a kv head; of a unit, at most
-    int groups;     // units of a kv head: ceil(G / 8)
+    int groups;     // units of a kv head: ceil(G / GP)
     int units;      // of a sequence
     int grid;
     float scale;

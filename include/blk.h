@@ -412,7 +412,8 @@ typedef struct {
  *   alibi_slopes: as for blk_attn_prefill
  *   o [batch, n_heads, head_dim], contiguous
  * GQA: kv head = h / (n_heads / n_kv_heads), any ratio; above 8 the cache is read
- * once for every 8 query heads of a kv head. Sums and statistics are in 32 bits; softmax weights enter the product
+ * once for every 8 query heads of a kv head (16 over a 16-bit cache with head_dim 128
+ * or 160, where there are two launches). Sums and statistics are in 32 bits; softmax weights enter the product
  * with V rounded: to dt over a 16-bit cache; over e4m3, to sums of two (bf16) or three
  * (fp16) e4m3 numbers, at most 2^-9 or 2^-14 off, relative, or 2^-21 and 2^-26 of the largest.
  * Two launches. The workspace holds partial results, at least

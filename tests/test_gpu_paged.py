@@ -148,6 +148,19 @@ def test_every_kernel(G, d, dt, bits):
 
 @pytest.mark.parametrize("bits", [8, 16])
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("d", [64, 128, 160])
+@pytest.mark.parametrize("G", [9, 16, 17, 40])
+def test_many_heads_of_a_kv_head(G, d, dt, bits):
+    """More than eight query heads on a kv head, the last unit full, part empty or of one head:
+    with several segments per CTA, and in one launch; with ALiBi too."""
+    lens = [(211 * i) % 1700 for i in range(27)]
+    run(27, 3 * G, 3, d, 32, lens, dt, bits, True, seed=G + d, spread=6.0)
+    run(27, 3 * G, 3, d, 64, lens, dt, bits, False, seed=G + d + 1)
+    run(9, 2 * G, 2, d, 16, [(53 * i) % 400 for i in range(9)], dt, bits, True, seed=G + d + 2, spread=6.0)
+
+
+@pytest.mark.parametrize("bits", [8, 16])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
 @pytest.mark.parametrize("case", CASES, ids=lambda c: "B{}H{}Hk{}d{}p{}".format(*c[:5]))
 def test_matches_definition(case, dt, bits):
     """With room to spare in the block table, every case takes the two launches."""
