@@ -33,6 +33,71 @@ __device__ __forceinline__ int cta_of(int64_t t, int64_t W, int n) {
     return c;
 }
 
+// The records of a row: the first one's number and how many they are (0: no key).
+struct Records {
+    int64_t first;
+    int n;
+};
+__device__ __forceinline__ Records records_of(const MergeArgs& a, int64_t row) {
+    const int b = static_cast<int>(row / a.H), h = static_cast<int>(row - static_cast<int64_t>(b) * a.H);
+    const int g = h / a.G, in = h - g * a.G;  // kv head, and head of its group
+    const int u = g * a.groups + in / a.GP;
+    const int n = min(max(a.lens[b], 0), a.capacity);
+    if (n == 0) return {0, 0};
+    const int64_t W = a.cum[a.batch] * a.units, nt = (n + kTK - 1) / kTK;
+    const int64_t t0 = a.cum[b] * a.units + u * nt;
+    const int ctas = static_cast<int>(min(static_cast<int64_t>(a.grid), W));
+    const int c0 = cta_of(t0, W, ctas), c1 = cta_of(t0 + nt - 1, W, ctas);
+    return {(c0 + static_cast<int64_t>(b) * a.units + u) * a.GP + in % a.GP, c1 - c0 + 1};
+}
+
+// Eight columns of records [from, n) in steps, joined: f of sum l and reference m.
+template <int D>
+__device__ __forceinline__ void join(const MergeArgs& a, const Records& r, int col, int from, int step, float& m,
+                                     float& l, float (&f)[8]) {
+    const float* p = a.po + r.first * D + col;
+    const float2* s = a.pm + r.first;
+    m = -INFINITY;
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = 0.f;
+    // Four records' loads at a time, the ones behind the last without effect: a row of two or three has
+    // them all on their way at once (64 sequences of up to 1000 keys, 32/8 x 128: 18.0 -> 17.3 us).
+    for (int k = from; k < r.n; k += 4 * step) {
+        float4 x[4], y[4];
+        float2 ml[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i] = y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            ml[i] = make_float2(-INFINITY, 0.f);
+            if (k + i * step < r.n) {
+                const int64_t at = static_cast<int64_t>(k + i * step) * a.GP;
+                const float4* q = reinterpret_cast<const float4*>(p + at * D);
+                x[i] = q[0];
+                y[i] = q[1];
+                ml[i] = s[at];
+            }
+        }
+        float mn = m;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mn = fmaxf(mn, ml[i].x);
+        const float base = mn == -INFINITY ? 0.f : mn;
+        const float keep = m == -INFINITY ? 0.f : exp2f(m - mn);
+        m = mn;
+        l *= keep;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] *= keep;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float w = ml[i].x == -INFINITY && ml[i].y == 0.f ? 0.f : exp2f(ml[i].x - base);
+            l = fmaf(w, ml[i].y, l);
+            const float v[8] = {x[i].x, x[i].y, x[i].z, x[i].w, y[i].x, y[i].y, y[i].z, y[i].w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = fmaf(w, v[e], f[e]);
+        }
+    }
+}
+
 // D / 8 threads per row of 8 columns each.
 template <typename T, int D>
 __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const MergeArgs a) {
@@ -41,49 +106,73 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const MergeA
     const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kPer;
     const int col = threadIdx.x % kPer * 8;
     if (threadIdx.x >= kRows * kPer || row >= a.rows) return;
-    const int b = static_cast<int>(row / a.H), h = static_cast<int>(row - static_cast<int64_t>(b) * a.H);
-    const int g = h / a.G, in = h - g * a.G;  // kv head, and head of its group
-    const int u = g * a.groups + in / a.GP;
-    const int n = min(max(a.lens[b], 0), a.capacity);
-    float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (n > 0) {
-        const int64_t W = a.cum[a.batch] * a.units, nt = (n + kTK - 1) / kTK;
-        const int64_t t0 = a.cum[b] * a.units + u * nt;
-        const int ctas = static_cast<int>(min(static_cast<int64_t>(a.grid), W));
-        const int c0 = cta_of(t0, W, ctas), c1 = cta_of(t0 + nt - 1, W, ctas);
-        const int64_t rec = (c0 + static_cast<int64_t>(b) * a.units + u) * a.GP + in % a.GP;
-        const float* p = a.po + rec * D + col;
-        const float2* s = a.pm + rec;
-        float m = -INFINITY, l = 0.f;
-#pragma unroll 4
-        for (int k = 0; k <= c1 - c0; ++k) {
-            const float4* q = reinterpret_cast<const float4*>(p + static_cast<int64_t>(k) * a.GP * D);
-            const float4 x = q[0], y = q[1];
-            const float2 ml = s[static_cast<int64_t>(k) * a.GP];
-            const float mn = fmaxf(m, ml.x);
-            const float keep = m == -INFINITY ? 0.f : exp2f(m - mn);
-            const float w = ml.x == -INFINITY && ml.y == 0.f ? 0.f : exp2f(ml.x - (mn == -INFINITY ? 0.f : mn));
-            m = mn;
-            l = fmaf(l, keep, w * ml.y);
-            const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    float m, l, f[8];
+    join<D>(a, records_of(a, row), col, 0, 1, m, l, f);
+    const float inv = l == 0.f ? 0.f : 1.0f / l;  // no key seen: a zero row
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = fmaf(f[e], keep, w * v[e]);
-        }
-        const float inv = l == 0.f ? 0.f : 1.0f / l;  // no key seen: a zero row
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= inv;
-    }
+    for (int e = 0; e < 8; ++e) f[e] *= inv;
     store8(static_cast<T*>(a.o) + row * D + col, f);
 }
 
+// The same by a block per row, whose teams of D / 8 threads take records in turn and join theirs
+// through shared memory, for few rows: then a row's records are many (one of nearly each CTA where a
+// long sequence has few heads) and one load behind the other is what takes the time. One sequence, e4m3,
+// 32/8 x 128, 4096, 16384 and 65536 keys: 16.3 -> 8.2 us, 23.8 -> 13.9 and 36.1 -> 27.0; 16 of up to
+// 2000: 14.6 -> 13.7. With more rows than in launch_merge_d the blocks are many more than the GPU
+// holds at a time, and most rows have two records: 200 of up to 600 keys 28.1 -> 36.3. Blocks of 256 and
+// 512 threads: level for one sequence, 14.3 and 16.5 for the sixteen.
+constexpr int kRowThreads = 128;
+template <typename T, int D>
+__global__ void __launch_bounds__(kRowThreads) paged_merge_row_kernel(const MergeArgs a) {
+    constexpr int kPer = D / 8, kTeams = kRowThreads / kPer;
+    __shared__ __align__(16) float parts[kTeams][D];
+    __shared__ float2 ml[kTeams];
+    if (a.pdl) pdl_wait();
+    const int64_t row = blockIdx.x;
+    const int team = threadIdx.x / kPer, col = threadIdx.x % kPer * 8;
+    const Records r = records_of(a, row);
+    if (team < kTeams && team < r.n) {
+        float m, l, f[8];
+        join<D>(a, r, col, team, kTeams, m, l, f);
+        float4* to = reinterpret_cast<float4*>(parts[team] + col);
+        to[0] = make_float4(f[0], f[1], f[2], f[3]);
+        to[1] = make_float4(f[4], f[5], f[6], f[7]);
+        if (col == 0) ml[team] = make_float2(m, l);
+    }
+    __syncthreads();
+    const int n = min(r.n, kTeams);
+    float top = -INFINITY;
+    for (int k = 0; k < n; ++k) top = fmaxf(top, ml[k].x);
+    const float base = top == -INFINITY ? 0.f : top;
+    for (int c = threadIdx.x; c < D; c += kRowThreads) {
+        float l = 0.f, f = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+            const float2 x = ml[k];
+            const float w = x.x == -INFINITY && x.y == 0.f ? 0.f : exp2f(x.x - base);
+            l = fmaf(w, x.y, l);
+            f = fmaf(w, parts[k][c], f);
+        }
+        f = l == 0.f ? 0.f : f * (1.0f / l);
+        static_cast<uint16_t*>(a.o)[row * D + c] = static_cast<uint16_t>(dt_traits<T>::pack2(f, 0.f));
+    }
+}
+
+template <typename T, int D>
+cudaError_t launch_merge_d(const MergeArgs& a, int sms, cudaStream_t s) {
+    if (a.rows <= 8 * sms)  // one round of such blocks
+        return launch_pdl(a.pdl != 0, paged_merge_row_kernel<T, D>, dim3(static_cast<unsigned>(a.rows)),
+                          dim3(kRowThreads), 0, s, a);
+    constexpr int per = kMergeThreads / (D / 8);
+    return launch_pdl(a.pdl != 0, paged_merge_kernel<T, D>, dim3(static_cast<unsigned>((a.rows + per - 1) / per)),
+                      dim3(kMergeThreads), 0, s, a);
+}
 template <typename T>
-cudaError_t launch_merge(const MergeArgs& a, int d, cudaStream_t s) {
-    const int per = kMergeThreads / (d / 8);
-    const dim3 grid(static_cast<unsigned>((a.rows + per - 1) / per)), block(kMergeThreads);
+cudaError_t launch_merge(const MergeArgs& a, int d, int sms, cudaStream_t s) {
     switch (d) {
-        case 64: return launch_pdl(a.pdl != 0, paged_merge_kernel<T, 64>, grid, block, 0, s, a);
-        case 128: return launch_pdl(a.pdl != 0, paged_merge_kernel<T, 128>, grid, block, 0, s, a);
-        default: return launch_pdl(a.pdl != 0, paged_merge_kernel<T, 160>, grid, block, 0, s, a);
+        case 64: return launch_merge_d<T, 64>(a, sms, s);
+        case 128: return launch_merge_d<T, 128>(a, sms, s);
+        default: return launch_merge_d<T, 160>(a, sms, s);
     }
 }
 
@@ -241,7 +330,7 @@ blk_status blk_attn_decode_paged(const blk_decode_paged_desc* d, const void* q, 
         m.capacity = a.c.max_pages << a.c.page_log2;
         m.grid = a.grid;
         m.pdl = a.pdl;
-        e = dt == BLK_F16 ? launch_merge<__half>(m, a.c.d, cs) : launch_merge<__nv_bfloat16>(m, a.c.d, cs);
+        e = dt == BLK_F16 ? launch_merge<__half>(m, a.c.d, sms, cs) : launch_merge<__nv_bfloat16>(m, a.c.d, sms, cs);
     }
     return e == cudaSuccess ? BLK_OK
                             : report_error_status(BLK_ECUDA, "paged decode launch: %s", cudaGetErrorString(e));

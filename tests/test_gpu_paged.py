@@ -160,6 +160,16 @@ def test_many_heads_of_a_kv_head(G, d, dt, bits):
 
 
 @pytest.mark.parametrize("bits", [8, 16])
+@pytest.mark.parametrize("d,H,Hk", [(64, 2, 2), (128, 8, 1), (160, 4, 1)])
+@pytest.mark.parametrize("B", [1, 5, 700])
+def test_one_long_sequence(B, d, H, Hk, bits):
+    """A row joined from nearly every CTA's part of it, alone and among many rows of one part or none."""
+    lens = [i % 9 for i in range(B)]
+    lens[B // 2] = 50003
+    run(B, H, Hk, d, 64, lens, "fp16", bits, B == 5, seed=B + d)
+
+
+@pytest.mark.parametrize("bits", [8, 16])
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
 @pytest.mark.parametrize("case", CASES, ids=lambda c: "B{}H{}Hk{}d{}p{}".format(*c[:5]))
 def test_matches_definition(case, dt, bits):
