@@ -17,19 +17,24 @@
 // 8 bits: a product of kind f8f6f4 takes 8-bit operands on both sides, so the queries and the
 // weights are written as sums of e4m3 numbers, in columns of their own:
 //     q = 2^e (q1 + 2^-5 q2 + 2^-10 q3),   q1 = e4m3(2^-e q), q2 = e4m3(2^5 (2^-e q - q1)), ...
-// with 2^e such that the row's largest is in [128, 256). Each e4m3 holds 4 significant bits, a
-// remainder is at most 2^-5 of its number, so two parts hold a bf16 number and three an fp16
-// number exactly, down to 2^-22 and 2^-27 of the row's largest. (The columns are there
-// anyway: N is at least 16.) Weights, likewise: two parts (bf16) are at most 2^-9 off, relative, three
-// (fp16) 2^-14, which is less than the output's own rounding; their sums are of the 32-bit
-// weights. Where a weight is far below the largest, the error is absolute, 2^-21 and
-// 2^-26 of that one.
+// with 2^e such that the row's largest is in [128, 256). An e4m3 holds 4 significant bits: a
+// remainder is at most 2^-4 of the power of two below its number, so 32 times it at most 256, and takes the
+// next 5 bits. Two parts hold the 8 bits of a bf16 number and three the 11 of an fp16 number exactly, down to 2^-22
+// and 2^-27 of the row's largest. (The columns are there
+// anyway: N is at least 16.) Weights are three parts, at most 2^-9 2^-5 = 2^-14 off, relative; their sums are
+// of the 32-bit weights. Where a weight is far below the largest, the error is absolute, 2^-26 of that one.
 // A page's scales are factors of its keys: that of K multiplies the score, that of V
 // the weight ahead of its rounding. So that the weight times scale stays in e4m3's range whatever the
 // scales are, the running reference that is subtracted is of score + log2(scale of V), not of the score.
 // The sum of the weights has the same reference; scales of V below 2^-40 count as 2^-40 in it.
 //
-// 16 bits: the operands in the storage type, weights rounded to it (as in the prefill kernels).
+// 16 bits: the operands in the storage type, a weight as the sum of two such numbers (the second one's columns are
+// there anyway too), 2^-16 off in bf16, 2^-22 in fp16 (held times 2^7, its second part times 2^11: weights down to 2^-21 of
+// the largest in fp16's normal range). With weights of one part (two in bf16 over e4m3) the outputs of few keys, which do not
+// average their errors, were up to 8 % further from the definition than the output's rounding leaves them. The times are the same
+// (48 sequences of up to 8192 keys: within 1 %) but for e4m3 with eight heads and more on a kv head, bf16: 256
+// sequences, 8 on one, 42.8 -> 36.1 us at head_dim 64 (two CTAs per SM in the place of four, whose registers spilled),
+// 39.4 at 128, 47.1 -> 49.0 at 160.
 //
 // Work: a unit is (sequence, kv head, up to eight of its query heads, sixteen over wide 16-bit
 // rows: unit_heads in attn_paged.cu) of ceil(len / 128) key tiles. The tiles of all units, in one
@@ -72,23 +77,28 @@ struct Cfg {
     static constexpr int kRow = 128 * kWide + 64 * kNarrow;
     static constexpr int kTile = kTK * kRow;
     static constexpr int kStepKeys = 32 / kElem;  // keys of a product's step: 32 bytes of P
-    static constexpr int kParts = !E8 ? 1 : dt_traits<T>::mma_fmt == 0 ? 3 : 2;
-    static constexpr int kUsed = kParts * GP;  // columns with something in them
-    static constexpr int kN = kUsed <= 16 ? 16 : 32;
+    static constexpr bool kF16 = dt_traits<T>::mma_fmt == 0;
+    static constexpr int kQParts = !E8 ? 1 : kF16 ? 3 : 2, kPParts = E8 ? 3 : 2;  // of queries, of weights
+    // each part, next to the one before it, is held times this
+    static constexpr float kUp = E8 ? 32.f : kF16 ? 2048.f : 256.f;
+    static constexpr int kQUsed = kQParts * GP, kPUsed = kPParts * GP;  // columns with something in them
+    static constexpr int columns(int used) { return used <= 16 ? 16 : 32; }
+    static constexpr int kNS = columns(kQUsed), kNO = columns(kPUsed);
     // ... and the operands' rows for them in groups of 8; what follows in shared
     // memory makes up the rest (columns do not mix, and none of the rest is read)
-    static constexpr int kRows = (kUsed + 7) / 8 * 8;
-    static constexpr int kLd = kUsed == 3 ? 4 : kUsed == 12 ? 16 : kUsed == 24 ? 32 : kUsed;
+    static constexpr int kQRows = (kQUsed + 7) / 8 * 8, kPRows = (kPUsed + 7) / 8 * 8;
+    static constexpr int loads(int used) { return used == 3 ? 4 : used == 12 ? 16 : used; }
+    static constexpr int kLdS = loads(kQUsed), kLdO = loads(kPUsed);
     static constexpr int kBlocks = D > 128 ? 2 : 1;  // of O's rows: 128 and 64
     // (each buffer at a multiple of the swizzle's 1024 bytes)
-    static constexpr int kQBytes = (kRows * kRow + 1023) / 1024 * 1024, kPBytes = kRows * 128 * kElem;
+    static constexpr int kQBytes = (kQRows * kRow + 1023) / 1024 * 1024, kPBytes = kPRows * 128 * kElem;
     static constexpr int kHeads = GP > 8 ? GP : 8;  // that the small arrays have room for
     static constexpr int kFixed =
         2 * kQBytes + 2 * kPBytes + 8 * 2 * 8 * 4 + 4 * kHeads * 4 * 4 + 2 * kHeads * 4 + 512 + 16;
     // two CTAs per SM, so that one's chain of scores, softmax and product fills the
     // other's gaps; four where tiles are short, one where three of them do not fit twice
     static constexpr int fit(int ctas) { return (228 * 1024 / ctas - 2048 - 64 - kFixed) / kTile; }
-    static constexpr int kCtas = E8 && D == 64 && kN == 16 ? 4 : fit(2) < 3 ? 1 : 2;
+    static constexpr int kCtas = E8 && D == 64 && kNO == 16 ? 4 : fit(2) < 3 ? 1 : 2;
     static constexpr int kFit = fit(kCtas);
     static constexpr int kSlots = kFit < 6 ? kFit : 6;
     static_assert(kSlots >= 3 && kSlots <= 6, "a ring of tiles, and the scales' ring of eight");
@@ -103,11 +113,11 @@ struct Cfg {
     static constexpr int kSmem = kOffSlot + 16 + 1024;  // + alignment slack
     static_assert(kCtas * (kSmem + 1024 + 64) <= 228 * 1024, "shared memory of an SM");
     // TMEM: S^T twice (by tile), O^T twice (by segment)
-    static constexpr uint32_t kColO = 2 * kN;
-    static constexpr uint32_t kCols = kN == 16 ? 128 : 256;
-    static_assert(2 * kN + 2 * kBlocks * kN <= static_cast<int>(kCols) && kCtas * kCols <= 512, "TMEM");
-    // weights are at most 2 (threshold below) times 128; 16 bits: as they are
-    static constexpr float kTop = E8 ? 128.f : 1.f;
+    static constexpr uint32_t kColO = 2 * kNS;
+    static constexpr uint32_t kCols = 2 * kNS + 2 * kBlocks * kNO <= 128 ? 128 : 256;
+    static_assert(2 * kNS + 2 * kBlocks * kNO <= static_cast<int>(kCols) && kCtas * kCols <= 512, "TMEM");
+    // weights are at most 2^threshold times this: 2^8 in e4m3, 2^15 in fp16
+    static constexpr float kTop = E8 || kF16 ? 128.f : 1.f;
     static constexpr float kThreshold = E8 ? 1.f : 8.f;  // log2 of the largest weight before a rescale
 };
 
@@ -131,6 +141,15 @@ __device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&r)[N]) {
                        "=r"(r[6]), "=r"(r[7]) : "r"(taddr) : "memory");
     else if constexpr (N == 16)
         tmem_ld16(taddr, r);
+    else if constexpr (N == 24)  // (the first load must not overwrite the second's address)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+                     "%13, %14, %15}, [%24];\n\t"
+                     "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16, %17, %18, %19, %20, %21, %22, %23}, [%25];\n\t"
+                     "tcgen05.wait::ld.sync.aligned;"
+                     : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]), "=&r"(r[6]),
+                       "=&r"(r[7]), "=&r"(r[8]), "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11]), "=&r"(r[12]), "=&r"(r[13]),
+                       "=&r"(r[14]), "=&r"(r[15]), "=&r"(r[16]), "=&r"(r[17]), "=&r"(r[18]), "=&r"(r[19]), "=&r"(r[20]),
+                       "=&r"(r[21]), "=&r"(r[22]), "=&r"(r[23]) : "r"(taddr), "r"(taddr + 16) : "memory");
     else
         tmem_ld32(taddr, r);
 }
@@ -151,7 +170,16 @@ __device__ __forceinline__ void st_cols(uint32_t taddr, const uint32_t (&r)[N]) 
                      "r"(r[6]), "r"(r[7]) : "memory");
     else if constexpr (N == 16)
         tmem_st16_nowait(taddr, r);
-    else
+    else if constexpr (N == 24) {
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+                     "%12, %13, %14, %15, %16};"
+                     ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                     "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+                     "r"(r[15]) : "memory");
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                     ::"r"(taddr + 16), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+                     "r"(r[22]), "r"(r[23]) : "memory");
+    } else
         tmem_st32_nowait(taddr, r);
     tmem_st_wait();
 }
@@ -182,21 +210,26 @@ __device__ __forceinline__ float2 of_codes(uint32_t c) {
     return __half22float2(
         __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c), __NV_E4M3)));
 }
-// ... and the numbers' parts: c[i] holds the codes of part i of both.
-template <int PARTS>
+// The numbers' parts, each remainder times 32 (e4m3), 2^11 (fp16) or 2^8 (bf16): c[i] holds the codes, or the 16-bit
+// numbers, of part i of both.
+template <typename T, bool E8, int PARTS>
 __device__ __forceinline__ void split_parts(float x, float y, uint32_t (&c)[PARTS]) {
+    constexpr float up = Cfg<T, E8, 64, 1>::kUp;
 #pragma unroll
     for (int i = 0; i < PARTS; ++i) {
-        c[i] = to_codes(x, y);
+        c[i] = E8 ? to_codes(x, y) : dt_traits<T>::pack2(x, y);
         if (i + 1 < PARTS) {
-            const float2 f = of_codes(c[i]);
-            x = (x - f.x) * 32.f;
-            y = (y - f.y) * 32.f;
+            const float2 f = E8 ? of_codes(c[i]) : dt_traits<T>::unpack2(c[i]);
+            x = (x - f.x) * up;
+            y = (y - f.y) * up;
         }
     }
 }
 __device__ __forceinline__ void st_byte(uint32_t at, uint32_t v) {
     asm volatile("st.shared.b8 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_half(uint32_t at, uint32_t v) {
+    asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(static_cast<uint16_t>(v)) : "memory");
 }
 
 // 4 bytes to shared memory, with nothing waited for ...
@@ -456,7 +489,7 @@ template <typename T, bool E8, int D, int GP>
 __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& tm, Tiles tiles,
                                            uint8_t* smem, uint32_t tmem, int warp, int lane) {
     using C = Cfg<T, E8, D, GP>;
-    constexpr int kSlots = C::kSlots, N = C::kN;
+    constexpr int kSlots = C::kSlots, NS = C::kNS, NO = C::kNO;
     const uint32_t sKV = smem_u32(smem);
     const uint32_t sQ = sKV + C::kOffQ, sP = sKV + C::kOffP;
     const Bars<kSlots> bar{sKV + C::kOffBar};
@@ -536,14 +569,14 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
     } else if (warp == 1) {
         if (lane == 0) {
             constexpr uint32_t fmt = E8 ? 0 : dt_traits<T>::mma_fmt;  // e4m3 is 0 too
-            constexpr uint32_t idesc_s = make_idesc_f16(fmt, kTK, N, false);
+            constexpr uint32_t idesc_s = make_idesc_f16(fmt, kTK, NS, false);
             // A MN-major
-            constexpr uint32_t idesc_o = make_idesc_f16(fmt, D == 64 ? 64 : 128, N, false) | (1u << 15);
-            constexpr uint32_t idesc_o2 = make_idesc_f16(fmt, 64, N, false) | (1u << 15);
+            constexpr uint32_t idesc_o = make_idesc_f16(fmt, D == 64 ? 64 : 128, NO, false) | (1u << 15);
+            constexpr uint32_t idesc_o2 = make_idesc_f16(fmt, 64, NO, false) | (1u << 15);
             constexpr uint32_t kSlotStep = C::kTile >> 4;
             // offsets in 16 bytes of the narrow slices, and of V's second block of rows
             constexpr uint32_t kNarrowK = (C::kWide * kTK * 128) >> 4;
-            constexpr uint32_t kNarrowQ = (C::kWide * C::kRows * 128) >> 4;
+            constexpr uint32_t kNarrowQ = (C::kWide * C::kQRows * 128) >> 4;
             constexpr uint32_t kSecond = (D > 128 ? (E8 ? 1 : 2) * kTK * 128 : 0) >> 4;
             const uint64_t dk0 = make_sdesc_sw128(sKV, 16, 1024), dk0n = make_sdesc_sw64(sKV, 16, 512);
             const uint64_t dv0 = make_sdesc_sw128(sKV, kTK * 128, 1024);
@@ -569,10 +602,10 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
                 for (int ks = 0; ks < D * C::kElem / 32; ++ks) {
                     const uint32_t in = (ks % 4) * 2;
                     if (ks / 4 < C::kWide)
-                        mma(tmem + N * (x.t & 1), desc_at(dk0, k + (ks / 4) * ((kTK * 128) >> 4) + in),
-                            desc_at(dq0, q + (ks / 4) * ((C::kRows * 128) >> 4) + in), idesc_s, ks > 0 ? 1u : 0u);
+                        mma(tmem + NS * (x.t & 1), desc_at(dk0, k + (ks / 4) * ((kTK * 128) >> 4) + in),
+                            desc_at(dq0, q + (ks / 4) * ((C::kQRows * 128) >> 4) + in), idesc_s, ks > 0 ? 1u : 0u);
                     else
-                        mma(tmem + N * (x.t & 1), desc_at(dk0n, k + kNarrowK + in),
+                        mma(tmem + NS * (x.t & 1), desc_at(dk0n, k + kNarrowK + in),
                             desc_at(dq0n, q + kNarrowQ + in), idesc_s, ks > 0 ? 1u : 0u);
                 }
                 tc_commit(bar.s_full(x.t & 1));
@@ -591,12 +624,12 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
                 tc_fence_after();
                 const int sl = (2 * x.t + 1) % kSlots;
                 const uint32_t v = sl * kSlotStep, p = (x.t & 1) * (C::kPBytes >> 4);
-                const uint32_t o = tmem + C::kColO + C::kBlocks * N * (x.it & 1);
+                const uint32_t o = tmem + C::kColO + C::kBlocks * NO * (x.it & 1);
                 const int steps = (min(x.keys, kTK) + C::kStepKeys - 1) / C::kStepKeys;
 #pragma unroll
                 for (int ks = 0; ks < kTK / C::kStepKeys; ++ks) {
                     if (ks >= steps) continue;
-                    const uint64_t dp = desc_at(dp0, p + (ks / 4) * ((C::kRows * 128) >> 4) + (ks % 4) * 2);
+                    const uint64_t dp = desc_at(dp0, p + (ks / 4) * ((C::kPRows * 128) >> 4) + (ks % 4) * 2);
                     const uint32_t acc = !x.first || ks > 0 ? 1u : 0u;
                     constexpr uint32_t kStep = (C::kStepKeys * 128) >> 4;
                     if (C::kWide > 0)
@@ -605,9 +638,9 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
                         mma(o, desc_at(dk0n, v + ks * (kStep / 2)), dp, idesc_o, acc);
                     if (C::kBlocks > 1) {
                         if (C::kNarrow)
-                            mma(o + N, desc_at(dk0n, v + kSecond + ks * (kStep / 2)), dp, idesc_o2, acc);
+                            mma(o + NO, desc_at(dk0n, v + kSecond + ks * (kStep / 2)), dp, idesc_o2, acc);
                         else
-                            mma(o + N, desc_at(dv0, v + kSecond + ks * kStep), dp, idesc_o2, acc);
+                            mma(o + NO, desc_at(dv0, v + kSecond + ks * kStep), dp, idesc_o2, acc);
                     }
                 }
                 tc_commit(bar.pv_done(x.t & 1));
@@ -698,9 +731,9 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
                 for (int i = 0; i < kPairs; ++i) {
                     const int col = 2 * (lane + 32 * i) * C::kElem;  // byte of the row
                     if (2 * (lane + 32 * i) >= D) continue;
-                    uint32_t c8[C::kParts];
+                    uint32_t c8[C::kQParts];
                     if (E8) {
-                        split_parts<C::kParts>(f[h][i].x * down, f[h][i].y * down, c8);
+                        split_parts<T, true>(f[h][i].x * down, f[h][i].y * down, c8);
                         // an infinity is no code: a NaN, as its scores' softmax is
                         if (isinf(f[h][i].x)) c8[0] |= 0x7fu;
                         if (isinf(f[h][i].y)) c8[0] |= 0x7f00u;
@@ -708,13 +741,13 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
                         c8[0] = dt_traits<T>::pack2(f[h][i].x, f[h][i].y);
                     }
 #pragma unroll
-                    for (int s = 0; s < C::kParts; ++s) {
+                    for (int s = 0; s < C::kQParts; ++s) {
                         const int n = s * GP + h;
                         uint32_t at;
                         if (col < 128 * C::kWide)
-                            at = dst + (col / 128) * C::kRows * 128 + n * 128 + ((col & 127) ^ ((n & 7) << 4));
+                            at = dst + (col / 128) * C::kQRows * 128 + n * 128 + ((col & 127) ^ ((n & 7) << 4));
                         else
-                            at = dst + C::kWide * C::kRows * 128 + n * 64 +
+                            at = dst + C::kWide * C::kQRows * 128 + n * 64 +
                                  ((col - 128 * C::kWide) ^ (((n >> 1) & 3) << 4));
                         if (E8)
                             asm volatile("st.shared.b16 [%0], %1;" ::"r"(at),
@@ -744,10 +777,10 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
         auto read_out = [&]() -> bool {
             if (!mbar_wait(bar.pv_done(pend_t & 1), (pend_t >> 1) & 1, a.err)) return false;
             tc_fence_after();
-            uint32_t o[C::kBlocks][C::kLd];
+            uint32_t o[C::kBlocks][C::kLdO];
 #pragma unroll
             for (int mb = 0; mb < C::kBlocks; ++mb)
-                ld_cols<C::kLd>(tO + N * (C::kBlocks * pend_buf + mb), o[mb]);
+                ld_cols<C::kLdO>(tO + NO * (C::kBlocks * pend_buf + mb), o[mb]);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar.o_free(pend_buf));
@@ -768,10 +801,9 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
                 if ((!half || lane < 16) && dim < D) {
 #pragma unroll
                     for (int h = 0; h < GP; ++h) {
-                        float v = __uint_as_float(o[mb][h]);
-                        if (C::kParts > 1) v = fmaf(__uint_as_float(o[mb][GP + h]), 1.f / 32, v);
-                        if (C::kParts > 2)
-                            v = fmaf(__uint_as_float(o[mb][(C::kParts - 1) * GP + h]), 1.f / 1024, v);
+                        float v = fmaf(__uint_as_float(o[mb][GP + h]), 1.f / C::kUp, __uint_as_float(o[mb][h]));
+                        if (C::kPParts > 2)
+                            v = fmaf(__uint_as_float(o[mb][(C::kPParts - 1) * GP + h]), 1.f / (C::kUp * C::kUp), v);
                         if (!a.direct) {
                             a.po[(pend_rec * GP + h) * D + dim] = v * (1.f / C::kTop);
                         } else if (h < pend_heads) {
@@ -813,8 +845,8 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
                     break;
                 }
                 tc_fence_after();
-                uint32_t r[C::kLd];
-                ld_cols<C::kLd>(tS + N * (t & 1), r);
+                uint32_t r[C::kLdS];
+                ld_cols<C::kLdS>(tS + NS * (t & 1), r);
                 const float ks = scales[(t & 7) * 16 + key / 16];
                 const float vs = scales[(t & 7) * 16 + 8 + key / 16];
                 tc_fence_before();
@@ -830,9 +862,9 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
 #pragma unroll
                 for (int h = 0; h < GP; ++h) {
                     float v = __uint_as_float(r[h]);
-                    if (C::kParts > 1) v = fmaf(__uint_as_float(r[GP + h]), 1.f / 32, v);
-                    if (C::kParts > 2)
-                        v = fmaf(__uint_as_float(r[(C::kParts - 1) * GP + h]), 1.f / 1024, v);
+                    if (C::kQParts > 1) v = fmaf(__uint_as_float(r[GP + h]), 1.f / 32, v);
+                    if (C::kQParts > 2)
+                        v = fmaf(__uint_as_float(r[(C::kQParts - 1) * GP + h]), 1.f / 1024, v);
                     s[h] = seen ? fmaf(v, E8 ? mul[h] * ks : mul[h], slope[h] * back) : -INFINITY;
                     const float w = warp_max(s[h] + shift);
                     if (lane == h) rm[h * 4 + quarter] = w;
@@ -870,30 +902,24 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
                     l[h] = fmaf(l[h], corr[h], p[h]);
                 }
                 const uint32_t p_buf = sP + (t & 1) * C::kPBytes;
-                if constexpr (E8) {
-                    const float top = vs * C::kTop;
-                    constexpr int kStep = GP > 1 ? 2 : 1;
+                const float top = E8 ? vs * C::kTop : C::kTop;
+                constexpr int kStep = GP > 1 ? 2 : 1;
 #pragma unroll
-                    for (int h = 0; h < GP; h += kStep) {
-                        uint32_t c8[C::kParts];
-                        split_parts<C::kParts>(p[h] * top, GP > 1 ? p[h + kStep - 1] * top : 0.f, c8);
+                for (int h = 0; h < GP; h += kStep) {
+                    uint32_t c[C::kPParts];
+                    split_parts<T, E8>(p[h] * top, GP > 1 ? p[h + kStep - 1] * top : 0.f, c);
 #pragma unroll
-                        for (int q = 0; q < C::kParts; ++q)
+                    for (int q = 0; q < C::kPParts; ++q)
 #pragma unroll
-                            for (int e = 0; e < kStep; ++e) {
-                                const int n = q * GP + h + e;
-                                st_byte(p_buf + n * 128 + (key ^ ((n & 7) << 4)), c8[q] >> (8 * e));
-                            }
-                    }
-                } else {
-                    const uint32_t p_row = p_buf + (key / 64) * C::kRows * 128;
-#pragma unroll
-                    for (int h = 0; h < GP; ++h) {
-                        const uint32_t at =
-                            p_row + h * 128 + (((key & 63) * 2) ^ (static_cast<uint32_t>(h & 7) << 4));
-                        const uint16_t bits = static_cast<uint16_t>(dt_traits<T>::pack2(p[h], 0.f));
-                        asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(bits) : "memory");
-                    }
+                        for (int e = 0; e < kStep; ++e) {
+                            const int n = q * GP + h + e;
+                            if constexpr (E8)
+                                st_byte(p_buf + n * 128 + (key ^ ((n & 7) << 4)), c[q] >> (8 * e));
+                            else
+                                st_half(p_buf + (key / 64) * C::kPRows * 128 + n * 128 +
+                                            (((key & 63) * 2) ^ ((n & 7) << 4)),
+                                        c[q] >> (16 * e));
+                        }
                 }
                 if (keys < kTK && (keys & 15) && quarter == 0) {
                     // values behind the tile's end, up to the next copied box
@@ -921,13 +947,13 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
                     tc_fence_after();
 #pragma unroll
                     for (int mb = 0; mb < C::kBlocks; ++mb) {
-                        uint32_t o[C::kLd];
-                        const uint32_t col = tO + N * (C::kBlocks * (c.it & 1) + mb);
-                        ld_cols<C::kLd>(col, o);
+                        uint32_t o[C::kLdO];
+                        const uint32_t col = tO + NO * (C::kBlocks * (c.it & 1) + mb);
+                        ld_cols<C::kLdO>(col, o);
 #pragma unroll
-                        for (int n = 0; n < C::kUsed; ++n)
+                        for (int n = 0; n < C::kPUsed; ++n)
                             o[n] = __float_as_uint(__uint_as_float(o[n]) * corr[n % GP]);
-                        st_cols<C::kLd>(col, o);
+                        st_cols<C::kLdO>(col, o);
                     }
                     tc_fence_before();
                 }

@@ -414,8 +414,8 @@ typedef struct {
  * GQA: kv head = h / (n_heads / n_kv_heads), any ratio; above 8 the cache is read
  * once for every 8 query heads of a kv head (16 over a 16-bit cache with head_dim 128
  * or 160, where there are two launches). Sums and statistics are in 32 bits; softmax weights enter the product
- * with V rounded: to dt over a 16-bit cache; over e4m3, to sums of two (bf16) or three
- * (fp16) e4m3 numbers, at most 2^-9 or 2^-14 off, relative, or 2^-21 and 2^-26 of the largest.
+ * with V as sums of numbers of its operands' type: two of dt over a 16-bit cache, at most 2^-16 (bf16) or 2^-22
+ * (fp16) off, relative; three e4m3 numbers over e4m3, at most 2^-14, or, absolute, 2^-26 of the largest weight times scale.
  * Two launches. The workspace holds partial results, at least
  * blk_attn_decode_paged_workspace_size bytes, 16-byte aligned; calls whose
  * kernels overlap on the GPU need a workspace each. Where block_table has room for a
