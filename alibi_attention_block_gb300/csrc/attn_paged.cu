@@ -1,6 +1,7 @@
 // K8 host side and merge: one decode step of attention over a paged cache. The kernel
 // (attn_paged.cuh) leaves a partial result for each CTA's stay in a unit; the merge
-// joins them: o = sum_i w_i O_i / sum_i w_i l_i, w_i = 2^(m_i - max m).
+// joins them: o = sum_i w_i O_i / sum_i w_i l_i, w_i = 2^(m_i - max m) (as the square of 2^((m_i - max m) / 2): with
+// 8 bits w_i alone may be too small a number, where l_i is large).
 #include <cmath>
 
 #include "attn_paged.h"
@@ -82,15 +83,16 @@ __device__ __forceinline__ void join(const MergeArgs& a, const Records& r, int c
 #pragma unroll
         for (int i = 0; i < 4; ++i) mn = fmaxf(mn, ml[i].x);
         const float base = mn == -INFINITY ? 0.f : mn;
-        const float keep = m == -INFINITY ? 0.f : exp2f(m - mn);
+        const float keep = m == -INFINITY ? 0.f : exp2f(0.5f * (m - mn));
         m = mn;
-        l *= keep;
+        l = l * keep * keep;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= keep;
+        for (int e = 0; e < 8; ++e) f[e] *= keep * keep;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float w = ml[i].x == -INFINITY && ml[i].y == 0.f ? 0.f : exp2f(ml[i].x - base);
-            l = fmaf(w, ml[i].y, l);
+            const float half = ml[i].x == -INFINITY && ml[i].y == 0.f ? 0.f : exp2f(0.5f * (ml[i].x - base));
+            const float w = half * half;
+            l = fmaf(half, half * ml[i].y, l);
             const float v[8] = {x[i].x, x[i].y, x[i].z, x[i].w, y[i].x, y[i].y, y[i].z, y[i].w};
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] = fmaf(w, v[e], f[e]);
@@ -149,9 +151,9 @@ __global__ void __launch_bounds__(kRowThreads) paged_merge_row_kernel(const Merg
 #pragma unroll 4
         for (int k = 0; k < n; ++k) {
             const float2 x = ml[k];
-            const float w = x.x == -INFINITY && x.y == 0.f ? 0.f : exp2f(x.x - base);
-            l = fmaf(w, x.y, l);
-            f = fmaf(w, parts[k][c], f);
+            const float half = x.x == -INFINITY && x.y == 0.f ? 0.f : exp2f(0.5f * (x.x - base));
+            l = fmaf(half, half * x.y, l);
+            f = fmaf(half * half, parts[k][c], f);
         }
         f = l == 0.f ? 0.f : f * (1.0f / l);
         static_cast<uint16_t*>(a.o)[row * D + c] = static_cast<uint16_t>(dt_traits<T>::pack2(f, 0.f));

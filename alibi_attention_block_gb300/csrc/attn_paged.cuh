@@ -26,7 +26,11 @@
 // A page's scales are factors of its keys: that of K multiplies the score, that of V
 // the weight ahead of its rounding. So that the weight times scale stays in e4m3's range whatever the
 // scales are, the running reference that is subtracted is of score + log2(scale of V), not of the score.
-// The sum of the weights has the same reference; scales of V below 2^-40 count as 2^-40 in it.
+// The sum of the weights has the same reference, less 36 (kShift): in it the largest weight is 2^(36 - up) to 2^(37 - up) for a
+// scale of 2^up, so that at scales of up to 2^128 weights down to 2^-34 of the largest are numbers of 32 bits, and the sum of
+// 2^26 weights at 2^-60 (2^123) is one too. Scales of V below 2^-60, the least that appending sets, count as 2^-60 in it.
+// References of different pages may so be 2^188 apart with equal weights: a sum is brought from one to the other by two factors
+// of half the way, here and in the merge (what O holds at the lower one is then nothing next to the other).
 //
 // 16 bits: the operands in the storage type, a weight as the sum of two such numbers (the second one's columns are
 // there anyway too), 2^-16 off in bf16, 2^-22 in fp16 (held times 2^7, its second part times 2^11: weights down to 2^-21 of
@@ -118,6 +122,7 @@ struct Cfg {
     static_assert(2 * kNS + 2 * kBlocks * kNO <= static_cast<int>(kCols) && kCtas * kCols <= 512, "TMEM");
     // weights are at most 2^threshold times this: 2^8 in e4m3, 2^15 in fp16
     static constexpr float kTop = E8 || kF16 ? 128.f : 1.f;
+    static constexpr float kBack = E8 ? 1.f / (1ull << 36) : 1.f, kShift = E8 ? 36.f : 0.f;  // 2^-shift
     static constexpr float kThreshold = E8 ? 1.f : 8.f;  // log2 of the largest weight before a rescale
 };
 
@@ -790,7 +795,7 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
                 for (int h = 0; h < GP; ++h) {
                     const float4 w = *reinterpret_cast<const float4*>(red_sum + h * 4);
                     const float sum = (w.x + w.y) + (w.z + w.w);
-                    inv[h] = sum == 0.f ? 0.f : 1.f / (sum * C::kTop);
+                    inv[h] = sum == 0.f ? 0.f : 1.f / (sum * (C::kTop * C::kBack));
                 }
             }
 #pragma unroll
@@ -805,7 +810,7 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
                         if (C::kPParts > 2)
                             v = fmaf(__uint_as_float(o[mb][(C::kPParts - 1) * GP + h]), 1.f / (C::kUp * C::kUp), v);
                         if (!a.direct) {
-                            a.po[(pend_rec * GP + h) * D + dim] = v * (1.f / C::kTop);
+                            a.po[(pend_rec * GP + h) * D + dim] = v * (1.f / (C::kTop * C::kBack));
                         } else if (h < pend_heads) {
                             const uint16_t bits =
                                 static_cast<uint16_t>(dt_traits<T>::pack2(v * inv[h], 0.f));
@@ -856,7 +861,7 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
                 const float back = static_cast<float>(row + key - (c.len - 1));
                 // the scale of V is at most 2^up
                 const int up = static_cast<int>((__float_as_uint(vs) + 0x7fffffu) >> 23) - 127;
-                const float shift = E8 ? static_cast<float>(max(up, -40)) : 0.f;
+                const float shift = E8 ? static_cast<float>(max(up, -60)) - C::kShift : 0.f;
                 float s[GP];
                 float* rm = red_max + (t & 1) * 4 * C::kHeads;
 #pragma unroll
@@ -884,7 +889,10 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
                     const float mx = fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w));
                     corr[h] = 1.f;
                     if (mx > m[h] + C::kThreshold) {
-                        corr[h] = ex2_approx(m[h] - mx);
+                        // (in halves: references may lie further apart than the sum is small)
+                        const float half = ex2_approx(0.5f * (m[h] - mx));
+                        corr[h] = half * half;
+                        l[h] = l[h] * half * half;
                         m[h] = mx;
                         moved = true;
                     }
@@ -899,10 +907,10 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
                 for (int h = 0; h < GP; ++h) {
                     // (nothing seen so far: 0, not a NaN)
                     p[h] = ex2_approx(s[h] - (m[h] == -INFINITY ? 0.f : m[h]));
-                    l[h] = fmaf(l[h], corr[h], p[h]);
+                    l[h] += p[h];
                 }
                 const uint32_t p_buf = sP + (t & 1) * C::kPBytes;
-                const float top = E8 ? vs * C::kTop : C::kTop;
+                const float top = E8 ? vs * (C::kTop * C::kBack) : C::kTop;
                 constexpr int kStep = GP > 1 ? 2 : 1;
 #pragma unroll
                 for (int h = 0; h < GP; h += kStep) {

@@ -415,7 +415,8 @@ typedef struct {
  * once for every 8 query heads of a kv head (16 over a 16-bit cache with head_dim 128
  * or 160, where there are two launches). Sums and statistics are in 32 bits; softmax weights enter the product
  * with V as sums of numbers of its operands' type: two of dt over a 16-bit cache, at most 2^-16 (bf16) or 2^-22
- * (fp16) off, relative; three e4m3 numbers over e4m3, at most 2^-14, or, absolute, 2^-26 of the largest weight times scale.
+ * (fp16) off, relative; three e4m3 numbers over e4m3, at most 2^-14, or, absolute, 2^-26 of the largest weight times scale
+ * of V (of 2^-60 at least, for this).
  * Two launches. The workspace holds partial results, at least
  * blk_attn_decode_paged_workspace_size bytes, 16-byte aligned; calls whose
  * kernels overlap on the GPU need a workspace each. Where block_table has room for a

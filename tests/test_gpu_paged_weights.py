@@ -125,3 +125,24 @@ def test_many_small_weights(B, n, d, dt):
     bound = (PARTS[16, dt] + 2 * e + 2.0 ** -19 + ref.HALF_STEP[dt] * (1 + 2.0 ** -10)) * want
     worst = np.abs(o - want).max()
     assert worst <= bound, f"{worst / bound:.2f} of the bound"
+
+
+@pytest.mark.parametrize("d,G", [(64, 1), (128, 4), (160, 8)])
+@pytest.mark.parametrize("lo,hi", [(118, 118), (112, 119), (-59, -59), (-60, -50), (-60, 118)])
+def test_scales_at_the_ends(lo, hi, d, G):
+    """Scales of V of 2^lo to 2^hi, from page to page: those that appended bf16 values take are 2^-60 to 2^120."""
+    B, page, Hk = 6, 16, 2
+    g = torch.Generator(device="cuda")
+    g.manual_seed(d + lo)
+    lens = [300, 17, 500, 2, 129, 40]
+    k, v = ((torch.randn((200, Hk, page, d), generator=g, device="cuda") * 60).clamp(-448, 448).to(torch.float8_e4m3fn)
+            for _ in "kv")
+    ks = torch.full((200, Hk), 2.0 ** -6, device="cuda")
+    vs = torch.exp2(torch.randint(lo, hi + 1, (200, Hk), generator=g, device="cuda").double()).float()
+    q = torch.randn((B, Hk * G, d), generator=g, device="cuda").bfloat16()
+    for room in (0, 60):
+        table = torch.full((B, 32 + room), -1, dtype=torch.int32)
+        table[:, :32] = torch.arange(B * 32, dtype=torch.int32).reshape(B, 32)
+        o = blk.attn_decode_paged(q, k, v, table.cuda(), i32(lens), k_scale=ks, v_scale=vs)
+        check(o, q, k, v, ks, vs, table, lens, page, "bf16", name=f"room {room}")
+    blk.check_device_status()
