@@ -881,6 +881,8 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
                     break;
                 }
                 // the same decision in every thread
+                // (8 bits: half of the way, since references may lie further apart than a number is small)
+                constexpr float kWay = E8 ? 0.5f : 1.f;
                 float corr[GP];
                 bool moved = false;
 #pragma unroll
@@ -889,10 +891,7 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
                     const float mx = fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w));
                     corr[h] = 1.f;
                     if (mx > m[h] + C::kThreshold) {
-                        // (in halves: references may lie further apart than the sum is small)
-                        const float half = ex2_approx(0.5f * (m[h] - mx));
-                        corr[h] = half * half;
-                        l[h] = l[h] * half * half;
+                        corr[h] = ex2_approx(kWay * (m[h] - mx));
                         m[h] = mx;
                         moved = true;
                     }
@@ -907,7 +906,7 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
                 for (int h = 0; h < GP; ++h) {
                     // (nothing seen so far: 0, not a NaN)
                     p[h] = ex2_approx(s[h] - (m[h] == -INFINITY ? 0.f : m[h]));
-                    l[h] += p[h];
+                    l[h] = fmaf(E8 ? l[h] * corr[h] : l[h], corr[h], p[h]);
                 }
                 const uint32_t p_buf = sP + (t & 1) * C::kPBytes;
                 const float top = E8 ? vs * (C::kTop * C::kBack) : C::kTop;
@@ -953,6 +952,9 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
                         break;
                     }
                     tc_fence_after();
+                    if (E8)
+#pragma unroll
+                        for (int h = 0; h < GP; ++h) corr[h] *= corr[h];
 #pragma unroll
                     for (int mb = 0; mb < C::kBlocks; ++mb) {
                         uint32_t o[C::kLdO];
