@@ -1,7 +1,8 @@
 // K8 host side and merge: one decode step of attention over a paged cache. The kernel
 // (attn_paged.cuh) leaves a partial result for each CTA's stay in a unit; the merge
 // joins them: o = sum_i w_i O_i / sum_i w_i l_i, w_i = 2^(m_i - max m) (as the square of 2^((m_i - max m) / 2): with
-// 8 bits w_i alone may be too small a number, where l_i is large).
+// 8 bits w_i alone may be too small a number, where l_i is large). m_i = -inf: no key seen (l_i = 0), or each with a score of
+// -inf (l_i their number), which leaves no softmax, NaN, where no other record has a finite one.
 #include <cmath>
 
 #include "attn_paged.h"
@@ -82,15 +83,14 @@ __device__ __forceinline__ void join(const MergeArgs& a, const Records& r, int c
         float mn = m;
 #pragma unroll
         for (int i = 0; i < 4; ++i) mn = fmaxf(mn, ml[i].x);
-        const float base = mn == -INFINITY ? 0.f : mn;
-        const float keep = m == -INFINITY ? 0.f : exp2f(0.5f * (m - mn));
+        const float keep = m == mn ? 1.f : exp2f(0.5f * (m - mn));
         m = mn;
         l = l * keep * keep;
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] *= keep * keep;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float half = ml[i].x == -INFINITY && ml[i].y == 0.f ? 0.f : exp2f(0.5f * (ml[i].x - base));
+            const float half = ml[i].x == mn ? 1.f : exp2f(0.5f * (ml[i].x - mn));
             const float w = half * half;
             l = fmaf(half, half * ml[i].y, l);
             const float v[8] = {x[i].x, x[i].y, x[i].z, x[i].w, y[i].x, y[i].y, y[i].z, y[i].w};
@@ -98,6 +98,11 @@ __device__ __forceinline__ void join(const MergeArgs& a, const Records& r, int c
             for (int e = 0; e < 8; ++e) f[e] = fmaf(w, v[e], f[e]);
         }
     }
+}
+
+// What a row's sums are multiplied by: zeros where no key was seen.
+__device__ __forceinline__ float share(float m, float l) {
+    return l == 0.f ? 0.f : m == -INFINITY ? NAN : 1.0f / l;
 }
 
 // D / 8 threads per row of 8 columns each.
@@ -110,7 +115,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const MergeA
     if (threadIdx.x >= kRows * kPer || row >= a.rows) return;
     float m, l, f[8];
     join<D>(a, records_of(a, row), col, 0, 1, m, l, f);
-    const float inv = l == 0.f ? 0.f : 1.0f / l;  // no key seen: a zero row
+    const float inv = share(m, l);
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] *= inv;
     store8(static_cast<T*>(a.o) + row * D + col, f);
@@ -145,17 +150,16 @@ __global__ void __launch_bounds__(kRowThreads) paged_merge_row_kernel(const Merg
     const int n = min(r.n, kTeams);
     float top = -INFINITY;
     for (int k = 0; k < n; ++k) top = fmaxf(top, ml[k].x);
-    const float base = top == -INFINITY ? 0.f : top;
     for (int c = threadIdx.x; c < D; c += kRowThreads) {
         float l = 0.f, f = 0.f;
 #pragma unroll 4
         for (int k = 0; k < n; ++k) {
             const float2 x = ml[k];
-            const float half = x.x == -INFINITY && x.y == 0.f ? 0.f : exp2f(0.5f * (x.x - base));
+            const float half = x.x == top ? 1.f : exp2f(0.5f * (x.x - top));
             l = fmaf(half, half * x.y, l);
             f = fmaf(half * half, parts[k][c], f);
         }
-        f = l == 0.f ? 0.f : f * (1.0f / l);
+        f *= share(top, l);
         static_cast<uint16_t*>(a.o)[row * D + c] = static_cast<uint16_t>(dt_traits<T>::pack2(f, 0.f));
     }
 }

@@ -824,6 +824,7 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
         };
         while (ok && c.valid) {
             float m[GP], l[GP], slope[GP], mul[GP];
+            bool any = false;  // 16 bits: a key of the segment seen
             if (!(ok = mbar_wait(bar.q_full(c.it & 1), (c.it >> 1) & 1, a.err))) break;
             const int g = c.u / a.groups, h0 = g * a.G + (c.u - g * a.groups) * GP;
 #pragma unroll
@@ -858,6 +859,7 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar.s_free(t & 1));
                 const bool seen = key < keys && !(ks < 0.f);
+                if (!E8) any = any || seen;
                 const float back = static_cast<float>(row + key - (c.len - 1));
                 // the scale of V is at most 2^up
                 const int up = static_cast<int>((__float_as_uint(vs) + 0x7fffffu) >> 23) - 127;
@@ -980,6 +982,9 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
 #pragma unroll
             for (int h = 0; h < GP; ++h) {
                 float v = l[h];
+                // keys seen, each with a score of -inf: no softmax (0 / 0) unless another segment has a finite one (over e4m3
+                // such a score is NaN: the queries' operand has no infinity, and codes are none)
+                if (!E8 && any && m[h] == -INFINITY && v == 0.f) v = a.direct ? NAN : 1.f;
 #pragma unroll
                 for (int x = 16; x > 0; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
                 if (lane == h) red_sum[((c.it & 1) * C::kHeads + h) * 4 + quarter] = v;

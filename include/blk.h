@@ -407,7 +407,8 @@ typedef struct {
  *     lens[b] - 1
  *   the cache, its scales, block_table and lens as above (scales finite and >= 0; any, not powers of two only).
  *     lens is clamped to [0, max_pages * page_tokens]; 0: a zero row. Keys in a
- *     page outside the pool take no part (a row without any key is zero).
+ *     page outside the pool take no part (a row without any key is zero; one whose
+ *     keys all have a score of -inf is NaN).
  *     Pages may be shared by sequences, or occur twice.
  *   alibi_slopes: as for blk_attn_prefill
  *   o [batch, n_heads, head_dim], contiguous

@@ -146,3 +146,43 @@ def test_scales_at_the_ends(lo, hi, d, G):
         o = blk.attn_decode_paged(q, k, v, table.cuda(), i32(lens), k_scale=ks, v_scale=vs)
         check(o, q, k, v, ks, vs, table, lens, page, "bf16", name=f"room {room}")
     blk.check_device_status()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("d,G", [(64, 1), (128, 4), (128, 16), (160, 8)])
+@pytest.mark.parametrize("room,times", [(0, 1), (200, 1), (200, 90)])
+def test_scores_of_minus_infinity(room, times, d, G, dt):
+    """Seen keys whose scores are all -inf leave no softmax: NaN, as the definition's 0 / 0; with a finite one beside
+    them they weigh nothing; without any seen key the row is zero. 16 bits, several of a CTA's ranges or one;
+    the batch many times over (few rows and many are joined differently)."""
+    page, Hk, t = 16, 2, ref.DTYPES[dt]
+    B, cols = 8, 32
+    g = torch.Generator(device="cuda")
+    g.manual_seed(d + G)
+    k, v = (torch.randn((B * cols, Hk, page, d), generator=g, device="cuda").to(t) for _ in "kv")
+    q = torch.randn((B, Hk * G, d), generator=g, device="cuda").to(t)
+    lens = [500, 400, 512, 512, 300, 300, 0, 100]
+    table = torch.full((B, cols + room), -1, dtype=torch.int32)
+    table[:, :cols] = torch.arange(B * cols, dtype=torch.int32).reshape(B, cols)
+    rows = k.view(B, cols, Hk, page, d)
+    q[:, :, 0] = 1
+    q[0, :, 0] = float("inf")
+    rows[0, :, :, :, 0] = -1                    # an infinite query against keys of the other sign
+    rows[1, :, :, :, 0] = -float("inf")         # infinite keys, all of them
+    rows[2, :16, :, :, 0] = -float("inf")       # the oldest 256
+    rows[3, 16:, :, :, 0] = -float("inf")       # the newest 256
+    table[4] = 2 ** 30                          # no page is there
+    table[5, 3:] = -1                           # those that are there have infinite keys
+    rows[5, :, :, :, 0] = -float("inf")
+    rows[7, :, :, :, 0] = float("inf")          # +inf - inf: NaN
+    o = f64(blk.attn_decode_paged(q.repeat(times, 1, 1), k, v, table.repeat(times, 1).cuda(), i32(lens * times)).float())
+    o = o.reshape(times, B, Hk * G, d)
+    blk.check_device_status()
+    for b in (0, 1, 5, 7):
+        assert np.isnan(o[:, b]).all(), f"row {b}"
+    assert not o[:, 4].any() and not o[:, 6].any()
+    for b, part in ((2, slice(16, 32)), (3, slice(0, 16))):
+        kr, vr = (f64(x.view(B, cols, Hk, page, d)[b, part].transpose(0, 1).reshape(Hk, 256, d).float()) for x in (k, v))
+        want, mag, p = ref.decode(f64(q[b].float()), kr, vr, np.ones(256, bool))
+        bound = bound_of(f64(q[b].float()), kr, vr, None, want, mag, p, dt, 16, d ** -0.5)
+        assert (np.abs(o[:, b] - want) <= bound).all(), f"row {b}"
