@@ -677,6 +677,8 @@ extern "C" blk_status blk_kv_append_paged(const blk_append_desc* d, const blk_ro
                     "strides must be multiples of 8 elements");
         REQUIRE(i > 1 || strides[i][1] < (int64_t(1) << 24), "token strides of k and v must be below 2^24");
     }
+    REQUIRE(!q || places_apart(d->n_heads, d->tokens, d->q_out_head_stride, d->q_out_token_stride, a.c.d),
+            "an output's strides make it overlap itself");
     REQUIRE(!q || q != q_out || (strides[2][0] == strides[3][0] && strides[2][1] == strides[3][1]),
             "an output in place has the input's strides");
     for (int i = 0; i < 3; ++i) {

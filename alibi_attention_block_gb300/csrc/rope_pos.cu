@@ -153,6 +153,9 @@ blk_status blk_rope_positions(const blk_rope_pos_desc* d, const blk_rope_plan* p
             REQUIRE(strides[i][j] >= 0 && strides[i][j] % 8 == 0 && strides[i][j] <= (int64_t(1) << 40),
                     "strides must be multiples of 8 elements");
     }
+    REQUIRE(places_apart(d->n_heads, d->tokens, d->q_out_head_stride, d->q_out_token_stride, d->head_dim) &&
+                (!k || places_apart(d->n_k_heads, d->tokens, d->k_out_head_stride, d->k_out_token_stride, d->head_dim)),
+            "an output's strides make it overlap itself");
     RopePosArgs a{};
     a.turn.plan = *plan;
     a.turn.inverse = d->inverse;

@@ -172,6 +172,16 @@ struct Angles {
 // The widest pieces that a span and a head allow.
 inline int turn_width(int pairs) { return pairs % 8 == 0 ? 8 : pairs % 4 == 0 ? 4 : 1; }
 
+// Whether the heads and tokens of an output [heads][tokens][d] each have a place of their own: the shorter
+// stride holds a head, the longer one all that the shorter one reaches.
+inline bool places_apart(int64_t heads, int64_t tokens, int64_t head_stride, int64_t token_stride, int64_t d) {
+    if (heads <= 1) return tokens <= 1 || token_stride >= d;
+    if (tokens <= 1) return head_stride >= d;
+    const bool inner_heads = head_stride < token_stride;
+    const int64_t inner = inner_heads ? head_stride : token_stride, outer = inner_heads ? token_stride : head_stride;
+    return inner >= d && (outer - d) / inner >= (inner_heads ? heads : tokens) - 1;
+}
+
 // blk_rope_plan_init fills `check` with this: a call refuses a plan that it did not make.
 constexpr int32_t kPlanMade = 0x524f5045;
 inline bool plan_made(const blk_rope_plan* p, int64_t head_dim) {

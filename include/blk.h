@@ -319,7 +319,8 @@ typedef struct {
     int64_t head_dim;             /* a multiple of 16, at most 256, at least the plan's span */
     int32_t inverse;              /* 1: turn back (the transposed matrix, so the gradient's call) */
     /* elements from head to head and from token to token, multiples of 8; a
-     * head's dims are contiguous */
+     * head's dims are contiguous. Inputs may have any (0: one for all); an output's shorter
+     * one is at least head_dim, its longer one at least what the shorter one spans */
     int64_t q_head_stride, q_token_stride, q_out_head_stride, q_out_token_stride;
     int64_t k_head_stride, k_token_stride, k_out_head_stride, k_out_token_stride;
 } blk_rope_pos_desc;
