@@ -70,6 +70,9 @@ namespace {
 constexpr int kThreads = 224;
 constexpr int kTK = 128;
 constexpr float kLog2e = 1.4426950408889634f;
+// The queries' warp waits for a buffer as long as its segment takes, up to 2^19 tiles. A tile takes 3.1 us where all CTAs
+// share the memory's 6.5 TB/s (16 bits, head_dim 128: 64 KB, 304 CTAs), so 1.6 s, which is near the limit of the other waits.
+constexpr unsigned long long kTileLimitNs = 20000;
 
 template <typename T, bool E8, int D, int GP>
 struct Cfg {
@@ -695,6 +698,7 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
         // queries: rows of the operand are part * GP + head
         Segments& c = tiles.c;
         constexpr int kPairs = (D + 63) / 64;  // of neighbouring dims, per lane
+        unsigned long long tiles_of[2] = {0, 0};  // the buffers' segments
         while (ok && c.valid) {
             const int qb = c.it & 1;
             const int g = c.u / a.groups, h0 = g * a.G + (c.u - g * a.groups) * GP;
@@ -711,8 +715,10 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
                                   : make_float2(0.f, 0.f);
                 }
             }
-            ok = __all_sync(0xffffffffu, mbar_wait(bar.q_empty(qb), ((c.it >> 1) & 1) ^ 1u, a.err));
+            ok = __all_sync(0xffffffffu, mbar_wait_inl(bar.q_empty(qb), ((c.it >> 1) & 1) ^ 1u, a.err,
+                                                       kWaitLimitNs + tiles_of[qb] * kTileLimitNs));
             if (!ok) break;
+            tiles_of[qb] = c.n;
             const uint32_t dst = sQ + qb * C::kQBytes;
 #pragma unroll
             for (int h = 0; h < GP; ++h) {

@@ -16,8 +16,8 @@ namespace blk {
 enum : unsigned { DEV_ERR_NONE = 0u, DEV_ERR_TIMEOUT = 1u };
 
 // Upper bound on any single wait inside a kernel. Legitimate waits in these
-// kernels last microseconds; a wait this long means a lost arrival. (One may last
-// longer and has a limit that grows: idle_limit_ns in attn_plan.cuh.)
+// kernels last microseconds; a wait this long means a lost arrival. (Two may last
+// longer and have limits that grow: idle_limit_ns in attn_plan.cuh, kTileLimitNs in attn_paged.cuh.)
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;
 
 __device__ __forceinline__ uint64_t globaltimer_ns() {

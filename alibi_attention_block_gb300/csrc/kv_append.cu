@@ -592,8 +592,7 @@ blk_status check_paged_desc(const blk_paged_desc* d) {
             "batch or max_pages out of range");
     if (d->page_tokens != 16 && d->page_tokens != 32 && d->page_tokens != 64 && d->page_tokens != 128)
         return report_error_status(BLK_EUNSUPPORTED, "page_tokens must be 16, 32, 64 or 128");
-    // (a decode step's block that has one unit to itself waits for its queries' next turn as long as
-    // its tiles take, about 0.7 s at this length; waits give up after 2 s)
+    // (a unit's tiles are then 2^19 at most, by which attn_paged.cuh counts and sets a wait's limit)
     REQUIRE(d->max_pages * d->page_tokens <= (int64_t(1) << 26), "max_pages * page_tokens out of range");
     REQUIRE(d->n_kv_heads >= 1 && d->n_kv_heads <= 4096, "n_kv_heads out of range");
     if (d->head_dim < 16 || d->head_dim % 16 != 0 || d->head_dim > 256)
