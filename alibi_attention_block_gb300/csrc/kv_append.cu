@@ -201,10 +201,11 @@ __device__ __forceinline__ void turn_queries(const AppendArgs& a, const ItemRows
 // table) is a chain of dependent loads, which its teams and heads share: with a block of one warp for
 // each page and head, 5713 tokens of 32 x 64 heads took 47 us, with teams 34, and 24.5 with the steps
 // below.
-// ROUNDS: for pages of more values than 512 threads hold: 256 read the rows twice (a variant of its own,
+// ROUNDS (8 bits): for pages of more values than 512 threads hold: 256 read the rows twice (a variant of its own,
 // since its registers would be the other's spills).
 template <typename T, bool E8, int VP, int IT, bool ROUNDS>
 __global__ void __launch_bounds__(IT * VP > 8 ? 768 : 1024) kv_append_kernel(const __grid_constant__ AppendArgs a) {
+    static_assert(E8 || !ROUNDS, "16-bit items fit a block");
     __shared__ float most[2][32];
     extern __shared__ float4 angles[];
     __shared__ uint64_t plan[kMaxRotaryPairs];
@@ -401,49 +402,40 @@ __global__ void __launch_bounds__(IT * VP > 8 ? 768 : 1024) kv_append_kernel(con
             }
             return 1.0f / now;
         };
-        if (ROUNDS) {
+        if constexpr (ROUNDS) {
             // the largest first, then the rows again (from the L2 cache), turned again
             for (int s = s0; s < s1; s += a.teams) {
                 float v[IT][2][VP];
                 bool in[IT];
-                float inv = 1.f;
-                if constexpr (E8) {
-                    const float held = in_page > 0 ? *scale : 0.f;
-                    float top = 0.f;
-                    for (int finite = 0; finite < 2; ++finite) {
-                        for (int c = 0; c < chunks; ++c) {
-                            rounds(c, v, in);
+                const float held = in_page > 0 ? *scale : 0.f;
+                float top = 0.f;
+                for (int finite = 0; finite < 2; ++finite) {
+                    for (int c = 0; c < chunks; ++c) {
+                        rounds(c, v, in);
 #pragma unroll
-                            for (int i = 0; i < IT; ++i)
+                        for (int i = 0; i < IT; ++i)
 #pragma unroll
-                                for (int e = 0; e < VP; ++e)
-                                    top = finite ? fmaxf(top, fmaxf(if_finite(v[i][0][e]), if_finite(v[i][1][e])))
-                                                 : max_abs(top, v[i][0][e], v[i][1][e]);
-                        }
-                        top = of_team(top);
-                        if (top < INFINITY) break;
-                        top = 0.f;
+                            for (int e = 0; e < VP; ++e)
+                                top = finite ? fmaxf(top, fmaxf(if_finite(v[i][0][e]), if_finite(v[i][1][e])))
+                                             : max_abs(top, v[i][0][e], v[i][1][e]);
                     }
-                    inv = set_scale(top, held);
+                    top = of_team(top);
+                    if (top < INFINITY) break;
+                    top = 0.f;
                 }
+                const float inv = set_scale(top, held);
                 for (int c = 0; c < chunks; ++c) {
                     rounds(c, v, in);
 #pragma unroll
                     for (int i = 0; i < IT; ++i) {
                         if (!in[i]) continue;
                         const int at_row = (place + (c * IT + i) * a.kv_rows) * d;
-                        if constexpr (E8) {
-                            store_codes<VP>(codes + at_row + at.a, v[i][0], inv);
-                            store_codes<VP>(codes + at_row + at.b, v[i][1], inv);
-                        } else {
-                            store_piece(cache + at_row + at.a, v[i][0]);
-                            store_piece(cache + at_row + at.b, v[i][1]);
-                        }
+                        store_codes<VP>(codes + at_row + at.a, v[i][0], inv);
+                        store_codes<VP>(codes + at_row + at.b, v[i][1], inv);
                     }
                 }
                 x += a.head_hop[kValues];
                 codes += a.cache_hop;
-                cache += a.cache_hop;
                 scale += a.teams;
             }
             return;
@@ -527,8 +519,10 @@ cudaError_t launch_append(AppendArgs& a, int sms, cudaStream_t s) {
     const int units = a.c.d / (2 * VP);
     // An item of keys and values is a page, whose largest value is one; in 16 bits at most 32 tokens
     // (16 prompts of 994 tokens, 16 x 128, pages of 128: 76 us with items of a page, 64 with these)
-    a.kv_log2 = E8 ? a.c.page_log2 : std::min(a.c.page_log2, 5);
+    constexpr int kLog2 = 5;
+    a.kv_log2 = E8 ? a.c.page_log2 : std::min(a.c.page_log2, kLog2);
     a.team = (units * (((1 << a.kv_log2) + IT - 1) / IT) + 31) / 32 * 32;
+    static_assert(E8 || 256 / (2 * VP) * (((1 << kLog2) + IT - 1) / IT) <= 512, "16-bit items are not read in rounds");
     const bool rounds = a.team > 512;
     if (rounds) a.team = 256;
     const int teams = a.team >= 256 ? 1 : 256 / a.team, threads = teams * a.team;
@@ -564,8 +558,9 @@ cudaError_t launch_append(AppendArgs& a, int sms, cudaStream_t s) {
     if (all > 0x7fffffff) return cudaErrorInvalidConfiguration;
     a.kv_items = static_cast<unsigned>(kv_items);
     a.q_items = static_cast<unsigned>(q_items);
-    return rounds ? launch_variant<T, E8, VP, IT, E8>(a, static_cast<unsigned>(all), threads, s)
-                  : launch_variant<T, E8, VP, IT, false>(a, static_cast<unsigned>(all), threads, s);
+    if constexpr (E8)
+        if (rounds) return launch_variant<T, E8, VP, IT, true>(a, static_cast<unsigned>(all), threads, s);
+    return launch_variant<T, E8, VP, IT, false>(a, static_cast<unsigned>(all), threads, s);
 }
 template <typename T, bool E8>
 cudaError_t launch_append_w(AppendArgs& a, int sms, cudaStream_t s) {
