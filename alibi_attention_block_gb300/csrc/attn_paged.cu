@@ -205,11 +205,22 @@ blk_status check_desc(const blk_decode_paged_desc* d) {
     return BLK_OK;
 }
 
-// Whether a sequence's tiles are so few that a CTA takes each unit whole.
-constexpr int64_t kDirectTiles = 4;
-bool is_direct(const blk_paged_desc& c) {
+// Whether a sequence's tiles, and the units (of eight heads), are so few that a CTA takes each unit whole: 512 keys, and
+// 256 units for each CTA that an SM holds (Cfg::kCtas), not much over one round of CTAs. Above that a CTA's start for every unit, and
+// units of unequal length, cost more than the second launch. One launch and two, in us, bf16 (units: of up to 100 keys, of up to 500):
+//   16/16 x 64, e4m3 (4):     512: 6.7, 9.8 and 9.9, 12.1    1024: 10.5, 12.6 and 15.8, 16.0   1536: 14.1, 13.7 and 21.3, 17.4
+//   32/8 x 128, e4m3 (2):     256: 6.2, 9.8 and 9.4, 12.1     512: 11.1, 11.0 and 14.8, 14.8   1024: 19.2, 14.6 and 25.5, 19.8
+//   16/16 x 128, 16 bits (2): 256: 5.7, 8.9 and 10.1, 11.7    512: 10.1, 11.2 and 16.2, 15.7   1024: 18.1, 15.2 and 26.4, 23.8
+//   32/8 x 160, 16 bits (1):  256: 11.6, 13.0 and 18.7, 16.9  512: 20.3, 16.7 and 30.0, 23.7
+// and four sequences of up to 1000 keys: 10.3-13.8 and 8.9-10.3.
+constexpr int64_t kDirectTiles = 4, kDirectUnits = 256;
+bool is_direct(const blk_decode_paged_desc* d) {
+    const blk_paged_desc& c = d->cache;
+    const int64_t G = d->n_heads / c.n_kv_heads;
+    const bool e8 = c.kind == BLK_CACHE_E4M3;
+    const int ctas = e8 && c.head_dim == 64 && G <= 4 ? 4 : !e8 && c.head_dim == 160 ? 1 : 2;
     return c.max_pages * c.page_tokens <= kDirectTiles * kTK &&
-           c.batch * c.n_kv_heads <= (int64_t(1) << 24);
+           c.batch * c.n_kv_heads * ((G + 7) / 8) <= kDirectUnits * ctas;
 }
 
 // Query heads of a unit. Sixteen, each reading of the cache for twice the heads, where the bytes bound
@@ -220,7 +231,7 @@ bool is_direct(const blk_paged_desc& c) {
 int unit_heads(const blk_decode_paged_desc* d) {
     const int64_t G = d->n_heads / d->cache.n_kv_heads;
     if (G <= 8) return G == 1 ? 1 : G <= 4 ? 4 : 8;
-    return d->cache.kind == BLK_CACHE_16BIT && d->cache.head_dim >= 128 && !is_direct(d->cache) ? 16 : 8;
+    return d->cache.kind == BLK_CACHE_16BIT && d->cache.head_dim >= 128 && !is_direct(d) ? 16 : 8;
 }
 // ... and units of a kv head
 int64_t unit_groups(const blk_decode_paged_desc* d) {
@@ -236,7 +247,7 @@ Layout layout(const blk_decode_paged_desc* d) {
                         unit_heads(d);
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
     Layout L{};
-    if (is_direct(d->cache)) return L;
+    if (is_direct(d)) return L;
     L.po = 0;
     L.pm = up(recs * d->cache.head_dim * 4);
     L.cum = L.pm + up(recs * 8);

@@ -422,7 +422,7 @@ typedef struct {
  * Two launches. The workspace holds partial results, at least
  * blk_attn_decode_paged_workspace_size bytes, 16-byte aligned; calls whose
  * kernels overlap on the GPU need a workspace each. Where block_table has room for a
- * few hundred keys only: one launch, 0 bytes (NULL will do). */
+ * few hundred keys only and sequences are few: one launch, 0 bytes (NULL will do). */
 blk_status blk_attn_decode_paged_workspace_size(const blk_decode_paged_desc* d, size_t* bytes);
 blk_status blk_attn_decode_paged(const blk_decode_paged_desc* d, const void* q, const void* k_cache,
                                  const void* v_cache, const float* k_scale, const float* v_scale,

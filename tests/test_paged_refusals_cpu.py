@@ -1,7 +1,8 @@
 """More refusals of the paged cache's calls and of the rotary's plan, without a GPU: outputs that lie
-on top of themselves."""
+on top of themselves; and where a paged decode step takes one launch."""
 import pytest
 
+import alibi_attention_block_gb300 as blk
 from tests.test_paged_abi_cpu import EINVAL, FAKE, append, lib, rope  # noqa: F401
 
 OVERLAPS = [  # strides of heads and tokens of an output [4, 10, 128]
@@ -29,3 +30,15 @@ def test_outputs_apart_are_not_refused(lib, head, token):  # noqa: F811
     assert rope(lib, qo=FAKE, **out) == EINVAL and b"in place" in lib.blk_last_error()
     assert rope(lib, qo=FAKE, tokens=1, **one) == EINVAL and b"in place" in lib.blk_last_error()
     assert append(lib, n_heads=4, q=FAKE, qo=FAKE, **out) == EINVAL and b"in place" in lib.blk_last_error()
+
+
+@pytest.mark.parametrize("kind,H,Hk,d,most", [  # units (eight query heads of a kv head) of one launch
+    (1, 16, 16, 64, 1024), (1, 64, 16, 64, 1024), (1, 32, 4, 64, 512), (0, 16, 16, 64, 512), (1, 32, 8, 128, 512),
+    (0, 16, 4, 128, 512), (0, 16, 1, 128, 256), (1, 32, 2, 160, 256), (0, 32, 8, 160, 256)])
+def test_few_units_take_one_launch(lib, kind, H, Hk, d, most):  # noqa: F811
+    """Many sequences of few keys take two launches, and need a workspace for them."""
+    def need(batch, keys):
+        fields = (9, 16, Hk, d, batch, keys // 16, Hk * 16 * d, kind)
+        return blk.attn_decode_paged_workspace_size(blk.decode_paged_desc(fields, H, H * d, d))
+    assert need(most // Hk, 512) == 0 and need(1, 16) == 0
+    assert need(most // Hk + 1, 512) > 0 and need(most // Hk + 1, 16) > 0 and need(1, 528) > 0
