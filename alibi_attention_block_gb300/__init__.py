@@ -371,6 +371,8 @@ def rope_plan(span, base=10000.0, interleaved=False, scaling="none", factor=1.0,
     with the same values share it."""
     if scaling not in _SCALING:
         raise ValueError(f"scaling must be one of {sorted(_SCALING)}")
+    if not -2 ** 31 <= span < 2 ** 31 or span != int(span):
+        raise ValueError(f"span must be a whole number of 32 bits, got {span}")
     return _rope_plan(int(span), 1 if interleaved else 0, float(base), _SCALING[scaling], float(amplitude),
                       float(factor), float(original_len), float(beta_slow), float(beta_fast))
 

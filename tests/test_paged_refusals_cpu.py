@@ -1,5 +1,5 @@
 """More refusals of the paged cache's calls and of the rotary's plan, without a GPU: outputs that lie
-on top of themselves; and where a paged decode step takes one launch."""
+on top of themselves, spans; and where a paged decode step takes one launch."""
 import pytest
 
 import alibi_attention_block_gb300 as blk
@@ -42,3 +42,11 @@ def test_few_units_take_one_launch(lib, kind, H, Hk, d, most):  # noqa: F811
         return blk.attn_decode_paged_workspace_size(blk.decode_paged_desc(fields, H, H * d, d))
     assert need(most // Hk, 512) == 0 and need(1, 16) == 0
     assert need(most // Hk + 1, 512) > 0 and need(most // Hk + 1, 16) > 0 and need(1, 528) > 0
+
+
+@pytest.mark.parametrize("span", [2 ** 32 + 64, 2 ** 31, -2 ** 32 + 64, 64.5, float("nan"), float("inf")])
+def test_spans_that_are_no_32_bit_numbers(lib, span):  # noqa: F811
+    """... were cut to the 32 bits, or to the whole number, that the library took for a span."""
+    with pytest.raises(ValueError):
+        blk.rope_plan(span)
+    assert blk.rope_plan(64.0) is blk.rope_plan(64)
