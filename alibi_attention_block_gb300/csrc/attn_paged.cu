@@ -208,11 +208,11 @@ blk_status check_desc(const blk_decode_paged_desc* d) {
 // Whether a sequence's tiles, and the units (of eight heads), are so few that a CTA takes each unit whole: 512 keys, and
 // 256 units for each CTA that an SM holds (Cfg::kCtas), not much over one round of CTAs. Above that a CTA's start for every unit, and
 // units of unequal length, cost more than the second launch. One launch and two, in us, bf16 (units: of up to 100 keys, of up to 500):
-//   16/16 x 64, e4m3 (4):     512: 6.7, 9.8 and 9.9, 12.1    1024: 10.5, 12.6 and 15.8, 16.0   1536: 14.1, 13.7 and 21.3, 17.4
-//   32/8 x 128, e4m3 (2):     256: 6.2, 9.8 and 9.4, 12.1     512: 11.1, 11.0 and 14.8, 14.8   1024: 19.2, 14.6 and 25.5, 19.8
-//   16/16 x 128, 16 bits (2): 256: 5.7, 8.9 and 10.1, 11.7    512: 10.1, 11.2 and 16.2, 15.7   1024: 18.1, 15.2 and 26.4, 23.8
-//   32/8 x 160, 16 bits (1):  256: 11.6, 13.0 and 18.7, 16.9  512: 20.3, 16.7 and 30.0, 23.7
-// and four sequences of up to 1000 keys: 10.3-13.8 and 8.9-10.3.
+//   16/16 x 64, e4m3 (4):     512: 5.7, 9.1 and 8.1, 11.4     1024: 9.7, 11.8 and 15.2, 15.4   1536: 13.6, 13.1 and 20.1, 16.9
+//   32/8 x 128, e4m3 (2):     256: 5.3, 9.1 and 7.9, 11.0     512: 10.1, 10.3 and 14.4, 13.9   1024: 18.8, 14.2 and 24.9, 19.2
+//   16/16 x 128, 16 bits (2): 256: 4.9, 8.1 and 9.0, 10.7     512: 8.8, 10.4 and 13.4, 13.8    1024: 17.4, 14.5 and 24.8, 22.1
+//   32/8 x 160, 16 bits (1):  256: 10.1, 12.3 and 15.5, 14.8  512: 19.8, 16.0 and 28.6, 22.3
+// and four sequences of up to 1000 keys (in a graph): 10.3-13.8 and 8.9-10.3.
 constexpr int64_t kDirectTiles = 4, kDirectUnits = 256;
 bool is_direct(const blk_decode_paged_desc* d) {
     const blk_paged_desc& c = d->cache;
