@@ -83,14 +83,14 @@ __device__ __forceinline__ void join(const MergeArgs& a, const Records& r, int c
         float mn = m;
 #pragma unroll
         for (int i = 0; i < 4; ++i) mn = fmaxf(mn, ml[i].x);
-        const float keep = m == mn ? 1.f : exp2f(0.5f * (m - mn));
+        const float keep = m == mn ? 1.f : ex2_approx(0.5f * (m - mn));
         m = mn;
         l = l * keep * keep;
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] *= keep * keep;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float half = ml[i].x == mn ? 1.f : exp2f(0.5f * (ml[i].x - mn));
+            const float half = ml[i].x == mn ? 1.f : ex2_approx(0.5f * (ml[i].x - mn));
             const float w = half * half;
             l = fmaf(half, half * ml[i].y, l);
             const float v[8] = {x[i].x, x[i].y, x[i].z, x[i].w, y[i].x, y[i].y, y[i].z, y[i].w};
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kRowThreads) paged_merge_row_kernel(const Merg
 #pragma unroll 4
         for (int k = 0; k < n; ++k) {
             const float2 x = ml[k];
-            const float half = x.x == top ? 1.f : exp2f(0.5f * (x.x - top));
+            const float half = x.x == top ? 1.f : ex2_approx(0.5f * (x.x - top));
             l = fmaf(half, half * x.y, l);
             f = fmaf(half * half, parts[k][c], f);
         }
