@@ -367,7 +367,8 @@ def rope_plan(span, base=10000.0, interleaved=False, scaling="none", factor=1.0,
     """The plan of a rotary for ``rope_positions`` and ``kv_append_paged``, made
     once: span dims of a head, in halves or interleaved pairs, with positions
     scaled "linear" or "by_parts" (blk_rope_scaling in include/blk.h says
-    how), turned dims times amplitude. Plain host data, not to be changed: calls
+    how; the parts are weighted by a pair's turns, not by its index), turned
+    dims times amplitude. Plain host data, not to be changed: calls
     with the same values share it."""
     if scaling not in _SCALING:
         raise ValueError(f"scaling must be one of {sorted(_SCALING)}")

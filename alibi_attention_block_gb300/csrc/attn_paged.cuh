@@ -36,9 +36,9 @@
 // there anyway too), 2^-16 off in bf16, 2^-22 in fp16 (held times 2^7, its second part times 2^11: weights down to 2^-21 of
 // the largest in fp16's normal range). With weights of one part (two in bf16 over e4m3) the outputs of few keys, which do not
 // average their errors, were up to 8 % further from the definition than the output's rounding leaves them. The times are the same
-// (48 sequences of up to 8192 keys: within 1 %) but for e4m3 with eight heads and more on a kv head, bf16: 256
-// sequences, 8 on one, 42.8 -> 36.1 us at head_dim 64 (two CTAs per SM in the place of four, whose registers spilled),
-// 39.4 at 128, 47.1 -> 49.0 at 160.
+// (48 sequences of up to 8192 keys: within 1 %) but for many heads on a kv head, 256 sequences, bf16, 8 on one: e4m3 42.1 ->
+// 36.4 us at head_dim 64 (two CTAs per SM in the place of four), 45.8 -> 49.5 at 160, 16 bits 36.4 -> 37.5 at 64; 32 on one
+// 126 -> 117, 139 -> 166 (spills) and 107 -> 110, 16 bits at 128 115 -> 122.
 //
 // Work: a unit is (sequence, kv head, up to eight of its query heads, sixteen over wide 16-bit
 // rows: unit_heads in attn_paged.cu) of ceil(len / 128) key tiles. The tiles of all units, in one
@@ -103,7 +103,9 @@ struct Cfg {
     static constexpr int kFixed =
         2 * kQBytes + 2 * kPBytes + 8 * 2 * 8 * 4 + 4 * kHeads * 4 * 4 + 2 * kHeads * 4 + 512 + 16;
     // two CTAs per SM, so that one's chain of scores, softmax and product fills the
-    // other's gaps; four where tiles are short, one where three of them do not fit twice
+    // other's gaps; four where tiles are short, one where three of them do not fit twice (16 x 64, e4m3, by four, three and
+    // two: 256 sequences of up to 1000 keys 46.1, 48.9 and 63.3 us, 48 of up to 8192 56.4, 52.2 and 60.7; 16/4 x 64: 23.9, 24.8 and
+    // 24.8, 24.2, 23.7 and 24.4; with eight heads on a kv head four spilled, 42.8 us for the 36.1 of two)
     static constexpr int fit(int ctas) { return (228 * 1024 / ctas - 2048 - 64 - kFixed) / kTile; }
     static constexpr int kCtas = E8 && D == 64 && kNO == 16 ? 4 : fit(2) < 3 ? 1 : 2;
     static constexpr int kFit = fit(kCtas);

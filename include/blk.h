@@ -287,7 +287,9 @@ typedef enum {
     BLK_ROPE_LINEAR = 1,   /* theta_j / factor (positions interpolated) */
     BLK_ROPE_BY_PARTS = 2  /* by a pair's turns in the original context, r_j = original_len theta_j /
                               (2 pi): g theta_j + (1 - g) theta_j / factor with
-                              g = clamp((r_j - beta_slow) / (beta_fast - beta_slow), 0, 1) */
+                              g = clamp((r_j - beta_slow) / (beta_fast - beta_slow), 0, 1): linear in the
+                              turns. (Others of this name are linear in the pair's index j, between two
+                              rounded bounds: other frequencies, which no plan has) */
 } blk_rope_scaling;
 
 typedef struct {
