@@ -34,7 +34,7 @@
 //
 // 16 bits: the operands in the storage type, a weight as the sum of two such numbers (the second one's columns are
 // there anyway too), 2^-16 off in bf16, 2^-22 in fp16 (held times 2^7, its second part times 2^11: weights down to 2^-21 of
-// the largest in fp16's normal range). With weights of one part (two in bf16 over e4m3) the outputs of few keys, which do not
+// the largest in fp16's normal range), neither of them below 0, so that infinite values stay infinite. With weights of one part (two in bf16 over e4m3) the outputs of few keys, which do not
 // average their errors, were up to 8 % further from the definition than the output's rounding leaves them. The times are the same
 // (48 sequences of up to 8192 keys: within 1 %) but for many heads on a kv head, 256 sequences, bf16, 8 on one: e4m3 42.1 ->
 // 36.4 us at head_dim 64 (two CTAs per SM in the place of four), 45.8 -> 49.5 at 160, 16 bits 36.4 -> 37.5 at 64; 32 on one
@@ -87,7 +87,7 @@ struct Cfg {
     static constexpr bool kF16 = dt_traits<T>::mma_fmt == 0;
     static constexpr int kQParts = !E8 ? 1 : kF16 ? 3 : 2, kPParts = E8 ? 3 : 2;  // of queries, of weights
     // each part, next to the one before it, is held times this
-    static constexpr float kUp = E8 ? 32.f : kF16 ? 2048.f : 256.f;
+    static constexpr int kUp = E8 ? 32 : kF16 ? 2048 : 256;
     static constexpr int kQUsed = kQParts * GP, kPUsed = kPParts * GP;  // columns with something in them
     static constexpr int columns(int used) { return used <= 16 ? 16 : 32; }
     static constexpr int kNS = columns(kQUsed), kNO = columns(kPUsed);
@@ -220,20 +220,29 @@ __device__ __forceinline__ float2 of_codes(uint32_t c) {
     return __half22float2(
         __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c), __NV_E4M3)));
 }
-// The numbers' parts, each remainder times 32 (e4m3), 2^11 (fp16) or 2^8 (bf16): c[i] holds the codes, or the 16-bit
-// numbers, of part i of both.
-template <typename T, bool E8, int PARTS>
+// The numbers' parts, each remainder times 32: c[i] holds the codes of part i of both.
+template <int PARTS>
 __device__ __forceinline__ void split_parts(float x, float y, uint32_t (&c)[PARTS]) {
-    constexpr float up = Cfg<T, E8, 64, 1>::kUp;
 #pragma unroll
     for (int i = 0; i < PARTS; ++i) {
-        c[i] = E8 ? to_codes(x, y) : dt_traits<T>::pack2(x, y);
+        c[i] = to_codes(x, y);
         if (i + 1 < PARTS) {
-            const float2 f = E8 ? of_codes(c[i]) : dt_traits<T>::unpack2(c[i]);
-            x = (x - f.x) * up;
-            y = (y - f.y) * up;
+            const float2 f = of_codes(c[i]);
+            x = (x - f.x) * 32.f;
+            y = (y - f.y) * 32.f;
         }
     }
+}
+// Two numbers of at least 0 as sums of two 16-bit ones, the first towards zero, the remainder times UP. The second is never 0
+// (least: the type's least number): both parts times an infinity are that infinity, and their sum is.
+template <typename T, int UP>
+__device__ __forceinline__ void split_16(float x, float y, uint32_t (&c)[2]) {
+    constexpr bool f16 = dt_traits<T>::mma_fmt == 0;
+    constexpr float least = f16 ? 0x1p-24f : 0x1p-126f;
+    if (f16) asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(c[0]) : "f"(y), "f"(x));
+    else asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(c[0]) : "f"(y), "f"(x));
+    const float2 f = dt_traits<T>::unpack2(c[0]);
+    c[1] = dt_traits<T>::pack2(fmaxf((x - f.x) * UP, least), fmaxf((y - f.y) * UP, least));
 }
 __device__ __forceinline__ void st_byte(uint32_t at, uint32_t v) {
     asm volatile("st.shared.b8 [%0], %1;" ::"r"(at), "r"(v) : "memory");
@@ -746,7 +755,7 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
                     if (2 * (lane + 32 * i) >= D) continue;
                     uint32_t c8[C::kQParts];
                     if (E8) {
-                        split_parts<T, true>(f[h][i].x * down, f[h][i].y * down, c8);
+                        split_parts<C::kQParts>(f[h][i].x * down, f[h][i].y * down, c8);
                         // an infinity is no code: a NaN, as its scores' softmax is
                         if (isinf(f[h][i].x)) c8[0] |= 0x7fu;
                         if (isinf(f[h][i].y)) c8[0] |= 0x7f00u;
@@ -814,9 +823,10 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
                 if ((!half || lane < 16) && dim < D) {
 #pragma unroll
                     for (int h = 0; h < GP; ++h) {
-                        float v = fmaf(__uint_as_float(o[mb][GP + h]), 1.f / C::kUp, __uint_as_float(o[mb][h]));
+                        float v = fmaf(__uint_as_float(o[mb][GP + h]), 1.f / static_cast<float>(C::kUp),
+                                       __uint_as_float(o[mb][h]));
                         if (C::kPParts > 2)
-                            v = fmaf(__uint_as_float(o[mb][(C::kPParts - 1) * GP + h]), 1.f / (C::kUp * C::kUp), v);
+                            v = fmaf(__uint_as_float(o[mb][(C::kPParts - 1) * GP + h]), 1.f / static_cast<float>(C::kUp * C::kUp), v);
                         if (!a.direct) {
                             a.po[(pend_rec * GP + h) * D + dim] = v * (1.f / (C::kTop * C::kBack));
                         } else if (h < pend_heads) {
@@ -922,7 +932,9 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
 #pragma unroll
                 for (int h = 0; h < GP; h += kStep) {
                     uint32_t c[C::kPParts];
-                    split_parts<T, E8>(p[h] * top, GP > 1 ? p[h + kStep - 1] * top : 0.f, c);
+                    const float x = p[h] * top, y = GP > 1 ? p[h + kStep - 1] * top : 0.f;
+                    if constexpr (E8) split_parts<C::kPParts>(x, y, c);
+                    else split_16<T, C::kUp>(x, y, c);
 #pragma unroll
                     for (int q = 0; q < C::kPParts; ++q)
 #pragma unroll

@@ -186,3 +186,38 @@ def test_scores_of_minus_infinity(room, times, d, G, dt):
         want, mag, p = ref.decode(f64(q[b].float()), kr, vr, np.ones(256, bool))
         bound = bound_of(f64(q[b].float()), kr, vr, None, want, mag, p, dt, 16, d ** -0.5)
         assert (np.abs(o[:, b] - want) <= bound).all(), f"row {b}"
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("d,G", [(64, 1), (128, 4), (128, 16), (160, 8)])
+@pytest.mark.parametrize("room", [0, 200])
+def test_infinite_values(room, d, G, dt):
+    """An infinity among a seen key's values is one in the output (its weight is above 0), whatever the weight's parts are;
+    two of both signs are a NaN; a masked key's reach nothing. 16 bits."""
+    page, Hk, t = 16, 2, ref.DTYPES[dt]
+    B, cols = 4, 32
+    g = torch.Generator(device="cuda")
+    g.manual_seed(d + G)
+    k, v = (torch.randn((B * cols, Hk, page, d), generator=g, device="cuda").to(t) for _ in "kv")
+    q = torch.randn((B, Hk * G, d), generator=g, device="cuda").to(t)
+    lens = [500, 3, 257, 130]
+    table = torch.full((B, cols + room), -1, dtype=torch.int32)
+    table[:, :cols] = torch.arange(B * cols, dtype=torch.int32).reshape(B, cols)
+    good = blk.attn_decode_paged(q, k, v, table.cuda(), i32(lens))
+    rows = v.view(B, cols, Hk, page, d)
+    want = good.clone().view(B, Hk, G, d)
+    inf = float("inf")
+    for b, n in enumerate(lens):
+        for i, key in enumerate((0, 1, n // 2, n - 2, n - 1)):  # each in a dim of its own; in 20 + i: its negative
+            rows[b, key // page, :, key % page, i] = inf
+            rows[b, key // page, :, key % page, 20 + i] = -inf
+            want[b, :, :, i], want[b, :, :, 20 + i] = inf, -inf
+        rows[b, 0, :, 0, 40], rows[b, (n - 1) // page, :, (n - 1) % page, 40] = inf, -inf
+        want[b, :, :, 40] = float("nan")
+        if n % page:
+            rows[b, n // page, :, n % page:] = inf  # behind the length
+    o = blk.attn_decode_paged(q, k, v, table.cuda(), i32(lens))
+    blk.check_device_status()
+    want = want.view_as(o)
+    assert torch.equal(torch.isnan(o), torch.isnan(want))
+    assert torch.equal(o.nan_to_num(7.0, 1e4, -1e4), want.nan_to_num(7.0, 1e4, -1e4))
