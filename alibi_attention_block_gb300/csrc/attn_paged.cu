@@ -224,8 +224,8 @@ bool is_direct(const blk_decode_paged_desc* d) {
 }
 
 // Query heads of a unit. Sixteen, each reading of the cache for twice the heads, where the bytes bound
-// (256 sequences of up to 8192 keys, 16 heads on one, 16 bits: 93 -> 67 us at head_dim 128, 144 -> 91 at 160;
-// 32 on one: 178 -> 122, 280 -> 171); not at 64 (59 -> 57, but a call of 32 sequences 16.7 -> 17.6), not over e4m3,
+// (256 sequences of up to 8192 keys, 16 heads on one, 16 bits: 93 -> 67 us at head_dim 128, 144 -> 94 at 160;
+// 32 on one: 178 -> 123, 280 -> 177); not at 64 (59 -> 57, but a call of 32 sequences 16.7 -> 17.6), not over e4m3,
 // where the softmax of each head costs more than its bytes (64 -> 77), and not where a CTA takes a unit
 // whole, which halves the CTAs (4 sequences of 500 keys, 32/2: 9.0 -> 9.8).
 int unit_heads(const blk_decode_paged_desc* d) {

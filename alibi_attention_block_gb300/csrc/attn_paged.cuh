@@ -38,7 +38,7 @@
 // average their errors, were up to 8 % further from the definition than the output's rounding leaves them. The times are the same
 // (48 sequences of up to 8192 keys: within 1 %) but for many heads on a kv head, 256 sequences, bf16, 8 on one: e4m3 42.1 ->
 // 36.4 us at head_dim 64 (two CTAs per SM in the place of four), 45.8 -> 49.5 at 160, 16 bits 36.4 -> 37.5 at 64; 32 on one
-// 126 -> 117, 139 -> 166 (spills) and 107 -> 110, 16 bits at 128 115 -> 122.
+// 126 -> 117, 139 -> 166 (spills) and 107 -> 111, 16 bits at 128 115 -> 123, at 160 161 -> 177.
 //
 // Work: a unit is (sequence, kv head, up to eight of its query heads, sixteen over wide 16-bit
 // rows: unit_heads in attn_paged.cu) of ceil(len / 128) key tiles. The tiles of all units, in one
@@ -997,7 +997,7 @@ __device__ __forceinline__ void paged_body(const PagedArgs& a, const PagedMaps& 
             }
             if (!ok) break;
             // Keys seen, each with a score of -inf: no softmax (0 / 0) unless another segment has a finite one. Whether any is
-            // seen is looked up again (kept from tile to tile: 127 us for 122, 256 sequences, 32 heads on a kv head). Over
+            // seen is looked up again (kept from tile to tile: 127 us for 122, 256 sequences, 32 heads on one). Over
             // e4m3 such a score is NaN: the queries' operand has no infinity, and codes are none.
             if (!E8) {
                 bool none = false;
